@@ -312,6 +312,12 @@ def _own(s, op):
     return s["out"], s["lse"]
 
 
+def _gated(o, gate):
+    """The gate is defined on BF16 operands: the attention result and the sigmoid are rounded, then their product,
+    so that a fused call equals attention followed by the standalone gate."""
+    return (o.to(torch.bfloat16).float() * torch.sigmoid(gate.float()).to(torch.bfloat16).float()).to(torch.bfloat16)
+
+
 def _decode(s):
     c = s["case"]
     b, hq, hkv = c["batch"], c["hq"], c["hkv"]
@@ -341,7 +347,7 @@ def _decode(s):
     o = p @ v
     o = torch.where(total[..., None] > 0, o / total[..., None], torch.zeros_like(o)).view(b, hq, D)
     lse = (safe + torch.log(total)).view(b, hq)
-    return (o * torch.sigmoid(s["gate"].float())).to(torch.bfloat16), lse
+    return _gated(o, s["gate"]), lse
 
 
 def _cache(s):
@@ -408,7 +414,7 @@ def _packed(s):
     total = p.sum(-1, keepdim=True)
     o = ((p @ v) / total).permute(2, 0, 1, 3).reshape(tq, hq, D)
     lse = (top + torch.log(total)).view(hq, tq)
-    return (o * torch.sigmoid(s["gate"].float())).to(torch.bfloat16), lse
+    return _gated(o, s["gate"]), lse
 
 
 # ---------------------------------------------------------------- the definition in 64 bits

@@ -16,6 +16,12 @@ attention output sigmoid gate into the existing Triton decode stage2"):
 
 K/V pools of dtype torch.float8_e4m3fn (or uint8 e4m3 codes) select the FP8-cache
 kernels; their values are ``k_descale * e4m3(code)`` and ``v_descale * e4m3(code)``.
+
+A 4-bit cache is two uint8 pools of codes [num_slots, Hkv, D / 2] and their scales
+``kv_scales`` [num_slots, Hkv, 2, D / 16]: passing ``kv_scales`` to ``decode`` or
+``decode_ex`` selects it.  ``kv_write_fp4`` and ``qk_norm_mrope_kv_write`` write it,
+``kv_gather_fp4`` reads rows back.  A prompt of packed sequences goes
+``qk_norm_mrope_kv_write`` -> ``prefill_packed``.
 """
 from __future__ import annotations
 
@@ -25,16 +31,17 @@ import threading
 from typing import Optional
 
 __all__ = [
-    "load", "decode", "decode_ex", "decode_noalloc", "decode_step_host", "StepHost", "step_layout", "small_path_cluster", "auto_splits", "pack_step", "STEP_MAP_IN", "STEP_MAP_OUT", "prefill", "prefill_read_error", "qk_norm_rope_kv_write", "gate", "workspace_bytes", "workspace_init", "reserve",
+    "load", "decode", "decode_ex", "decode_noalloc", "decode_step_host", "StepHost", "step_layout", "small_path_cluster", "auto_splits", "pack_step", "STEP_MAP_IN", "STEP_MAP_OUT", "prefill", "prefill_read_error", "qk_norm_rope_kv_write", "prefill_packed", "qk_norm_mrope_kv_write", "mrope_pair_axis",
+    "kv_write_fp4", "kv_gather_fp4", "gate", "workspace_bytes", "workspace_init", "reserve",
     "read_error", "debug_wait_limit", "timing_begin", "timing_end", "status_str", "version", "GdaError", "VARIANT_AUTO", "VARIANT_MMA",
-    "VARIANT_SIMT", "VARIANT_TMA", "MAX_SPLITS", "LIB_PATH", "KV_BF16", "KV_E4M3",
+    "VARIANT_SIMT", "VARIANT_TMA", "MAX_SPLITS", "LIB_PATH", "KV_BF16", "KV_E4M3", "KV_E2M1",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libgda.so")
 
 VARIANT_AUTO, VARIANT_MMA, VARIANT_SIMT, VARIANT_TMA = 0, 1, 2, 3
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_E2M1 = 0, 1, 3
 MAX_SPLITS = 256
 NOALLOC_SCRATCH_BYTES = 16 << 20
 DEVERR_INDEX, DEVERR_TIMEOUT = 0x1, 0x2
@@ -59,7 +66,32 @@ class _Args(ctypes.Structure):
         ("check_indices", ctypes.c_int), ("variant", ctypes.c_int), ("min_chunk", ctypes.c_int),
         ("window", ctypes.c_int), ("sinks", ctypes.c_void_p), ("kv_dtype", ctypes.c_int),
         ("k_descale", ctypes.c_float), ("v_descale", ctypes.c_float), ("max_len", ctypes.c_int),
-        ("total_len", ctypes.c_int64),
+        ("total_len", ctypes.c_int64), ("kv_scales", ctypes.c_void_p),
+    ]
+
+
+class _MropeArgs(ctypes.Structure):
+    _fields_ = [
+        ("qgkv", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("w_q_norm", ctypes.c_void_p),
+        ("w_k_norm", ctypes.c_void_p), ("eps", ctypes.c_float), ("n_axes", ctypes.c_int),
+        ("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p), ("rope_dim", ctypes.c_int), ("kv_dtype", ctypes.c_int),
+        ("q_out", ctypes.c_void_p), ("gate_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p), ("kv_scales", ctypes.c_void_p), ("k_descale", ctypes.c_float),
+        ("v_descale", ctypes.c_float), ("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int),
+    ]
+
+
+class _PackedArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("error_word", ctypes.c_void_p),
     ]
 
 
@@ -85,6 +117,16 @@ def load(path: Optional[str] = None):
         lib.gda_decode_ex.restype = i32
         lib.gda_decode_e4m3.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, f32, i32, vp]
         lib.gda_decode_e4m3.restype = i32
+        lib.gda_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, f32, i32, vp]
+        lib.gda_decode_fp4.restype = i32
+        lib.gda_kv_write_fp4.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, f32, f32, i64, i32, i32, vp]
+        lib.gda_kv_write_fp4.restype = i32
+        lib.gda_kv_gather_fp4.argtypes = [vp, vp, vp, i64, vp, i64, f32, f32, vp, vp, i32, i32, vp]
+        lib.gda_kv_gather_fp4.restype = i32
+        lib.gda_qk_norm_mrope_kv_write.argtypes = [ctypes.POINTER(_MropeArgs), vp]
+        lib.gda_qk_norm_mrope_kv_write.restype = i32
+        lib.gda_prefill_packed.argtypes = [ctypes.POINTER(_PackedArgs), vp]
+        lib.gda_prefill_packed.restype = i32
         lib.gda_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp]
         lib.gda_prefill.restype = i32
         lib.gda_prefill_read_error.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_uint32)]
@@ -186,8 +228,86 @@ def _kv_dtype(k_pool) -> int:
         else KV_BF16
 
 
-def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out):
-    """Checks tensor metadata; returns the pools' element type (KV_BF16 or KV_E4M3)."""
+def _tokens(name, t, heads=None, dim=None, device=None):
+    """Checks a [T, H, D] bf16 CUDA tensor whose tokens may be any distance apart (the parts of
+    a projection's rows) and returns that distance in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 3:
+        raise ValueError("%s must have 3 dims" % name)
+    T, H, D = t.shape
+    if (heads is not None and H != heads) or (dim is not None and D != dim):
+        raise ValueError("%s must be [T, %s, %s]" % (name, "H" if heads is None else heads, "D" if dim is None else dim))
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError("the heads and dims of a token of %s must be contiguous" % name)
+    # one token (or none): its distance to the next is never used
+    return int(st[0]) if T > 1 else max(H * D, 8)
+
+
+def _check_fp4(k_pool, v_pool, kv_scales, D=None, device=None):
+    """Checks a 4-bit cache; returns (num_slots, Hkv)."""
+    import torch
+    _check_tensor("k_pool", k_pool, torch.uint8, 3, device)
+    _check_tensor("v_pool", v_pool, torch.uint8, 3, k_pool.device)
+    kv_scales = _scale_bytes(kv_scales)
+    _check_tensor("kv_scales", kv_scales, torch.uint8, 4, k_pool.device)
+    n, h, half = k_pool.shape
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    if half % 8 != 0 or tuple(kv_scales.shape) != (n, h, 2, half // 8):
+        raise ValueError("kv_scales must be [num_slots, Hkv, 2, D / 16] for pools [num_slots, Hkv, D / 2]")
+    if D is not None and 2 * half != D:
+        raise ValueError("head dims of q and the pools differ")
+    return n, h
+
+
+def _scale_bytes(kv_scales):
+    """kv_scales given as float8_e4m3fn or as its bytes."""
+    import torch
+    if isinstance(kv_scales, torch.Tensor) and kv_scales.dtype == torch.float8_e4m3fn:
+        return kv_scales.view(torch.uint8)
+    return kv_scales
+
+
+class _On:
+    """The device a call's tensors live on: made current for the call (the library launches on
+    the current device), with that device's current stream as the default."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._guard = None
+        if device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+        self._device, self._stream = device, stream
+
+    def __enter__(self):
+        import torch
+        if self._guard is not None:
+            self._guard.__enter__()
+        if self._stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+        if self._stream.device.index != self._device.index:
+            if self._guard is not None:
+                self._guard.__exit__(None, None, None)
+            raise ValueError("stream is on %s, the tensors on %s" % (self._stream.device, self._device))
+        return ctypes.c_void_p(self._stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+
+def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_scales=None):
+    """Checks tensor metadata; returns the pools' element type (KV_BF16, KV_E4M3 or KV_E2M1)."""
     import torch
     _check_tensor("q", q, torch.bfloat16, 3)
     dev = q.device
@@ -195,17 +315,21 @@ def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out):
         _check_tensor("gate", gate_t, torch.bfloat16, 3, dev)
         if gate_t.shape != q.shape:
             raise ValueError("gate must have q's shape")
-    kv = _kv_dtype(k_pool)
-    kdt = k_pool.dtype if kv == KV_E4M3 else torch.bfloat16
-    _check_tensor("k_pool", k_pool, kdt, 3, dev)
-    _check_tensor("v_pool", v_pool, kdt, 3, dev)
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must have the same shape")
+    if kv_scales is not None:
+        kv = KV_E2M1
+        _check_fp4(k_pool, v_pool, kv_scales, q.shape[2], dev)
+    else:
+        kv = _kv_dtype(k_pool)
+        kdt = k_pool.dtype if kv == KV_E4M3 else torch.bfloat16
+        _check_tensor("k_pool", k_pool, kdt, 3, dev)
+        _check_tensor("v_pool", v_pool, kdt, 3, dev)
+        if v_pool.shape != k_pool.shape:
+            raise ValueError("k_pool and v_pool must have the same shape")
     _check_tensor("kv_indptr", kv_indptr, torch.int32, 1, dev)
     _check_tensor("kv_indices", kv_indices, torch.int32, 1, dev)
     if kv_indptr.numel() != q.shape[0] + 1:
         raise ValueError("kv_indptr must have B + 1 entries")
-    if k_pool.shape[2] != q.shape[2]:
+    if kv != KV_E2M1 and k_pool.shape[2] != q.shape[2]:
         raise ValueError("head dims of q and the pools differ")
     if out is not None:
         _check_tensor("out", out, torch.bfloat16, 3, dev)
@@ -215,21 +339,27 @@ def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out):
 
 
 def decode(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, scale: Optional[float] = None,
-           num_splits: int = 0, stream=None, k_descale: float = 1.0, v_descale: float = 1.0):
+           num_splits: int = 0, stream=None, k_descale: float = 1.0, v_descale: float = 1.0, kv_scales=None):
     """Gated GQA decode attention through ``gda_decode`` (library-owned workspace).
 
     q, gate_t: [B, Hq, D] bf16; k_pool, v_pool: [num_slots, Hkv, D] bf16, or
-    float8_e4m3fn / uint8 e4m3 codes (then ``gda_decode_e4m3`` with the descales);
-    kv_indptr: [B+1] int32; kv_indices: [nnz] int32 (all CUDA, contiguous).
+    float8_e4m3fn / uint8 e4m3 codes (then ``gda_decode_e4m3`` with the descales), or
+    with ``kv_scales`` a 4-bit cache (``gda_decode_fp4``); kv_indptr: [B+1] int32; kv_indices: [nnz] int32 (all CUDA, contiguous).
     ``num_splits <= 0`` lets the kernel plan the splits on the device."""
     import torch
-    kv = _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out)
+    kv = _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_scales)
     B, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     if out is None:
         out = torch.empty_like(q)
     if scale is None:
         scale = 1.0 / (D ** 0.5)
+    if kv == KV_E2M1:
+        with _On(q.device, stream) as s:
+            _check(load().gda_decode_fp4(_ptr(q), _ptr(gate_t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales),
+                                         _ptr(kv_indptr), _ptr(kv_indices), _ptr(out), B, Hq, Hkv, D, float(scale),
+                                         float(k_descale), float(v_descale), int(num_splits), s))
+        return out
     if kv == KV_E4M3:
         _check(load().gda_decode_e4m3(_ptr(q), _ptr(gate_t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indptr),
                                       _ptr(kv_indices), _ptr(out), B, Hq, Hkv, D, float(scale), float(k_descale),
@@ -369,23 +499,25 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
               scale: Optional[float] = None, num_splits: int = 0, fuse_gate: bool = True, lse=None,
               check_indices: bool = False, variant: int = VARIANT_AUTO, min_chunk: int = 0,
               window: int = 0, sinks=None, stream=None, k_descale: float = 1.0, v_descale: float = 1.0,
-              max_len: int = 0, total_len: int = 0):
+              max_len: int = 0, total_len: int = 0, kv_scales=None):
     """``gda_decode_ex``: caller workspace (allocated here when None), optional LSE
     output, the unfused first half (``fuse_gate=False``), device index checks, the
     stage-1 variant, a sliding window (last ``window`` positions), per-head
     attention sinks (``sinks``: [Hq] float32 CUDA tensor of logits), for e4m3
-    pools the per-tensor descales, and ``max_len``: a host-known bound on every
+    pools the per-tensor descales, ``kv_scales`` for a 4-bit cache (with the descales), and ``max_len``: a host-known bound on every
     sequence's length (0: none), which lets small batches run as one cluster kernel,
     and ``total_len``: the batch's exact number of KV positions (kv_indptr[B], 0: not
     given); with both, the split count is chosen on the host (``auto_splits``)."""
     import torch
-    kv = _decode_checks(q, gate_t if fuse_gate else None, k_pool, v_pool, kv_indptr, kv_indices, out)
+    kv = _decode_checks(q, gate_t if fuse_gate else None, k_pool, v_pool, kv_indptr, kv_indices, out, kv_scales)
     B, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     if out is None:
         out = torch.empty_like(q)
     if lse is not None:
         _check_tensor("lse", lse, torch.float32, 2, q.device)
+        if kv == KV_E2M1 and tuple(lse.shape) != (B, Hq):
+            raise ValueError("lse must be [B, Hq]")
     if sinks is not None:
         _check_tensor("sinks", sinks, torch.float32, 1, q.device)
         if sinks.numel() != q.shape[1]:
@@ -402,7 +534,12 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
               scale=float(scale), num_splits=int(num_splits), fuse_gate=1 if fuse_gate else 0,
               check_indices=1 if check_indices else 0, variant=int(variant), min_chunk=int(min_chunk),
               window=int(window), sinks=_ptr(sinks), kv_dtype=kv, k_descale=float(k_descale),
-              v_descale=float(v_descale), max_len=int(max_len), total_len=int(total_len))
+              v_descale=float(v_descale), max_len=int(max_len), total_len=int(total_len), kv_scales=_ptr(kv_scales))
+    if kv == KV_E2M1:
+        with _On(q.device, stream) as s:
+            _check(load().gda_decode_ex(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
+                                        workspace.numel() * workspace.element_size(), s))
+        return out
     _check(load().gda_decode_ex(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
                                 workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
@@ -450,6 +587,62 @@ def prefill(q, gate_t, k, v, *, kv_lens=None, out=None, lse=None, scale: Optiona
     return out
 
 
+def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, lse=None,
+                   scale: Optional[float] = None, causal: bool = True, error_word=None, stream=None):
+    """Gated SDPA over packed sequences through ``gda_prefill_packed``.
+
+    q, gate_t: [Tq, Hq, D] bf16 (gate_t None: out = bf16(O)); k, v: [Tk, Hkv, D] bf16; tokens
+    of each may be any multiple of 8 elements apart, so views of a projection's rows
+    serve as they are.  cu_seqlens: [B + 1] int32, each sequence's first query row;
+    cu_seqlens_k: the same for the keys (None: as the queries), where a sequence has
+    more keys than queries when it continues a prefix.  out: [Tq, Hq, D] contiguous (rows
+    of no sequence are left as they are: zeros in an ``out`` allocated here); lse:
+    [Hq, Tq] float32 or None; error_word as in prefill."""
+    import torch
+    sq = _tokens("q", q)
+    dev = q.device
+    Tq, Hq, D = q.shape
+    sg = 0
+    if gate_t is not None:
+        sg = _tokens("gate", gate_t, Hq, D, dev)
+        if gate_t.shape[0] != Tq:
+            raise ValueError("gate must have q's shape")
+    sk = _tokens("k", k, None, D, dev)
+    Tk, Hkv = k.shape[0], k.shape[1]
+    sv = _tokens("v", v, Hkv, D, dev)
+    if v.shape[0] != Tk:
+        raise ValueError("k and v must have the same shape")
+    _check_tensor("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have B + 1 entries")
+    if cu_seqlens_k is None:
+        if Tk != Tq:
+            raise ValueError("k must have q's tokens (or give cu_seqlens_k)")
+        cu_seqlens_k = cu_seqlens
+    else:
+        _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32, 1, dev)
+        if cu_seqlens_k.numel() != cu_seqlens.numel():
+            raise ValueError("cu_seqlens_k must have B + 1 entries")
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, 2, dev)
+        if tuple(lse.shape) != (Hq, Tq):
+            raise ValueError("lse must be [Hq, Tq]")
+    if out is None:
+        out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor("out", out, torch.bfloat16, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if scale is None:
+        scale = 1.0 / (D ** 0.5)
+    a = _PackedArgs(_ptr(q), _ptr(gate_t), _ptr(k), _ptr(v), sq, sg, sk, sv, _ptr(cu_seqlens), _ptr(cu_seqlens_k),
+                    _ptr(out), _ptr(lse), Tq, Tk, cu_seqlens.numel() - 1, Hq, Hkv, D, float(scale),
+                    1 if causal else 0, _ptr(error_word))
+    with _On(dev, stream) as s:
+        _check(load().gda_prefill_packed(ctypes.byref(a), s))
+    return out
+
+
 def prefill_read_error(clear: bool = True, stream=None) -> int:
     """The library's prefill error word on the current device (synchronises)."""
     w = ctypes.c_uint32(0)
@@ -484,6 +677,156 @@ def qk_norm_rope_kv_write(qgkv, slots, k_pool, v_pool, Hq: int, w_q_norm=None, w
         int(rope_dim), _ptr(slots), num_slots, _ptr(q_out), _ptr(gate_out), _ptr(k_pool), _ptr(v_pool),
         B, int(Hq), Hkv, D, _stream(stream)))
     return q_out, gate_out
+
+
+def mrope_pair_axis(sections, interleaved: bool = False):
+    """The axis of each rotated pair for ``sections`` (pairs per axis, e.g. of time, height
+    and width): the axes' pairs one after the other, or ``interleaved``: pair i goes to
+    axis i mod A while that axis has pairs left, and to axis 0 otherwise."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0:
+        raise ValueError("sections must be counts of pairs")
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    A, total = len(sections), sum(sections)
+    axis = [0] * total
+    for a in range(1, A):
+        if sections[a] and a + A * (sections[a] - 1) >= total:
+            raise ValueError("axis %d has too many pairs to interleave" % a)
+        for i in range(sections[a]):
+            axis[a + A * i] = a
+    return axis
+
+
+def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: int, w_q_norm=None, w_k_norm=None,
+                           eps: float = 1e-6, q_out=None, k_out=None, gate_out=None, slots=None, k_pool=None,
+                           v_pool=None, kv_scales=None, k_descale: float = 1.0, v_descale: float = 1.0, stream=None):
+    """The step before attention with rotary positions on several axes, through
+    ``gda_qk_norm_mrope_kv_write``: returns (q_out [T, Hq, D], k_out [T, Hkv, D]).
+
+    qgkv: [T, (2 Hq + 2 Hkv) * D] bf16 rows [q | gate | k | v] (rows may be further apart);
+    positions: [A, T] int32; inv_freq: [rope_dim / 2] float32; pair_axis: a sequence of
+    rope_dim / 2 axis numbers (``mrope_pair_axis``); gate_out: a [T, Hq, D] tensor to copy the
+    gate into, or None.  With slots, k_pool and v_pool (bf16, or uint8 codes with kv_scales:
+    a 4-bit cache) the K and V rows go into the cache too."""
+    import torch
+    _check_rows("qgkv", qgkv)
+    dev = qgkv.device
+    T, width = qgkv.shape
+    Hq, Hkv = int(Hq), int(Hkv)
+    if Hq < 1 or Hkv < 1 or width % (2 * Hq + 2 * Hkv) != 0:
+        raise ValueError("qgkv's rows must hold (2 Hq + 2 Hkv) * D elements")
+    D = width // (2 * Hq + 2 * Hkv)
+    axis = bytes(pair_axis)
+    rope_dim = 2 * len(axis)
+    if rope_dim:
+        _check_tensor("positions", positions, torch.int32, 2, dev)
+        if positions.shape[1] != T:
+            raise ValueError("positions must be [A, T]")
+        _check_tensor("inv_freq", inv_freq, torch.float32, 1, dev)
+        if inv_freq.numel() != len(axis):
+            raise ValueError("inv_freq and pair_axis must have rope_dim / 2 entries")
+        if max(axis) >= positions.shape[0]:
+            raise ValueError("pair_axis names an axis that positions lacks")
+    for name, t in (("w_q_norm", w_q_norm), ("w_k_norm", w_k_norm)):
+        if t is not None:
+            _check_tensor(name, t, torch.bfloat16, 1, dev)
+            if t.numel() != D:
+                raise ValueError("%s must have D entries" % name)
+    outs = []
+    for name, t, h in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("gate_out", gate_out, Hq)):
+        if t is not None:
+            _check_tensor(name, t, torch.bfloat16, 3, dev)
+            if tuple(t.shape) != (T, h, D):
+                raise ValueError("%s must be [T, %d, D]" % (name, h))
+        elif name != "gate_out":
+            t = torch.empty(T, h, D, dtype=torch.bfloat16, device=dev)
+        outs.append(t)
+    q_out, k_out, gate_out = outs
+    num_slots, kv = 0, KV_BF16
+    if k_pool is not None or v_pool is not None or slots is not None or kv_scales is not None:
+        if k_pool is None or v_pool is None or slots is None:
+            raise ValueError("a cache write needs slots, k_pool and v_pool")
+        _check_tensor("slots", slots, torch.int32, 1, dev)
+        if slots.numel() != T:
+            raise ValueError("slots must have T entries")
+        if kv_scales is not None:
+            kv = KV_E2M1
+            num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
+        else:
+            _check_tensor("k_pool", k_pool, torch.bfloat16, 3, dev)
+            _check_tensor("v_pool", v_pool, torch.bfloat16, 3, dev)
+            num_slots, h = k_pool.shape[0], k_pool.shape[1]
+            if v_pool.shape != k_pool.shape or k_pool.shape[2] != D:
+                raise ValueError("k_pool and v_pool must be [num_slots, Hkv, D]")
+        if h != Hkv:
+            raise ValueError("the pools must have Hkv heads")
+    a = _MropeArgs(_ptr(qgkv), qgkv.stride(0) if T > 1 else width, _ptr(w_q_norm), _ptr(w_k_norm), float(eps),
+                   positions.shape[0] if rope_dim else 0, _ptr(positions) if rope_dim else None,
+                   T if rope_dim else 0, _ptr(inv_freq) if rope_dim else None,
+                   ctypes.cast(ctypes.c_char_p(axis), ctypes.c_void_p), rope_dim, kv, _ptr(q_out), _ptr(gate_out),
+                   _ptr(k_out), _ptr(slots), num_slots, _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), float(k_descale),
+                   float(v_descale), T, Hq, Hkv, D)
+    with _On(dev, stream) as s:
+        _check(load().gda_qk_norm_mrope_kv_write(ctypes.byref(a), s))
+    return q_out, k_out
+
+
+def _check_rows(name, t):
+    """A 2-D bf16 CUDA tensor with contiguous rows, any distance apart."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must have 2 dims and contiguous rows" % name)
+
+
+def kv_write_fp4(k, v, slots, k_pool, v_pool, kv_scales, k_descale: float = 1.0, v_descale: float = 1.0, stream=None):
+    """Quantise the rows of k and v ([T, Hkv, D] bf16, tokens any multiple of 8 elements apart)
+    into a 4-bit cache at ``slots`` ([T] int32), through ``gda_kv_write_fp4``."""
+    import torch
+    sk = _tokens("k", k)
+    T, Hkv, D = k.shape
+    sv = _tokens("v", v, Hkv, D, k.device)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same shape")
+    _check_tensor("slots", slots, torch.int32, 1, k.device)
+    if slots.numel() != T:
+        raise ValueError("slots must have T entries")
+    num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, k.device)
+    if h != Hkv:
+        raise ValueError("the pools must have Hkv heads")
+    with _On(k.device, stream) as s:
+        _check(load().gda_kv_write_fp4(_ptr(k), sk, _ptr(v), sv, _ptr(slots), num_slots, _ptr(k_pool), _ptr(v_pool),
+                                       _ptr(kv_scales), float(k_descale), float(v_descale), T, Hkv, D, s))
+
+
+def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_descale: float = 1.0, k_out=None,
+                  v_out=None, stream=None):
+    """The rows of a 4-bit cache that ``indices`` ([N] int32) name, as bf16 [N, Hkv, D] tensors
+    (k, v), through ``gda_kv_gather_fp4``; an index outside the pools gives zeros."""
+    import torch
+    num_slots, Hkv = _check_fp4(k_pool, v_pool, kv_scales)
+    dev, D = k_pool.device, 2 * k_pool.shape[2]
+    _check_tensor("indices", indices, torch.int32, 1, dev)
+    N = indices.numel()
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(N, Hkv, D, dtype=torch.bfloat16, device=dev)
+        else:
+            _check_tensor(name, t, torch.bfloat16, 3, dev)
+            if tuple(t.shape) != (N, Hkv, D):
+                raise ValueError("%s must be [N, Hkv, D]" % name)
+        outs.append(t)
+    with _On(dev, stream) as s:
+        _check(load().gda_kv_gather_fp4(_ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), num_slots, _ptr(indices), N,
+                                        float(k_descale), float(v_descale), _ptr(outs[0]), _ptr(outs[1]), Hkv, D, s))
+    return outs[0], outs[1]
 
 
 def gate(o, gate_t, out=None, stream=None):

@@ -52,6 +52,13 @@ int g_tmax = 0, g_tused = 0;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Bounds of the row-wise entry points: launch grids and row indexes stay within 31 bits.
+constexpr int64_t kMaxRows = 0x7FFFFF00LL;  // and a 128-row tile past the last row
+constexpr int kMaxHeads = 4096;
+
+// A factor that values are divided by.
+bool descale_ok(float d) { return isfinite(d) && d > 0.0f; }
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int check_sizes(int B, int Hq, int Hkv, int D, int num_splits) {
@@ -115,14 +122,19 @@ int validate_args(const gda_args* a) {
   if (a->check_indices && a->num_slots < 0) return GDA_ERR_SHAPE;
   if (a->variant < 0 || a->variant > GDA_VARIANT_TMA) return GDA_ERR_UNSUPPORTED;
   if (a->min_chunk < 0 || a->window < 0 || a->max_len < 0 || a->total_len < 0) return GDA_ERR_SHAPE;
-  if (a->kv_dtype != GDA_KV_BF16 && a->kv_dtype != GDA_KV_E4M3) return GDA_ERR_UNSUPPORTED;
-  if (a->kv_dtype == GDA_KV_E4M3) {
+  if (a->kv_dtype != GDA_KV_BF16 && a->kv_dtype != GDA_KV_E4M3 && a->kv_dtype != GDA_KV_E2M1)
+    return GDA_ERR_UNSUPPORTED;
+  if (a->kv_dtype != GDA_KV_BF16) {
     if (a->variant != GDA_VARIANT_AUTO && a->variant != GDA_VARIANT_MMA) return GDA_ERR_UNSUPPORTED;
     if (!isfinite(a->k_descale) || !isfinite(a->v_descale)) return GDA_ERR_ARG;
   }
   if (a->B == 0) return GDA_OK;
   if (!a->q || !a->k_pool || !a->v_pool || !a->kv_indptr || !a->kv_indices || !a->out) return GDA_ERR_NULL;
   if (a->fuse_gate && !a->gate) return GDA_ERR_NULL;
+  if (a->kv_dtype == GDA_KV_E2M1) {
+    if (!a->kv_scales) return GDA_ERR_NULL;
+    if (!aligned(a->kv_scales, 16)) return GDA_ERR_ALIGN;
+  }
   if (!aligned(a->q, 16) || !aligned(a->k_pool, 16) || !aligned(a->v_pool, 16) || !aligned(a->out, 16) ||
       (a->gate && !aligned(a->gate, 16)) || !aligned(a->kv_indptr, 4) || !aligned(a->kv_indices, 4) ||
       (a->lse && !aligned(a->lse, 4)) || (a->sinks && !aligned(a->sinks, 4)))
@@ -187,12 +199,13 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
     ps.Hq = a->Hq;
     ps.Hkv = a->Hkv;
     ps.G = a->Hq / a->Hkv;
-    const bool fp8 = a->kv_dtype == GDA_KV_E4M3;
-    // e4m3 pools: k_descale joins the score scale (one rounding, from double)
-    ps.scale_log2 = fp8 ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
+    const bool codes = a->kv_dtype != GDA_KV_BF16;
+    // pools of codes: k_descale joins the score scale (one rounding, from double)
+    ps.scale_log2 = codes ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
                         : a->scale * 1.44269504088896340736f;
-    ps.kv_fp8 = fp8 ? 1 : 0;
-    ps.v_descale = fp8 ? a->v_descale : 1.0f;
+    ps.kv = a->kv_dtype == GDA_KV_E2M1 ? 2 : codes ? 1 : 0;
+    ps.scales = a->kv_scales;
+    ps.v_descale = codes ? a->v_descale : 1.0f;
     ps.window = a->window;
     ps.fuse_gate = a->fuse_gate ? 1 : 0;
     cudaEvent_t s_end = nullptr;
@@ -212,7 +225,7 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   const Layout l = layout(a->B, a->Hq, a->Hkv, a->D, a->num_splits);
   unsigned char* base = static_cast<unsigned char*>(ws);
   const int npass = passes(a->Hq, a->Hkv);
-  const bool fp8 = a->kv_dtype == GDA_KV_E4M3;
+  const bool fp8 = a->kv_dtype == GDA_KV_E4M3, fp4 = a->kv_dtype == GDA_KV_E2M1;
   const int variant = (a->variant == GDA_VARIANT_SIMT)  ? gda::kVariantSimt
                       : (a->variant == GDA_VARIANT_TMA) ? gda::kVariantTma
                                                         : gda::kVariantMma;
@@ -221,7 +234,8 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   // FP8 kernel in pairs, except for three groups (a half-empty pair costs a full one, and
   // two pairs measured no faster than three single passes on b64_l4096 lengths: 135.0
   // us for G = 32's two pairs against 135.9 us for G = 24's three passes)
-  const int team = (variant != gda::kVariantMma || npass < 2) ? 1 : fp8 ? (npass == 3 ? 1 : 2) : team_size(npass);
+  // (over a 4-bit cache every group of 8 query heads reads the rows for itself)
+  const int team = (variant != gda::kVariantMma || npass < 2 || fp4) ? 1 : fp8 ? (npass == 3 ? 1 : 2) : team_size(npass);
   const int nteam = (npass + team - 1) / team;
   // the heads that split the batch into segments for the schedule
   const long long vheads = (long long)a->Hkv * nteam;
@@ -229,7 +243,7 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   // the rule's e4m3 variant: a position streams in half the time, so the per-CTA bound
   // for the stream schedule is twice as many positions and S_opt comes from 16 S^2 >
   // lmax (half the BF16 count)
-  const int kv8 = fp8 ? 1 : 0;
+  const int kv8 = fp8 || fp4 ? 1 : 0;
   const int auto_grid = sms < gda::kAutoMaxCtas ? sms : gda::kAutoMaxCtas;
   int splits = a->num_splits > 0 ? a->num_splits : 0;
   if (splits == 0 && a->window == 0 && a->max_len > 0 && a->total_len > 0) {
@@ -273,15 +287,16 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   p1.team = team;
   p1.nteam = nteam;
   p1.window = a->window;
-  // e4m3 pools: k_descale joins the score scale (one rounding, from double)
-  p1.scale_log2 = fp8 ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
+  // pools of codes: k_descale joins the score scale (one rounding, from double)
+  p1.scale_log2 = fp8 || fp4 ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
                       : a->scale * 1.44269504088896340736f;
-  p1.v_descale = fp8 ? a->v_descale : 1.0f;
+  p1.v_descale = fp8 || fp4 ? a->v_descale : 1.0f;
+  p1.scales = a->kv_scales;
   p1.num_splits = splits;
   p1.min_chunk = min_chunk;
   // automatic stream schedule with more segments than CTAs: a segment start costs a CTA
   // about as much as kPieceCost positions (twice as many positions of an e4m3 cache)
-  p1.piece_cost = (splits == 0 && (long long)a->B * vheads > grid) ? (fp8 ? gda::kPieceCostE4m3 : gda::kPieceCost) : 0;
+  p1.piece_cost = (splits == 0 && (long long)a->B * vheads > grid) ? (kv8 ? gda::kPieceCostE4m3 : gda::kPieceCost) : 0;
   p1.rule_kv8 = kv8;
   p1.check_indices = a->check_indices ? 1 : 0;
   p1.wait_limit = wait_limit();
@@ -294,8 +309,9 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
       ++g_tused;
     }
   }
-  const cudaError_t le =
-      fp8 ? gda::launch_stage1_fp8(p1, grid, stream) : gda::launch_stage1(p1, variant, grid, stream);
+  const cudaError_t le = fp4   ? gda::launch_stage1_fp4(p1, grid, stream)
+                         : fp8 ? gda::launch_stage1_fp8(p1, grid, stream)
+                               : gda::launch_stage1(p1, variant, grid, stream);
   if (le != cudaSuccess) return GDA_ERR_CUDA;
   if (t_end != nullptr && cudaEventRecord(t_end, stream) != cudaSuccess) return GDA_ERR_CUDA;
 
@@ -501,6 +517,215 @@ int gda_decode_e4m3(const gda_bf16* q, const gda_bf16* gate, const uint8_t* k_po
   return enqueue(&a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int gda_decode_fp4(const gda_bf16* q, const gda_bf16* gate, const uint8_t* k_pool, const uint8_t* v_pool,
+                   const uint8_t* kv_scales, const int32_t* kv_indptr, const int32_t* kv_indices, gda_bf16* out, int B,
+                   int Hq, int Hkv, int D, float scale, float k_descale, float v_descale, int num_splits,
+                   gda_stream_t stream) {
+  gda_args a = {};
+  a.q = q;
+  a.gate = gate;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.kv_scales = kv_scales;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.out = out;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.scale = scale;
+  a.num_splits = num_splits;
+  a.fuse_gate = 1;
+  a.variant = GDA_VARIANT_AUTO;
+  a.kv_dtype = GDA_KV_E2M1;
+  a.k_descale = k_descale;
+  a.v_descale = v_descale;
+  int rc = validate_args(&a);
+  if (rc != GDA_OK) return rc;
+  if (B == 0) return GDA_OK;
+  void* ws = nullptr;
+  const size_t need = gda_workspace_bytes(B, Hq, Hkv, D, num_splits);
+  rc = ensure_workspace(need, reinterpret_cast<cudaStream_t>(stream), true, &ws);
+  if (rc != GDA_OK) return rc;
+  return enqueue(&a, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gda_kv_write_fp4(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, int64_t v_stride, const int32_t* slots,
+                     int64_t num_slots, uint8_t* k_pool, uint8_t* v_pool, uint8_t* kv_scales, float k_descale,
+                     float v_descale, int64_t T, int Hkv, int D, gda_stream_t stream) {
+  if (T < 0 || Hkv < 1 || D < 1 || num_slots < 0) return GDA_ERR_SHAPE;
+  if (D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D) return GDA_ERR_SHAPE;
+  if (T > kMaxRows / Hkv) return GDA_ERR_SHAPE;
+  if (!descale_ok(k_descale) || !descale_ok(v_descale)) return GDA_ERR_ARG;
+  if (T == 0) return GDA_OK;
+  if (!k || !v || !slots || !k_pool || !v_pool || !kv_scales) return GDA_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(slots, 4) ||
+      !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(kv_scales, 16))
+    return GDA_ERR_ALIGN;
+  gda::Kv4WriteParams p;
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.num_slots = num_slots;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.scales = kv_scales;
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.T = T;
+  p.Hkv = Hkv;
+  if (gda::launch_kv4_write(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+int gda_kv_gather_fp4(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales, int64_t num_slots,
+                      const int32_t* indices, int64_t N, float k_descale, float v_descale, gda_bf16* k_out,
+                      gda_bf16* v_out, int Hkv, int D, gda_stream_t stream) {
+  if (N < 0 || Hkv < 1 || D < 1 || num_slots < 0) return GDA_ERR_SHAPE;
+  if (D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (N > kMaxRows / Hkv) return GDA_ERR_SHAPE;
+  if (!isfinite(k_descale) || !isfinite(v_descale)) return GDA_ERR_ARG;
+  if (N == 0) return GDA_OK;
+  if (!k_pool || !v_pool || !kv_scales || !indices || !k_out || !v_out) return GDA_ERR_NULL;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(kv_scales, 16) || !aligned(indices, 4) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return GDA_ERR_ALIGN;
+  gda::Kv4GatherParams p;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.scales = kv_scales;
+  p.num_slots = num_slots;
+  p.indices = indices;
+  p.N = N;
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  p.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.Hkv = Hkv;
+  if (gda::launch_kv4_gather(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+int gda_qk_norm_mrope_kv_write(const gda_mrope_args* a, gda_stream_t stream) {
+  if (a == nullptr) return GDA_ERR_NULL;
+  if (a->T < 0 || a->Hq < 1 || a->Hkv < 1 || a->D < 1 || a->num_slots < 0) return GDA_ERR_SHAPE;
+  if (a->D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (a->Hq > kMaxHeads || a->Hkv > kMaxHeads) return GDA_ERR_SHAPE;
+  if (a->row_stride < (2 * (int64_t)a->Hq + 2 * (int64_t)a->Hkv) * a->D) return GDA_ERR_SHAPE;
+  if (a->rope_dim < 0 || a->rope_dim > a->D) return GDA_ERR_SHAPE;
+  if (a->rope_dim % 16 != 0) return GDA_ERR_UNSUPPORTED;
+  if (!(a->eps >= 0.0f)) return GDA_ERR_SHAPE;
+  if (a->T > kMaxRows) return GDA_ERR_SHAPE;
+  const bool pool = a->k_pool != nullptr || a->v_pool != nullptr;
+  if (a->rope_dim > 0) {
+    if (!a->pair_axis) return GDA_ERR_NULL;
+    if (a->n_axes < 1 || a->n_axes > 255) return GDA_ERR_SHAPE;
+    for (int i = 0; i < a->rope_dim / 2; ++i)
+      if (a->pair_axis[i] >= a->n_axes) return GDA_ERR_ARG;
+    if (a->n_axes > 1 && a->pos_stride < a->T) return GDA_ERR_SHAPE;
+  }
+  if (pool) {
+    if (a->kv_dtype != GDA_KV_BF16 && a->kv_dtype != GDA_KV_E2M1) return GDA_ERR_UNSUPPORTED;
+    if (a->kv_dtype == GDA_KV_E2M1 && (!descale_ok(a->k_descale) || !descale_ok(a->v_descale))) return GDA_ERR_ARG;
+  }
+  if (a->T == 0) return GDA_OK;
+  if (!a->qgkv || !a->q_out) return GDA_ERR_NULL;
+  if (!pool && !a->k_out) return GDA_ERR_NULL;  // the keys have to go somewhere
+  if (a->rope_dim > 0 && (!a->positions || !a->inv_freq)) return GDA_ERR_NULL;
+  if (pool && (!a->k_pool || !a->v_pool || !a->slots || (a->kv_dtype == GDA_KV_E2M1 && !a->kv_scales)))
+    return GDA_ERR_NULL;
+  if (!aligned(a->qgkv, 16) || a->row_stride % 8 != 0 || !aligned(a->q_out, 16) || (a->k_out && !aligned(a->k_out, 16)) ||
+      (a->gate_out && !aligned(a->gate_out, 16)) || (a->w_q_norm && !aligned(a->w_q_norm, 16)) ||
+      (a->w_k_norm && !aligned(a->w_k_norm, 16)) || (a->positions && !aligned(a->positions, 4)) ||
+      (a->inv_freq && !aligned(a->inv_freq, 4)) ||
+      (pool && (!aligned(a->k_pool, 16) || !aligned(a->v_pool, 16) || !aligned(a->slots, 4) ||
+                (a->kv_scales && !aligned(a->kv_scales, 16)))))
+    return GDA_ERR_ALIGN;
+  gda::MropeParams p = {};
+  p.qgkv = reinterpret_cast<const __nv_bfloat16*>(a->qgkv);
+  p.row_stride = a->row_stride;
+  p.w_q = reinterpret_cast<const __nv_bfloat16*>(a->w_q_norm);
+  p.w_k = reinterpret_cast<const __nv_bfloat16*>(a->w_k_norm);
+  p.eps = a->eps;
+  p.positions = a->positions;
+  p.pos_stride = a->pos_stride;
+  p.inv_freq = a->inv_freq;
+  p.rope_dim = a->rope_dim;
+  for (int i = 0; i < a->rope_dim / 2; ++i) p.pair_axis[i] = a->pair_axis[i];
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(a->q_out);
+  p.gate_out = reinterpret_cast<__nv_bfloat16*>(a->gate_out);
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(a->k_out);
+  p.slots = a->slots;
+  p.num_slots = a->num_slots;
+  p.k_pool = a->k_pool;
+  p.v_pool = a->v_pool;
+  p.scales = a->kv_scales;
+  p.k_descale = a->k_descale;
+  p.v_descale = a->v_descale;
+  p.pool = !pool ? 0 : a->kv_dtype == GDA_KV_BF16 ? 1 : 2;
+  p.T = a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  if (gda::launch_mrope(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+int gda_prefill_packed(const gda_packed_args* a, gda_stream_t stream) {
+  if (a == nullptr) return GDA_ERR_NULL;
+  if (a->B < 0 || a->total_q < 0 || a->total_k < 0 || a->Hq < 1 || a->Hkv < 1 || a->D < 1 || a->Hq % a->Hkv != 0)
+    return GDA_ERR_SHAPE;
+  if (a->D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (!isfinite(a->scale) || !(a->scale > 0.0f)) return GDA_ERR_ARG;
+  if (a->total_q > kMaxRows || a->total_k > kMaxRows || a->Hq > kMaxHeads) return GDA_ERR_SHAPE;
+  const int64_t wq = (int64_t)a->Hq * a->D, wk = (int64_t)a->Hkv * a->D;
+  if (a->q_stride < wq || (a->gate && a->gate_stride < wq) || a->k_stride < wk || a->v_stride < wk) return GDA_ERR_SHAPE;
+  if (a->B == 0 || a->total_q == 0) return GDA_OK;
+  if (gda::packed_blocks(a->total_q, a->B) * a->Hq > 0x7FFFFFFFLL) return GDA_ERR_SHAPE;
+  if (!a->q || !a->out || !a->cu_seqlens_q || !a->cu_seqlens_k || (a->total_k > 0 && (!a->k || !a->v)))
+    return GDA_ERR_NULL;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || (a->k && !aligned(a->k, 16)) || (a->v && !aligned(a->v, 16)) ||
+      (a->gate && !aligned(a->gate, 16)) || !aligned(a->cu_seqlens_q, 4) || !aligned(a->cu_seqlens_k, 4) ||
+      (a->lse && !aligned(a->lse, 4)) || (a->error_word && !aligned(a->error_word, 4)) || a->q_stride % 8 != 0 ||
+      (a->gate && a->gate_stride % 8 != 0) || a->k_stride % 8 != 0 || a->v_stride % 8 != 0)
+    return GDA_ERR_ALIGN;
+  unsigned int* err = a->error_word;
+  if (err == nullptr) {
+    int rc = prefill_error_word(&err);
+    if (rc != GDA_OK) return rc;
+  }
+  gda::PrefillParams p = {};
+  p.out = reinterpret_cast<__nv_bfloat16*>(a->out);
+  p.lse = a->lse;
+  p.gate = reinterpret_cast<const __nv_bfloat16*>(a->gate);
+  p.gate_stride = a->gate_stride;
+  p.kv_lens = nullptr;
+  p.cu_q = a->cu_seqlens_q;
+  p.cu_k = a->cu_seqlens_k;
+  p.error = err;
+  p.B = a->B;
+  p.Sq = (int)a->total_q;
+  p.Skv = (int)a->total_k;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.scale_log2 = a->scale * 1.44269504088896340736f;
+  p.causal = a->causal ? 1 : 0;
+  p.fuse_gate = a->gate ? 1 : 0;
+  p.wait_limit = wait_limit();
+  // with no keys the key maps still need a valid base and pitch: the queries' (never loaded)
+  const bool keys = a->total_k > 0;
+  const cudaError_t le = gda::launch_prefill_packed(
+      p, a->q, a->q_stride, keys ? (const void*)a->k : (const void*)a->q, keys ? a->k_stride : a->q_stride,
+      keys ? (const void*)a->v : (const void*)a->q, keys ? a->v_stride : a->q_stride, a->gate,
+      reinterpret_cast<cudaStream_t>(stream));
+  if (le == cudaErrorStreamCaptureUnsupported) return GDA_ERR_CAPTURE;  // first use while capturing
+  if (le != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
 int gda_decode_noalloc(const gda_bf16* q, const gda_bf16* gate, const gda_bf16* k_pool, const gda_bf16* v_pool,
                        const int32_t* kv_indptr, const int32_t* kv_indices, gda_bf16* out, int B, int Hq, int Hkv,
                        int D, float scale, int num_splits, gda_stream_t stream) {
@@ -675,6 +900,7 @@ int gda_decode_step_host(const void* host_in, void* dev_in, size_t in_bytes, con
                          int flags, int synchronize, gda_stream_t stream) {
   if (B < 0 || nnz < 0) return GDA_ERR_SHAPE;
   if ((flags & ~(GDA_STEP_MAP_IN | GDA_STEP_MAP_OUT)) != 0) return GDA_ERR_ARG;
+  if (kv_dtype == GDA_KV_E2M1) return GDA_ERR_UNSUPPORTED;  // (it takes no scale pool)
   if (B == 0) return GDA_OK;
   size_t off[4];
   const size_t total = gda_step_layout(B, Hq, D, nnz, off);
@@ -867,6 +1093,6 @@ int gda_debug_wait_limit(int64_t cycles) {
   return GDA_OK;
 }
 
-int gda_version(void) { return 300; }  // 0.3.0: gda_debug_wait_limit
+int gda_version(void) { return 400; }  // 0.4.0: the 4-bit cache, packed prompts, multi-axis rotary
 
 }  // extern "C"

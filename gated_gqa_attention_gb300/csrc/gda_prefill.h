@@ -19,10 +19,25 @@ struct PrefillParams {
   int fuse_gate;
   long long wait_limit;        // SM cycles after which a pipeline wait gives up (kWaitLimitCycles;
                                // shorter only in the failure-path test)
+  // packed form (one [T, H, D] tensor each, B sequences): Sq and Skv are the tensors' rows
+  const int* cu_q = nullptr;   // [B + 1] first query row of each sequence
+  const int* cu_k = nullptr;   // [B + 1] first key row
+  long long gate_stride = 0;   // elements between the gate's tokens
 };
+
+// The most 128-row query blocks that B sequences of `rows` rows in all can have.
+inline long long packed_blocks(long long rows, long long B) {
+  const long long n = rows / 128 + B;  // each sequence ends at most one block early
+  return n < rows ? n : rows;
+}
 
 // Prefill / extend gated SDPA (tcgen05); q, k, v, gate are [B, S, H, 256] BF16.
 cudaError_t launch_prefill(const PrefillParams& p, const void* q, const void* k, const void* v, const void* gate,
                            cudaStream_t stream);
+
+// The same over packed sequences; pitches are elements between tokens.
+cudaError_t launch_prefill_packed(const PrefillParams& p, const void* q, int64_t q_pitch, const void* k,
+                                  int64_t k_pitch, const void* v, int64_t v_pitch, const void* gate,
+                                  cudaStream_t stream);
 
 }  // namespace gda

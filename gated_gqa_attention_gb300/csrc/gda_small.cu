@@ -23,6 +23,7 @@
 // second kernel runs.
 #include <atomic>
 #include "gda_device.cuh"
+#include "gda_kv4.cuh"
 #include "gda_small.h"
 
 namespace gda {
@@ -106,12 +107,14 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 }  // namespace
 
-// F8: the pools hold e4m3 codes; K and V are widened to FP16 while being staged, Q
-// goes to FP16 with one power-of-two factor per group, the MMAs run in FP16, and
-// v_descale scales the merged O (k_descale is in scale_log2)
-template <int C, bool F8>
+// KV: the pools hold BF16 (0), e4m3 codes (1) or 4-bit codes with block scales (2).  For
+// the codes (F8) K and V are widened to FP16 while being staged, which is exact, Q goes
+// to FP16 with one power-of-two factor per group, the MMAs run in FP16, and v_descale
+// scales the merged O (k_descale is in scale_log2)
+template <int C, int KV>
 __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p) {
   static_assert(C == 1 || C == 2 || C == 4 || C == 8, "cluster sizes");
+  constexpr bool F8 = KV != 0;
   constexpr int kFin = kG / C;  // query heads each CTA finalises
   extern __shared__ __align__(128) unsigned char smem_raw[];
   SmallSmem& sm = *reinterpret_cast<SmallSmem*>(smem_raw);
@@ -181,38 +184,74 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
   // e4m3 rows (256 B): thread t loads the 64-byte piece t % 4 of the K and V rows of
   // position t / 4 into registers; store_chunk widens them to FP16 into buffer c & 1
   // (the same row layout as BF16 rows).  Positions past the range read as zeros.
-  uint4 rk[4], rv[4];
+  // 4-bit rows: the piece is 32 bytes of codes and four scales, dims 64 (t % 4) .. + 63.
+  uint4 rk[KV == 2 ? 2 : 4], rv[KV == 2 ? 2 : 4];
+  uint32_t sk = 0u, sv = 0u;
   auto fetch_raw = [&](int cidx) {
     const int pos = lo + cidx * kChunk + (tid >> 2);
     const bool ok = cidx < nch && pos < hi;
     const int slot = ok ? __ldg(p.indices + base + pos) : 0;
-    const size_t off = ((size_t)slot * row_stride + (size_t)kvh * kD) + (size_t)qd * 64;  // bytes (1 per code)
-    const uint4* ks = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p.k_pool) + off);
-    const uint4* vs = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p.v_pool) + off);
+    if constexpr (KV == 2) {
+      const size_t row = (size_t)slot * p.Hkv + kvh;
+      const uint4* k4 = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.k_pool) + row * kCodeBytes) + 2 * qd;
+      const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.v_pool) + row * kCodeBytes) + 2 * qd;
+      const uint32_t* s4 = reinterpret_cast<const uint32_t*>(p.scales + row * kScalePair) + qd;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rk[i] = ok ? __ldg(ks + i) : make_uint4(0u, 0u, 0u, 0u);
-      rv[i] = ok ? __ldg(vs + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 2; ++i) {
+        rk[i] = ok ? __ldg(k4 + i) : make_uint4(0u, 0u, 0u, 0u);
+        rv[i] = ok ? __ldg(v4 + i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      sk = ok ? __ldg(s4) : 0u;
+      sv = ok ? __ldg(s4 + kScaleBytes / 4) : 0u;
+    } else {
+      const size_t off = ((size_t)slot * row_stride + (size_t)kvh * kD) + (size_t)qd * 64;  // bytes (1 per code)
+      const uint4* ks = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p.k_pool) + off);
+      const uint4* vs = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p.v_pool) + off);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rk[i] = ok ? __ldg(ks + i) : make_uint4(0u, 0u, 0u, 0u);
+        rv[i] = ok ? __ldg(vs + i) : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   };
   auto store_chunk = [&](int cidx) {
     const int j = tid >> 2;
+    if constexpr (KV == 2) {
+      auto widen = [&](const uint4* r, uint32_t sc, unsigned char* dst) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t wk[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w}, wv[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
-      uint32_t fk[8], fv[8];
+        for (int blk = 0; blk < 4; ++blk) {  // 16 dims: words 2 (blk % 2), + 1 of r[blk / 2]
+          const uint32_t pair = e4m3x2_to_f16x2(sc >> (16 * (blk >> 1)));
+          const uint32_t s2 = __byte_perm(pair, 0u, (blk & 1) ? 0x3232 : 0x1010);
+          const uint4& v = r[blk >> 1];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        e4m3x4_to_f16(wk[u], fk[2 * u], fk[2 * u + 1]);
-        e4m3x4_to_f16(wv[u], fv[2 * u], fv[2 * u + 1]);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t f[4];
+            e2m1x8_to_f16x2x4((blk & 1) ? (i ? v.w : v.z) : (i ? v.y : v.x), f);
+            reinterpret_cast<uint4*>(dst)[2 * blk + i] = make_uint4(f16x2_mul(f[0], s2), f16x2_mul(f[1], s2),
+                                                                    f16x2_mul(f[2], s2), f16x2_mul(f[3], s2));
+          }
+        }
+      };
+      widen(rk, sk, &sm.k[cidx & 1][j][128 * qd]);
+      widen(rv, sv, &sm.v[cidx & 1][j][128 * qd]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t wk[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w}, wv[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
+        uint32_t fk[8], fv[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          e4m3x4_to_f16(wk[u], fk[2 * u], fk[2 * u + 1]);
+          e4m3x4_to_f16(wv[u], fv[2 * u], fv[2 * u + 1]);
+        }
+        // codes 64 qd + 16 i .. + 15 -> FP16 elements at byte 2 (64 qd + 16 i)
+        uint4* dk = reinterpret_cast<uint4*>(&sm.k[cidx & 1][j][2 * (64 * qd + 16 * i)]);
+        uint4* dv = reinterpret_cast<uint4*>(&sm.v[cidx & 1][j][2 * (64 * qd + 16 * i)]);
+        dk[0] = make_uint4(fk[0], fk[1], fk[2], fk[3]);
+        dk[1] = make_uint4(fk[4], fk[5], fk[6], fk[7]);
+        dv[0] = make_uint4(fv[0], fv[1], fv[2], fv[3]);
+        dv[1] = make_uint4(fv[4], fv[5], fv[6], fv[7]);
       }
-      // codes 64 qd + 16 i .. + 15 -> FP16 elements at byte 2 (64 qd + 16 i)
-      uint4* dk = reinterpret_cast<uint4*>(&sm.k[cidx & 1][j][2 * (64 * qd + 16 * i)]);
-      uint4* dv = reinterpret_cast<uint4*>(&sm.v[cidx & 1][j][2 * (64 * qd + 16 * i)]);
-      dk[0] = make_uint4(fk[0], fk[1], fk[2], fk[3]);
-      dk[1] = make_uint4(fk[4], fk[5], fk[6], fk[7]);
-      dv[0] = make_uint4(fv[0], fv[1], fv[2], fv[3]);
-      dv[1] = make_uint4(fv[4], fv[5], fv[6], fv[7]);
     }
   };
   // BF16 rows: chunk c into buffer c & 1 by cp.async: thread t copies pieces t % 4 + 4 k
@@ -278,8 +317,13 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
     }
     // scores (log2 units) of positions 8 warp + 2 qd, + 1; past the chunk's end -inf
     const int j0 = 8 * warp + 2 * qd;
-    const float s0 = (j0 < n) ? sacc[0] * sl2 : -INFINITY;
-    const float s1 = (j0 + 1 < n) ? sacc[1] * sl2 : -INFINITY;
+    float s0 = (j0 < n) ? sacc[0] * sl2 : -INFINITY;
+    float s1 = (j0 + 1 < n) ? sacc[1] * sl2 : -INFINITY;
+    if (KV == 2) {
+      // a NaN score becomes +inf, which the maxima cannot pass over: it ends as a NaN output
+      s0 = (s0 != s0) ? INFINITY : s0;
+      s1 = (s1 != s1) ? INFINITY : s1;
+    }
     const float wm = quad_max(fmaxf(s0, s1));
     if (qd == 0) sm.wmax[warp][h] = wm;
     __syncthreads();
@@ -296,7 +340,8 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
     // P rounded to the MMA's type; the sum adds the rounded values the MMA uses
     const uint32_t pp = F8 ? f16x2_rn(p0, p1) : pack_bf16x2(p0, p1);
     sm.p[h][4 * warp + qd] = pp;
-    const float ws = quad_sum(F8 ? (f16_lo(pp) + f16_hi(pp))
+    const float ws = quad_sum(KV == 2 ? (p0 + p1)  // (4-bit: the sum before the rounding)
+                              : F8 ? (f16_lo(pp) + f16_hi(pp))
                                  : (__uint_as_float(pp << 16) + __uint_as_float(pp & 0xFFFF0000u)));
     if (qd == 0) sm.wsum[warp][h] = ws;
     __syncthreads();
@@ -397,10 +442,12 @@ namespace {
 
 template <int C>
 cudaError_t small_attr_c() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(small_decode_kernel<C, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+  cudaError_t e =
+      cudaFuncSetAttribute(small_decode_kernel<C, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(small_decode_kernel<C, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(small_decode_kernel<C, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(small_decode_kernel<C, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)kSmallSmem);
 }
 
@@ -451,11 +498,11 @@ int small_max_clusters(int C) {
     cudaLaunchAttribute attr[1];
     cluster_config(&cfg, attr, C, dim3((unsigned)C, 1, 1), nullptr);
     int got = 0;
-    // (the e4m3 instances have the same launch shape and shared memory)
-    const cudaError_t e = (C == 8)   ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<8, false>, &cfg)
-                          : (C == 4) ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<4, false>, &cfg)
-                          : (C == 2) ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<2, false>, &cfg)
-                                     : cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<1, false>, &cfg);
+    // (the instances for codes have the same launch shape and shared memory)
+    const cudaError_t e = (C == 8)   ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<8, 0>, &cfg)
+                          : (C == 4) ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<4, 0>, &cfg)
+                          : (C == 2) ? cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<2, 0>, &cfg)
+                                     : cudaOccupancyMaxActiveClusters(&got, small_decode_kernel<1, 0>, &cfg);
     if (e != cudaSuccess || got <= 0) {
       (void)cudaGetLastError();
       return 0;
@@ -485,16 +532,21 @@ cudaError_t launch_small(const SmallParams& p, int C, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  if (p.kv_fp8) {
-    if (C == 8) return cudaLaunchKernelEx(&cfg, small_decode_kernel<8, true>, p);
-    if (C == 4) return cudaLaunchKernelEx(&cfg, small_decode_kernel<4, true>, p);
-    if (C == 2) return cudaLaunchKernelEx(&cfg, small_decode_kernel<2, true>, p);
-    if (C == 1) return cudaLaunchKernelEx(&cfg, small_decode_kernel<1, true>, p);
+  if (p.kv == 2) {
+    if (C == 8) return cudaLaunchKernelEx(&cfg, small_decode_kernel<8, 2>, p);
+    if (C == 4) return cudaLaunchKernelEx(&cfg, small_decode_kernel<4, 2>, p);
+    if (C == 2) return cudaLaunchKernelEx(&cfg, small_decode_kernel<2, 2>, p);
+    if (C == 1) return cudaLaunchKernelEx(&cfg, small_decode_kernel<1, 2>, p);
+  } else if (p.kv == 1) {
+    if (C == 8) return cudaLaunchKernelEx(&cfg, small_decode_kernel<8, 1>, p);
+    if (C == 4) return cudaLaunchKernelEx(&cfg, small_decode_kernel<4, 1>, p);
+    if (C == 2) return cudaLaunchKernelEx(&cfg, small_decode_kernel<2, 1>, p);
+    if (C == 1) return cudaLaunchKernelEx(&cfg, small_decode_kernel<1, 1>, p);
   } else {
-    if (C == 8) return cudaLaunchKernelEx(&cfg, small_decode_kernel<8, false>, p);
-    if (C == 4) return cudaLaunchKernelEx(&cfg, small_decode_kernel<4, false>, p);
-    if (C == 2) return cudaLaunchKernelEx(&cfg, small_decode_kernel<2, false>, p);
-    if (C == 1) return cudaLaunchKernelEx(&cfg, small_decode_kernel<1, false>, p);
+    if (C == 8) return cudaLaunchKernelEx(&cfg, small_decode_kernel<8, 0>, p);
+    if (C == 4) return cudaLaunchKernelEx(&cfg, small_decode_kernel<4, 0>, p);
+    if (C == 2) return cudaLaunchKernelEx(&cfg, small_decode_kernel<2, 0>, p);
+    if (C == 1) return cudaLaunchKernelEx(&cfg, small_decode_kernel<1, 0>, p);
   }
   return cudaErrorInvalidValue;
 }

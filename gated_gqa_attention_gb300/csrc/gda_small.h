@@ -12,7 +12,7 @@ constexpr int kSmallMaxLen = 1024;  // longest sequence (host bound) the path ta
 struct SmallParams {
   const __nv_bfloat16* q;       // [B, Hq, D]
   const __nv_bfloat16* gate;    // [B, Hq, D] (fuse_gate)
-  const void* k_pool;           // [num_slots, Hkv, D] bf16, or e4m3 codes (kv_fp8)
+  const void* k_pool;           // [num_slots, Hkv, D] bf16, or codes (kv)
   const void* v_pool;           // [num_slots, Hkv, D] likewise
   const int32_t* indptr;        // [B + 1]
   const int32_t* indices;       // [indptr[B]]
@@ -20,9 +20,10 @@ struct SmallParams {
   float* lse_out;               // [B, Hq] natural log, or null
   const float* sinks;           // [Hq] sink logits, or null
   int B, Hq, Hkv, G;            // G = Hq / Hkv <= 8
-  float scale_log2;             // scale * log2(e) (times k_descale for e4m3 pools)
-  int kv_fp8;                   // the pools hold e4m3 codes
-  float v_descale;              // e4m3 pools: V = v_descale * e4m3(code)
+  float scale_log2;             // scale * log2(e) (times k_descale for codes)
+  int kv;                       // the pools hold 0: bf16, 1: e4m3 codes, 2: 4-bit codes
+  const unsigned char* scales;  // 4-bit pools: [num_slots, Hkv, 2, D / 16] e4m3
+  float v_descale;              // e4m3 and 4-bit pools: the factor of V
   int window;                   // > 0: the last `window` positions only
   int fuse_gate;
 };

@@ -1,0 +1,493 @@
+// gda_stage1_fp4.cu -- split-KV decode stage 1 over a 4-bit KV cache, sm_103a.
+//
+// The pools hold e2m1 codes with an e4m3 scale per 16 head dimensions (gda_kv4.cuh):
+//   K = k_descale * e4m3(s) * e2m1(c), V likewise.
+// Q stays BF16; the partial O and LSE are those of the other stage-1 kernels, so stage 2
+// (FP32 merge, sinks, the gate) is shared.
+//
+// What bounds it: 288 bytes per (position, KV head) against 1024 of a BF16 cache, so the
+// streaming time falls to a quarter while the arithmetic per position stays.  The design
+// spends as few instructions per code as it can:
+//  * Persistent grid, one CTA of 8 warps per SM; warp w takes 32-position tiles w, w + 8,
+//    ... of its CTA's piece.  K and V rows and their scales go through a per-warp ring of
+//    three 9 KB stages filled by cp.async two tiles ahead (216 KB a CTA in flight or in
+//    use; no registers held by loads, 18 copy instructions a tile).  A ring row is 128
+//    code bytes followed by its 16 scale bytes: the 144-byte pitch that keeps the 16-byte
+//    reads below free of bank conflicts is the row itself.
+//  * A code times its scale is exact in FP16, so cvt.rn.f16x2.e2m1x2 widens a byte (two
+//    codes), one packed multiply applies the scale, and the tiles run as m16n8k16 FP16
+//    MMAs with FP32 accumulation.  Q goes to FP16 with one power of two per piece (its
+//    largest magnitude lands in [2^14, 2^15)); that factor and k_descale are folded into
+//    the score scale, v_descale into the partial's normalisation.
+//  * QK: S^T[32 tok x 8 heads] = K Q^T, two m-tiles.  Lane (g, t) reads dims 64t .. 64t + 63
+//    of tokens g, g + 8 (m-tile 0), g + 16, g + 24 (m-tile 1): 32 code bytes and one word of
+//    four scales each.  K-step s takes dims 64t + 4s + {0,1} for k-slots (2t, 2t+1) and
+//    + {2,3} for (2t+8, 2t+9): byte 2s of the lane's codes and byte 2s + 1, so a byte is
+//    one A register; the Q^T fragments use the same order.
+//  * PV: O^T[256 x 8] += V^T P^T, two k-steps of 16 tokens.  An A register pairs two
+//    tokens of one dimension.  Lane (g, t) reads bytes 16g .. + 15 of its four tokens; two
+//    bit-selects on a pair of words turn (codes of T0, codes of T1) into bytes that hold one
+//    dimension's code of both tokens -- four registers per two selects -- and the scale
+//    pair is (scale of T0, scale of T1).  Row g of m-tile mt is dim 32g + 2mt, row g + 8 the
+//    next one.
+//  * P is rounded to FP16 for the MMA (it lies in [0, 2^8], 2^-11 relative, against the
+//    4-bit V it multiplies) and its sum is kept in FP32 before the rounding, so the LSE
+//    does not see it.
+//  * Merge: as in the e4m3 kernel -- each warp leaves its rescaled O^T fragments in ring
+//    stage 0, all threads add the 8 slices in a fixed order.  Tile k of a piece lives in
+//    stage (k + 1) % 3, so the next piece's first two tiles are on their way to stages 1
+//    and 2 while stage 0 serves the merge.
+#include <atomic>
+
+#include "gda_kernels.h"
+#include "gda_kv4.cuh"
+
+namespace gda {
+
+namespace {
+
+constexpr int kW4 = 8;            // warps per CTA
+constexpr int kTok4 = 32;         // tokens per warp tile
+constexpr int kNS4 = 3;           // ring stages per warp
+constexpr int kRow4 = kCodeBytes + kScaleBytes;   // ring row: codes, then scales (144 bytes)
+constexpr float kLazyLog2F4 = 8.0f;
+static_assert(kRow4 % 32 == 16, "the row pitch keeps 16-byte reads of 8 rows on different banks");
+
+struct Fp4Stage {
+  unsigned char k[kTok4][kRow4];
+  unsigned char v[kTok4][kRow4];
+};
+struct Fp4Smem {
+  uint2 qf[16][32];               // Q^T fragments (FP16, scaled), lane order
+  Fp4Stage ring[kW4][kNS4];       // per-warp rings; stage 0 also holds the merge slice
+  float mbuf[kW4][kG];            // each warp's running max
+  float lsum[kW4][kG];            // each warp's rescaled sum
+  unsigned int qmax;              // largest |q| of the piece's group (float bits)
+};
+static_assert(sizeof(float4) * 16 * 32 <= sizeof(Fp4Stage), "merge slice fits a ring stage");
+static_assert(sizeof(Fp4Smem) <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(src_bytes), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+struct KvRows {  // one KV head's rows of the three pools
+  const unsigned char *k, *v, *s;
+  size_t code_stride, scale_stride;  // bytes between slots
+};
+
+// The copies of one tile (tokens of `slot_lane`, -1: zeros) as one group: per
+// instruction four rows of codes, or 16 rows' scale chunks.
+__device__ __forceinline__ void issue_tile(Fp4Stage& st, const KvRows& r, int slot_lane, int lane, uint64_t policy) {
+  const int sub = lane >> 3, chunk = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + sub;
+    const int s = __shfl_sync(0xffffffffu, slot_lane, row);
+    const size_t off = (size_t)max(s, 0) * r.code_stride + 16 * chunk;
+    cp_async16(smem_u32(&st.k[row][16 * chunk]), r.k + off, s >= 0 ? 16u : 0u, policy);
+    cp_async16(smem_u32(&st.v[row][16 * chunk]), r.v + off, s >= 0 ? 16u : 0u, policy);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * i + (lane >> 1);
+    const int s = __shfl_sync(0xffffffffu, slot_lane, row);
+    const unsigned char* src = r.s + (size_t)max(s, 0) * r.scale_stride + 16 * (lane & 1);
+    unsigned char* dst = (lane & 1) ? &st.v[row][kCodeBytes] : &st.k[row][kCodeBytes];
+    cp_async16(smem_u32(dst), src, s >= 0 ? 16u : 0u, policy);
+  }
+  cp_commit();
+}
+
+struct Fp4WarpState {
+  float o[16][4];
+  float m0, m1, l0, l1;
+  uint32_t P[4];  // FP16 probabilities, P[j] = tokens g + 8j, heads (2t, 2t+1)
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.0f;
+  }
+
+  // S^T of the tile's K rows, then the softmax update; nv tokens of the tile are valid
+  __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[32], int nv, float sl2, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float s[8];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t r0 = smem_u32(&st.k[g + 16 * mt][0]), r1 = r0 + 8 * kRow4;
+      const uint32_t w0 = lds_u32(r0 + kCodeBytes + 4 * t), w1 = lds_u32(r1 + kCodeBytes + 4 * t);
+      float acc[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.0f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // dims 64t + 32 half .. + 31: two scale blocks
+        const uint4 c0 = lds_v4(r0 + 32 * t + 16 * half), c1 = lds_v4(r1 + 32 * t + 16 * half);
+        const uint32_t p0 = e4m3x2_to_f16x2(w0 >> (16 * half)), p1 = e4m3x2_to_f16x2(w1 >> (16 * half));
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          const uint32_t s0 = __byte_perm(p0, 0u, blk ? 0x3232 : 0x1010);
+          const uint32_t s1 = __byte_perm(p1, 0u, blk ? 0x3232 : 0x1010);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t f0[4], f1[4];
+            e2m1x8_to_f16x2x4(word4(c0, 2 * blk + i), f0);
+            e2m1x8_to_f16x2x4(word4(c1, 2 * blk + i), f1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int ks = 8 * half + 4 * blk + 2 * i + k;
+              const uint2 b = qf[ks][lane];
+              mma_f16(acc[k], f16x2_mul(f0[2 * k], s0), f16x2_mul(f1[2 * k], s1), f16x2_mul(f0[2 * k + 1], s0),
+                      f16x2_mul(f1[2 * k + 1], s1), b.x, b.y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[4 * mt + i] = (acc[0][i] + acc[1][i]) * sl2;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // a NaN score becomes +inf, which the running max cannot pass over: the head's sum
+        // and output then end as NaN instead of as if the position were absent
+        float& x = s[2 * j + i];
+        x = (g + 8 * j >= nv) ? -INFINITY : (x != x) ? INFINITY : x;
+      }
+    }
+    // Lazy rescale: the reference maxima move only when a score exceeds them by more
+    // than kLazyLog2F4, so probabilities stay <= 2^8.
+    const float xa0 = fmaxf(fmaxf(s[0], s[2]), fmaxf(s[4], s[6]));
+    const float xb0 = fmaxf(fmaxf(s[1], s[3]), fmaxf(s[5], s[7]));
+    const bool grow = xa0 > m0 + kLazyLog2F4 || xb0 > m1 + kLazyLog2F4;
+    if (__any_sync(0xffffffffu, grow)) {
+      float xa = xa0, xb = xb0;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, off));
+        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, off));
+      }
+      const float na = fmaxf(m0, xa), nb = fmaxf(m1, xb);
+      const float aa = safe_exp2_diff(m0, na), ab = safe_exp2_diff(m1, nb);
+      l0 *= aa;
+      l1 *= ab;
+      m0 = na;
+      m1 = nb;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        o[i][0] *= aa;
+        o[i][1] *= ab;
+        o[i][2] *= aa;
+        o[i][3] *= ab;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float pa = safe_exp2_diff(s[2 * j], m0), pb = safe_exp2_diff(s[2 * j + 1], m1);
+      P[j] = pack_f16(pa, pb);
+      l0 += pa;
+      l1 += pb;
+    }
+  }
+
+  // O^T += V^T P^T over the tile's V rows
+  __device__ __forceinline__ void pv(const Fp4Stage& st, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t base = smem_u32(&st.v[0][0]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t b0 = movmatrix_trans(P[2 * ks]), b1 = movmatrix_trans(P[2 * ks + 1]);
+      uint4 c[4];       // tokens 16ks + (2t, 2t+1, 2t+8, 2t+9): codes of dims 32g .. + 31
+      uint32_t sc[4];   // their scales of blocks 2g, 2g + 1
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t row = base + (16 * ks + 2 * t + (i & 1) + 8 * (i >> 1)) * kRow4;
+        c[i] = lds_v4(row + 16 * g);
+        sc[i] = lds_u16(row + kCodeBytes + 2 * g);
+      }
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(sc[0], sc[1], blk ? 0x51 : 0x40));
+        const uint32_t s23 = e4m3x2_to_f16x2(__byte_perm(sc[2], sc[3], blk ? 0x51 : 0x40));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int wi = 2 * blk + i;
+          const uint32_t x0 = word4(c[0], wi), x1 = word4(c[1], wi), x2 = word4(c[2], wi), x3 = word4(c[3], wi);
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims: (T0, T1), (T2, T3)
+          e2m1x8_to_f16x2x4((x0 & kLow) | ((x1 << 4) & ~kLow), e01);
+          e2m1x8_to_f16x2x4(((x0 >> 4) & kLow) | (x1 & ~kLow), o01);
+          e2m1x8_to_f16x2x4((x2 & kLow) | ((x3 << 4) & ~kLow), e23);
+          e2m1x8_to_f16x2x4(((x2 >> 4) & kLow) | (x3 & ~kLow), o23);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16(o[4 * wi + k], f16x2_mul(e01[k], s01), f16x2_mul(o01[k], s01), f16x2_mul(e23[k], s23),
+                    f16x2_mul(o23[k], s23), b0, b1);
+        }
+      }
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  Fp4Smem& sm = *reinterpret_cast<Fp4Smem*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) sm.qmax = 0u;
+  Sched sched;
+  sched.begin(p.indptr, p.B, p.Hkv * p.npass, p.num_splits, gridDim.x, blockIdx.x, p.min_chunk, p.window,
+              p.piece_cost, p.rule_kv8);
+  const uint64_t policy = l2_policy_evict_first();
+
+  auto nmine_of = [&](int len) -> int {
+    const int ntiles = (len + kTok4 - 1) / kTok4;
+    return (ntiles > warp) ? (ntiles - warp + kW4 - 1) / kW4 : 0;
+  };
+  auto tile_n = [&](int k, int len, int nmine) -> int {
+    return (k < nmine) ? min(kTok4, len - kTok4 * (warp + kW4 * k)) : 0;
+  };
+  // slot of token `lane` of this warp's tile k (-1 past the tile's end or for a bad index)
+  auto fetch = [&](const int* idx, int k, int len, int nmine) -> int {
+    int s = -1;
+    if (lane < tile_n(k, len, nmine)) {
+      s = __ldg(idx + kTok4 * (warp + kW4 * k) + lane);
+      if (p.check_indices && (s < 0 || (long long)s >= p.num_slots)) {
+        atomicOr(&p.hdr->error, kErrIndex);
+        s = -1;
+      }
+    }
+    return s;
+  };
+  auto rows_of = [&](const Piece& pp) -> KvRows {
+    const size_t h = (size_t)(pp.kvh / p.npass);
+    return {p.k_pool + h * kCodeBytes, p.v_pool + h * kCodeBytes, p.scales + h * kScalePair,
+            (size_t)p.Hkv * kCodeBytes, (size_t)p.Hkv * kScalePair};
+  };
+
+  Fp4WarpState st;
+  Fp4Stage* ring = sm.ring[warp];
+  uint2 qraw[2];  // this thread's two BF16 Q^T fragments of the next piece
+  int s2 = -1, s3 = -1;
+  // Head of a piece: its Q rows, the slots of this warp's first four tiles and the copies of
+  // its first two (one group each).  For every piece after the first this runs before the
+  // previous piece's merge.
+  auto piece_head = [&](const Piece& pp) {
+    const int kvh = pp.kvh / p.npass, pass = pp.kvh - kvh * p.npass;
+    const int gv = min(kG, p.G - kG * pass);
+    const __nv_bfloat16* qg = p.q + ((size_t)pp.b * p.Hq + (size_t)kvh * p.G + (size_t)kG * pass) * kD;
+    const int* idx = p.indices + pp.base + pp.j0;
+    const int len = pp.j1 - pp.j0, nmine = nmine_of(len);
+    const int s0 = fetch(idx, 0, len, nmine), s1 = fetch(idx, 1, len, nmine);
+    s2 = fetch(idx, 2, len, nmine);
+    s3 = fetch(idx, 3, len, nmine);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int e = threadIdx.x + r * kW4 * 32;
+      const int ks = e >> 5, ln = e & 31, g = ln >> 2, t = ln & 3;
+      const __nv_bfloat16* row = qg + min(g, gv - 1) * kD;  // never addresses a row beyond the group
+      qraw[r] = (g < gv) ? __ldg(reinterpret_cast<const uint2*>(row + 64 * t + 4 * ks)) : make_uint2(0u, 0u);
+    }
+    if (nmine > 0) {
+      const KvRows kv = rows_of(pp);
+      issue_tile(ring[1], kv, s0, lane, policy);
+      if (nmine > 1) issue_tile(ring[2], kv, s1, lane, policy); else cp_commit();
+    }
+  };
+
+  __syncthreads();  // qmax initialised
+  Piece pc;
+  bool have = sched.next(pc);
+  // an idle CTA exits without the trigger, so stage 2 is placed after it has left
+  if (have) pdl_launch_dependents();
+  if (have) piece_head(pc);
+  while (have) {
+    const KvRows kv = rows_of(pc);
+    const int* idx = p.indices + pc.base + pc.j0;
+    const int len = pc.j1 - pc.j0;
+    const int nmine = nmine_of(len);
+    st.reset();
+
+    // Q into FP16: one power-of-two factor 2^e for the group puts its largest
+    // magnitude in [2^14, 2^15)
+    {
+      float mx = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t w2[2] = {qraw[r].x, qraw[r].y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] << 16)));
+          mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] & 0xFFFF0000u)));
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      if (lane == 0) atomicMax(&sm.qmax, __float_as_uint(mx));
+    }
+    __syncthreads();  // also: the previous piece's merge is done with stage 0 and the Q fragments
+    const unsigned int qm = sm.qmax;
+    int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);  // 2^e * max in [2^14, 2^15)
+    e = max(-126, min(127, e));
+    const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float sl2 = ldexpf(p.scale_log2, -e);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = threadIdx.x + r * kW4 * 32;
+      const uint32_t x = qraw[r].x, y = qraw[r].y;
+      sm.qf[i >> 5][i & 31] =
+          make_uint2(pack_f16(__uint_as_float(x << 16) * qs, __uint_as_float(x & 0xFFFF0000u) * qs),
+                     pack_f16(__uint_as_float(y << 16) * qs, __uint_as_float(y & 0xFFFF0000u) * qs));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sm.qmax = 0u;  // every thread has read it; the next write follows a barrier
+
+    int cur = 1;  // the stage of tile k; tile k + 2 goes to the stage before it (that of tile k - 1)
+    for (int k = 0; k < nmine; ++k) {
+      Fp4Stage& far = ring[cur == 0 ? 2 : cur - 1];
+      if (k + 2 < nmine) issue_tile(far, kv, s2, lane, policy); else cp_commit();
+      s2 = s3;
+      s3 = fetch(idx, k + 4, len, nmine);
+      cp_wait<2>();
+      __syncwarp();
+      st.qk_softmax(ring[cur], sm.qf, tile_n(k, len, nmine), sl2, lane);
+      st.pv(ring[cur], lane);
+      __syncwarp();
+      cur = cur == 2 ? 0 : cur + 1;
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // look ahead: the next piece's first loads go out before this piece's merge
+    Piece nx;
+    const bool have_next = sched.next(nx);
+    if (have_next) piece_head(nx);
+
+    // ---- merge: fragment-order slices in stage 0 of the rings, summed in a fixed order
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, off);
+      st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, off);
+    }
+    if (lane < 4) {
+      sm.mbuf[warp][2 * lane] = st.m0;
+      sm.mbuf[warp][2 * lane + 1] = st.m1;
+    }
+    __syncthreads();
+    {
+      const int ha = 2 * (lane & 3), hb = ha + 1;
+      float Ma = sm.mbuf[0][ha], Mb = sm.mbuf[0][hb];
+#pragma unroll
+      for (int x = 1; x < kW4; ++x) {
+        Ma = fmaxf(Ma, sm.mbuf[x][ha]);
+        Mb = fmaxf(Mb, sm.mbuf[x][hb]);
+      }
+      const float fa = (Ma == -INFINITY) ? 0.0f : safe_exp2_diff(st.m0, Ma);
+      const float fb = (Mb == -INFINITY) ? 0.0f : safe_exp2_diff(st.m1, Mb);
+      float4* slice = reinterpret_cast<float4*>(&ring[0]);
+#pragma unroll
+      for (int mt = 0; mt < 16; ++mt)
+        slice[mt * 32 + lane] = make_float4(st.o[mt][0] * fa, st.o[mt][1] * fb, st.o[mt][2] * fa, st.o[mt][3] * fb);
+      if (lane < 4) {
+        sm.lsum[warp][ha] = st.l0 * fa;
+        sm.lsum[warp][hb] = st.l1 * fb;
+      }
+    }
+    __syncthreads();
+    float* op = p.o_part + pc.id * (kG * kD);
+    for (int f = threadIdx.x; f < 16 * 32; f += blockDim.x) {
+      const int mt = f >> 5, ln = f & 31;
+      const int g = ln >> 2, ha = 2 * (ln & 3), hb = ha + 1;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float la = 0.0f, lb = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kW4; ++x) {
+        const float4 v = reinterpret_cast<const float4*>(&sm.ring[x][0])[f];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        la += sm.lsum[x][ha];
+        lb += sm.lsum[x][hb];
+      }
+      const float ia = (la != 0.0f) ? p.v_descale / la : 0.0f;  // a NaN sum makes a NaN partial
+      const float ib = (lb != 0.0f) ? p.v_descale / lb : 0.0f;
+      const int d0 = 32 * g + 2 * mt;
+      *reinterpret_cast<float2*>(op + ha * kD + d0) = make_float2(acc.x * ia, acc.z * ia);
+      *reinterpret_cast<float2*>(op + hb * kD + d0) = make_float2(acc.y * ib, acc.w * ib);
+    }
+    if (threadIdx.x < kG) {
+      float M = sm.mbuf[0][threadIdx.x], lt = 0.0f;
+#pragma unroll
+      for (int x = 1; x < kW4; ++x) M = fmaxf(M, sm.mbuf[x][threadIdx.x]);
+#pragma unroll
+      for (int x = 0; x < kW4; ++x) lt += sm.lsum[x][threadIdx.x];
+      // (stage 2 takes the largest LSE as its reference: +inf carries a NaN through it)
+      p.lse_part[pc.id * kG + threadIdx.x] = (lt > 0.0f) ? M + log2f(lt) : (lt == 0.0f) ? -INFINITY : INFINITY;
+    }
+    __syncthreads();  // stage 0, Q fragments and merge buffers free for the next piece
+    pc = nx;
+    have = have_next;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_stage1_fp4(const Stage1Params& p, int grid, cudaStream_t stream) {
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(stage1_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Fp4Smem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  stage1_fp4_kernel<<<grid, kW4 * 32, sizeof(Fp4Smem), stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace gda

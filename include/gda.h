@@ -87,6 +87,20 @@ typedef enum gda_status {
 #define GDA_KV_BF16 0            /* bf16 values */
 #define GDA_KV_E4M3 1            /* e4m3 codes (torch.float8_e4m3fn bytes) with per-tensor descales:
                                     K = k_descale * e4m3(code), V = v_descale * e4m3(code) */
+#define GDA_KV_E2M1 3            /* a 4-bit cache: e2m1 codes with an e4m3 scale per 16 head
+                                    dimensions (gda_args.kv_scales) and per-tensor descales */
+/*
+ * The 4-bit cache.  A row (one slot, one KV head) of K or V is D / 2 bytes of codes and
+ * D / 16 scales:
+ *   value[d] = descale * e4m3(scale[d / 16]) * e2m1(code[d]),
+ *   e2m1(0 .. 7) = 0, 1/2, 1, 3/2, 2, 3, 4, 6; codes 8 .. 15 are their negatives.
+ * Byte i of a row's codes holds dimension 2i in its low half and 2i + 1 in its high half.
+ *   k_pool, v_pool  [num_slots, Hkv, D / 2] bytes
+ *   kv_scales       [num_slots, Hkv, 2, D / 16] e4m3 bytes: the K row's scales, then the
+ *                   V row's
+ * gda_kv_write_fp4 and gda_qk_norm_mrope_kv_write write rows, gda_decode_ex and
+ * gda_decode_fp4 attend over them, gda_kv_gather_fp4 reads them back as BF16.
+ */
 
 /*
  * Full argument set of gda_decode_ex.
@@ -121,13 +135,14 @@ typedef enum gda_status {
  *               O = sum_j e^{s_j} V_j / (e^{sink_h} + sum_j e^{s_j}); lse includes it.
  *   kv_dtype    GDA_KV_BF16 or GDA_KV_E4M3 (an FP8 KV cache, cuDNN FE-OSS "Gated Attention
  *               Block (SM107)", API, QuantSpec: static per-tensor scales, e4m3 codes).
- *               E4M3 is served by GDA_VARIANT_AUTO / GDA_VARIANT_MMA only.
- *   k_descale, v_descale  per-tensor factors of an e4m3 cache (finite; else GDA_ERR_ARG);
- *               not used for bf16 pools.
+ *               E4M3 and E2M1 are served by GDA_VARIANT_AUTO / GDA_VARIANT_MMA only.
+ *               E2M1 reads the rows once per group of 8 query heads.  A NaN in a row that
+ *               the batch names (a NaN scale) gives NaN in the query heads that see it.
+ *   k_descale, v_descale  per-tensor factors of an e4m3 or 4-bit cache (finite; else
+ *               GDA_ERR_ARG); not used for bf16 pools.
  *   max_len     0, or an upper bound on every sequence's KV length that the caller knows
  *               on the host (a scheduler's batch maximum).  With a bound of at most
- *               1024, automatic splits (num_splits <= 0), GDA_VARIANT_AUTO, bf16 or e4m3
- *               pools, no check_indices, Hq / Hkv <= 8, and few enough (sequence, KV head) pairs
+ *               1024, automatic splits (num_splits <= 0), GDA_VARIANT_AUTO, no check_indices, Hq / Hkv <= 8, and few enough (sequence, KV head) pairs
  *               (gda_small_path_cluster), the call runs as ONE kernel: a thread-block
  *               cluster of 8, 4, 2 or 1 CTAs per (sequence, KV head) (the most that fit in
  *               one wave, at most 128 positions per CTA) that merges its partial
@@ -140,6 +155,8 @@ typedef enum gda_status {
  *               split count is chosen on the host (gda_auto_splits with lmax = max_len)
  *               and uniform splits launch as explicit ones: no scan of kv_indptr on the
  *               device and no idle CTAs.  A wrong value changes only the speed.
+ *   kv_scales   GDA_KV_E2M1: the pools' scales [num_slots, Hkv, 2, D / 16] (16-byte
+ *               aligned); not used for other pools.
  * (FreeToken PR #781, Automatic dispatch and Correctness: window, sinks, custom scale
  * and non-power-of-two GQA groups are the cases of the general path.)
  */
@@ -167,6 +184,7 @@ typedef struct gda_args {
     float v_descale;
     int max_len;
     int64_t total_len;
+    const uint8_t* kv_scales;
 } gda_args;
 
 /* Bytes of workspace gda_decode_ex needs for these sizes (FreeToken PR #781 Summary:
@@ -215,6 +233,40 @@ int gda_decode_e4m3(const gda_bf16* q, const gda_bf16* gate, const uint8_t* k_po
                     gda_bf16* out, int B, int Hq, int Hkv, int D, float scale, float k_descale,
                     float v_descale, int num_splits, gda_stream_t stream);
 
+/* As gda_decode over a 4-bit KV cache (GDA_KV_E2M1 above): k_pool and v_pool hold codes,
+ * kv_scales their scales.  q and gate stay bf16, the output and its rounding are those
+ * of gda_decode.  Same library-owned workspace.  Non-finite descales: GDA_ERR_ARG. */
+int gda_decode_fp4(const gda_bf16* q, const gda_bf16* gate, const uint8_t* k_pool, const uint8_t* v_pool,
+                   const uint8_t* kv_scales, const int32_t* kv_indptr, const int32_t* kv_indices, gda_bf16* out,
+                   int B, int Hq, int Hkv, int D, float scale, float k_descale, float v_descale, int num_splits,
+                   gda_stream_t stream);
+
+/* Quantise the K and V rows of T tokens into a 4-bit cache (GDA_KV_E2M1 above).
+ *   k, v       [T, Hkv, D] bf16, token t at k + t * k_stride elements (the heads of a token
+ *              contiguous, so parts of projection rows serve as they are); strides are
+ *              multiples of 8 and at least Hkv * D
+ *   slots      [T] int32: each token's slot; a slot outside [0, num_slots) is not written.
+ *              Slots are distinct: two tokens that name one slot leave a mix of their rows
+ *   k_pool, v_pool, kv_scales  the cache (16-byte aligned)
+ * Per block of 16 dimensions, with y = x / descale in FP32:
+ *   scale = nearest e4m3 to max |y| / 6 (at most 448); code = nearest e2m1 to y / e4m3(scale)
+ * both to nearest, ties to even, beyond the largest to the largest; the divisions are
+ * IEEE.  A block with a NaN gets the NaN scale, one whose scale rounds to 0 codes 0.
+ * Descales have to be finite and > 0 (GDA_ERR_ARG).  D = 256 (else GDA_ERR_UNSUPPORTED).
+ * Enqueues one kernel; T = 0 enqueues nothing. */
+int gda_kv_write_fp4(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, int64_t v_stride, const int32_t* slots,
+                     int64_t num_slots, uint8_t* k_pool, uint8_t* v_pool, uint8_t* kv_scales, float k_descale,
+                     float v_descale, int64_t T, int Hkv, int D, gda_stream_t stream);
+
+/* Read rows of a 4-bit cache back as BF16, e.g. the cached prefix that a prompt continues
+ * (gda_prefill_packed reads packed rows):
+ *   k_out[n, h, :] = RNE_bf16(value of the K row of slot indices[n]), v_out likewise,
+ * [N, Hkv, D] bf16.  An index outside [0, num_slots) gives zeros; indices may repeat.
+ * Descales have to be finite.  D = 256.  Enqueues one kernel; N = 0 enqueues nothing. */
+int gda_kv_gather_fp4(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales, int64_t num_slots,
+                      const int32_t* indices, int64_t N, float k_descale, float v_descale, gda_bf16* k_out,
+                      gda_bf16* v_out, int Hkv, int D, gda_stream_t stream);
+
 /* Prefill / extend gated SDPA (cuDNN FE-OSS "Gated Attention Block (SM107)", Overview
  * stages (4) SDPA with GQA H_q / H_kv and (5) the gate; Fusion knobs: fuse_gate puts
  * O *= sigmoid(GATE) in the SDPA epilogue, after the dead-row select; Forward:
@@ -239,6 +291,52 @@ int gda_decode_e4m3(const gda_bf16* q, const gda_bf16* gate, const uint8_t* k_po
 int gda_prefill(const gda_bf16* q, const gda_bf16* gate, const gda_bf16* k, const gda_bf16* v,
                 const int32_t* kv_lens, gda_bf16* out, float* lse, int B, int Sq, int Skv, int Hq, int Hkv,
                 int D, float scale, int causal, uint32_t* error_word, gda_stream_t stream);
+
+/*
+ * Prefill / extend gated SDPA over packed sequences of different lengths: the function of
+ * gda_prefill for each sequence, with no padding between them.
+ *   q, gate   [total_q, Hq, D] bf16         queries and gate (gate NULL: out = RNE_bf16(O))
+ *   k, v      [total_k, Hkv, D] bf16        keys and values
+ *   q_stride, gate_stride, k_stride, v_stride  elements from one token to the next (heads and
+ *             dimensions of a token contiguous), multiples of 8: the parts of a projection's
+ *             rows serve as they are
+ *   cu_seqlens_q, cu_seqlens_k  [B + 1] int32, device: sequence b has the query rows
+ *             [cu_seqlens_q[b], cu_seqlens_q[b + 1]) and likewise keys (the same pointer for
+ *             plain prompts).  Non-decreasing; sequences may be empty, and rows may lie
+ *             before the first or behind the last one.  Their contents are not checked:
+ *             values are clamped to [0, total], so nothing outside the tensors is read or
+ *             written
+ *   out       [total_q, Hq, D] bf16, contiguous.  Rows of no sequence are left as they are
+ *   lse       [Hq, total_q] float or NULL   natural-log log-sum-exp (-inf for a dead row)
+ *   causal    1: key j of a sequence is visible to its query i when j <= i + (keys - queries);
+ *             0: every key of the sequence is visible
+ *   error_word  as gda_prefill
+ * A query with no visible key gives O = 0 (out = 0) and lse = -inf.  Keys and values of
+ * other sequences and of rows of no sequence never reach a result, whatever they hold.
+ * Within a sequence a non-finite value row may also reach earlier queries of its 128-key
+ * tile (its probability there is 0, and 0 times it is NaN).
+ * scale, D, alignment, the first call on a device and stream capture are as for
+ * gda_prefill.  The lengths are read on the device: one kernel, no read back, no plan to
+ * keep, and a captured call follows cu_seqlens as they are at each replay.
+ */
+typedef struct gda_packed_args {
+    const gda_bf16* q;
+    const gda_bf16* gate;
+    const gda_bf16* k;
+    const gda_bf16* v;
+    int64_t q_stride, gate_stride, k_stride, v_stride;
+    const int32_t* cu_seqlens_q;
+    const int32_t* cu_seqlens_k;
+    gda_bf16* out;
+    float* lse;
+    int64_t total_q, total_k;
+    int B, Hq, Hkv, D;
+    float scale;
+    int causal;
+    uint32_t* error_word;
+} gda_packed_args;
+
+int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
 
 /* The library's prefill error word (used when gda_prefill gets error_word == NULL) on
  * the current device: synchronises `stream`, stores the bits in *error_word, clears
@@ -320,7 +418,7 @@ size_t gda_step_layout(int B, int Hq, int D, int64_t nnz, size_t offsets[4]);
  *      (skipped with GDA_STEP_MAP_IN: the kernels then read host_in in place);
  *   2. gda_decode on the views of dev_in, with the device-resident caches k_pool and
  *      v_pool (GDA_KV_BF16, or GDA_KV_E4M3 codes with k_descale and v_descale as in
- *      gda_args), into dev_out [B, Hq, D] (into host_out with GDA_STEP_MAP_OUT);
+ *      gda_args; GDA_KV_E2M1: GDA_ERR_UNSUPPORTED), into dev_out [B, Hq, D] (into host_out with GDA_STEP_MAP_OUT);
  *   3. one copy of dev_out (B * Hq * D bf16) to host_out (skipped with GDA_STEP_MAP_OUT);
  *   4. with synchronize != 0, a wait for the stream, after which host_out holds the
  *      gated output and host_in may be reused.
@@ -377,6 +475,58 @@ int gda_qk_norm_rope_kv_write(const gda_bf16* qgkv, int64_t row_stride, const gd
                               int64_t num_slots, gda_bf16* q_out, gda_bf16* gate_out,
                               gda_bf16* k_pool, gda_bf16* v_pool, int B, int Hq, int Hkv, int D,
                               gda_stream_t stream);
+
+/*
+ * The step before attention for the tokens of prompts or of a decode step, with rotary
+ * positions on several axes (time, height and width of images and video).  From token t's
+ * projection row [q (Hq*D) | gate (Hq*D) | k (Hkv*D) | v (Hkv*D)] it writes
+ *   q_out[t,h,:]  = rope(rmsnorm(q[t,h,:], w_q_norm))
+ *   k_out[t,h,:]  = rope(rmsnorm(k[t,h,:], w_k_norm))      (skipped when k_out is NULL)
+ *   gate_out[t]   = gate[t]                                (skipped when gate_out is NULL)
+ * and, with pools, the same K row and the V row at slots[t] (quantised as
+ * gda_kv_write_fp4 does for GDA_KV_E2M1).  rmsnorm as in gda_qk_norm_rope_kv_write; rope
+ * turns pair i = (dimension i, dimension i + rope_dim / 2), 0 <= i < rope_dim / 2, by
+ *   positions[pair_axis[i], t] * inv_freq[i]   radians,
+ * the angle exact to about 2^-24 at any int32 position.  FP32 arithmetic, one RNE
+ * rounding to bf16.
+ *   qgkv       [T, row_stride] bf16, row_stride >= (2 Hq + 2 Hkv) D, a multiple of 8
+ *   positions  [n_axes, T] int32, axis a at positions + a * pos_stride
+ *   inv_freq   [rope_dim / 2] float, finite, device
+ *   pair_axis  [rope_dim / 2] bytes in HOST memory, each below n_axes (read during the call)
+ *   slots      [T] int32; a slot outside [0, num_slots) is not written; slots are distinct
+ *   k_pool, v_pool  both NULL (no cache write; k_out is then required), or [num_slots, Hkv,
+ *              D] bf16 (kv_dtype GDA_KV_BF16), or the codes of a 4-bit cache (GDA_KV_E2M1,
+ *              with kv_scales and descales as in gda_kv_write_fp4)
+ * D = 256, rope_dim a multiple of 16 up to D (0: no rotation).  One kernel, nothing allocated.
+ */
+typedef struct gda_mrope_args {
+    const gda_bf16* qgkv;
+    int64_t row_stride;
+    const gda_bf16* w_q_norm;
+    const gda_bf16* w_k_norm;
+    float eps;
+    int n_axes;
+    const int32_t* positions;
+    int64_t pos_stride;
+    const float* inv_freq;
+    const uint8_t* pair_axis;
+    int rope_dim;
+    int kv_dtype;
+    gda_bf16* q_out;
+    gda_bf16* gate_out;
+    gda_bf16* k_out;
+    const int32_t* slots;
+    int64_t num_slots;
+    void* k_pool;
+    void* v_pool;
+    uint8_t* kv_scales;
+    float k_descale;
+    float v_descale;
+    int64_t T;
+    int Hq, Hkv, D;
+} gda_mrope_args;
+
+int gda_qk_norm_mrope_kv_write(const gda_mrope_args* args, gda_stream_t stream);
 
 /* Standalone gate, the second half of the unfused path (FreeToken PR #781,
  * Correctness: the fused output equals Torch sigmoid followed by Torch multiply):

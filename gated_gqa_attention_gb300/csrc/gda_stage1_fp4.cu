@@ -46,9 +46,9 @@ namespace gda {
 
 namespace {
 
-constexpr int kW4 = 8;            // warps per CTA
+constexpr int kW4 = 12;           // warps per CTA
 constexpr int kTok4 = 32;         // tokens per warp tile
-constexpr int kNS4 = 3;           // ring stages per warp
+constexpr int kNS4 = 2;           // ring stages per warp
 constexpr int kRow4 = kCodeBytes + kScaleBytes;   // ring row: codes, then scales (144 bytes)
 constexpr float kLazyLog2F4 = 8.0f;
 static_assert(kRow4 % 32 == 16, "the row pitch keeps 16-byte reads of 8 rows on different banks");
@@ -79,6 +79,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// 2^x on the SFU (2 ulp; results below the normal range are 0): P is rounded to FP16
+// right after, and 2^-126 against a sum of at least 2^-8 does not count.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -94,10 +101,15 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(addr));
   return v;
 }
+template <bool kAll>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
-               "r"(src_bytes), "l"(policy)
-               : "memory");
+  if (kAll)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(src_bytes), "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -110,28 +122,29 @@ __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
 
 struct KvRows {  // one KV head's rows of the three pools
   const unsigned char *k, *v, *s;
-  size_t code_stride, scale_stride;  // bytes between slots
+  uint32_t code_stride, scale_stride;  // bytes between slots
 };
 
-// The copies of one tile (tokens of `slot_lane`, -1: zeros) as one group: per
-// instruction four rows of codes, or 16 rows' scale chunks.
+// The copies of one tile (tokens of `slot_lane`) as one group: per instruction four rows of
+// codes, or 16 rows' scale chunks.  kAll: every slot is a row; else -1 stands for zeros.
+template <bool kAll>
 __device__ __forceinline__ void issue_tile(Fp4Stage& st, const KvRows& r, int slot_lane, int lane, uint64_t policy) {
   const int sub = lane >> 3, chunk = lane & 7;
+  const unsigned char *kc = r.k + 16 * chunk, *vc = r.v + 16 * chunk, *sc = r.s + 16 * (lane & 1);
+  const uint32_t dk = smem_u32(&st.k[sub][16 * chunk]), dv = smem_u32(&st.v[sub][16 * chunk]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + sub;
-    const int s = __shfl_sync(0xffffffffu, slot_lane, row);
-    const size_t off = (size_t)max(s, 0) * r.code_stride + 16 * chunk;
-    cp_async16(smem_u32(&st.k[row][16 * chunk]), r.k + off, s >= 0 ? 16u : 0u, policy);
-    cp_async16(smem_u32(&st.v[row][16 * chunk]), r.v + off, s >= 0 ? 16u : 0u, policy);
+    const int s = __shfl_sync(0xffffffffu, slot_lane, 4 * i + sub);
+    const size_t row = kAll ? (size_t)(uint32_t)s : (size_t)max(s, 0);
+    cp_async16<kAll>(dk + 4 * i * kRow4, kc + row * r.code_stride, s >= 0 ? 16u : 0u, policy);
+    cp_async16<kAll>(dv + 4 * i * kRow4, vc + row * r.code_stride, s >= 0 ? 16u : 0u, policy);
   }
+  const uint32_t ds = smem_u32((lane & 1) ? &st.v[lane >> 1][kCodeBytes] : &st.k[lane >> 1][kCodeBytes]);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int row = 16 * i + (lane >> 1);
-    const int s = __shfl_sync(0xffffffffu, slot_lane, row);
-    const unsigned char* src = r.s + (size_t)max(s, 0) * r.scale_stride + 16 * (lane & 1);
-    unsigned char* dst = (lane & 1) ? &st.v[row][kCodeBytes] : &st.k[row][kCodeBytes];
-    cp_async16(smem_u32(dst), src, s >= 0 ? 16u : 0u, policy);
+    const int s = __shfl_sync(0xffffffffu, slot_lane, 16 * i + (lane >> 1));
+    const size_t row = kAll ? (size_t)(uint32_t)s : (size_t)max(s, 0);
+    cp_async16<kAll>(ds + 16 * i * kRow4, sc + row * r.scale_stride, s >= 0 ? 16u : 0u, policy);
   }
   cp_commit();
 }
@@ -153,52 +166,61 @@ struct Fp4WarpState {
   // S^T of the tile's K rows, then the softmax update; nv tokens of the tile are valid
   __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[32], int nv, float sl2, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float s[8];
+    uint32_t row[4], sw[4];  // tokens g + 8j: address of the K row, the lane's four scales
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t r0 = smem_u32(&st.k[g + 16 * mt][0]), r1 = r0 + 8 * kRow4;
-      const uint32_t w0 = lds_u32(r0 + kCodeBytes + 4 * t), w1 = lds_u32(r1 + kCodeBytes + 4 * t);
-      float acc[2][4];
+    for (int j = 0; j < 4; ++j) {
+      row[j] = smem_u32(&st.k[g + 8 * j][0]);
+      sw[j] = lds_u32(row[j] + kCodeBytes + 4 * t);
+    }
+    float acc[4][4];  // [m-tile * 2 + k-step parity][4]
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.0f;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // dims 64t + 32 half .. + 31: two scale blocks
-        const uint4 c0 = lds_v4(r0 + 32 * t + 16 * half), c1 = lds_v4(r1 + 32 * t + 16 * half);
-        const uint32_t p0 = e4m3x2_to_f16x2(w0 >> (16 * half)), p1 = e4m3x2_to_f16x2(w1 >> (16 * half));
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          const uint32_t s0 = __byte_perm(p0, 0u, blk ? 0x3232 : 0x1010);
-          const uint32_t s1 = __byte_perm(p1, 0u, blk ? 0x3232 : 0x1010);
+    for (int half = 0; half < 2; ++half) {  // dims 64t + 32 half .. + 31: two scale blocks
+      uint4 c[4];
+      uint32_t sp[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < 4; ++j) {
+        c[j] = lds_v4(row[j] + 32 * t + 16 * half);
+        sp[j] = e4m3x2_to_f16x2(half ? sw[j] >> 16 : sw[j]);
+      }
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        uint32_t sc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = __byte_perm(sp[j], 0u, blk ? 0x3232 : 0x1010);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint2 b[2] = {qf[8 * half + 4 * blk + 2 * i][lane], qf[8 * half + 4 * blk + 2 * i + 1][lane]};
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
             uint32_t f0[4], f1[4];
-            e2m1x8_to_f16x2x4(word4(c0, 2 * blk + i), f0);
-            e2m1x8_to_f16x2x4(word4(c1, 2 * blk + i), f1);
+            e2m1x8_to_f16x2x4(word4(c[2 * mt], 2 * blk + i), f0);
+            e2m1x8_to_f16x2x4(word4(c[2 * mt + 1], 2 * blk + i), f1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int ks = 8 * half + 4 * blk + 2 * i + k;
-              const uint2 b = qf[ks][lane];
-              mma_f16(acc[k], f16x2_mul(f0[2 * k], s0), f16x2_mul(f1[2 * k], s1), f16x2_mul(f0[2 * k + 1], s0),
-                      f16x2_mul(f1[2 * k + 1], s1), b.x, b.y);
-            }
+            for (int k = 0; k < 2; ++k)
+              mma_f16(acc[2 * mt + k], f16x2_mul(f0[2 * k], sc[2 * mt]), f16x2_mul(f1[2 * k], sc[2 * mt + 1]),
+                      f16x2_mul(f0[2 * k + 1], sc[2 * mt]), f16x2_mul(f1[2 * k + 1], sc[2 * mt + 1]), b[k].x, b[k].y);
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[4 * mt + i] = (acc[0][i] + acc[1][i]) * sl2;
     }
+    float s[8];  // s[2j], s[2j + 1]: token g + 8j, heads 2t, 2t + 1 (log2 units)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < 4; ++i) {
+      s[i] = (acc[0][i] + acc[1][i]) * sl2;
+      s[4 + i] = (acc[2][i] + acc[3][i]) * sl2;
+    }
+    if (nv < kTok4) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // a NaN score becomes +inf, which the running max cannot pass over: the head's sum
-        // and output then end as NaN instead of as if the position were absent
-        float& x = s[2 * j + i];
-        x = (g + 8 * j >= nv) ? -INFINITY : (x != x) ? INFINITY : x;
-      }
+      for (int j = 0; j < 4; ++j)
+        if (g + 8 * j >= nv) s[2 * j] = s[2 * j + 1] = -INFINITY;
     }
     // Lazy rescale: the reference maxima move only when a score exceeds them by more
-    // than kLazyLog2F4, so probabilities stay <= 2^8.
+    // than kLazyLog2F4, so probabilities stay <= 2^8.  (A NaN score moves no maximum; its
+    // probability is NaN, which the sum and the output keep.)
     const float xa0 = fmaxf(fmaxf(s[0], s[2]), fmaxf(s[4], s[6]));
     const float xb0 = fmaxf(fmaxf(s[1], s[3]), fmaxf(s[5], s[7]));
     const bool grow = xa0 > m0 + kLazyLog2F4 || xb0 > m1 + kLazyLog2F4;
@@ -223,9 +245,11 @@ struct Fp4WarpState {
         o[i][3] *= ab;
       }
     }
+    // (no score above -inf yet: reference 0, so that -inf gives probability 0)
+    const float ra = (m0 == -INFINITY) ? 0.0f : m0, rb = (m1 == -INFINITY) ? 0.0f : m1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float pa = safe_exp2_diff(s[2 * j], m0), pb = safe_exp2_diff(s[2 * j + 1], m1);
+      const float pa = ex2(s[2 * j] - ra), pb = ex2(s[2 * j + 1] - rb);
       P[j] = pack_f16(pa, pb);
       l0 += pa;
       l1 += pb;
@@ -304,37 +328,40 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
   auto rows_of = [&](const Piece& pp) -> KvRows {
     const size_t h = (size_t)(pp.kvh / p.npass);
     return {p.k_pool + h * kCodeBytes, p.v_pool + h * kCodeBytes, p.scales + h * kScalePair,
-            (size_t)p.Hkv * kCodeBytes, (size_t)p.Hkv * kScalePair};
+            (uint32_t)p.Hkv * kCodeBytes, (uint32_t)p.Hkv * kScalePair};
   };
 
   Fp4WarpState st;
   Fp4Stage* ring = sm.ring[warp];
-  uint2 qraw[2];  // this thread's two BF16 Q^T fragments of the next piece
-  int s2 = -1, s3 = -1;
-  // Head of a piece: its Q rows, the slots of this warp's first four tiles and the copies of
-  // its first two (one group each).  For every piece after the first this runs before the
-  // previous piece's merge.
+  constexpr int kQr = (16 * 32 + kW4 * 32 - 1) / (kW4 * 32);
+  uint2 qraw[kQr];  // this thread's BF16 Q^T fragments of the next piece
+  int s1 = -1, s2 = -1;
+  auto issue = [&](Fp4Stage& stage, const KvRows& kv, int slot, int n) {
+    if (n == kTok4 && !p.check_indices) issue_tile<true>(stage, kv, slot, lane, policy);
+    else issue_tile<false>(stage, kv, slot, lane, policy);
+  };
+  // Head of a piece: its Q rows, the slots of this warp's first three tiles and the copies of
+  // its first one.  For every piece after the first this runs before the previous piece's
+  // merge.
   auto piece_head = [&](const Piece& pp) {
     const int kvh = pp.kvh / p.npass, pass = pp.kvh - kvh * p.npass;
     const int gv = min(kG, p.G - kG * pass);
     const __nv_bfloat16* qg = p.q + ((size_t)pp.b * p.Hq + (size_t)kvh * p.G + (size_t)kG * pass) * kD;
     const int* idx = p.indices + pp.base + pp.j0;
     const int len = pp.j1 - pp.j0, nmine = nmine_of(len);
-    const int s0 = fetch(idx, 0, len, nmine), s1 = fetch(idx, 1, len, nmine);
+    const int s0 = fetch(idx, 0, len, nmine);
+    s1 = fetch(idx, 1, len, nmine);
     s2 = fetch(idx, 2, len, nmine);
-    s3 = fetch(idx, 3, len, nmine);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kQr; ++r) {
       const int e = threadIdx.x + r * kW4 * 32;
+      qraw[r] = make_uint2(0u, 0u);
+      if (e >= 16 * 32) continue;
       const int ks = e >> 5, ln = e & 31, g = ln >> 2, t = ln & 3;
       const __nv_bfloat16* row = qg + min(g, gv - 1) * kD;  // never addresses a row beyond the group
-      qraw[r] = (g < gv) ? __ldg(reinterpret_cast<const uint2*>(row + 64 * t + 4 * ks)) : make_uint2(0u, 0u);
+      if (g < gv) qraw[r] = __ldg(reinterpret_cast<const uint2*>(row + 64 * t + 4 * ks));
     }
-    if (nmine > 0) {
-      const KvRows kv = rows_of(pp);
-      issue_tile(ring[1], kv, s0, lane, policy);
-      if (nmine > 1) issue_tile(ring[2], kv, s1, lane, policy); else cp_commit();
-    }
+    if (nmine > 0) issue(ring[1], rows_of(pp), s0, tile_n(0, len, nmine));
   };
 
   __syncthreads();  // qmax initialised
@@ -355,7 +382,7 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
     {
       float mx = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kQr; ++r) {
         const uint32_t w2[2] = {qraw[r].x, qraw[r].y};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -374,8 +401,9 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
     const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
     const float sl2 = ldexpf(p.scale_log2, -e);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kQr; ++r) {
       const int i = threadIdx.x + r * kW4 * 32;
+      if (i >= 16 * 32) continue;
       const uint32_t x = qraw[r].x, y = qraw[r].y;
       sm.qf[i >> 5][i & 31] =
           make_uint2(pack_f16(__uint_as_float(x << 16) * qs, __uint_as_float(x & 0xFFFF0000u) * qs),
@@ -384,18 +412,16 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
     __syncthreads();
     if (threadIdx.x == 0) sm.qmax = 0u;  // every thread has read it; the next write follows a barrier
 
-    int cur = 1;  // the stage of tile k; tile k + 2 goes to the stage before it (that of tile k - 1)
     for (int k = 0; k < nmine; ++k) {
-      Fp4Stage& far = ring[cur == 0 ? 2 : cur - 1];
-      if (k + 2 < nmine) issue_tile(far, kv, s2, lane, policy); else cp_commit();
-      s2 = s3;
-      s3 = fetch(idx, k + 4, len, nmine);
-      cp_wait<2>();
+      const int cur = (k + 1) & 1;  // tile k's stage
+      if (k + 1 < nmine) issue(ring[cur ^ 1], kv, s1, tile_n(k + 1, len, nmine)); else cp_commit();
+      s1 = s2;
+      s2 = fetch(idx, k + 3, len, nmine);
+      cp_wait<1>();
       __syncwarp();
       st.qk_softmax(ring[cur], sm.qf, tile_n(k, len, nmine), sl2, lane);
       st.pv(ring[cur], lane);
       __syncwarp();
-      cur = cur == 2 ? 0 : cur + 1;
     }
     cp_wait<0>();
     __syncwarp();

@@ -234,8 +234,8 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   // FP8 kernel in pairs, except for three groups (a half-empty pair costs a full one, and
   // two pairs measured no faster than three single passes on b64_l4096 lengths: 135.0
   // us for G = 32's two pairs against 135.9 us for G = 24's three passes)
-  // (over a 4-bit cache every group of 8 query heads reads the rows for itself)
-  const int team = (variant != gda::kVariantMma || npass < 2 || fp4) ? 1 : fp8 ? (npass == 3 ? 1 : 2) : team_size(npass);
+  // (the 4-bit kernel: pairs always, a widened row serves both groups' MMAs)
+  const int team = (variant != gda::kVariantMma || npass < 2) ? 1 : fp4 ? 2 : fp8 ? (npass == 3 ? 1 : 2) : team_size(npass);
   const int nteam = (npass + team - 1) / team;
   // the heads that split the batch into segments for the schedule
   const long long vheads = (long long)a->Hkv * nteam;
@@ -244,7 +244,8 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   // for the stream schedule is twice as many positions and S_opt comes from 16 S^2 >
   // lmax (half the BF16 count)
   const int kv8 = fp8 || fp4 ? 1 : 0;
-  const int auto_grid = sms < gda::kAutoMaxCtas ? sms : gda::kAutoMaxCtas;
+  const int slots = fp4 ? gda::kFp4CtasPerSm * sms : sms;  // stage-1 CTAs resident at once
+  const int auto_grid = slots < gda::kAutoMaxCtas ? slots : gda::kAutoMaxCtas;
   int splits = a->num_splits > 0 ? a->num_splits : 0;
   if (splits == 0 && a->window == 0 && a->max_len > 0 && a->total_len > 0) {
     // the caller knows a bound on the longest length and the exact total: the rule
@@ -264,7 +265,7 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   int grid;
   if (splits > 0) {
     const long long units = (long long)a->B * vheads * splits;
-    grid = (int)(units < sms ? units : sms);
+    grid = (int)(units < slots ? units : slots);
   } else {
     grid = auto_grid;
   }

@@ -148,7 +148,8 @@ cudaError_t launch_mrope(const MropeParams& p, cudaStream_t stream);
 cudaError_t launch_stage1(const Stage1Params& p, int variant, int grid, cudaStream_t stream);
 // Stage 1 over e4m3 K/V pools (same partials, same schedule).
 cudaError_t launch_stage1_fp8(const Stage1Params& p, int grid, cudaStream_t stream);
-// Stage 1 over 4-bit K/V pools (same partials, same schedule).
+// Stage 1 over 4-bit K/V pools (same partials, same schedule); kFp4CtasPerSm CTAs share an SM.
+constexpr int kFp4CtasPerSm = 2;
 cudaError_t launch_stage1_fp4(const Stage1Params& p, int grid, cudaStream_t stream);
 // Stage 2: FP32 LSE merge + gate epilogue, launched as a programmatic dependent of stage 1.
 cudaError_t launch_stage2(const Stage2Params& p, cudaStream_t stream);

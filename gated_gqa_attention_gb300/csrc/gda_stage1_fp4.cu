@@ -46,9 +46,7 @@ namespace gda {
 
 namespace {
 
-constexpr int kW4 = 12;           // warps per CTA
 constexpr int kTok4 = 32;         // tokens per warp tile
-constexpr int kNS4 = 2;           // ring stages per warp
 constexpr int kRow4 = kCodeBytes + kScaleBytes;   // ring row: codes, then scales (144 bytes)
 constexpr float kLazyLog2F4 = 8.0f;
 static_assert(kRow4 % 32 == 16, "the row pitch keeps 16-byte reads of 8 rows on different banks");
@@ -57,15 +55,16 @@ struct Fp4Stage {
   unsigned char k[kTok4][kRow4];
   unsigned char v[kTok4][kRow4];
 };
+// NG groups of 8 query heads per piece, W warps per CTA
+template <int NG, int W>
 struct Fp4Smem {
-  uint2 qf[16][32];               // Q^T fragments (FP16, scaled), lane order
-  Fp4Stage ring[kW4][kNS4];       // per-warp rings; stage 0 also holds the merge slice
-  float mbuf[kW4][kG];            // each warp's running max
-  float lsum[kW4][kG];            // each warp's rescaled sum
-  unsigned int qmax;              // largest |q| of the piece's group (float bits)
+  uint2 qf[NG][16][32];           // Q^T fragments (FP16, scaled), lane order
+  Fp4Stage ring[W][2];            // per-warp rings; stage 0 also holds the merge slice
+  float mbuf[W][kG];              // each warp's running max
+  float lsum[W][kG];              // each warp's rescaled sum
+  unsigned int qmax[NG];          // largest |q| of each group of the piece (float bits)
 };
 static_assert(sizeof(float4) * 16 * 32 <= sizeof(Fp4Stage), "merge slice fits a ring stage");
-static_assert(sizeof(Fp4Smem) <= 227 * 1024, "shared memory per CTA");
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -89,11 +88,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
@@ -149,42 +143,46 @@ __device__ __forceinline__ void issue_tile(Fp4Stage& st, const KvRows& r, int sl
   cp_commit();
 }
 
+template <int NG>
 struct Fp4WarpState {
-  float o[16][4];
-  float m0, m1, l0, l1;
-  uint32_t P[4];  // FP16 probabilities, P[j] = tokens g + 8j, heads (2t, 2t+1)
+  float o[NG][16][4];
+  float m[NG][2], l[NG][2];  // heads 2t, 2t + 1 of each group
+  uint32_t P[NG][4];         // FP16 probabilities, P[.][j] = tokens g + 8j, heads (2t, 2t+1)
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int n = 0; n < NG; ++n) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.0f;
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
   }
 
   // S^T of the tile's K rows, then the softmax update; nv tokens of the tile are valid
-  __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[32], int nv, float sl2, int lane) {
+  __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[16][32], int nv, const float* sl2,
+                                             int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t row[4], sw[4];  // tokens g + 8j: address of the K row, the lane's four scales
+    float acc[NG][4][4];  // [group][m-tile * 2 + k-step parity][4]
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      row[j] = smem_u32(&st.k[g + 8 * j][0]);
-      sw[j] = lds_u32(row[j] + kCodeBytes + 4 * t);
-    }
-    float acc[4][4];  // [m-tile * 2 + k-step parity][4]
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.0f;
+    const uint32_t row0 = smem_u32(&st.k[g][0]);  // token g + 8j: + 8 j kRow4
+    // dims 64t + 32 half .. + 31: two scale blocks.  (Rolled: the loop body is what a CTA
+    // first fetches from the instruction cache.)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {  // dims 64t + 32 half .. + 31: two scale blocks
+    for (int half = 0; half < 2; ++half) {
       uint4 c[4];
       uint32_t sp[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        c[j] = lds_v4(row[j] + 32 * t + 16 * half);
-        sp[j] = e4m3x2_to_f16x2(half ? sw[j] >> 16 : sw[j]);
+        c[j] = lds_v4(row0 + 8 * j * kRow4 + 32 * t + 16 * half);
+        sp[j] = e4m3x2_to_f16x2(lds_u16(row0 + 8 * j * kRow4 + kCodeBytes + 4 * t + 2 * half));
       }
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
@@ -193,81 +191,96 @@ struct Fp4WarpState {
         for (int j = 0; j < 4; ++j) sc[j] = __byte_perm(sp[j], 0u, blk ? 0x3232 : 0x1010);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint2 b[2] = {qf[8 * half + 4 * blk + 2 * i][lane], qf[8 * half + 4 * blk + 2 * i + 1][lane]};
+          uint2 b[NG][2];
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) b[n][k] = qf[n][8 * half + 4 * blk + 2 * i + k][lane];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
             uint32_t f0[4], f1[4];
             e2m1x8_to_f16x2x4(word4(c[2 * mt], 2 * blk + i), f0);
             e2m1x8_to_f16x2x4(word4(c[2 * mt + 1], 2 * blk + i), f1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_f16(acc[2 * mt + k], f16x2_mul(f0[2 * k], sc[2 * mt]), f16x2_mul(f1[2 * k], sc[2 * mt + 1]),
-                      f16x2_mul(f0[2 * k + 1], sc[2 * mt]), f16x2_mul(f1[2 * k + 1], sc[2 * mt + 1]), b[k].x, b[k].y);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a0 = f16x2_mul(f0[2 * k], sc[2 * mt]), a1 = f16x2_mul(f1[2 * k], sc[2 * mt + 1]);
+              const uint32_t a2 = f16x2_mul(f0[2 * k + 1], sc[2 * mt]), a3 = f16x2_mul(f1[2 * k + 1], sc[2 * mt + 1]);
+#pragma unroll
+              for (int n = 0; n < NG; ++n) mma_f16(acc[n][2 * mt + k], a0, a1, a2, a3, b[n][k].x, b[n][k].y);
+            }
           }
         }
       }
     }
-    float s[8];  // s[2j], s[2j + 1]: token g + 8j, heads 2t, 2t + 1 (log2 units)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = (acc[0][i] + acc[1][i]) * sl2;
-      s[4 + i] = (acc[2][i] + acc[3][i]) * sl2;
-    }
-    if (nv < kTok4) {
+    for (int n = 0; n < NG; ++n) {
+      float s[8];  // s[2j], s[2j + 1]: token g + 8j, heads 2t, 2t + 1 (log2 units)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (g + 8 * j >= nv) s[2 * j] = s[2 * j + 1] = -INFINITY;
-    }
-    // Lazy rescale: the reference maxima move only when a score exceeds them by more
-    // than kLazyLog2F4, so probabilities stay <= 2^8.  (A NaN score moves no maximum; its
-    // probability is NaN, which the sum and the output keep.)
-    const float xa0 = fmaxf(fmaxf(s[0], s[2]), fmaxf(s[4], s[6]));
-    const float xb0 = fmaxf(fmaxf(s[1], s[3]), fmaxf(s[5], s[7]));
-    const bool grow = xa0 > m0 + kLazyLog2F4 || xb0 > m1 + kLazyLog2F4;
-    if (__any_sync(0xffffffffu, grow)) {
-      float xa = xa0, xb = xb0;
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, off));
-        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, off));
+      for (int i = 0; i < 4; ++i) {
+        s[i] = (acc[n][0][i] + acc[n][1][i]) * sl2[n];
+        s[4 + i] = (acc[n][2][i] + acc[n][3][i]) * sl2[n];
       }
-      const float na = fmaxf(m0, xa), nb = fmaxf(m1, xb);
-      const float aa = safe_exp2_diff(m0, na), ab = safe_exp2_diff(m1, nb);
-      l0 *= aa;
-      l1 *= ab;
-      m0 = na;
-      m1 = nb;
+      if (nv < kTok4) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        o[i][0] *= aa;
-        o[i][1] *= ab;
-        o[i][2] *= aa;
-        o[i][3] *= ab;
+        for (int j = 0; j < 4; ++j)
+          if (g + 8 * j >= nv) s[2 * j] = s[2 * j + 1] = -INFINITY;
       }
-    }
-    // (no score above -inf yet: reference 0, so that -inf gives probability 0)
-    const float ra = (m0 == -INFINITY) ? 0.0f : m0, rb = (m1 == -INFINITY) ? 0.0f : m1;
+      // Lazy rescale: the reference maxima move only when a score exceeds them by more
+      // than kLazyLog2F4, so probabilities stay <= 2^8.  (A NaN score moves no maximum; its
+      // probability is NaN, which the sum and the output keep.)
+      const float xa0 = fmaxf(fmaxf(s[0], s[2]), fmaxf(s[4], s[6]));
+      const float xb0 = fmaxf(fmaxf(s[1], s[3]), fmaxf(s[5], s[7]));
+      const bool grow = xa0 > m[n][0] + kLazyLog2F4 || xb0 > m[n][1] + kLazyLog2F4;
+      if (__any_sync(0xffffffffu, grow)) {
+        float xa = xa0, xb = xb0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float pa = ex2(s[2 * j] - ra), pb = ex2(s[2 * j + 1] - rb);
-      P[j] = pack_f16(pa, pb);
-      l0 += pa;
-      l1 += pb;
+        for (int off = 4; off < 32; off <<= 1) {
+          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, off));
+          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, off));
+        }
+        const float na = fmaxf(m[n][0], xa), nb = fmaxf(m[n][1], xb);
+        const float aa = safe_exp2_diff(m[n][0], na), ab = safe_exp2_diff(m[n][1], nb);
+        l[n][0] *= aa;
+        l[n][1] *= ab;
+        m[n][0] = na;
+        m[n][1] = nb;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[n][i][0] *= aa;
+          o[n][i][1] *= ab;
+          o[n][i][2] *= aa;
+          o[n][i][3] *= ab;
+        }
+      }
+      // (no score above -inf yet: reference 0, so that -inf gives probability 0)
+      const float ra = (m[n][0] == -INFINITY) ? 0.0f : m[n][0], rb = (m[n][1] == -INFINITY) ? 0.0f : m[n][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float pa = ex2(s[2 * j] - ra), pb = ex2(s[2 * j + 1] - rb);
+        P[n][j] = pack_f16(pa, pb);
+        l[n][0] += pa;
+        l[n][1] += pb;
+      }
     }
   }
 
   // O^T += V^T P^T over the tile's V rows
   __device__ __forceinline__ void pv(const Fp4Stage& st, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t base = smem_u32(&st.v[0][0]);
+    uint32_t base = smem_u32(&st.v[2 * t][0]);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const uint32_t b0 = movmatrix_trans(P[2 * ks]), b1 = movmatrix_trans(P[2 * ks + 1]);
+    for (int ks = 0; ks < 2; ++ks, base += 16 * kRow4) {
+      uint32_t b0[NG], b1[NG];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        b0[n] = movmatrix_trans(ks ? P[n][2] : P[n][0]);
+        b1[n] = movmatrix_trans(ks ? P[n][3] : P[n][1]);
+      }
       uint4 c[4];       // tokens 16ks + (2t, 2t+1, 2t+8, 2t+9): codes of dims 32g .. + 31
       uint32_t sc[4];   // their scales of blocks 2g, 2g + 1
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t row = base + (16 * ks + 2 * t + (i & 1) + 8 * (i >> 1)) * kRow4;
+        const uint32_t row = base + ((i & 1) + 8 * (i >> 1)) * kRow4;
         c[i] = lds_v4(row + 16 * g);
         sc[i] = lds_u16(row + kCodeBytes + 2 * g);
       }
@@ -286,38 +299,42 @@ struct Fp4WarpState {
           e2m1x8_to_f16x2x4((x2 & kLow) | ((x3 << 4) & ~kLow), e23);
           e2m1x8_to_f16x2x4(((x2 >> 4) & kLow) | (x3 & ~kLow), o23);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16(o[4 * wi + k], f16x2_mul(e01[k], s01), f16x2_mul(o01[k], s01), f16x2_mul(e23[k], s23),
-                    f16x2_mul(o23[k], s23), b0, b1);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = f16x2_mul(e01[k], s01), a1 = f16x2_mul(o01[k], s01);
+            const uint32_t a2 = f16x2_mul(e23[k], s23), a3 = f16x2_mul(o23[k], s23);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) mma_f16(o[n][4 * wi + k], a0, a1, a2, a3, b0[n], b1[n]);
+          }
         }
       }
     }
   }
 };
 
-__global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p) {
+template <int NG, int W>
+__global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage1Params p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  Fp4Smem& sm = *reinterpret_cast<Fp4Smem*>(smem_raw);
+  Fp4Smem<NG, W>& sm = *reinterpret_cast<Fp4Smem<NG, W>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) sm.qmax = 0u;
+  if (threadIdx.x < NG) sm.qmax[threadIdx.x] = 0u;
   Sched sched;
-  sched.begin(p.indptr, p.B, p.Hkv * p.npass, p.num_splits, gridDim.x, blockIdx.x, p.min_chunk, p.window,
+  sched.begin(p.indptr, p.B, p.Hkv * p.nteam, p.num_splits, gridDim.x, blockIdx.x, p.min_chunk, p.window,
               p.piece_cost, p.rule_kv8);
   const uint64_t policy = l2_policy_evict_first();
 
   auto nmine_of = [&](int len) -> int {
     const int ntiles = (len + kTok4 - 1) / kTok4;
-    return (ntiles > warp) ? (ntiles - warp + kW4 - 1) / kW4 : 0;
+    return (ntiles > warp) ? (ntiles - warp + W - 1) / W : 0;
   };
   auto tile_n = [&](int k, int len, int nmine) -> int {
-    return (k < nmine) ? min(kTok4, len - kTok4 * (warp + kW4 * k)) : 0;
+    return (k < nmine) ? min(kTok4, len - kTok4 * (warp + W * k)) : 0;
   };
   // slot of token `lane` of this warp's tile k (-1 past the tile's end or for a bad index)
   auto fetch = [&](const int* idx, int k, int len, int nmine) -> int {
     int s = -1;
     if (lane < tile_n(k, len, nmine)) {
-      s = __ldg(idx + kTok4 * (warp + kW4 * k) + lane);
+      s = __ldg(idx + kTok4 * (warp + W * k) + lane);
       if (p.check_indices && (s < 0 || (long long)s >= p.num_slots)) {
         atomicOr(&p.hdr->error, kErrIndex);
         s = -1;
@@ -326,42 +343,46 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
     return s;
   };
   auto rows_of = [&](const Piece& pp) -> KvRows {
-    const size_t h = (size_t)(pp.kvh / p.npass);
+    const size_t h = (size_t)(pp.kvh / p.nteam);
     return {p.k_pool + h * kCodeBytes, p.v_pool + h * kCodeBytes, p.scales + h * kScalePair,
             (uint32_t)p.Hkv * kCodeBytes, (uint32_t)p.Hkv * kScalePair};
   };
 
-  Fp4WarpState st;
+  Fp4WarpState<NG> st;
   Fp4Stage* ring = sm.ring[warp];
-  constexpr int kQr = (16 * 32 + kW4 * 32 - 1) / (kW4 * 32);
-  uint2 qraw[kQr];  // this thread's BF16 Q^T fragments of the next piece
-  int s1 = -1, s2 = -1;
+  int s1 = -1, s2 = -1, s3 = -1;
   auto issue = [&](Fp4Stage& stage, const KvRows& kv, int slot, int n) {
     if (n == kTok4 && !p.check_indices) issue_tile<true>(stage, kv, slot, lane, policy);
-    else issue_tile<false>(stage, kv, slot, lane, policy);
+    else if (n > 0) issue_tile<false>(stage, kv, slot, lane, policy);
+    else cp_commit();  // (an empty group keeps the count)
   };
-  // Head of a piece: its Q rows, the slots of this warp's first three tiles and the copies of
-  // its first one.  For every piece after the first this runs before the previous piece's
-  // merge.
+  // Q^T fragments of a piece: this warp's (group, k-step) items w = warp + r W
+  constexpr int kQr = (NG * 16 + W - 1) / W;
+  uint2 qraw[kQr];
+  auto load_q = [&](const Piece& pp) {
+    const int kvh = pp.kvh / p.nteam, pass0 = (pp.kvh - kvh * p.nteam) * NG;
+    const __nv_bfloat16* qg = p.q + ((size_t)pp.b * p.Hq + (size_t)kvh * p.G) * kD;
+#pragma unroll
+    for (int r = 0; r < kQr; ++r) {
+      const int w = warp + r * W;
+      const int g = lane >> 2, t = lane & 3, hq = kG * (pass0 + (w >> 4)) + g;
+      qraw[r] = make_uint2(0u, 0u);  // (heads past the KV head's group are zeros)
+      if (w < NG * 16 && hq < p.G)
+        qraw[r] = __ldg(reinterpret_cast<const uint2*>(qg + (size_t)hq * kD + 64 * t + 4 * (w & 15)));
+    }
+  };
+  // Head of a piece: the slots of this warp's first four tiles, the copies of its first one
+  // and Q (for a pair of groups Q waits: its registers are taken).  For every piece after
+  // the first this runs before the previous piece's merge.
   auto piece_head = [&](const Piece& pp) {
-    const int kvh = pp.kvh / p.npass, pass = pp.kvh - kvh * p.npass;
-    const int gv = min(kG, p.G - kG * pass);
-    const __nv_bfloat16* qg = p.q + ((size_t)pp.b * p.Hq + (size_t)kvh * p.G + (size_t)kG * pass) * kD;
     const int* idx = p.indices + pp.base + pp.j0;
     const int len = pp.j1 - pp.j0, nmine = nmine_of(len);
     const int s0 = fetch(idx, 0, len, nmine);
     s1 = fetch(idx, 1, len, nmine);
     s2 = fetch(idx, 2, len, nmine);
-#pragma unroll
-    for (int r = 0; r < kQr; ++r) {
-      const int e = threadIdx.x + r * kW4 * 32;
-      qraw[r] = make_uint2(0u, 0u);
-      if (e >= 16 * 32) continue;
-      const int ks = e >> 5, ln = e & 31, g = ln >> 2, t = ln & 3;
-      const __nv_bfloat16* row = qg + min(g, gv - 1) * kD;  // never addresses a row beyond the group
-      if (g < gv) qraw[r] = __ldg(reinterpret_cast<const uint2*>(row + 64 * t + 4 * ks));
-    }
-    if (nmine > 0) issue(ring[1], rows_of(pp), s0, tile_n(0, len, nmine));
+    s3 = fetch(idx, 3, len, nmine);
+    if (NG == 1) load_q(pp);
+    issue(ring[1], rows_of(pp), s0, tile_n(0, len, nmine));
   };
 
   __syncthreads();  // qmax initialised
@@ -370,58 +391,67 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
   // an idle CTA exits without the trigger, so stage 2 is placed after it has left
   if (have) pdl_launch_dependents();
   if (have) piece_head(pc);
+  bool first = true;
   while (have) {
     const KvRows kv = rows_of(pc);
     const int* idx = p.indices + pc.base + pc.j0;
     const int len = pc.j1 - pc.j0;
     const int nmine = nmine_of(len);
     st.reset();
+    // tile 1: at once for the first piece; else when the merge is done with stage 0 (below)
+    if (first) issue(ring[0], kv, s1, tile_n(1, len, nmine));
 
-    // Q into FP16: one power-of-two factor 2^e for the group puts its largest
-    // magnitude in [2^14, 2^15)
-    {
-      float mx = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kQr; ++r) {
-        const uint32_t w2[2] = {qraw[r].x, qraw[r].y};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] << 16)));
-          mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] & 0xFFFF0000u)));
-        }
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      if (lane == 0) atomicMax(&sm.qmax, __float_as_uint(mx));
-    }
-    __syncthreads();  // also: the previous piece's merge is done with stage 0 and the Q fragments
-    const unsigned int qm = sm.qmax;
-    int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);  // 2^e * max in [2^14, 2^15)
-    e = max(-126, min(127, e));
-    const float qs = __uint_as_float((uint32_t)(e + 127) << 23);
-    const float sl2 = ldexpf(p.scale_log2, -e);
+    if (NG > 1) load_q(pc);
 #pragma unroll
     for (int r = 0; r < kQr; ++r) {
-      const int i = threadIdx.x + r * kW4 * 32;
-      if (i >= 16 * 32) continue;
+      const int w = warp + r * W;
+      if (w >= NG * 16) continue;
+      const uint32_t w2[2] = {qraw[r].x, qraw[r].y};
+      float mx = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] << 16)));
+        mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] & 0xFFFF0000u)));
+      }
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      if (lane == 0) atomicMax(&sm.qmax[w >> 4], bits);
+    }
+    __syncthreads();  // also: the previous piece's merge is done with stage 0 and the Q fragments
+    if (!first) issue(ring[0], kv, s1, tile_n(1, len, nmine));
+    first = false;
+    // Q into FP16: one power-of-two factor 2^e per group puts its largest magnitude in
+    // [2^14, 2^15)
+    float sl2[NG], qs[NG];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const unsigned int qm = sm.qmax[n];
+      int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);
+      e = max(-126, min(127, e));
+      qs[n] = __uint_as_float((uint32_t)(e + 127) << 23);
+      sl2[n] = ldexpf(p.scale_log2, -e);
+    }
+#pragma unroll
+    for (int r = 0; r < kQr; ++r) {
+      const int w = warp + r * W;
+      if (w >= NG * 16) continue;
       const uint32_t x = qraw[r].x, y = qraw[r].y;
-      sm.qf[i >> 5][i & 31] =
-          make_uint2(pack_f16(__uint_as_float(x << 16) * qs, __uint_as_float(x & 0xFFFF0000u) * qs),
-                     pack_f16(__uint_as_float(y << 16) * qs, __uint_as_float(y & 0xFFFF0000u) * qs));
+      const float f = NG == 1 ? qs[0] : (w >> 4) ? qs[NG - 1] : qs[0];
+      sm.qf[w >> 4][w & 15][lane] = make_uint2(pack_f16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f),
+                                               pack_f16(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f));
     }
     __syncthreads();
-    if (threadIdx.x == 0) sm.qmax = 0u;  // every thread has read it; the next write follows a barrier
+    if (threadIdx.x < NG) sm.qmax[threadIdx.x] = 0u;  // every thread has read it; the next write follows a barrier
 
     for (int k = 0; k < nmine; ++k) {
-      const int cur = (k + 1) & 1;  // tile k's stage
-      if (k + 1 < nmine) issue(ring[cur ^ 1], kv, s1, tile_n(k + 1, len, nmine)); else cp_commit();
-      s1 = s2;
-      s2 = fetch(idx, k + 3, len, nmine);
+      Fp4Stage& cur = ring[(k + 1) & 1];
       cp_wait<1>();
       __syncwarp();
-      st.qk_softmax(ring[cur], sm.qf, tile_n(k, len, nmine), sl2, lane);
-      st.pv(ring[cur], lane);
+      st.qk_softmax(cur, sm.qf, tile_n(k, len, nmine), sl2, lane);
+      st.pv(cur, lane);
       __syncwarp();
+      issue(cur, kv, s2, tile_n(k + 2, len, nmine));  // into the stage just read
+      s2 = s3;
+      s3 = fetch(idx, k + 4, len, nmine);
     }
     cp_wait<0>();
     __syncwarp();
@@ -431,89 +461,103 @@ __global__ void __launch_bounds__(kW4 * 32, 1) stage1_fp4_kernel(Stage1Params p)
     const bool have_next = sched.next(nx);
     if (have_next) piece_head(nx);
 
-    // ---- merge: fragment-order slices in stage 0 of the rings, summed in a fixed order
+    // ---- merge, group by group: fragment-order slices in stage 0 of the rings, summed in a
+    // fixed order
+    const int ha = 2 * (lane & 3), hb = ha + 1;
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, off);
-      st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, off);
-    }
-    if (lane < 4) {
-      sm.mbuf[warp][2 * lane] = st.m0;
-      sm.mbuf[warp][2 * lane + 1] = st.m1;
-    }
-    __syncthreads();
-    {
-      const int ha = 2 * (lane & 3), hb = ha + 1;
-      float Ma = sm.mbuf[0][ha], Mb = sm.mbuf[0][hb];
+    for (int n = 0; n < NG; ++n) {
 #pragma unroll
-      for (int x = 1; x < kW4; ++x) {
-        Ma = fmaxf(Ma, sm.mbuf[x][ha]);
-        Mb = fmaxf(Mb, sm.mbuf[x][hb]);
+      for (int off = 4; off < 32; off <<= 1) {
+        st.l[n][0] += __shfl_xor_sync(0xffffffffu, st.l[n][0], off);
+        st.l[n][1] += __shfl_xor_sync(0xffffffffu, st.l[n][1], off);
       }
-      const float fa = (Ma == -INFINITY) ? 0.0f : safe_exp2_diff(st.m0, Ma);
-      const float fb = (Mb == -INFINITY) ? 0.0f : safe_exp2_diff(st.m1, Mb);
-      float4* slice = reinterpret_cast<float4*>(&ring[0]);
-#pragma unroll
-      for (int mt = 0; mt < 16; ++mt)
-        slice[mt * 32 + lane] = make_float4(st.o[mt][0] * fa, st.o[mt][1] * fb, st.o[mt][2] * fa, st.o[mt][3] * fb);
       if (lane < 4) {
-        sm.lsum[warp][ha] = st.l0 * fa;
-        sm.lsum[warp][hb] = st.l1 * fb;
+        sm.mbuf[warp][ha] = st.m[n][0];
+        sm.mbuf[warp][hb] = st.m[n][1];
       }
-    }
-    __syncthreads();
-    float* op = p.o_part + pc.id * (kG * kD);
-    for (int f = threadIdx.x; f < 16 * 32; f += blockDim.x) {
-      const int mt = f >> 5, ln = f & 31;
-      const int g = ln >> 2, ha = 2 * (ln & 3), hb = ha + 1;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+      {
+        float Ma = sm.mbuf[0][ha], Mb = sm.mbuf[0][hb];
+#pragma unroll
+        for (int x = 1; x < W; ++x) {
+          Ma = fmaxf(Ma, sm.mbuf[x][ha]);
+          Mb = fmaxf(Mb, sm.mbuf[x][hb]);
+        }
+        const float fa = (Ma == -INFINITY) ? 0.0f : safe_exp2_diff(st.m[n][0], Ma);
+        const float fb = (Mb == -INFINITY) ? 0.0f : safe_exp2_diff(st.m[n][1], Mb);
+        float4* slice = reinterpret_cast<float4*>(&ring[0]);
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt)
+          slice[mt * 32 + lane] =
+              make_float4(st.o[n][mt][0] * fa, st.o[n][mt][1] * fb, st.o[n][mt][2] * fa, st.o[n][mt][3] * fb);
+        if (lane < 4) {
+          sm.lsum[warp][ha] = st.l[n][0] * fa;
+          sm.lsum[warp][hb] = st.l[n][1] * fb;
+        }
+      }
+      __syncthreads();
+      const long long id = pc.id * NG + n;
+      float* op = p.o_part + id * (kG * kD);
       float la = 0.0f, lb = 0.0f;
 #pragma unroll
-      for (int x = 0; x < kW4; ++x) {
-        const float4 v = reinterpret_cast<const float4*>(&sm.ring[x][0])[f];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+      for (int x = 0; x < W; ++x) {
         la += sm.lsum[x][ha];
         lb += sm.lsum[x][hb];
       }
       const float ia = (la != 0.0f) ? p.v_descale / la : 0.0f;  // a NaN sum makes a NaN partial
       const float ib = (lb != 0.0f) ? p.v_descale / lb : 0.0f;
-      const int d0 = 32 * g + 2 * mt;
-      *reinterpret_cast<float2*>(op + ha * kD + d0) = make_float2(acc.x * ia, acc.z * ia);
-      *reinterpret_cast<float2*>(op + hb * kD + d0) = make_float2(acc.y * ib, acc.w * ib);
-    }
-    if (threadIdx.x < kG) {
-      float M = sm.mbuf[0][threadIdx.x], lt = 0.0f;
+      for (int mt = warp; mt < 16; mt += W) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 1; x < kW4; ++x) M = fmaxf(M, sm.mbuf[x][threadIdx.x]);
+        for (int x = 0; x < W; ++x) {
+          const float4 v = reinterpret_cast<const float4*>(&sm.ring[x][0])[mt * 32 + lane];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+        const int d0 = 32 * (lane >> 2) + 2 * mt;
+        *reinterpret_cast<float2*>(op + ha * kD + d0) = make_float2(acc.x * ia, acc.z * ia);
+        *reinterpret_cast<float2*>(op + hb * kD + d0) = make_float2(acc.y * ib, acc.w * ib);
+      }
+      if (threadIdx.x < kG) {
+        float M = sm.mbuf[0][threadIdx.x], lt = 0.0f;
 #pragma unroll
-      for (int x = 0; x < kW4; ++x) lt += sm.lsum[x][threadIdx.x];
-      // (stage 2 takes the largest LSE as its reference: +inf carries a NaN through it)
-      p.lse_part[pc.id * kG + threadIdx.x] = (lt > 0.0f) ? M + log2f(lt) : (lt == 0.0f) ? -INFINITY : INFINITY;
+        for (int x = 1; x < W; ++x) M = fmaxf(M, sm.mbuf[x][threadIdx.x]);
+#pragma unroll
+        for (int x = 0; x < W; ++x) lt += sm.lsum[x][threadIdx.x];
+        // (stage 2 takes the largest LSE as its reference: +inf carries a NaN through it)
+        p.lse_part[id * kG + threadIdx.x] = (lt > 0.0f) ? M + log2f(lt) : (lt == 0.0f) ? -INFINITY : INFINITY;
+      }
+      __syncthreads();  // stage 0, Q fragments and merge buffers free for the next group or piece
     }
-    __syncthreads();  // stage 0, Q fragments and merge buffers free for the next piece
     pc = nx;
     have = have_next;
   }
 }
 
-}  // namespace
-
-cudaError_t launch_stage1_fp4(const Stage1Params& p, int grid, cudaStream_t stream) {
-  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+template <int NG, int W>
+cudaError_t launch_fp4(const Stage1Params& p, int grid, cudaStream_t stream, std::atomic<bool>* attr_set) {
+  static_assert(kFp4CtasPerSm * (sizeof(Fp4Smem<NG, W>) + 1024) <= 228 * 1024, "shared memory per SM");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(stage1_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Fp4Smem));
+    e = cudaFuncSetAttribute(stage1_fp4_kernel<NG, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Fp4Smem<NG, W>));
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  stage1_fp4_kernel<<<grid, kW4 * 32, sizeof(Fp4Smem), stream>>>(p);
+  stage1_fp4_kernel<NG, W><<<grid, W * 32, sizeof(Fp4Smem<NG, W>), stream>>>(p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_stage1_fp4(const Stage1Params& p, int grid, cudaStream_t stream) {
+  static std::atomic<bool> one_set[64], pair_set[64];  // zero-initialised: false
+  return p.team == 2 ? launch_fp4<2, 4>(p, grid, stream, pair_set) : launch_fp4<1, 6>(p, grid, stream, one_set);
 }
 
 }  // namespace gda

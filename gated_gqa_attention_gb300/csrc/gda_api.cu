@@ -150,7 +150,9 @@ int host_uniform_splits(long long B, long long heads, long long grid, int min_ch
   const long long units1 = B * heads;
   if (units1 > grid) return 0;
   if (units1 == 0) return 1;
-  if (heads * n >= (long long)gda::kStreamMinPerCta * (kv8 ? 2 : 1) * grid) return 0;
+  // 4-bit caches: one wave that keeps 95 % of the CTAs busy beats the stream at any length
+  const bool fills = kv8 == 2 && 20 * (grid / units1) * units1 >= 19 * grid;
+  if (!fills && heads * n >= (long long)gda::kStreamMinPerCta * (kv8 ? 2 : 1) * grid) return 0;
   if (4 * lmax * B > 5 * n) return 0;
   long long s_opt = 1;
   const long long k = kv8 ? 16 : 4;
@@ -158,6 +160,7 @@ int host_uniform_splits(long long B, long long heads, long long grid, int min_ch
   const long long s_len = lmax > 0 ? (lmax + min_chunk - 1) / min_chunk : 1;
   long long s = s_opt < s_len ? s_opt : s_len;
   const long long s_wave = grid / units1;
+  if (s >= s_wave && fills) return (int)s_wave;
   if (s >= s_wave) {
     long long p2 = 1;
     while (2 * p2 <= s_wave) p2 *= 2;
@@ -243,7 +246,8 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   // the rule's e4m3 variant: a position streams in half the time, so the per-CTA bound
   // for the stream schedule is twice as many positions and S_opt comes from 16 S^2 >
   // lmax (half the BF16 count)
-  const int kv8 = fp8 || fp4 ? 1 : 0;
+  // (2: the 4-bit cache's further variant)
+  const int kv8 = fp4 ? 2 : fp8 ? 1 : 0;
   const int slots = fp4 ? gda::kFp4CtasPerSm * sms : sms;  // stage-1 CTAs resident at once
   const int auto_grid = slots < gda::kAutoMaxCtas ? slots : gda::kAutoMaxCtas;
   int splits = a->num_splits > 0 ? a->num_splits : 0;
@@ -297,7 +301,7 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   p1.min_chunk = min_chunk;
   // automatic stream schedule with more segments than CTAs: a segment start costs a CTA
   // about as much as kPieceCost positions (twice as many positions of an e4m3 cache)
-  p1.piece_cost = (splits == 0 && (long long)a->B * vheads > grid) ? (kv8 ? gda::kPieceCostE4m3 : gda::kPieceCost) : 0;
+  p1.piece_cost = (splits == 0 && (long long)a->B * vheads > grid) ? (fp4 ? gda::kPieceCostFp4 : fp8 ? gda::kPieceCostE4m3 : gda::kPieceCost) : 0;
   p1.rule_kv8 = kv8;
   p1.check_indices = a->check_indices ? 1 : 0;
   p1.wait_limit = wait_limit();

@@ -249,6 +249,8 @@ constexpr int kStreamMinPerCta = 3072;
 // is 0 (the host passes the cost it picks).
 constexpr int kPieceCost = 300;
 constexpr int kPieceCostE4m3 = 600;
+// (a 4-bit cache, two CTAs per SM: 0 113.1, 200 104.7, 400 101.6, 600 102.7, 900 104.0 us)
+constexpr int kPieceCostFp4 = 400;
 
 struct Sched {
   const int* indptr;
@@ -413,7 +415,8 @@ struct Sched {
   //    merges S partials per head), c/b ~ 2 positions (stage 2 keeps four partials'
   //    loads in flight), so the best S is near sqrt(lmax / 2): S_opt, the smallest
   //    power of two with 4 S^2 > lmax, and at most ceil(lmax / min_chunk).  An e4m3
-  //    cache (kv8) streams a position in half the time, c/b ~ 8: 16 S^2 > lmax;
+  //    cache (kv8) streams a position in half the time, c/b ~ 8: 16 S^2 > lmax, and a 4-bit
+  //    cache (kv8 = 2) takes the same;
   //  * at most one wave of CTAs (B Hkv S <= grid); when the wave bounds S, the
   //    power of two below the bound if it keeps >= 80 % of the CTAs busy (pieces
   //    aligned to the warps' tiles), else the bound itself, and with < 80 % busy
@@ -440,7 +443,13 @@ struct Sched {
       lmax = max(lmax, __shfl_xor_sync(0xffffffffu, lmax, off));
       n += __shfl_xor_sync(0xffffffffu, n, off);
     }
-    if ((long long)Hkv * n >= (long long)kStreamMinPerCta * (kv8 ? 2 : 1) * grid) return 0;
+    // 4-bit caches (kv8 == 2; two CTAs per SM): one wave that keeps 95 % of the CTAs busy
+    // beats the stream at any length and a rounded-down power of two (measured: 16 segments
+    // x 131072 on 304 CTAs, 19 splits 115.3 us, stream 119.4 us; with pairs of groups x
+    // 32769 51.4 us against 57.2 us for 16 splits and 57.3 us for the stream)
+    const int s_wave = grid / units1;
+    const bool fills = kv8 == 2 && 20 * s_wave * units1 >= 19 * grid;
+    if (!fills && (long long)Hkv * n >= (long long)kStreamMinPerCta * (kv8 ? 2 : 1) * grid) return 0;
     if (4LL * lmax * B > 5LL * n) return 0;
     // (closed forms, short dependent chains: every CTA's start waits on this)
     // s_opt: the smallest power of two p with 4 p^2 > lmax, 2^(h / 2) with h the index
@@ -448,7 +457,7 @@ struct Sched {
     const int s_opt = (lmax > 0) ? (1 << max(0, ((31 - __clz(lmax)) >> 1) - (kv8 ? 1 : 0))) : 1;
     const int s_len = max(1, (lmax + min_chunk - 1) / min_chunk);
     int s = min(s_opt, s_len);
-    const int s_wave = grid / units1;
+    if (s >= s_wave && fills) return s_wave;
     if (s >= s_wave) {
       const int p2 = 1 << (31 - __clz(s_wave));  // the largest power of two <= s_wave
       s = (5 * p2 * units1 >= 4 * grid) ? p2 : s_wave;

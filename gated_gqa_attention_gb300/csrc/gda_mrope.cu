@@ -14,13 +14,19 @@
 // turn dropped by the integer wrap, its upper 32 bits go to sincospi, and the error stays
 // below 2^-25 turns at any 32-bit position.
 //
-// Layout.  A block of 8 warps walks the tokens; per token the first rope_dim / 2 threads
-// put cos and sin into shared memory, once for all heads, and each warp takes rows in turn
-// (lane l owns dimensions 8l .. 8l + 7: one 16-byte load and store; the rotation partner
-// is lane l +- rope_dim / 16).  The loads of a warp's first rows go out before the cos and
-// sin are computed.  FP32 arithmetic, one rounding to BF16; a 4-bit cache quantises that
-// BF16 value, so its rows equal k_out quantised.  Bound by HBM: every row in once and out
-// once.
+// Layout.  `wpt` warps share a token's rows (1 for prompts; as many as it takes to fill the
+// GPU when there are few tokens), each walking its share of the tokens with no block
+// barrier.  Per token a warp takes cos and sin of every pair once (lanes stride over the
+// pairs) and reads back those of its own dimensions: lane l owns dimensions 8l .. 8l + 7
+// (one 16-byte load and store a row), the partner of a rotated dimension is in lane
+// l +- rope_dim / 16, and the norm weights are folded into cos and sin:
+//   y = rinv (x (w cos) +- x_partner (w_partner sin)),
+// so a row costs four shuffles of packed pairs and two multiply-adds per element.  Up to
+// four rows are in flight per warp.  FP32 arithmetic, one rounding to BF16; a 4-bit cache
+// quantises that BF16 value, so its rows equal k_out quantised.  Bound by HBM for prompts
+// (every row in once and out once), by latency for a decode step.
+#include <type_traits>
+
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
 
@@ -28,122 +34,198 @@ namespace gda {
 
 namespace {
 
-constexpr int kMropeWarps = 8;
+constexpr int kMropeWarps = 8;   // per block
+constexpr int kMropeRows = 2;    // rows in flight per warp
+constexpr int kMropeBlocksPerSm = 4;
 
-__device__ __forceinline__ void bf16x8_to_float(const uint4& r, float* f) {
+// eight BF16 values as four FP32 pairs
+__device__ __forceinline__ void unpack(const uint4& r, float2* f) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 float_to_bf16x8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+// two FP32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// a BF16 row into row r of a pool of codes
+__device__ __forceinline__ void store_bf16_row4(const uint4& v, float descale, void* pool, unsigned char* scales, size_t r,
+                                                int lane) {
+  float2 f[4];
+  unpack(v, f);
+  const float x[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  store_row4(x, descale, static_cast<unsigned char*>(pool) + r * kCodeBytes, scales, lane);
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
-__global__ void __launch_bounds__(kMropeWarps * 32) mrope_kernel(const __grid_constant__ MropeParams p) {
-  __shared__ __align__(16) float s_cos[2][kMropeMaxPairs], s_sin[2][kMropeMaxPairs];
+// frac(f / 2 pi) * 2^64 modulo 2^64, from f = m 2^-s by one 24 x 64 bit product with
+// floor(2^64 / 2 pi) (FP64 arithmetic would cost every warp more than the rest of its start).
+__device__ __forceinline__ unsigned long long turn_fraction(float f) {
+  const uint32_t b = __float_as_uint(f);
+  const int e = (int)((b >> 23) & 0xFFu);
+  const unsigned long long m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int s = 150 - (e ? e : 1);
+  constexpr unsigned long long kInv2Pi = 0x28BE60DB9391054AULL;
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  unsigned long long r;
+  if (s <= 0) r = -s < 64 ? lo << -s : 0ull;
+  else if (s < 64) r = (lo >> s) | (hi << (64 - s));
+  else r = s < 128 ? hi >> (s - 64) : 0ull;
+  return (b >> 31) ? 0ull - r : r;
+}
+
+__global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_kernel(const __grid_constant__ MropeParams p, int wpt) {
+  __shared__ __align__(16) float s_cs[kMropeWarps][2][kMropeMaxPairs];
+  __shared__ unsigned long long s_freq[kMropeMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int npair = p.rope_dim / 2;
-  const bool trig = (int)threadIdx.x < npair;
-  unsigned long long F = 0ull;
-  const int* pos = p.positions;
-  if (trig) {
-    double turns = (double)__ldg(p.inv_freq + threadIdx.x) * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= floor(turns);
-    F = (unsigned long long)(turns * 18446744073709551616.0);  // 2^64 (1.0 saturates: one part in 2^64 off)
-    pos += (long long)p.pair_axis[threadIdx.x] * p.pos_stride;
-  }
-  // rows of a token in the order the warps take them: q, k, v (with a cache), gate
-  const int n_v = p.pool != 0 ? p.Hkv : 0;
-  const int n_g = p.gate_out != nullptr ? p.Hq : 0;
-  const int rows = p.Hq + p.Hkv + n_v + n_g;
-  auto source = [&](long long t, int r) -> const uint4* {
-    const int at = r < p.Hq ? r : r < p.Hq + p.Hkv + n_v ? r + p.Hq : r - p.Hkv - n_v;
-    return reinterpret_cast<const uint4*>(p.qgkv + t * p.row_stride + (long long)at * kD) + lane;
-  };
-  int buf = 0;
-  for (long long t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    if (warp < rows) next = __ldg(source(t, warp));
+  const int npair = p.rope_dim / 2, hl = p.rope_dim / 16;  // hl lanes hold the first halves of the pairs
+  const bool rot = lane < 2 * hl, first = lane < hl;
+  const int partner = rot ? (first ? lane + hl : lane - hl) : lane;
+  const int pair0 = 8 * (first ? lane : lane - hl);        // the lane's first pair
+  const long long gw = (long long)blockIdx.x * kMropeWarps + warp, nw = (long long)gridDim.x * kMropeWarps;
+  const int sub = (int)(gw % wpt);
+  const uint4* qgkv = reinterpret_cast<const uint4*>(p.qgkv) + lane;
+  const long long pitch = p.row_stride / 8;                // in 16-byte words
+
+  // frequencies as 64-bit fractions of a turn, once per block
+  for (int i = threadIdx.x; i < npair; i += kMropeWarps * 32) s_freq[i] = turn_fraction(__ldg(p.inv_freq + i));
+  __syncthreads();
+
+  const long long step = nw / wpt;
+  for (long long t = gw / wpt; t < p.T; t += step) {
+    const uint4* row = qgkv + t * pitch;
     const int slot = p.pool != 0 ? __ldg(p.slots + t) : -1;
     const bool slot_ok = slot >= 0 && (long long)slot < p.num_slots;
-    if (trig) {
-      const unsigned long long u = (unsigned long long)(long long)__ldg(pos + t) * F;
+    const size_t cache_row = (size_t)max(slot, 0) * p.Hkv;  // first row of the token's slot
+    __syncwarp();  // the previous token's cos and sin have been read
+    for (int i = lane; i < npair; i += 32) {
+      const int pos = __ldg(p.positions + (long long)p.pair_axis[i] * p.pos_stride + t);
+      const unsigned long long u = (unsigned long long)(long long)pos * s_freq[i];
       float s, c;
       sincospif((float)(int)(u >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-      s_cos[buf][threadIdx.x] = c;
-      s_sin[buf][threadIdx.x] = s;
+      s_cs[warp][0][i] = c;
+      s_cs[warp][1][i] = s;
     }
-    __syncthreads();  // (the other buffer's readers of token t - grid passed this barrier before the next write to it)
-    for (int r = warp; r < rows; r += kMropeWarps) {
-      const uint4 raw = next;
-      if (r + kMropeWarps < rows) next = __ldg(source(t, r + kMropeWarps));
-      if (r >= p.Hq + p.Hkv) {
-        const int h = r - p.Hq - p.Hkv;
-        if (h >= n_v) {  // gate: copied out
-          reinterpret_cast<uint4*>(p.gate_out + (t * p.Hq + (h - n_v)) * kD)[lane] = raw;
-        } else if (slot_ok) {  // v: into its slot
-          const size_t row = (size_t)slot * p.Hkv + h;
-          if (p.pool == 1) {
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pool) + row * kD)[lane] = raw;
-          } else {
-            float x[8];
-            bf16x8_to_float(raw, x);
-            store_row4(x, p.v_descale, static_cast<unsigned char*>(p.v_pool) + row * kCodeBytes,
-                       p.scales + row * kScalePair + kScaleBytes, lane);
-          }
+    __syncwarp();
+
+    // q rows, then k rows: norm and rotation
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+      const int heads = kind ? p.Hkv : p.Hq;
+      int h = kind ? (sub - p.Hq % wpt + wpt) % wpt : sub;  // this warp's first head
+      if (h >= heads) continue;
+      const uint4* src = row + ((kind ? 2 * p.Hq : 0) + h) * (kD / 8);
+      const __nv_bfloat16* w = kind ? p.w_k : p.w_q;
+      float2 cw[4], sw[4];  // dims 8 lane + 2i, + 1: the norm weight times cos, the partner's times +-sin
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cw[i] = make_float2(1.0f, 1.0f);
+        sw[i] = make_float2(0.0f, 0.0f);
+        if (rot) {
+          cw[i] = *reinterpret_cast<const float2*>(&s_cs[warp][0][pair0 + 2 * i]);
+          sw[i] = *reinterpret_cast<const float2*>(&s_cs[warp][1][pair0 + 2 * i]);
+          if (first) sw[i] = make_float2(-sw[i].x, -sw[i].y);
         }
-        continue;
       }
-      const bool is_q = r < p.Hq;
-      float x[8];
-      bf16x8_to_float(raw, x);
-      const __nv_bfloat16* w = is_q ? p.w_q : p.w_k;
       if (w != nullptr) {
-        float ss = 0.0f;
+        float2 a[4], b[4];
+        unpack(__ldg(reinterpret_cast<const uint4*>(w) + lane), a);
+        unpack(__ldg(reinterpret_cast<const uint4*>(w) + partner), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float rinv = 1.0f / sqrtf(ss * (1.0f / kD) + p.eps);
-        float wv[8];
-        bf16x8_to_float(__ldg(reinterpret_cast<const uint4*>(w) + lane), wv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * rinv * wv[i];
-      }
-      if (p.rope_dim > 0) {
-        const int hl = p.rope_dim / 16;  // lanes holding the first halves of the pairs
-        const bool first = lane < hl;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], (first ? lane + hl : lane - hl) & 31);
-        if (lane < 2 * hl) {
-          const int pair = 8 * (first ? lane : lane - hl);
-          const float sign = first ? -1.0f : 1.0f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * s_cos[buf][pair + i] + sign * (y[i] * s_sin[buf][pair + i]);
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = mul2(cw[i], a[i]);
+          sw[i] = mul2(sw[i], b[i]);
         }
       }
-      const uint4 o = float_to_bf16x8(x);
-      if (is_q) {
-        reinterpret_cast<uint4*>(p.q_out + (t * p.Hq + r) * kD)[lane] = o;
-      } else {
-        const int h = r - p.Hq;
-        if (p.k_out != nullptr) reinterpret_cast<uint4*>(p.k_out + (t * p.Hkv + h) * kD)[lane] = o;
-        if (slot_ok) {
-          const size_t row = (size_t)slot * p.Hkv + h;
-          if (p.pool == 1) {
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_pool) + row * kD)[lane] = o;
-          } else {
-            bf16x8_to_float(o, x);
-            store_row4(x, p.k_descale, static_cast<unsigned char*>(p.k_pool) + row * kCodeBytes,
-                       p.scales + row * kScalePair, lane);
+      uint4* dst = reinterpret_cast<uint4*>(kind ? p.k_out : p.q_out);
+      if (dst != nullptr) dst += (t * heads + h) * (kD / 8) + lane;
+      const long long pitch_h = (long long)wpt * (kD / 8);  // from one of the warp's heads to the next
+      // N rows at once: their loads, sums and shuffles overlap
+      auto rows = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        uint4 raw[N];
+        float rinv[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) raw[j] = __ldcs(src + j * pitch_h);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float2 x[4];
+          unpack(raw[j], x);
+          float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+          rinv[j] = ss.x + ss.y;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+          for (int j = 0; j < N; ++j) rinv[j] += __shfl_xor_sync(0xffffffffu, rinv[j], off);
+#pragma unroll
+        for (int j = 0; j < N; ++j) rinv[j] = (w != nullptr) ? rsqrtf(rinv[j] * (1.0f / kD) + p.eps) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float2 x[4], y[4];
+          unpack(raw[j], x);
+          uint4 o;
+          o.x = __shfl_sync(0xffffffffu, raw[j].x, partner);
+          o.y = __shfl_sync(0xffffffffu, raw[j].y, partner);
+          o.z = __shfl_sync(0xffffffffu, raw[j].z, partner);
+          o.w = __shfl_sync(0xffffffffu, raw[j].w, partner);
+          unpack(o, y);
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 v = mul2(x[i], cw[i]);
+            if (rot) v = fma2(y[i], sw[i], v);  // (other lanes' values never reach an unrotated one)
+            v = mul2(v, make_float2(rinv[j], rinv[j]));
+            out[i] = bf16x2(v.x, v.y);
+          }
+          const uint4 o4 = make_uint4(out[0], out[1], out[2], out[3]);
+          if (dst != nullptr) dst[j * pitch_h] = o4;
+          if (kind && slot_ok) {
+            const size_t r = cache_row + h + j * wpt;
+            if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_pool) + r * kD)[lane] = o4;
+            else store_bf16_row4(o4, p.k_descale, p.k_pool, p.scales + r * kScalePair, r, lane);
           }
         }
+        h += N * wpt;
+        src += N * pitch_h;
+        if (dst != nullptr) dst += N * pitch_h;
+      };
+      while (h + (kMropeRows - 1) * wpt < heads) rows(std::integral_constant<int, kMropeRows>());
+      while (h < heads) rows(std::integral_constant<int, 1>());
+    }
+    // v rows into the cache, gate rows out: copies (v quantised for a 4-bit cache)
+    if (slot_ok) {
+      for (int h = (sub - (p.Hq + p.Hkv) % wpt + wpt) % wpt; h < p.Hkv; h += wpt) {
+        const uint4 raw = __ldcs(row + (2LL * p.Hq + p.Hkv + h) * (kD / 8));
+        const size_t r = cache_row + h;
+        if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pool) + r * kD)[lane] = raw;
+        else store_bf16_row4(raw, p.v_descale, p.v_pool, p.scales + r * kScalePair + kScaleBytes, r, lane);
       }
+    }
+    if (p.gate_out != nullptr) {
+      uint4* dst = reinterpret_cast<uint4*>(p.gate_out + t * p.Hq * kD) + lane;
+      const uint4* src = row + (long long)p.Hq * (kD / 8);
+#pragma unroll 4
+      for (int h = (sub - (p.Hq + 2 * p.Hkv) % wpt + wpt) % wpt; h < p.Hq; h += wpt) dst[h * (kD / 8)] = __ldcs(src + h * (kD / 8));
     }
   }
 }
@@ -155,8 +237,16 @@ cudaError_t launch_mrope(const MropeParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long full = 8LL * sms;  // 8 blocks of 256 threads fill an SM
-  mrope_kernel<<<(unsigned)(p.T < full ? p.T : full), kMropeWarps * 32, 0, stream>>>(p);
+  // warps per token: as many as there are rows to share while that leaves SMs idle
+  const long long warps = (long long)kMropeBlocksPerSm * kMropeWarps * sms;  // resident at once
+  const int rows = p.Hq + 2 * p.Hkv + (p.gate_out != nullptr ? p.Hq : 0);
+  long long wpt = warps / p.T;
+  wpt = wpt < 1 ? 1 : wpt > rows ? rows : wpt;
+  // whole tokens per pass of the grid: a multiple of wpt warps
+  long long blocks = (p.T * wpt + kMropeWarps - 1) / kMropeWarps;
+  const long long full = warps / kMropeWarps;
+  if (blocks > full) blocks = full;
+  mrope_kernel<<<(unsigned)blocks, kMropeWarps * 32, 0, stream>>>(p, (int)wpt);
   return cudaGetLastError();
 }
 

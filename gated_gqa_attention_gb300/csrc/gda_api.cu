@@ -59,6 +59,20 @@ constexpr int kMaxHeads = 4096;
 // A factor that values are divided by.
 bool descale_ok(float d) { return isfinite(d) && d > 0.0f; }
 
+// Whether dividing by d is multiplying by 1 / d: a power of two whose reciprocal is normal.
+bool power_of_two(float d) {
+  int e;
+  return frexpf(d, &e) == 0.5f && e > -120 && e < 120;
+}
+
+// The factors of a cache write: exact reciprocals of both descales, or the descales.
+template <typename P>
+void set_factors(P* p, float k_descale, float v_descale) {
+  p->inv = power_of_two(k_descale) && power_of_two(v_descale) ? 1 : 0;
+  p->k_factor = p->inv ? 1.0f / k_descale : k_descale;
+  p->v_factor = p->inv ? 1.0f / v_descale : v_descale;
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int check_sizes(int B, int Hq, int Hkv, int D, int num_splits) {
@@ -579,8 +593,7 @@ int gda_kv_write_fp4(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, int
   p.k_pool = k_pool;
   p.v_pool = v_pool;
   p.scales = kv_scales;
-  p.k_descale = k_descale;
-  p.v_descale = v_descale;
+  set_factors(&p, k_descale, v_descale);
   p.T = T;
   p.Hkv = Hkv;
   if (gda::launch_kv4_write(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
@@ -669,8 +682,7 @@ int gda_qk_norm_mrope_kv_write(const gda_mrope_args* a, gda_stream_t stream) {
   p.k_pool = a->k_pool;
   p.v_pool = a->v_pool;
   p.scales = a->kv_scales;
-  p.k_descale = a->k_descale;
-  p.v_descale = a->v_descale;
+  set_factors(&p, a->k_descale, a->v_descale);
   p.pool = !pool ? 0 : a->kv_dtype == GDA_KV_BF16 ? 1 : 2;
   p.T = a->T;
   p.Hq = a->Hq;

@@ -97,7 +97,8 @@ struct Kv4WriteParams {
   unsigned char* k_pool;       // [num_slots, Hkv, D / 2] codes
   unsigned char* v_pool;
   unsigned char* scales;       // [num_slots, Hkv, 2, D / 16]
-  float k_descale, v_descale;
+  float k_factor, v_factor;    // inv: exact reciprocals of the descales, else the descales
+  int inv;
   long long T;
   int Hkv;
 };
@@ -136,7 +137,8 @@ struct MropeParams {
   void* k_pool;                // pool == 1: [num_slots, Hkv, D] BF16; pool == 2: 4-bit codes
   void* v_pool;
   unsigned char* scales;       // pool == 2
-  float k_descale, v_descale;
+  float k_factor, v_factor;    // pool == 2; inv: exact reciprocals of the descales, else the descales
+  int inv;
   int pool;                    // 0: no cache write, 1: BF16, 2: 4-bit
   long long T;
   int Hq, Hkv;

@@ -39,22 +39,23 @@ __device__ __forceinline__ uint4 row4_to_bf16(uint32_t c, uint32_t scale, float 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+template <bool kInv>
 __global__ void __launch_bounds__(256) kv4_write_kernel(Kv4WriteParams p) {
   const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (w >= p.T * p.Hkv) return;  // whole warps
   const long long t = w / p.Hkv;
   const int h = (int)(w - t * p.Hkv);
-  const uint4 rk = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (long long)h * kD) + lane);
-  const uint4 rv = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (long long)h * kD) + lane);
+  const uint4 rk = __ldcs(reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (long long)h * kD) + lane);
+  const uint4 rv = __ldcs(reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (long long)h * kD) + lane);
   const int slot = __ldg(p.slots + t);
   if (slot < 0 || (long long)slot >= p.num_slots) return;
   const size_t row = (size_t)slot * p.Hkv + h;
   float x[8];
   bf16x8_to_float(rk, x);
-  store_row4(x, p.k_descale, p.k_pool + row * kCodeBytes, p.scales + row * kScalePair, lane);
+  store_row4<kInv>(x, p.k_factor, p.k_pool + row * kCodeBytes, p.scales + row * kScalePair, lane);
   bf16x8_to_float(rv, x);
-  store_row4(x, p.v_descale, p.v_pool + row * kCodeBytes, p.scales + row * kScalePair + kScaleBytes, lane);
+  store_row4<kInv>(x, p.v_factor, p.v_pool + row * kCodeBytes, p.scales + row * kScalePair + kScaleBytes, lane);
 }
 
 __global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4GatherParams p) {
@@ -67,10 +68,10 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4GatherParams p) {
   uint32_t ck = 0u, cv = 0u, sk = 0u, sv = 0u;  // an index outside the pool reads zeros
   if (slot >= 0 && (long long)slot < p.num_slots) {
     const size_t row = (size_t)slot * p.Hkv + h;
-    ck = __ldg(reinterpret_cast<const uint32_t*>(p.k_pool + row * kCodeBytes) + lane);
-    cv = __ldg(reinterpret_cast<const uint32_t*>(p.v_pool + row * kCodeBytes) + lane);
-    sk = __ldg(p.scales + row * kScalePair + (lane >> 1));
-    sv = __ldg(p.scales + row * kScalePair + kScaleBytes + (lane >> 1));
+    ck = __ldcs(reinterpret_cast<const uint32_t*>(p.k_pool + row * kCodeBytes) + lane);
+    cv = __ldcs(reinterpret_cast<const uint32_t*>(p.v_pool + row * kCodeBytes) + lane);
+    sk = __ldcs(p.scales + row * kScalePair + (lane >> 1));
+    sv = __ldcs(p.scales + row * kScalePair + kScaleBytes + (lane >> 1));
   }
   const size_t out = (size_t)w * kD;
   reinterpret_cast<uint4*>(p.k_out + out)[lane] = row4_to_bf16(ck, sk, p.k_descale);
@@ -80,14 +81,15 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4GatherParams p) {
 }  // namespace
 
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t stream) {
-  const long long blocks = (p.T * p.Hkv + 7) / 8;
-  kv4_write_kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
+  const unsigned blocks = (unsigned)((p.T * p.Hkv + 7) / 8);
+  if (p.inv) kv4_write_kernel<true><<<blocks, 256, 0, stream>>>(p);
+  else kv4_write_kernel<false><<<blocks, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherParams& p, cudaStream_t stream) {
-  const long long blocks = (p.N * p.Hkv + 7) / 8;
-  kv4_gather_kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
+  const unsigned blocks = (unsigned)((p.N * p.Hkv + 7) / 8);
+  kv4_gather_kernel<<<blocks, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

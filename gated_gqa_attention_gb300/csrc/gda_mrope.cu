@@ -62,12 +62,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 // a BF16 row into row r of a pool of codes
-__device__ __forceinline__ void store_bf16_row4(const uint4& v, float descale, void* pool, unsigned char* scales, size_t r,
-                                                int lane) {
+__device__ __forceinline__ void store_bf16_row4(const uint4& v, float factor, int inv, void* pool, unsigned char* scales,
+                                                size_t r, int lane) {
   float2 f[4];
   unpack(v, f);
   const float x[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-  store_row4(x, descale, static_cast<unsigned char*>(pool) + r * kCodeBytes, scales, lane);
+  unsigned char* codes = static_cast<unsigned char*>(pool) + r * kCodeBytes;
+  if (inv) store_row4<true>(x, factor, codes, scales, lane);
+  else store_row4<false>(x, factor, codes, scales, lane);
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t d;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
           if (kind && slot_ok) {
             const size_t r = cache_row + h + j * wpt;
             if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_pool) + r * kD)[lane] = o4;
-            else store_bf16_row4(o4, p.k_descale, p.k_pool, p.scales + r * kScalePair, r, lane);
+            else store_bf16_row4(o4, p.k_factor, p.inv, p.k_pool, p.scales + r * kScalePair, r, lane);
           }
         }
         h += N * wpt;
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
         const uint4 raw = __ldcs(row + (2LL * p.Hq + p.Hkv + h) * (kD / 8));
         const size_t r = cache_row + h;
         if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pool) + r * kD)[lane] = raw;
-        else store_bf16_row4(raw, p.v_descale, p.v_pool, p.scales + r * kScalePair + kScaleBytes, r, lane);
+        else store_bf16_row4(raw, p.v_factor, p.inv, p.v_pool, p.scales + r * kScalePair + kScaleBytes, r, lane);
       }
     }
     if (p.gate_out != nullptr) {

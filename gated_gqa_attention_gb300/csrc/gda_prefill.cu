@@ -177,6 +177,29 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return d;
 }
 
+// two FP32 operations, or two BF16 products (each correctly rounded), in one instruction
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // TMA: a 5-D tile into shared memory, completing on `bar`
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
                                             uint64_t* bar) {
@@ -748,54 +771,71 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // every BF16 rounding here is done two values at a time (cvt.rn.bf16x2.f32)
           uint32_t ob[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) ob[e] = bf16x2_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+          for (int e = 0; e < 16; ++e) {
+            const float2 v = mul_f32x2(make_float2(o[2 * e], o[2 * e + 1]), make_float2(inv, inv));
+            ob[e] = bf16x2_rn(v.x, v.y);
+          }
           if (p.fuse_gate) {
-            // RNE_bf16(sigmoid(g)) from the SFU: for |g| <= 16, 1 / (1 + 2^(-g log2 e))
-            // (2^x and 1/x approximations) is within 24 float ulp of the real value
-            // (argument rounding |g| log2 e * 2^-24, 2^x ~2^-22, the add and 1/x ~2^-23),
-            // so its BF16 rounding is the correct one unless its low 16 bits lie within 32
-            // of the tie.  Branch-free over the 32 elements (so their SFU chains
-            // interleave); an element that needs the exact path (|g| > 16 or NaN, a
-            // sigmoid near a tie, a product below the float normal range) is staged
-            // ungated, marked, and redone after the chunk from the table of all 65 536
-            // BF16 sigmoids.  Exhaustively checked against the FP64 oracle on all 65 536
-            // gate codes through this epilogue.
+            // RNE_bf16(sigmoid(g)) from the SFU, two values at a time: for |g| <= 16, with
+            // d = 1 + 2^(-g log2 e) for both and one reciprocal, d1 / (d0 d1) and d0 / (d0 d1)
+            // are within 38 * 2^-24 relative of the real values (argument rounding
+            // |g| log2 e * 1.5 * 2^-24 in the exponent, 24; 2^x 4; the sum 1; the product,
+            // reciprocal and quotients 4; both widened below, 1 each), so their BF16 rounding is
+            // the correct one unless the roundings of s (1 - 48 * 2^-24) and s (1 + 48 * 2^-24)
+            // differ -- by one step, so in their last bit.  Branch-free over the 32 elements
+            // (so their SFU chains interleave); an element whose two roundings differ, or of a
+            // pair with |g| > 16 or NaN, is staged ungated, marked, and redone after the chunk
+            // from the table of all 65 536 BF16 sigmoids.  The product of two BF16 values is
+            // one correctly rounded instruction.  Exhaustively checked against the standalone
+            // gate and the FP64 oracle on all 65 536 gate codes through this epilogue.
             uint32_t gp[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int d = c0 + 2 * e;  // gate elements d, d + 1 of row r
+            for (int u = 0; u < 4; ++u) {
+              const int d = c0 + 8 * u;  // gate elements d .. d + 7 of row r
+              uint4 v;
               if (ntiles > 0) {
                 const int cb = d >> 6, ch = (d & 63) >> 3;
-                gp[e] = *reinterpret_cast<const uint32_t*>(grow + cb * kBlk + 16 * (ch ^ (r & 7)) + 2 * (d & 7));
+                v = *reinterpret_cast<const uint4*>(grow + cb * kBlk + 16 * (ch ^ (r & 7)));
               } else {
-                gp[e] = __ldg(reinterpret_cast<const uint32_t*>(gate_row(p, kPacked, b, q0 + qi, h) + d));
+                v = __ldg(reinterpret_cast<const uint4*>(gate_row(p, kPacked, b, q0 + qi, h) + d));
               }
+              gp[4 * u] = v.x;
+              gp[4 * u + 1] = v.y;
+              gp[4 * u + 2] = v.z;
+              gp[4 * u + 3] = v.w;
             }
-            uint32_t need = 0u;
+            uint32_t need = 0u;   // bit e: element 2 e of the chunk, bit 16 + e: element 2 e + 1
+            uint32_t gmax = 0u;   // per half: the largest |g| code
+            uint32_t dif[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float sg[2], pr[2];
+              gmax = __vmaxu2(gmax, gp[e] & 0x7FFF7FFFu);
+              const float2 x = mul_f32x2(make_float2(__uint_as_float(gp[e] << 16), __uint_as_float(gp[e] & 0xFFFF0000u)),
+                                         make_float2(-1.44269504088896341f, -1.44269504088896341f));
+              const float2 d = add_f32x2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
+              float rc;
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(d.x * d.y));
+              const float2 sg = mul_f32x2(make_float2(rc, rc), make_float2(d.y, d.x));
+              constexpr float kEps = 48.0f / 16777216.0f;
+              const float2 lo = mul_f32x2(sg, make_float2(1.0f - kEps, 1.0f - kEps));
+              const float2 hi = mul_f32x2(sg, make_float2(1.0f + kEps, 1.0f + kEps));
+              const uint32_t sv = bf16x2_rn(lo.x, lo.y);
+              dif[e] = sv ^ bf16x2_rn(hi.x, hi.y);
+              need |= (dif[e] & 0x00010001u) << e;
+              res[e] = mul_bf16x2(ob[e], sv);
+            }
+            const bool wide = (gmax & 0xFFFFu) > 0x4180u || (gmax >> 16) > 0x4180u;  // a |g| > 16 or NaN
+            if (need != 0u || wide) {
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const float g = __uint_as_float(t ? (gp[e] & 0xFFFF0000u) : (gp[e] << 16));
-                float ex, rc;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(g * -1.44269504088896341f));
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.0f + ex));
-                sg[t] = rc;
-                const uint32_t low = __float_as_uint(rc) & 0xFFFFu;
-                need |= (!(fabsf(g) <= 16.0f) || (low - 0x7FE0u <= 0x40u)) ? (1u << (2 * e + t)) : 0u;
+              for (int e = 0; e < 16; ++e) {
+                uint32_t m2 = (dif[e] & 0x00010001u) * 0xFFFFu;
+                const uint32_t ga = gp[e] & 0x7FFF7FFFu;
+                if (wide && ((ga & 0xFFFFu) > 0x4180u || (ga >> 16) > 0x4180u)) {
+                  m2 = 0xFFFFFFFFu;
+                  need |= 0x00010001u << e;
+                }
+                res[e] = (res[e] & ~m2) | (ob[e] & m2);
               }
-              const uint32_t sv = bf16x2_rn(sg[0], sg[1]);
-              pr[0] = __fmul_rn(__uint_as_float(ob[e] << 16), __uint_as_float(sv << 16));
-              pr[1] = __fmul_rn(__uint_as_float(ob[e] & 0xFFFF0000u), __uint_as_float(sv & 0xFFFF0000u));
-#pragma unroll
-              for (int t = 0; t < 2; ++t)
-                need |= (fabsf(pr[t]) < 1.17549435e-38f && pr[t] != 0.0f) ? (1u << (2 * e + t)) : 0u;
-              res[e] = bf16x2_rn(pr[0], pr[1]);
-              // a marked element is staged as O (BF16) and finished below
-              const uint32_t m2 = (need >> (2 * e)) & 3u;
-              if (m2) res[e] = (res[e] & ~((m2 & 1u) * 0xFFFFu) & ~((m2 >> 1) * 0xFFFF0000u)) |
-                               (ob[e] & (((m2 & 1u) * 0xFFFFu) | ((m2 >> 1) * 0xFFFF0000u)));
             }
             needs[ci] = need;
           } else {
@@ -817,7 +857,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         uint32_t m = needs[ci];
         const int c0 = 32 * ((warp < kSoftmaxWarps) ? (4 * (warp >> 2) + ci) : (ci ? 7 : 3));
         while (m != 0u) {
-          const int d = c0 + __ffs(m) - 1;
+          const int bit = __ffs(m) - 1, d = c0 + 2 * (bit & 15) + (bit >> 4);
           m &= m - 1u;
           const int cb = d >> 6, ch = (d & 63) >> 3;
           uint16_t* op = reinterpret_cast<uint16_t*>(orow + cb * kBlk + 16 * (ch ^ (r & 7)) + 2 * (d & 7));

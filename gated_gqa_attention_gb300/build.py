@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgda.so")
 SOURCES = ["gda_api.cu", "gda_stage1.cu", "gda_stage1_fp8.cu", "gda_stage1_tma.cu", "gda_stage2.cu", "gda_small.cu",
-           "gda_prep.cu", "gda_prefill.cu", "gda_stage1_fp4.cu", "gda_kv4.cu", "gda_mrope.cu"]
+           "gda_prep.cu", "gda_prefill.cu", "gda_prefill_packed.cu", "gda_stage1_fp4.cu", "gda_kv4.cu", "gda_mrope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I" + INCLUDE, "-I" + CSRC]

@@ -45,9 +45,9 @@
 
 #include <mutex>
 
-#include "gda_device.cuh"
 #include "gda_kernels.h"
 #include "gda_prefill.h"
+#include "gda_tc.cuh"
 
 namespace gda {
 
@@ -82,166 +82,6 @@ static_assert(2 * kHalf >= 4 * kBlk, "the output tile fits the V halves");
 static_assert(kNSB * kPN <= kTmemO, "S / P buffers below O");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
-// ---- PTX wrappers (tcgen05, TMA) ----
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D (TMEM) += A (shared memory descriptor) * B (shared memory descriptor)
-__device__ __forceinline__ void umma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// D (TMEM) += A (TMEM) * B (shared memory descriptor)
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// all prior tcgen05 MMAs of this thread arrive on `bar` when complete
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-// 32 lanes x 32 columns of 32 bits: thread t of the warp gets lane (warp base + t), columns col .. col+31
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 2^x on the SFU (ex2.approx, subnormal results flushed): P is rounded to BF16 right
-// after, far coarser than the instruction's error.
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// {lo, hi} -> BF16x2, round to nearest even (lo in the low half)
-__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-// two FP32 operations, or two BF16 products (each correctly rounded), in one instruction
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// TMA: a 5-D tile into shared memory, completing on `bar`
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-      "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// TMA: a 4-D tile from shared memory to global (rows past the tensor's end are
-// dropped); completion tracked by the bulk-group mechanism
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int x, int y, int z, int w, const void* src) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(src))
-               : "memory");
-}
-__device__ __forceinline__ void tma_store_commit_and_wait_read() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Shared-memory matrix descriptor, 128-byte swizzle (descriptor version 1):
-// start address, leading and stride byte offsets, all encoded >> 4.
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// Instruction descriptor, kind::f16: FP32 accumulator, BF16 A and B, A K-major,
-// B K-major (b_mn = 0) or MN-major (b_mn = 1), N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
 // BF16 sigmoid table: entry g = RNE_bf16(sigmoid(g)) for every BF16 code g, filled
 // once per device with the certified sigmoid_bf16 (FreeToken PR #781, Summary: a
 // per-device table of BF16 sigmoid values, 128 KiB).  The prefill epilogue gates
@@ -268,20 +108,6 @@ __global__ void sigmoid_table_kernel() {
   if (i < 65536) g_sigmoid_table[i] = sigmoid_bf16((uint16_t)i);
 }
 
-// Gate row of query `row` (packed: of the whole tensor; else of sequence b) and head h.
-__device__ __forceinline__ const __nv_bfloat16* gate_row(const PrefillParams& p, bool packed, int b, int row, int h) {
-  return packed ? p.gate + (size_t)row * p.gate_stride + (size_t)h * kD
-                : p.gate + (((size_t)b * p.Sq + row) * p.Hq + h) * kD;
-}
-
-struct PackedSeq {
-  int q0, nq, k0, nk;  // first query and key row, lengths (clamped to the tensors)
-};
-struct PackedTile {
-  int b, qb;           // sequence and its query block; b = -1: no such rank
-  PackedSeq s;
-};
-
 struct PrefillBars {
   uint64_t qf, g;                                   // Q tile landed; gate tile landed
   uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[2], v_empty[2];  // per half slot
@@ -291,114 +117,11 @@ struct PrefillBars {
   uint64_t ost;                                     // output tile staged (8 softmax warps)
   uint32_t tmem;
   int abort;
-  PackedTile tile;                                  // kPacked: the CTA's block
 };
 static_assert(sizeof(PrefillBars) <= 512, "barrier block");
 
 }  // namespace
 
-// Which (query block, sequence) the packed grid's `rank`-th block is, longest first: the
-// blocks of all sequences ordered by their number n of key tiles, descending, then by
-// sequence.  Nothing is sorted: the number of blocks with at least n tiles has a closed
-// form per sequence, so the warp sums it over the batch (lanes stride over the sequences)
-// and searches the n that holds the rank -- about log2(longest / 128) rounds, a few
-// hundred cycles -- then finds the sequence by a prefix sum.  (A plan kernel would cost
-// its own launch, and unsorted blocks leave the longest ones to the last wave.)
-__device__ __forceinline__ PackedSeq packed_seq(const PrefillParams& p, int b) {
-  PackedSeq s;
-  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-  const int k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
-  s.q0 = min(max(q0, 0), p.Sq);
-  s.nq = max(min(q1, p.Sq) - s.q0, 0);
-  s.k0 = min(max(k0, 0), p.Skv);
-  s.nk = max(min(k1, p.Skv) - s.k0, 0);
-  return s;
-}
-// the first query block of s with at least n key tiles, and how many have
-__device__ __forceinline__ int packed_first(const PackedSeq& s, int n, int causal) {
-  if (n <= 0 || !causal) return 0;
-  // block j's last visible key min(nk - 1, 128 j + 127 + off) is at least 128 (n - 1)
-  const int off = s.nk - s.nq;
-  return max(0, n - 1 - ((off + kPN - 1) >> 7));
-}
-__device__ __forceinline__ int packed_count(const PackedSeq& s, int n, int causal) {
-  const int nb = (s.nq + kPM - 1) / kPM;
-  if (n > 0 && s.nk - 1 < kPN * (n - 1)) return 0;
-  return max(0, nb - packed_first(s, n, causal));
-}
-__device__ __forceinline__ PackedTile packed_tile(const PrefillParams& p, int rank) {
-  const int lane = threadIdx.x & 31;
-  constexpr int kHeld = 4;  // sequences a lane keeps in registers: batches up to 128 load once
-  PackedSeq held[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int b = lane + 32 * i;
-    held[i] = {0, 0, 0, 0};
-    if (b < p.B) held[i] = packed_seq(p, b);
-  }
-  auto total = [&](int n) -> int {
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) c += packed_count(held[i], n, p.causal);
-    for (int b = lane + 32 * kHeld; b < p.B; b += 32) c += packed_count(packed_seq(p, b), n, p.causal);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int top = 0;  // the most key tiles of any block
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) top = max(top, held[i].nq > 0 ? held[i].nk : 0);
-  for (int b = lane + 32 * kHeld; b < p.B; b += 32) {
-    const PackedSeq s = packed_seq(p, b);
-    top = max(top, s.nq > 0 ? s.nk : 0);
-  }
-  int lo = 0, hi = (__reduce_max_sync(0xffffffffu, top) + kPN - 1) / kPN;
-  PackedTile t;
-  t.b = -1;
-  t.qb = 0;
-  t.s = {0, 0, 0, 0};
-  if (total(0) <= rank) return t;
-  while (lo < hi) {  // the largest n with total(n) > rank lies in [lo, hi]
-    const int mid = (lo + hi + 1) >> 1;
-    if (total(mid) > rank) lo = mid; else hi = mid - 1;
-  }
-  const int n = lo;
-  int r = rank - total(n + 1);  // among the blocks with exactly n tiles, in sequence order
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    PackedSeq s = {0, 0, 0, 0};
-    if (b < p.B) s = packed_seq(p, b);
-    const int mine = packed_count(s, n, p.causal) - packed_count(s, n + 1, p.causal);
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > r);
-    if (hit != 0u) {
-      const int src = __ffs(hit) - 1;
-      t.b = b0 + src;
-      t.qb = __shfl_sync(0xffffffffu, packed_first(s, n, p.causal) + r - (incl - mine), src);
-      t.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-      t.s.nq = __shfl_sync(0xffffffffu, s.nq, src);
-      t.s.k0 = __shfl_sync(0xffffffffu, s.k0, src);
-      t.s.nk = __shfl_sync(0xffffffffu, s.nk, src);
-      return t;
-    }
-    r -= __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return t;
-}
-
-// kPacked: the sequences lie one after the other in [T, H, D] tensors (row pitches of
-// their own), cu_q / cu_k give their rows, and the CTA takes its block by rank
-// (packed_tile).  A tile may run past its sequence's end into the next one:
-//  * keys past the end are masked as in the padded form; their V rows are zeroed in shared
-//    memory before the last PV (a NaN there times a probability of 0 would be NaN);
-//  * query rows past the end are computed and not stored: a block that holds any is
-//    written row by row instead of by a TMA store.
-// The row sums add the FP32 probabilities before their rounding to BF16, so lse does not
-// see that rounding.
-template <bool kPacked>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv,
@@ -416,18 +139,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* xbuf = reinterpret_cast<float*>(sm + kOffX);  // [parity][half][row]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nqb = (p.Sq + kPM - 1) / kPM;
-  // kPacked: warp 0 finds the CTA's block while the others set up below
-  if (kPacked && warp == 0) {
-    const PackedTile t = packed_tile(p, (int)blockIdx.x / p.Hq);
-    if (lane == 0) bars.tile = t;
-  }
   // CTAs start in linear order (x fastest): x enumerates (query block, head) with the
   // head fastest, so every head's longest causal blocks come first (longest-first
   // scheduling keeps the last wave short)
-  const int h = (int)blockIdx.x % p.Hq, b = kPacked ? 0 : blockIdx.y;
+  const int qb = nqb - 1 - (int)blockIdx.x / p.Hq;
+  const int h = (int)blockIdx.x % p.Hq, b = blockIdx.y;
   const int kvh = h / (p.Hq / p.Hkv);
+  const int L = p.kv_lens ? __ldg(p.kv_lens + b) : p.Skv;
+  const int i0 = qb * kPM;
+  const int off = L - p.Sq;  // causal: key j visible to query i when j <= i + off
+  int last_key = L - 1;
+  if (p.causal) last_key = min(last_key, i0 + kPM - 1 + off);
+  const int ntiles = (last_key >= 0) ? (last_key / kPN + 1) : 0;
 
-  if (tid == (kPacked ? 32 : 0)) {
+  if (tid == 0) {
     mbar_init(&bars.qf, 1);
     mbar_init(&bars.g, 1);
     for (int x = 0; x < kKSlots; ++x) {
@@ -460,20 +185,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  // the block's query rows [q0 + i0, ...) of a sequence of nq queries and L keys from row k0
-  const int q0 = kPacked ? bars.tile.s.q0 : 0, k0row = kPacked ? bars.tile.s.k0 : 0;
-  const int nq = kPacked ? bars.tile.s.nq : p.Sq;
-  if (kPacked && bars.tile.b < 0) {  // no such block (the same for the whole CTA)
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-    return;
-  }
-  const int qb = kPacked ? bars.tile.qb : nqb - 1 - (int)blockIdx.x / p.Hq;
-  const int L = kPacked ? bars.tile.s.nk : p.kv_lens ? __ldg(p.kv_lens + b) : p.Skv;
-  const int i0 = qb * kPM;
-  const int off = L - nq;  // causal: key j visible to query i when j <= i + off
-  int last_key = L - 1;
-  if (p.causal) last_key = min(last_key, i0 + kPM - 1 + off);
-  const int ntiles = (last_key >= 0) ? (last_key / kPN + 1) : 0;
   volatile int* abort_flag = &bars.abort;
   auto fail = [&]() {
     if (bars.abort == 0) atomicOr(p.error, kErrTimeout);
@@ -499,7 +210,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (is_k) {
         ++arm_g;
         mbar_arrive_expect_tx(&bars.qf, 4 * kBlk);
-        tma_load_5d(sm + kOffQ, &tq, 0, q0 + i0, 0, h, b, &bars.qf);
+        tma_load_5d(sm + kOffQ, &tq, 0, i0, 0, h, b, &bars.qf);
       }
       for (int n = 0; n < 2 * ntiles; ++n) {
         const int x = n % nslot, u = n / nslot;  // slot and its use count
@@ -507,7 +218,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ++arm[x];
         mbar_arrive_expect_tx(&full[x], kHalf);
         // box {64 elements, 128 rows, 2 column blocks}: keys 128 j .., head dimensions 128 h ..
-        tma_load_5d(sm + base + x * kHalf, map, 0, k0row + (n >> 1) * kPN, 2 * (n & 1), kvh, b, &full[x]);
+        tma_load_5d(sm + base + x * kHalf, map, 0, (n >> 1) * kPN, 2 * (n & 1), kvh, b, &full[x]);
       }
       if (ok && is_k && p.fuse_gate) {
         // the gate tile goes into the Q buffer once the last S product has read Q (its
@@ -517,7 +228,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (ok) {
           ++arm_gate;
           mbar_arrive_expect_tx(&bars.g, 4 * kBlk);
-          tma_load_5d(sm + kOffQ, &tg, 0, q0 + i0, 0, h, b, &bars.g);
+          tma_load_5d(sm + kOffQ, &tg, 0, i0, 0, h, b, &bars.g);
         }
       }
       if (!ok) {
@@ -689,25 +400,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float p0 = ex2_approx(fmaf(s[2 * e], p.scale_log2, mneg));
         const float p1 = ex2_approx(fmaf(s[2 * e + 1], p.scale_log2, mneg));
         w[e] = bf16x2_rn(p0, p1);
-        la += kPacked ? p0 : __uint_as_float(w[e] << 16);
-        lb += kPacked ? p1 : __uint_as_float(w[e] & 0xFFFF0000u);
+        la += __uint_as_float(w[e] << 16);
+        lb += __uint_as_float(w[e] & 0xFFFF0000u);
       }
       l_run += la + lb;
       tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc, w);
       tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc + 16, w + 16);
       tmem_wait_st();
-      if (kPacked && (j + 1) * kPN > L) {
-        // the last tile's V rows past the sequence's end (rows of the next sequence) become
-        // zeros: 256 threads, 16 bytes each, before this tile's PV may start
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_full[0], j & 1, abort_flag, p.wait_limit) &&
-                                         mbar_wait(&bars.v_full[1], j & 1, abort_flag, p.wait_limit));
-        if (!ok) break;
-        const int r0 = L - j * kPN;  // rows r0 .. 127 of each 64-dimension block
-        for (int x = tid; x < (kPN - r0) * 32; x += kSoftmaxWarps * 32)
-          *reinterpret_cast<uint4*>(sm + kOffV + ((x & 31) >> 3) * kBlk + (r0 + (x >> 5)) * 128 + (x & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        fence_async_shared();
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.p_full[sb]);
@@ -767,7 +466,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) res[e] = 0u;
         // a row past the end (after the warp-collective load) is not computed; TMA drops it
-        if (qi < nq) {
+        if (qi < p.Sq) {
           // every BF16 rounding here is done two values at a time (cvt.rn.bf16x2.f32)
           uint32_t ob[16];
 #pragma unroll
@@ -797,7 +496,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const int cb = d >> 6, ch = (d & 63) >> 3;
                 v = *reinterpret_cast<const uint4*>(grow + cb * kBlk + 16 * (ch ^ (r & 7)));
               } else {
-                v = __ldg(reinterpret_cast<const uint4*>(gate_row(p, kPacked, b, q0 + qi, h) + d));
+                v = __ldg(reinterpret_cast<const uint4*>(p.gate + (((size_t)b * p.Sq + qi) * p.Hq + h) * kD + d));
               }
               gp[4 * u] = v.x;
               gp[4 * u + 1] = v.y;
@@ -863,39 +562,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
           uint16_t* op = reinterpret_cast<uint16_t*>(orow + cb * kBlk + 16 * (ch ^ (r & 7)) + 2 * (d & 7));
           const uint16_t gb = (ntiles > 0)
               ? *reinterpret_cast<const uint16_t*>(grow + cb * kBlk + 16 * (ch ^ (r & 7)) + 2 * (d & 7))
-              : __ldg(reinterpret_cast<const uint16_t*>(gate_row(p, kPacked, b, q0 + qi, h) + d));
+              : __ldg(reinterpret_cast<const uint16_t*>(p.gate + (((size_t)b * p.Sq + qi) * p.Hq + h) * kD + d));
           *op = gate_product_fast(*op, __ldg(g_sigmoid_table + gb));
         }
       }
-      if (kPacked && p.lse && qi < nq && warp < 4) {
-        // (a NaN sum gives a NaN)
-        p.lse[(size_t)h * p.Sq + q0 + qi] =
-            (l_row == 0.0f) ? -INFINITY : (m_run + log2f(l_row)) * 0.69314718055994530942f;
-      }
-      if (!kPacked && p.lse && qi < p.Sq && warp < 4) {
+      if (p.lse && qi < p.Sq && warp < 4) {
         p.lse[((size_t)b * p.Hq + h) * p.Sq + qi] =
             (l_row > 0.0f) ? (m_run + log2f(l_row)) * 0.69314718055994530942f : -INFINITY;
       }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.ost);
-      if (kPacked && nq - i0 < kPM) {
-        // rows past the sequence's end belong to another sequence (or are not the call's):
-        // the block's own rows, 16 bytes a lane, one row of the head per warp
-        if (__all_sync(0xffffffffu, mbar_wait(&bars.ost, 0, abort_flag, p.wait_limit))) {
-          for (int x = warp; x < nq - i0; x += kPThreads / 32) {
-            const uint4 v = *reinterpret_cast<const uint4*>(ostage + (lane >> 3) * kBlk + x * 128 + 16 * ((lane & 7) ^ (x & 7)));
-            reinterpret_cast<uint4*>(p.out + ((size_t)(q0 + i0 + x) * p.Hq + h) * kD)[lane] = v;
-          }
-        } else {
-          fail();
-        }
-      } else if (tid == 0) {
+      if (tid == 0) {
         // every warp has staged its part: four TMA stores, then wait until they have read
         // the staging buffer before the CTA's shared memory goes away
         if (mbar_wait(&bars.ost, 0, abort_flag, p.wait_limit)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tma_store_4d(&to, 64 * c, h, q0 + i0, b, ostage + c * kBlk);
+          for (int c = 0; c < 4; ++c) tma_store_4d(&to, 64 * c, h, i0, b, ostage + c * kBlk);
           tma_store_commit_and_wait_read();
         } else {
           fail();
@@ -948,14 +631,16 @@ bool make_map(CUtensorMap* m, const void* base, int B, int S, int H, int rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // Q, K, V or the gate [B, S, H, D] BF16, `pitch` elements from one token to the next (H * D
 // when contiguous), as a 5-D tensor {64 elements, S, 4 column blocks, H, B} with box {64, rows, blocks, 1, 1}: one copy fills a tile laid out
 // [block][row][128 B] (128-byte swizzle), the layout the MMA descriptors read
-bool make_map_kv(CUtensorMap* m, const void* base, int B, int S, int H, int rows, int blocks, int64_t pitch = 0) {
+bool make_map_kv(CUtensorMap* m, const void* base, int B, int S, int H, int rows, int blocks, int64_t pitch) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[5] = {64, (cuuint64_t)S, 4, (cuuint64_t)H, (cuuint64_t)B};
-  const cuuint64_t tok = 2 * (pitch > 0 ? (cuuint64_t)pitch : (cuuint64_t)H * kD);
+  const cuuint64_t tok = 2 * (cuuint64_t)pitch;
   const cuuint64_t strides[4] = {tok, 128, (cuuint64_t)kD * 2, (cuuint64_t)S * tok};
   const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)blocks, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
@@ -964,13 +649,11 @@ bool make_map_kv(CUtensorMap* m, const void* base, int B, int S, int H, int rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
 // First use on a device: the kernel's shared-memory limit and the sigmoid table.
 // The table is built on a private stream that is waited for before the device is
 // marked ready, so every later call, on any stream or thread, finds it complete.
 // Refused while `stream` is capturing: the table must exist outside any graph.
-static cudaError_t prefill_init(int dev, cudaStream_t stream) {
+cudaError_t prefill_init(int dev, cudaStream_t stream) {
   static std::mutex mu;
   static bool ready[64] = {};
   std::lock_guard<std::mutex> lk(mu);
@@ -979,9 +662,9 @@ static cudaError_t prefill_init(int dev, cudaStream_t stream) {
   cudaError_t e = cudaStreamIsCapturing(stream, &cs);
   if (e != cudaSuccess) return e;
   if (cs != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
-  e = cudaFuncSetAttribute(prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  e = packed_init();
   if (e != cudaSuccess) return e;
   cudaStream_t own = nullptr;
   e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
@@ -996,14 +679,21 @@ static cudaError_t prefill_init(int dev, cudaStream_t stream) {
   return cudaSuccess;
 }
 
+cudaError_t sigmoid_table(const uint16_t** table) {
+  void* ptr = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&ptr, g_sigmoid_table);
+  *table = static_cast<const uint16_t*>(ptr);
+  return e;
+}
+
 cudaError_t launch_prefill(const PrefillParams& p, const void* q, const void* k, const void* v, const void* gate,
                            cudaStream_t stream) {
   CUtensorMap tq, tk, tv, tg, to;
   // S = 0 still needs a valid map: use extent 1 (nothing is loaded then)
-  if (!make_map_kv(&tq, q, p.B, p.Sq > 0 ? p.Sq : 1, p.Hq, kPM, 4) ||
-      !make_map_kv(&tk, k, p.B, p.Skv > 0 ? p.Skv : 1, p.Hkv, kPN, 2) ||
-      !make_map_kv(&tv, v, p.B, p.Skv > 0 ? p.Skv : 1, p.Hkv, kPN, 2) ||
-      !make_map_kv(&tg, gate ? gate : q, p.B, p.Sq > 0 ? p.Sq : 1, p.Hq, kPM, 4) ||
+  if (!make_map_kv(&tq, q, p.B, p.Sq > 0 ? p.Sq : 1, p.Hq, kPM, 4, p.Hq * kD) ||
+      !make_map_kv(&tk, k, p.B, p.Skv > 0 ? p.Skv : 1, p.Hkv, kPN, 2, p.Hkv * kD) ||
+      !make_map_kv(&tv, v, p.B, p.Skv > 0 ? p.Skv : 1, p.Hkv, kPN, 2, p.Hkv * kD) ||
+      !make_map_kv(&tg, gate ? gate : q, p.B, p.Sq > 0 ? p.Sq : 1, p.Hq, kPM, 4, p.Hq * kD) ||
       !make_map(&to, p.out, p.B, p.Sq > 0 ? p.Sq : 1, p.Hq, kPM))
     return cudaErrorInvalidValue;
   int dev = 0;
@@ -1013,30 +703,7 @@ cudaError_t launch_prefill(const PrefillParams& p, const void* q, const void* k,
   e = prefill_init(dev, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(((p.Sq + kPM - 1) / kPM) * p.Hq), (unsigned)p.B, 1u);
-  prefill_kernel<false><<<grid, kPThreads, kSmemBytes, stream>>>(tq, tk, tv, tg, to, p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_prefill_packed(const PrefillParams& p, const void* q, int64_t q_pitch, const void* k,
-                                  int64_t k_pitch, const void* v, int64_t v_pitch, const void* gate,
-                                  cudaStream_t stream) {
-  CUtensorMap tq, tk, tv, tg, to;
-  const int Sk = p.Skv > 0 ? p.Skv : 1;  // (no keys: nothing is loaded)
-  if (!make_map_kv(&tq, q, 1, p.Sq, p.Hq, kPM, 4, q_pitch) || !make_map_kv(&tk, k, 1, Sk, p.Hkv, kPN, 2, k_pitch) ||
-      !make_map_kv(&tv, v, 1, Sk, p.Hkv, kPN, 2, v_pitch) ||
-      !make_map_kv(&tg, gate ? gate : q, 1, p.Sq, p.Hq, kPM, 4, gate ? (int64_t)p.gate_stride : q_pitch) ||
-      !make_map(&to, p.out, 1, p.Sq, p.Hq, kPM))
-    return cudaErrorInvalidValue;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  e = prefill_init(dev, stream);
-  if (e != cudaSuccess) return e;
-  // The lengths are on the device, so the grid covers the most blocks that B sequences of
-  // Sq rows in all can have; CTAs past the last block leave at once.
-  const long long blocks = packed_blocks(p.Sq, p.B);
-  prefill_kernel<true><<<(unsigned)(blocks * p.Hq), kPThreads, kSmemBytes, stream>>>(tq, tk, tv, tg, to, p);
+  prefill_kernel<<<grid, kPThreads, kSmemBytes, stream>>>(tq, tk, tv, tg, to, p);
   return cudaGetLastError();
 }
 

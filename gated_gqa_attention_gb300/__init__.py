@@ -75,7 +75,7 @@ class _MropeArgs(ctypes.Structure):
         ("qgkv", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("w_q_norm", ctypes.c_void_p),
         ("w_k_norm", ctypes.c_void_p), ("eps", ctypes.c_float), ("n_axes", ctypes.c_int),
         ("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64), ("inv_freq", ctypes.c_void_p),
-        ("pair_axis", ctypes.c_void_p), ("rope_dim", ctypes.c_int), ("kv_dtype", ctypes.c_int),
+        ("pair_axis", ctypes.c_char_p), ("rope_dim", ctypes.c_int), ("kv_dtype", ctypes.c_int),
         ("q_out", ctypes.c_void_p), ("gate_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
         ("slots", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("k_pool", ctypes.c_void_p),
         ("v_pool", ctypes.c_void_p), ("kv_scales", ctypes.c_void_p), ("k_descale", ctypes.c_float),
@@ -228,13 +228,50 @@ def _kv_dtype(k_pool) -> int:
         else KV_BF16
 
 
+_th = None
+
+
+def _torch():
+    """torch, imported on first use."""
+    global _th
+    if _th is None:
+        import torch
+        _th = torch
+    return _th
+
+
+def _is(t, dtype, ndim, dev):
+    """Whether t is what _check_tensor wants, on device index dev (the quick test before it: these
+    calls take a few microseconds, and the checks of ten tensors have to fit in them)."""
+    try:
+        return t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+def _need(name, t, dtype, ndim, device):
+    if not _is(t, dtype, ndim, device.index):
+        _check_tensor(name, t, dtype, ndim, device)
+
+
+def _cuda_index(name, t, dtype):
+    """The device index of the call's first tensor."""
+    try:
+        i = t.get_device()
+    except AttributeError:
+        i = -1
+    if i < 0 or t.dtype is not dtype:
+        _check_tensor(name, t, dtype)
+    return i
+
+
 def _tokens(name, t, heads=None, dim=None, device=None):
     """Checks a [T, H, D] bf16 CUDA tensor whose tokens may be any distance apart (the parts of
     a projection's rows) and returns that distance in elements."""
-    import torch
+    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -249,20 +286,23 @@ def _tokens(name, t, heads=None, dim=None, device=None):
     if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
         raise ValueError("the heads and dims of a token of %s must be contiguous" % name)
     # one token (or none): its distance to the next is never used
-    return int(st[0]) if T > 1 else max(H * D, 8)
+    return st[0] if T > 1 else max(H * D, 8)
 
 
 def _check_fp4(k_pool, v_pool, kv_scales, D=None, device=None):
     """Checks a 4-bit cache; returns (num_slots, Hkv)."""
-    import torch
-    _check_tensor("k_pool", k_pool, torch.uint8, 3, device)
-    _check_tensor("v_pool", v_pool, torch.uint8, 3, k_pool.device)
+    torch = _torch()
+    idx = device.index if device is not None else _cuda_index("k_pool", k_pool, torch.uint8)
+    if not _is(k_pool, torch.uint8, 3, idx):
+        _check_tensor("k_pool", k_pool, torch.uint8, 3, device)
+    dev = k_pool.device if device is None else device
+    _need("v_pool", v_pool, torch.uint8, 3, dev)
     kv_scales = _scale_bytes(kv_scales)
-    _check_tensor("kv_scales", kv_scales, torch.uint8, 4, k_pool.device)
-    n, h, half = k_pool.shape
-    if v_pool.shape != k_pool.shape:
+    _need("kv_scales", kv_scales, torch.uint8, 4, dev)
+    n, h, half = shape = k_pool.shape
+    if v_pool.shape != shape:
         raise ValueError("k_pool and v_pool must have the same shape")
-    if half % 8 != 0 or tuple(kv_scales.shape) != (n, h, 2, half // 8):
+    if half % 8 != 0 or kv_scales.shape != (n, h, 2, half // 8):
         raise ValueError("kv_scales must be [num_slots, Hkv, 2, D / 16] for pools [num_slots, Hkv, D / 2]")
     if D is not None and 2 * half != D:
         raise ValueError("head dims of q and the pools differ")
@@ -271,69 +311,62 @@ def _check_fp4(k_pool, v_pool, kv_scales, D=None, device=None):
 
 def _scale_bytes(kv_scales):
     """kv_scales given as float8_e4m3fn or as its bytes."""
-    import torch
-    if isinstance(kv_scales, torch.Tensor) and kv_scales.dtype == torch.float8_e4m3fn:
+    torch = _torch()
+    if isinstance(kv_scales, torch.Tensor) and kv_scales.dtype is torch.float8_e4m3fn:
         return kv_scales.view(torch.uint8)
     return kv_scales
 
 
-class _On:
-    """The device a call's tensors live on: made current for the call (the library launches on
-    the current device), with that device's current stream as the default."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._guard = None
-        if device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        self._device, self._stream = device, stream
-
-    def __enter__(self):
-        import torch
-        if self._guard is not None:
-            self._guard.__enter__()
-        if self._stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
-        if self._stream.device.index != self._device.index:
-            if self._guard is not None:
-                self._guard.__exit__(None, None, None)
-            raise ValueError("stream is on %s, the tensors on %s" % (self._stream.device, self._device))
-        return ctypes.c_void_p(self._stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+def _launch(fn, dev, stream, *args):
+    """Call a library function on device index ``dev``, where its tensors live, with that device's
+    current stream as the default, and raise on an error status (the library launches on the
+    current device)."""
+    torch = _torch()
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev:
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        else:
+            with torch.cuda.device(dev):
+                rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        if stream.device.index != dev:
+            raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != 0:
+        _check(rc)
 
 
 def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_scales=None):
     """Checks tensor metadata; returns the pools' element type (KV_BF16, KV_E4M3 or KV_E2M1)."""
-    import torch
-    _check_tensor("q", q, torch.bfloat16, 3)
-    dev = q.device
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not _is(q, bf16, 3, _cuda_index("q", q, bf16)):
+        _check_tensor("q", q, bf16, 3)
+    dev, shape = q.device, q.shape
     if gate_t is not None:
-        _check_tensor("gate", gate_t, torch.bfloat16, 3, dev)
-        if gate_t.shape != q.shape:
+        _need("gate", gate_t, bf16, 3, dev)
+        if gate_t.shape != shape:
             raise ValueError("gate must have q's shape")
     if kv_scales is not None:
         kv = KV_E2M1
-        _check_fp4(k_pool, v_pool, kv_scales, q.shape[2], dev)
+        _check_fp4(k_pool, v_pool, kv_scales, shape[2], dev)
     else:
         kv = _kv_dtype(k_pool)
-        kdt = k_pool.dtype if kv == KV_E4M3 else torch.bfloat16
-        _check_tensor("k_pool", k_pool, kdt, 3, dev)
-        _check_tensor("v_pool", v_pool, kdt, 3, dev)
+        kdt = k_pool.dtype if kv == KV_E4M3 else bf16
+        _need("k_pool", k_pool, kdt, 3, dev)
+        _need("v_pool", v_pool, kdt, 3, dev)
         if v_pool.shape != k_pool.shape:
             raise ValueError("k_pool and v_pool must have the same shape")
-    _check_tensor("kv_indptr", kv_indptr, torch.int32, 1, dev)
-    _check_tensor("kv_indices", kv_indices, torch.int32, 1, dev)
-    if kv_indptr.numel() != q.shape[0] + 1:
+    _need("kv_indptr", kv_indptr, i32, 1, dev)
+    _need("kv_indices", kv_indices, i32, 1, dev)
+    if kv_indptr.numel() != shape[0] + 1:
         raise ValueError("kv_indptr must have B + 1 entries")
-    if kv != KV_E2M1 and k_pool.shape[2] != q.shape[2]:
+    if kv != KV_E2M1 and k_pool.shape[2] != shape[2]:
         raise ValueError("head dims of q and the pools differ")
     if out is not None:
-        _check_tensor("out", out, torch.bfloat16, 3, dev)
-        if out.shape != q.shape:
+        _need("out", out, bf16, 3, dev)
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
     return kv
 
@@ -355,10 +388,9 @@ def decode(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, scale: Op
     if scale is None:
         scale = 1.0 / (D ** 0.5)
     if kv == KV_E2M1:
-        with _On(q.device, stream) as s:
-            _check(load().gda_decode_fp4(_ptr(q), _ptr(gate_t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales),
-                                         _ptr(kv_indptr), _ptr(kv_indices), _ptr(out), B, Hq, Hkv, D, float(scale),
-                                         float(k_descale), float(v_descale), int(num_splits), s))
+        _launch((_lib or load()).gda_decode_fp4, q.get_device(), stream, _ptr(q), _ptr(gate_t), _ptr(k_pool), _ptr(v_pool),
+                _ptr(kv_scales), _ptr(kv_indptr), _ptr(kv_indices), _ptr(out), B, Hq, Hkv, D, float(scale),
+                float(k_descale), float(v_descale), int(num_splits))
         return out
     if kv == KV_E4M3:
         _check(load().gda_decode_e4m3(_ptr(q), _ptr(gate_t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indptr),
@@ -508,15 +540,15 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
     sequence's length (0: none), which lets small batches run as one cluster kernel,
     and ``total_len``: the batch's exact number of KV positions (kv_indptr[B], 0: not
     given); with both, the split count is chosen on the host (``auto_splits``)."""
-    import torch
+    torch = _torch()
     kv = _decode_checks(q, gate_t if fuse_gate else None, k_pool, v_pool, kv_indptr, kv_indices, out, kv_scales)
     B, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     if out is None:
         out = torch.empty_like(q)
     if lse is not None:
-        _check_tensor("lse", lse, torch.float32, 2, q.device)
-        if kv == KV_E2M1 and tuple(lse.shape) != (B, Hq):
+        _need("lse", lse, torch.float32, 2, q.device)
+        if kv == KV_E2M1 and lse.shape != (B, Hq):
             raise ValueError("lse must be [B, Hq]")
     if sinks is not None:
         _check_tensor("sinks", sinks, torch.float32, 1, q.device)
@@ -524,24 +556,20 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
             raise ValueError("sinks must have Hq entries")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
-    nbytes = workspace_bytes(B, Hq, Hkv, D, num_splits)
     if workspace is None:
+        nbytes = workspace_bytes(B, Hq, Hkv, D, num_splits)
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
         workspace_init(workspace, stream)
-    a = _Args(q=_ptr(q), gate=_ptr(gate_t) if fuse_gate else None, k_pool=_ptr(k_pool),
-              v_pool=_ptr(v_pool), kv_indptr=_ptr(kv_indptr), kv_indices=_ptr(kv_indices),
-              out=_ptr(out), lse=_ptr(lse), num_slots=int(k_pool.shape[0]), B=B, Hq=Hq, Hkv=Hkv, D=D,
-              scale=float(scale), num_splits=int(num_splits), fuse_gate=1 if fuse_gate else 0,
-              check_indices=1 if check_indices else 0, variant=int(variant), min_chunk=int(min_chunk),
-              window=int(window), sinks=_ptr(sinks), kv_dtype=kv, k_descale=float(k_descale),
-              v_descale=float(v_descale), max_len=int(max_len), total_len=int(total_len), kv_scales=_ptr(kv_scales))
+    a = _Args(_ptr(q), _ptr(gate_t) if fuse_gate else None, _ptr(k_pool), _ptr(v_pool), _ptr(kv_indptr),
+              _ptr(kv_indices), _ptr(out), _ptr(lse), int(k_pool.shape[0]), B, Hq, Hkv, D, float(scale),
+              int(num_splits), 1 if fuse_gate else 0, 1 if check_indices else 0, int(variant), int(min_chunk),
+              int(window), _ptr(sinks), kv, float(k_descale), float(v_descale), int(max_len), int(total_len),
+              _ptr(kv_scales))
+    nbytes = workspace.numel() * workspace.element_size()
     if kv == KV_E2M1:
-        with _On(q.device, stream) as s:
-            _check(load().gda_decode_ex(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
-                                        workspace.numel() * workspace.element_size(), s))
+        _launch((_lib or load()).gda_decode_ex, q.get_device(), stream, a, workspace.data_ptr(), nbytes)
         return out
-    _check(load().gda_decode_ex(ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
-                                workspace.numel() * workspace.element_size(), _stream(stream)))
+    _check(load().gda_decode_ex(a, workspace.data_ptr(), nbytes, _stream(stream)))
     return out
 
 
@@ -598,7 +626,7 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     more keys than queries when it continues a prefix.  out: [Tq, Hq, D] contiguous (rows
     of no sequence are left as they are: zeros in an ``out`` allocated here); lse:
     [Hq, Tq] float32 or None; error_word as in prefill."""
-    import torch
+    torch = _torch()
     sq = _tokens("q", q)
     dev = q.device
     Tq, Hq, D = q.shape
@@ -612,7 +640,7 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     sv = _tokens("v", v, Hkv, D, dev)
     if v.shape[0] != Tk:
         raise ValueError("k and v must have the same shape")
-    _check_tensor("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
+    _need("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
     if cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must have B + 1 entries")
     if cu_seqlens_k is None:
@@ -620,17 +648,17 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
             raise ValueError("k must have q's tokens (or give cu_seqlens_k)")
         cu_seqlens_k = cu_seqlens
     else:
-        _check_tensor("cu_seqlens_k", cu_seqlens_k, torch.int32, 1, dev)
+        _need("cu_seqlens_k", cu_seqlens_k, torch.int32, 1, dev)
         if cu_seqlens_k.numel() != cu_seqlens.numel():
             raise ValueError("cu_seqlens_k must have B + 1 entries")
     if lse is not None:
-        _check_tensor("lse", lse, torch.float32, 2, dev)
-        if tuple(lse.shape) != (Hq, Tq):
+        _need("lse", lse, torch.float32, 2, dev)
+        if lse.shape != (Hq, Tq):
             raise ValueError("lse must be [Hq, Tq]")
     if out is None:
         out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
     else:
-        _check_tensor("out", out, torch.bfloat16, 3, dev)
+        _need("out", out, torch.bfloat16, 3, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if scale is None:
@@ -638,8 +666,7 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     a = _PackedArgs(_ptr(q), _ptr(gate_t), _ptr(k), _ptr(v), sq, sg, sk, sv, _ptr(cu_seqlens), _ptr(cu_seqlens_k),
                     _ptr(out), _ptr(lse), Tq, Tk, cu_seqlens.numel() - 1, Hq, Hkv, D, float(scale),
                     1 if causal else 0, _ptr(error_word))
-    with _On(dev, stream) as s:
-        _check(load().gda_prefill_packed(ctypes.byref(a), s))
+    _launch((_lib or load()).gda_prefill_packed, dev.index, stream, a)
     return out
 
 
@@ -709,7 +736,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     rope_dim / 2 axis numbers (``mrope_pair_axis``); gate_out: a [T, Hq, D] tensor to copy the
     gate into, or None.  With slots, k_pool and v_pool (bf16, or uint8 codes with kv_scales:
     a 4-bit cache) the K and V rows go into the cache too."""
-    import torch
+    torch = _torch()
     _check_rows("qgkv", qgkv)
     dev = qgkv.device
     T, width = qgkv.shape
@@ -720,24 +747,24 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     axis = bytes(pair_axis)
     rope_dim = 2 * len(axis)
     if rope_dim:
-        _check_tensor("positions", positions, torch.int32, 2, dev)
+        _need("positions", positions, torch.int32, 2, dev)
         if positions.shape[1] != T:
             raise ValueError("positions must be [A, T]")
-        _check_tensor("inv_freq", inv_freq, torch.float32, 1, dev)
+        _need("inv_freq", inv_freq, torch.float32, 1, dev)
         if inv_freq.numel() != len(axis):
             raise ValueError("inv_freq and pair_axis must have rope_dim / 2 entries")
         if max(axis) >= positions.shape[0]:
             raise ValueError("pair_axis names an axis that positions lacks")
     for name, t in (("w_q_norm", w_q_norm), ("w_k_norm", w_k_norm)):
         if t is not None:
-            _check_tensor(name, t, torch.bfloat16, 1, dev)
+            _need(name, t, torch.bfloat16, 1, dev)
             if t.numel() != D:
                 raise ValueError("%s must have D entries" % name)
     outs = []
     for name, t, h in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("gate_out", gate_out, Hq)):
         if t is not None:
-            _check_tensor(name, t, torch.bfloat16, 3, dev)
-            if tuple(t.shape) != (T, h, D):
+            _need(name, t, torch.bfloat16, 3, dev)
+            if t.shape != (T, h, D):
                 raise ValueError("%s must be [T, %d, D]" % (name, h))
         elif name != "gate_out":
             t = torch.empty(T, h, D, dtype=torch.bfloat16, device=dev)
@@ -747,15 +774,15 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     if k_pool is not None or v_pool is not None or slots is not None or kv_scales is not None:
         if k_pool is None or v_pool is None or slots is None:
             raise ValueError("a cache write needs slots, k_pool and v_pool")
-        _check_tensor("slots", slots, torch.int32, 1, dev)
+        _need("slots", slots, torch.int32, 1, dev)
         if slots.numel() != T:
             raise ValueError("slots must have T entries")
         if kv_scales is not None:
             kv = KV_E2M1
             num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
         else:
-            _check_tensor("k_pool", k_pool, torch.bfloat16, 3, dev)
-            _check_tensor("v_pool", v_pool, torch.bfloat16, 3, dev)
+            _need("k_pool", k_pool, torch.bfloat16, 3, dev)
+            _need("v_pool", v_pool, torch.bfloat16, 3, dev)
             num_slots, h = k_pool.shape[0], k_pool.shape[1]
             if v_pool.shape != k_pool.shape or k_pool.shape[2] != D:
                 raise ValueError("k_pool and v_pool must be [num_slots, Hkv, D]")
@@ -764,20 +791,19 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     a = _MropeArgs(_ptr(qgkv), qgkv.stride(0) if T > 1 else width, _ptr(w_q_norm), _ptr(w_k_norm), float(eps),
                    positions.shape[0] if rope_dim else 0, _ptr(positions) if rope_dim else None,
                    T if rope_dim else 0, _ptr(inv_freq) if rope_dim else None,
-                   ctypes.cast(ctypes.c_char_p(axis), ctypes.c_void_p), rope_dim, kv, _ptr(q_out), _ptr(gate_out),
+                   axis, rope_dim, kv, _ptr(q_out), _ptr(gate_out),
                    _ptr(k_out), _ptr(slots), num_slots, _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), float(k_descale),
                    float(v_descale), T, Hq, Hkv, D)
-    with _On(dev, stream) as s:
-        _check(load().gda_qk_norm_mrope_kv_write(ctypes.byref(a), s))
+    _launch((_lib or load()).gda_qk_norm_mrope_kv_write, dev.index, stream, a)
     return q_out, k_out
 
 
 def _check_rows(name, t):
     """A 2-D bf16 CUDA tensor with contiguous rows, any distance apart."""
-    import torch
+    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -788,45 +814,44 @@ def _check_rows(name, t):
 def kv_write_fp4(k, v, slots, k_pool, v_pool, kv_scales, k_descale: float = 1.0, v_descale: float = 1.0, stream=None):
     """Quantise the rows of k and v ([T, Hkv, D] bf16, tokens any multiple of 8 elements apart)
     into a 4-bit cache at ``slots`` ([T] int32), through ``gda_kv_write_fp4``."""
-    import torch
     sk = _tokens("k", k)
-    T, Hkv, D = k.shape
-    sv = _tokens("v", v, Hkv, D, k.device)
+    (T, Hkv, D), dev = k.shape, k.device
+    sv = _tokens("v", v, Hkv, D, dev)
     if v.shape[0] != T:
         raise ValueError("k and v must have the same shape")
-    _check_tensor("slots", slots, torch.int32, 1, k.device)
+    _need("slots", slots, _th.int32, 1, dev)
     if slots.numel() != T:
         raise ValueError("slots must have T entries")
-    num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, k.device)
+    num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
     if h != Hkv:
         raise ValueError("the pools must have Hkv heads")
-    with _On(k.device, stream) as s:
-        _check(load().gda_kv_write_fp4(_ptr(k), sk, _ptr(v), sv, _ptr(slots), num_slots, _ptr(k_pool), _ptr(v_pool),
-                                       _ptr(kv_scales), float(k_descale), float(v_descale), T, Hkv, D, s))
+    _launch((_lib or load()).gda_kv_write_fp4, dev.index, stream, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(),
+            num_slots, k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), float(k_descale), float(v_descale),
+            T, Hkv, D)
 
 
 def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_descale: float = 1.0, k_out=None,
                   v_out=None, stream=None):
     """The rows of a 4-bit cache that ``indices`` ([N] int32) name, as bf16 [N, Hkv, D] tensors
     (k, v), through ``gda_kv_gather_fp4``; an index outside the pools gives zeros."""
-    import torch
+    torch = _torch()
     num_slots, Hkv = _check_fp4(k_pool, v_pool, kv_scales)
-    dev, D = k_pool.device, 2 * k_pool.shape[2]
-    _check_tensor("indices", indices, torch.int32, 1, dev)
+    dev, D, bf16 = k_pool.device, 2 * k_pool.shape[2], torch.bfloat16
+    _need("indices", indices, torch.int32, 1, dev)
     N = indices.numel()
-    outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(N, Hkv, D, dtype=torch.bfloat16, device=dev)
-        else:
-            _check_tensor(name, t, torch.bfloat16, 3, dev)
-            if tuple(t.shape) != (N, Hkv, D):
+        if t is not None:
+            _need(name, t, bf16, 3, dev)
+            if t.shape != (N, Hkv, D):
                 raise ValueError("%s must be [N, Hkv, D]" % name)
-        outs.append(t)
-    with _On(dev, stream) as s:
-        _check(load().gda_kv_gather_fp4(_ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), num_slots, _ptr(indices), N,
-                                        float(k_descale), float(v_descale), _ptr(outs[0]), _ptr(outs[1]), Hkv, D, s))
-    return outs[0], outs[1]
+    if k_out is None:
+        k_out = torch.empty((N, Hkv, D), dtype=bf16, device=dev)
+    if v_out is None:
+        v_out = torch.empty((N, Hkv, D), dtype=bf16, device=dev)
+    _launch((_lib or load()).gda_kv_gather_fp4, dev.index, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+            kv_scales.data_ptr(), num_slots, indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(),
+            v_out.data_ptr(), Hkv, D)
+    return k_out, v_out
 
 
 def gate(o, gate_t, out=None, stream=None):

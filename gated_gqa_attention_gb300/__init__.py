@@ -567,6 +567,8 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
               _ptr(kv_scales))
     nbytes = workspace.numel() * workspace.element_size()
     if kv == KV_E2M1:
+        if workspace.get_device() != q.get_device():
+            raise ValueError("workspace is on %s, expected %s" % (workspace.device, q.device))
         _launch((_lib or load()).gda_decode_ex, q.get_device(), stream, a, workspace.data_ptr(), nbytes)
         return out
     _check(load().gda_decode_ex(a, workspace.data_ptr(), nbytes, _stream(stream)))
@@ -663,6 +665,9 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
             raise ValueError("out must have q's shape")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
+    if error_word is not None and (error_word.get_device() != dev.index or error_word.element_size() != 4
+                                   or error_word.numel() < 1):
+        raise ValueError("error_word must be a 32-bit word on %s" % dev)
     a = _PackedArgs(_ptr(q), _ptr(gate_t), _ptr(k), _ptr(v), sq, sg, sk, sv, _ptr(cu_seqlens), _ptr(cu_seqlens_k),
                     _ptr(out), _ptr(lse), Tq, Tk, cu_seqlens.numel() - 1, Hq, Hkv, D, float(scale),
                     1 if causal else 0, _ptr(error_word))

@@ -213,3 +213,31 @@ def test_a_prompt_continued_from_the_cache(gda):
     nk = cu([120, 130])
     out = gda.prefill_packed(q, gate, K, V, cu(second), cu_seqlens_k=nk, scale=1 / 16)
     plain64.check(out, None, plain64.packed(q, gate, K, V, cu(second), nk, 1 / 16, True), BF16, 0)
+
+
+# ---------------------------------------------------------------- a wait that runs out
+
+def test_wait_limit_gives_a_typed_timeout(gda):
+    # 5 sequences, several items per CTA pair and more than one key tile: every role has waits
+    lens = (300, 1, 129, 0, 513)
+    T, hq, hkv = sum(lens), 16, 2
+    g = torch.Generator().manual_seed(23)
+    q, gate, k, v = (torch.randn(T, h, 256, generator=g).bfloat16().cuda() for h in (hq, hq, hkv, hkv))
+    cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: gda.prefill_packed(q, gate, k, v, cu, error_word=err)
+    want = call()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    try:
+        gda.debug_wait_limit(200)           # SM cycles: below the latency of a first load
+        call()
+        torch.cuda.synchronize()            # the call returns
+    finally:
+        gda.debug_wait_limit(0)
+    assert int(err.item()) & gda.DEVERR_TIMEOUT
+    err.zero_()
+    got = call()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))

@@ -496,7 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((j + 1) * kPN > L) {
           // the last tile's V rows past the sequence's end become zeros: 256 threads, 16 bytes
           // each, before this tile's PV may start
-          ok = __all_sync(0xffffffffu, wait(&bars.v_full[0], T) && wait(&bars.v_full[1], T));
+          // (the previous tile's PV first: until it is done the barriers may be a phase behind, and
+          // a wait on the phase after next returns at once)
+          ok = __all_sync(0xffffffffu, (T == 0 || wait(&bars.p_empty[(T - 1) & 1], (T - 1) >> 1)) &&
+                                           wait(&bars.v_full[0], T) && wait(&bars.v_full[1], T));
           if (!ok) break;
           const int r0 = L - j * kPN;  // rows r0 .. 127 of each 64-dimension block
 #pragma unroll 1

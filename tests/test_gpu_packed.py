@@ -241,3 +241,20 @@ def test_wait_limit_gives_a_typed_timeout(gda):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("lens", [(129, 195, 255, 131) * 8, (195,) * 24 + (1000,) * 4, (300, 449, 513) * 6])
+def test_the_last_tile_waits_for_its_own_values(gda, lens):
+    # ones as values: every output is the sum of the rounded probabilities over that of the unrounded
+    # ones, within 2^-8 of 1, then rounded to BF16: 1 + 2^-7 at most (the step there), 1 - 2^-8 at
+    # least.  Values cleared or replaced while a tile still reads them lower it
+    T, hq, hkv = sum(lens), 32, 2
+    g = torch.Generator().manual_seed(29)
+    q, k = (torch.randn(T, h, 256, generator=g).bfloat16().cuda() for h in (hq, hkv))
+    v = torch.ones(T, hkv, 256, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(24):
+        cold.fill_(i)
+        out = gda.prefill_packed(q, None, k, v, cu)
+        assert float((out.float() - 1.0).abs().max()) <= 2.0 ** -7, i

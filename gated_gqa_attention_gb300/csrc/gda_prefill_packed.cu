@@ -221,6 +221,14 @@ struct Finder {
 
 // RNE_bf16(o * s) for BF16 o and s below the float normal range, exactly
 __device__ __noinline__ uint16_t product_tiny(float o, float s) { return bf16_rne_from_double((double)o * (double)s); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ __nv_bfloat162 bits_bf162(uint32_t u) {
+  return __halves2bfloat162(__ushort_as_bfloat16((unsigned short)u), __ushort_as_bfloat16((unsigned short)(u >> 16)));
+}
 __device__ __forceinline__ uint16_t product_exact(uint16_t obits, uint16_t sbits) {
   const float o = bf16_bits_to_float(obits), s = bf16_bits_to_float(sbits);
   const float p = __fmul_rn(o, s);
@@ -230,48 +238,32 @@ __device__ __forceinline__ uint16_t product_exact(uint16_t obits, uint16_t sbits
 
 // 2 P BF16 outputs gated: RNE(o * RNE(sigmoid(g))), the P pairs without a branch between
 // them, so that their chains of SFU operations overlap.
-// The sigmoid: with log2 e = L1 + L2, L1 of 16 bits so that g L1 is exact,
-// e = 2^(-g L1) (1 - g L2 ln 2), d = 1 + e, s0 = d1 / (d0 d1), s1 = d0 / (d0 d1); within
-// 13 * 2^-24 relative (2^x 4, the correction 3, the sum 1, product, reciprocal and quotients
-// 4, the widened values 1) while d0 d1 stays below 2^100, so its BF16 rounding is the correct
-// one unless the roundings of s (1 - 16 * 2^-24) and s (1 + 16 * 2^-24) differ -- by one step,
-// so in their last bit (about one element in 3500).  Those, and pairs with a larger d0 d1 (g
-// far below 0) or a NaN, stay ungated and are returned as open: bit e for the first, 16 + e
-// for the second element of pair e (P <= 16).  The product of two BF16 values is one correctly rounded
-// instruction.
+// The sigmoid of a BF16 gate has 65536 arguments, so its approximation is judged by all of them:
+// 1 / (1 + 2^(-g log2 e)) with the approximate exponential and reciprocal rounds to the correct
+// BF16 value for every g >= -87 (also with the constant one step lower or two higher), so it needs no
+// test of its error.  Below that e leaves the range of the reciprocal, whose results are then
+// subnormal; pairs with such a gate or a NaN stay ungated and are returned as open: bit e for
+// the first, 16 + e for the second element of pair e (P <= 16).  The product of two BF16 values
+// is one correctly rounded instruction.
 template <int P>
 __device__ __forceinline__ uint32_t gate_pairs(uint32_t* o, const uint32_t* g) {
-  uint32_t dif[P], prod[P], any = 0u, pmax = 0u;
+  constexpr float kNegLog2e = -1.4426950408889634f, kLowest = -87.0f;
   uint32_t res[P];
-  constexpr float kL1 = 1.4426879883f;                      // 0x3FB8AA00
-  constexpr float kC = (float)((1.4426950408889634 - 1.44268798828125) * 0.69314718055994531);
-  constexpr float kEps = 16.0f / 16777216.0f;
-  constexpr uint32_t kFar = 0x71800000u;                    // 2^100
+  __nv_bfloat162 least = bits_bf162(g[0]);
 #pragma unroll
   for (int e = 0; e < P; ++e) {
-    const float2 gv = make_float2(__uint_as_float(g[e] << 16), __uint_as_float(g[e] & 0xFFFF0000u));
-    const float2 x = mul_f32x2(gv, make_float2(-kL1, -kL1));
-    float2 ex = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-    ex = fma_f32x2(ex, mul_f32x2(gv, make_float2(-kC, -kC)), ex);
-    const float2 d = add_f32x2(ex, make_float2(1.0f, 1.0f));
-    const float pr = d.x * d.y;
-    prod[e] = __float_as_uint(pr);
-    pmax = max(pmax, prod[e]);
-    float rc;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(pr));
-    const float2 sg = mul_f32x2(make_float2(rc, rc), make_float2(d.y, d.x));
-    const float2 lo = mul_f32x2(sg, make_float2(1.0f - kEps, 1.0f - kEps));
-    const float2 hi = mul_f32x2(sg, make_float2(1.0f + kEps, 1.0f + kEps));
-    const uint32_t sv = bf16x2_rn(lo.x, lo.y);
-    dif[e] = sv ^ bf16x2_rn(hi.x, hi.y);
-    any |= dif[e];
-    res[e] = mul_bf16x2(o[e], sv);
+    if (e > 0) least = __hmin2_nan(least, bits_bf162(g[e]));
+    const float2 x = mul_f32x2(make_float2(__uint_as_float(g[e] << 16), __uint_as_float(g[e] & 0xFFFF0000u)),
+                               make_float2(kNegLog2e, kNegLog2e));
+    const float2 d = add_f32x2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
+    res[e] = mul_bf16x2(o[e], bf16x2_rn(rcp_approx(d.x), rcp_approx(d.y)));
   }
   uint32_t open = 0u;
-  if (any != 0u || pmax > kFar) {
+  if (!(__low2float(least) >= kLowest && __high2float(least) >= kLowest)) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      const uint32_t m = prod[e] > kFar ? 0x00010001u : dif[e] & 0x00010001u;
+      const float2 v = __bfloat1622float2(bits_bf162(g[e]));
+      const uint32_t m = (v.x >= kLowest ? 0u : 1u) | (v.y >= kLowest ? 0u : 0x10000u);
       open |= m << e;
       res[e] = (res[e] & ~(m * 0xFFFFu)) | (o[e] & (m * 0xFFFFu));
     }
@@ -290,7 +282,7 @@ struct OpenRows {
   int n;
 };
 // The elements that gate_pairs left open (four rows from x on; ungated in `out`), from the
-// table of all 65 536 BF16 sigmoids.  Out of line: it is rare.
+// table of all 65536 BF16 sigmoids.  Out of line: gates below -87 are rare.
 __device__ __noinline__ void gate_open(const OpenRows& w, int x, uint32_t open) {
 #pragma unroll 1
   while (open != 0u) {
@@ -571,17 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (p.lse && hc == 0 && qi < t.s.nq) {
         p.lse[(size_t)t.h * p.Sq + t.s.q0 + qi] = -INFINITY;
       }
-      // four rows at a time: lane l takes dimensions 8l .. 8l + 7 of each.  What the gate leaves
-      // open waits (rows x0 .., elements m0; another in x1, m1), so that the item's table reads
-      // are made together at the end
+      // four rows at a time: lane l takes dimensions 8l .. 8l + 7 of each
       {
-        int x0 = 0, x1 = 0;
-        uint32_t m0 = 0u, m1 = 0u;
         const OpenRows w = {reinterpret_cast<uint16_t*>(ob), reinterpret_cast<const uint16_t*>(gb), p.table,
                             8 * os, p.gate_stride, nrow};
 #pragma unroll 1
         for (int x = 0; x < nrow; x += kRows) {
-          uint32_t o[4 * kRows], g[4 * kRows];
+          uint32_t o[4 * kRows], g[4 * kRows], open = 0u;
 #pragma unroll
           for (int y = 0; y < kRows; ++y) {
             const int row = w0 + x + y;  // (a staged row, also past the sequence's last: not stored then)
@@ -595,26 +583,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < kRows; ++y)
               if (x + y + kRows < nrow) gv[y] = __ldcs(gb + (x + y + kRows) * gs);
-            const uint32_t open = gate_pairs<4 * kRows>(o, g);
-            if (open != 0u) {
-              if (m1 != 0u) gate_open(w, x1, m1);
-              x1 = x0;
-              m1 = m0;
-              x0 = x;
-              m0 = open;
-            }
+            open = gate_pairs<4 * kRows>(o, g);
           }
 #pragma unroll
           for (int y = 0; y < kRows; ++y)
             if (x + y < nrow) ob[(x + y) * os] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          if (open != 0u) gate_open(w, x, open);
         }
         // (generic accesses to the V buffers before the next copies into them)
         fence_async_shared();
         __syncwarp();
         if (t.ntiles > 0 && lane == 0) mbar_arrive(&bars.v_free);
-#pragma unroll 1
-        for (int y = 0; y < 2; ++y, m0 = m1, x0 = x1)
-          if (m0 != 0u) gate_open(w, x0, m0);
       }
     }
     if (!ok) fail();

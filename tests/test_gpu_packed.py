@@ -258,3 +258,23 @@ def test_the_last_tile_waits_for_its_own_values(gda, lens):
         cold.fill_(i)
         out = gda.prefill_packed(q, None, k, v, cu)
         assert float((out.float() - 1.0).abs().max()) <= 2.0 ** -7, i
+
+
+def test_the_gate_alone_on_every_code(gda):
+    """One key with ones as values: the attention result is exactly 1, and the output is the sigmoid of the gate
+    to the nearest BF16, for all 65536 codes."""
+    codes = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    want = 1.0 / (1.0 + torch.exp(-codes.double()))
+    for lens in ([256], [1, 100, 155]):
+        q = torch.randn(256, 1, D, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+        one = torch.ones(len(lens), 1, D, dtype=torch.bfloat16, device="cuda")
+        cq = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+        ck = torch.arange(len(lens) + 1, dtype=torch.int32, device="cuda")
+        out = gda.prefill_packed(q, codes.cuda().view(256, 1, D), one, one, cq, ck, causal=False).cpu().view(-1)
+        got = out.double()
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        # a nearest value is within half a step of its own binade (2^-133 among the subnormal numbers), and no
+        # sigmoid but 1/2 and those that round to 0 and 1 is a tie
+        step = torch.maximum(torch.exp2(torch.floor(torch.log2(want[~nan].clamp(min=1e-45))) - 8), torch.tensor(2.0 ** -134))
+        assert bool(((got - want)[~nan].abs() <= step).all())

@@ -21,8 +21,8 @@
 // (one 16-byte load and store a row), the partner of a rotated dimension is in lane
 // l +- rope_dim / 16, and the norm weights are folded into cos and sin:
 //   y = rinv (x (w cos) +- x_partner (w_partner sin)),
-// so a row costs four shuffles of packed pairs and two multiply-adds per element.  Up to
-// four rows are in flight per warp.  FP32 arithmetic, one rounding to BF16; a 4-bit cache
+// so a row costs four shuffles of packed pairs and two multiply-adds per element.  Two
+// rows are in flight per warp.  FP32 arithmetic, one rounding to BF16; a 4-bit cache
 // quantises that BF16 value, so its rows equal k_out quantised.  Bound by HBM for prompts
 // (every row in once and out once), by latency for a decode step.
 #include <type_traits>

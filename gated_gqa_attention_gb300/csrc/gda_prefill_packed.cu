@@ -13,18 +13,21 @@
 // descending, then by sequence.  Nothing is sorted -- the number of blocks with at least n
 // tiles has a closed form per sequence, so a warp sums it over the batch (lanes stride over
 // the sequences) and searches the n that holds a rank, then finds the sequence by a prefix
-// sum -- a few hundred cycles for the first item, less for the next ones, ahead of their use.  CTA c takes the items in snake
-// order (c, 2G - 1 - c, 2G + c, ..), heads fastest: equal shares from a descending list, and
-// neighbouring CTAs read the same keys.
+// sum -- a few hundred cycles for the first item, less for the next ones, ahead of their use.
+// CTA c takes the items in snake order (c, 2G - 1 - c, 2G + c, ..), heads fastest: equal shares
+// from a descending list, and neighbouring CTAs read the same keys.
 //
-// Why persistent: with one CTA per item an item cost 11 us besides its tiles (set-up 1.5,
-// first loads 2.7, last PV 1.0, epilogue 3.6, stores 1.5, the next CTA's launch 0.7; a tile is
-// 1.4), most of the time of an ordinary batch (50 key tiles in 11 items per SM: 207 us).  Here
-// the next item's K and Q arrive and its first S products run during the epilogue, and an item
-// costs about 6 us besides its tiles (last PV 1.2, O to shared memory 0.6, gate and stores
-// 3 to 4): 162 us.  (Measured and dropped: the epilogue on four warps of its own, during the
-// next item's tiles -- 210 us.  It takes the issue slots and the instruction cache that the
-// softmax needs, and four warps are too few for the gate's chains of SFU operations.)
+// What bounds it: the tensor pipe for long prompts (a tile takes 1.43 us, 1.31 at the measured
+// BF16 rate), and for short ones what an item costs besides its tiles.  With one CTA per item
+// that was 11 us (set-up 1.5, first loads 2.7, last PV 1.0, epilogue 3.6, stores 1.5, the next
+// CTA's launch 0.7).  Here the next item's K and Q arrive and its first S products run during
+// the epilogue, and it is about 5 us (sigmoids and last PV 2.7 to 3, O to shared memory 0.5,
+// products and stores 1, the next S 0.3): 6001 tokens of nine prompts x 32 heads (53 to 56 key
+// tiles in 11 items per SM) 207 -> 148 us; 12288 tokens x 16 heads with prefixes 472 -> 427 us.
+// (Measured and dropped: four more warps that run the whole epilogue during the next item's
+// tiles, 210 us, or only its sigmoids, 161 us -- both take from the softmax what they save; the
+// sigmoids as a loop over registers that move up, or with reciprocals by Newton steps in place
+// of the SFU's, 148 to 153 us.)
 //
 // Shared memory (all of it): the Q tile [128 x 256], K as a ring of three half tiles (128
 // keys x 128 dimensions), V as two; at an item's end the V buffers hold its outputs.  TMEM
@@ -40,11 +43,12 @@
 //    probabilities before that rounding, so lse does not see it.  Before the last tile's PV
 //    they zero the V rows past the sequence's end (rows of the next sequence: a NaN there
 //    times a probability of 0 would be NaN).
-//  * their epilogue: O / l from TMEM as BF16 into the V buffers (row per lane; the next item's
-//    PV may then start), and from there, gated, four whole rows at a time into `out`.  The
-//    gate rows come straight from global memory, brought into the L2 at the item's start.
-// The code is kept short (rolled loops, one short wait): the roles run different parts of it
-// at a time, and unrolling the outer loops by two made the kernel 1.4 times slower.
+//  * their epilogue: while the last PV runs, the sigmoids of 16 whole rows per warp (the gate
+//    rows were sent to the L2 at the item's start); then O / l from TMEM as BF16 into the V
+//    buffers (row per lane; the next item's PV may start), and from there times the sigmoid
+//    into `out`.
+// The rest of the code is kept short (rolled loops, one short wait): the roles run different
+// parts of it at a time, and unrolling the outer loops by two made the kernel 1.4 times slower.
 // On a timeout the CTA records kErrTimeout, every role stops, waits (bounded) for the copies
 // and MMAs it started, the TMEM is freed and the CTA returns.  Warps meet at mbarriers only
 // (bounded waits), never at a hardware barrier before the end.
@@ -219,8 +223,6 @@ struct Finder {
 
 // ---- the gate
 
-// RNE_bf16(o * s) for BF16 o and s below the float normal range, exactly
-__device__ __noinline__ uint16_t product_tiny(float o, float s) { return bf16_rne_from_double((double)o * (double)s); }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -229,69 +231,41 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ __nv_bfloat162 bits_bf162(uint32_t u) {
   return __halves2bfloat162(__ushort_as_bfloat16((unsigned short)u), __ushort_as_bfloat16((unsigned short)(u >> 16)));
 }
-__device__ __forceinline__ uint16_t product_exact(uint16_t obits, uint16_t sbits) {
-  const float o = bf16_bits_to_float(obits), s = bf16_bits_to_float(sbits);
-  const float p = __fmul_rn(o, s);
-  if (fabsf(p) < 1.17549435e-38f && p != 0.0f) return product_tiny(o, s);
-  return __bfloat16_as_ushort(__float2bfloat16_rn(p));
+// the sigmoids of 8 gates from the table of all 65536 (rarely needed, out of line)
+__device__ __noinline__ uint4 table_sigmoids(uint4 g, const uint16_t* table) {
+  uint32_t v[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __ldg(table + (v[e] & 0xFFFFu)) | ((uint32_t)__ldg(table + (v[e] >> 16)) << 16);
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
-
-// 2 P BF16 outputs gated: RNE(o * RNE(sigmoid(g))), the P pairs without a branch between
-// them, so that their chains of SFU operations overlap.
-// The sigmoid of a BF16 gate has 65536 arguments, so its approximation is judged by all of them:
-// 1 / (1 + 2^(-g log2 e)) with the approximate exponential and reciprocal rounds to the correct
-// BF16 value for every g >= -87 (also with the constant one step lower or two higher), so it needs no
-// test of its error.  Below that e leaves the range of the reciprocal, whose results are then
-// subnormal; pairs with such a gate or a NaN stay ungated and are returned as open: bit e for
-// the first, 16 + e for the second element of pair e (P <= 16).  The product of two BF16 values
-// is one correctly rounded instruction.
-template <int P>
-__device__ __forceinline__ uint32_t gate_pairs(uint32_t* o, const uint32_t* g) {
+// 4 R pairs of BF16 gates become RNE_bf16(sigmoid), without a branch between them, so that
+// their chains of SFU operations overlap.  A BF16 gate has 65536 values, so the approximation
+// is judged by all of them: 1 / (1 + 2^(-g log2 e)) with the approximate exponential and
+// reciprocal rounds to the correct BF16 value for every g >= -87 (also with the constant one
+// step lower or two higher).  Below that the exponential leaves the reciprocal's range, whose
+// results would be subnormal: such gates and NaNs come from the table.
+template <int R>
+__device__ __forceinline__ void sigmoids(uint32_t* g, const uint16_t* table) {
   constexpr float kNegLog2e = -1.4426950408889634f, kLowest = -87.0f;
-  uint32_t res[P];
+  uint32_t sg[4 * R];
   __nv_bfloat162 least = bits_bf162(g[0]);
 #pragma unroll
-  for (int e = 0; e < P; ++e) {
+  for (int e = 0; e < 4 * R; ++e) {
     if (e > 0) least = __hmin2_nan(least, bits_bf162(g[e]));
     const float2 x = mul_f32x2(make_float2(__uint_as_float(g[e] << 16), __uint_as_float(g[e] & 0xFFFF0000u)),
                                make_float2(kNegLog2e, kNegLog2e));
     const float2 d = add_f32x2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
-    res[e] = mul_bf16x2(o[e], bf16x2_rn(rcp_approx(d.x), rcp_approx(d.y)));
+    sg[e] = bf16x2_rn(rcp_approx(d.x), rcp_approx(d.y));
   }
-  uint32_t open = 0u;
   if (!(__low2float(least) >= kLowest && __high2float(least) >= kLowest)) {
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const float2 v = __bfloat1622float2(bits_bf162(g[e]));
-      const uint32_t m = (v.x >= kLowest ? 0u : 1u) | (v.y >= kLowest ? 0u : 0x10000u);
-      open |= m << e;
-      res[e] = (res[e] & ~(m * 0xFFFFu)) | (o[e] & (m * 0xFFFFu));
+    for (int y = 0; y < R; ++y) {
+      const uint4 v = table_sigmoids(make_uint4(g[4 * y], g[4 * y + 1], g[4 * y + 2], g[4 * y + 3]), table);
+      sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
     }
   }
 #pragma unroll
-  for (int e = 0; e < P; ++e) o[e] = res[e];
-  return open;
-}
-
-// A lane's dimensions (8 of a row) of a warp's rows in `out` and the gate.
-struct OpenRows {
-  uint16_t* out;
-  const uint16_t* gate;
-  const uint16_t* table;
-  long long out_pitch, gate_pitch;  // elements between rows
-  int n;
-};
-// The elements that gate_pairs left open (four rows from x on; ungated in `out`), from the
-// table of all 65536 BF16 sigmoids.  Out of line: gates below -87 are rare.
-__device__ __noinline__ void gate_open(const OpenRows& w, int x, uint32_t open) {
-#pragma unroll 1
-  while (open != 0u) {
-    const int bit = __ffs(open) - 1, row = x + ((bit >> 2) & 3), at = 2 * (bit & 3) + (bit >> 4);
-    open &= open - 1u;
-    if (row >= w.n) continue;
-    uint16_t* o = w.out + row * w.out_pitch + at;
-    *o = product_exact(*o, __ldg(w.table + w.gate[row * w.gate_pitch + at]));
-  }
+  for (int e = 0; e < 4 * R; ++e) g[e] = sg[e];
 }
 
 }  // namespace
@@ -400,11 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w0 = 32 * rg + 16 * hc, nrow = min(16, t.s.nq - i0 - w0);
       uint4* ob = reinterpret_cast<uint4*>(p.out + ((size_t)(t.s.q0 + i0 + w0) * p.Hq + t.h) * kD) + lane;
       const __nv_bfloat16* gate_w = p.gate + (long long)(t.s.q0 + i0 + w0) * p.gate_stride + (long long)t.h * kD;
-      if (p.fuse_gate && (lane & 15) < nrow) {  // their gate on its way to the L2 while the item is computed
-        const __nv_bfloat16* line = gate_w + (lane & 15) * p.gate_stride + 64 * (lane >> 4);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128));
-      }
+      if (p.fuse_gate && lane < nrow)  // their gate on its way to the L2 while the item is computed
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gate_w + lane * p.gate_stride), "r"(2 * kD) : "memory");
       float m_run = -INFINITY, l_run = 0.0f;  // running row max (log2 units) and sum
 #pragma unroll 1
       for (int j = 0; j < t.ntiles; ++j, ++T) {
@@ -505,15 +476,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars.p_full[sb]);
       }
       if (!ok) break;
-      // ---- epilogue.  Gate rows of this warp, four at a time, a step ahead of their use
-      constexpr int kRows = 4;
-      uint4 gv[kRows] = {};
-      const uint4* gb = reinterpret_cast<const uint4*>(gate_w) + lane;
-      const long long gs = p.gate_stride / 8, os = (long long)p.Hq * (kD / 8);
+      // ---- epilogue.  While the last products run: the sigmoids of this warp's 16 rows, lane l
+      // dimensions 8l .. 8l + 7 of each (1 without a gate)
+      constexpr int kRows = 16;
+      uint32_t sg[4 * kRows];
+      const long long os = (long long)p.Hq * (kD / 8);
       if (p.fuse_gate) {
+        const uint4* gb = reinterpret_cast<const uint4*>(gate_w) + lane;
+        const long long gs = p.gate_stride / 8;
 #pragma unroll
-        for (int y = 0; y < kRows; ++y)
-          if (y < nrow) gv[y] = __ldcs(gb + y * gs);
+        for (int y = 0; y < kRows; ++y) {
+          const uint4 v = y < nrow ? __ldcs(gb + y * gs) : make_uint4(0u, 0u, 0u, 0u);
+          sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
+        }
+#pragma unroll
+        for (int y = 0; y < kRows; y += 4) sigmoids<4>(sg + 4 * y, p.table);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4 * kRows; ++e) sg[e] = 0x3F803F80u;
       }
       unsigned char* stage = sm + kOffV;
       if (t.ntiles > 0) {
@@ -563,32 +543,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (p.lse && hc == 0 && qi < t.s.nq) {
         p.lse[(size_t)t.h * p.Sq + t.s.q0 + qi] = -INFINITY;
       }
-      // four rows at a time: lane l takes dimensions 8l .. 8l + 7 of each
       {
-        const OpenRows w = {reinterpret_cast<uint16_t*>(ob), reinterpret_cast<const uint16_t*>(gb), p.table,
-                            8 * os, p.gate_stride, nrow};
-#pragma unroll 1
-        for (int x = 0; x < nrow; x += kRows) {
-          uint32_t o[4 * kRows], g[4 * kRows], open = 0u;
 #pragma unroll
-          for (int y = 0; y < kRows; ++y) {
-            const int row = w0 + x + y;  // (a staged row, also past the sequence's last: not stored then)
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (t.ntiles > 0)
-              v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
-            o[4 * y] = v.x, o[4 * y + 1] = v.y, o[4 * y + 2] = v.z, o[4 * y + 3] = v.w;
-            g[4 * y] = gv[y].x, g[4 * y + 1] = gv[y].y, g[4 * y + 2] = gv[y].z, g[4 * y + 3] = gv[y].w;
-          }
-          if (p.fuse_gate) {
-#pragma unroll
-            for (int y = 0; y < kRows; ++y)
-              if (x + y + kRows < nrow) gv[y] = __ldcs(gb + (x + y + kRows) * gs);
-            open = gate_pairs<4 * kRows>(o, g);
-          }
-#pragma unroll
-          for (int y = 0; y < kRows; ++y)
-            if (x + y < nrow) ob[(x + y) * os] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          if (open != 0u) gate_open(w, x, open);
+        for (int y = 0; y < kRows; ++y) {
+          const int row = w0 + y;  // (a staged row, also past the sequence's last: not stored then)
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (t.ntiles > 0)
+            v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+          // (a product of two BF16 values, correctly rounded by one instruction)
+          v.x = mul_bf16x2(v.x, sg[4 * y]), v.y = mul_bf16x2(v.y, sg[4 * y + 1]);
+          v.z = mul_bf16x2(v.z, sg[4 * y + 2]), v.w = mul_bf16x2(v.w, sg[4 * y + 3]);
+          if (y < nrow) ob[y * os] = v;
         }
         // (generic accesses to the V buffers before the next copies into them)
         fence_async_shared();

@@ -8,12 +8,15 @@
 // What bounds it: 288 bytes per (position, KV head) against 1024 of a BF16 cache, so the
 // streaming time falls to a quarter while the arithmetic per position stays.  The design
 // spends as few instructions per code as it can:
-//  * Persistent grid, one CTA of 8 warps per SM; warp w takes 32-position tiles w, w + 8,
-//    ... of its CTA's piece.  K and V rows and their scales go through a per-warp ring of
-//    three 9 KB stages filled by cp.async two tiles ahead (216 KB a CTA in flight or in
-//    use; no registers held by loads, 18 copy instructions a tile).  A ring row is 128
-//    code bytes followed by its 16 scale bytes: the 144-byte pitch that keeps the 16-byte
-//    reads below free of bank conflicts is the row itself.
+//  * Persistent grid, two CTAs of 6 warps per SM (of 4 warps for pairs of head groups, which
+//    hold two sets of accumulators); warp w takes 32-position tiles w, w + W, ... of its CTA's
+//    piece.  K and V rows and their scales go through a per-warp ring of two 9 KB stages filled
+//    by cp.async a tile ahead (108 KB a CTA in flight or in use; no registers held by loads, 18
+//    copy instructions a tile).  A ring row is 128 code bytes followed by its 16 scale bytes: the
+//    144-byte pitch that keeps the 16-byte reads below free of bank conflicts is the row itself.
+//    Two CTAs keep the pipes busy while one merges or waits: a ragged batch of 224 sequences took
+//    125 us with one CTA of 8 warps and three stages, 107 with one of 12 warps, 103 with two of
+//    6.  Of 120 us for 8 x 131072 positions the copies alone take 109 and the arithmetic alone 100.
 //  * A code times its scale is exact in FP16, so cvt.rn.f16x2.e2m1x2 widens a byte (two
 //    codes), one packed multiply applies the scale, and the tiles run as m16n8k16 FP16
 //    MMAs with FP32 accumulation.  Q goes to FP16 with one power of two per piece (its
@@ -33,10 +36,12 @@
 //  * P is rounded to FP16 for the MMA (it lies in [0, 2^8], 2^-11 relative, against the
 //    4-bit V it multiplies) and its sum is kept in FP32 before the rounding, so the LSE
 //    does not see it.
+//  * With more than 8 query heads per KV head, pairs of groups share one read of the rows and
+//    one widening of the codes (16 heads, 8 x 32769 positions: 84 -> 58 us).
 //  * Merge: as in the e4m3 kernel -- each warp leaves its rescaled O^T fragments in ring
-//    stage 0, all threads add the 8 slices in a fixed order.  Tile k of a piece lives in
-//    stage (k + 1) % 3, so the next piece's first two tiles are on their way to stages 1
-//    and 2 while stage 0 serves the merge.
+//    stage 0, all threads add the slices in a fixed order.  Tile k of a piece lives in stage
+//    (k + 1) % 2, so the next piece's first tile is on its way to stage 1 while stage 0 serves
+//    the merge.
 #include <atomic>
 
 #include "gda_kernels.h"

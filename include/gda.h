@@ -136,7 +136,7 @@ typedef enum gda_status {
  *   kv_dtype    GDA_KV_BF16 or GDA_KV_E4M3 (an FP8 KV cache, cuDNN FE-OSS "Gated Attention
  *               Block (SM107)", API, QuantSpec: static per-tensor scales, e4m3 codes).
  *               E4M3 and E2M1 are served by GDA_VARIANT_AUTO / GDA_VARIANT_MMA only.
- *               E2M1 reads the rows once per group of 8 query heads.  A NaN in a row that
+ *               E2M1 reads the rows once per 16 query heads of a KV head.  A NaN in a row that
  *               the batch names (a NaN scale) gives NaN in the query heads that see it.
  *   k_descale, v_descale  per-tensor factors of an e4m3 or 4-bit cache (finite; else
  *               GDA_ERR_ARG); not used for bf16 pools.
@@ -306,7 +306,8 @@ int gda_prefill(const gda_bf16* q, const gda_bf16* gate, const gda_bf16* k, cons
  *             before the first or behind the last one.  Their contents are not checked:
  *             values are clamped to [0, total], so nothing outside the tensors is read or
  *             written
- *   out       [total_q, Hq, D] bf16, contiguous.  Rows of no sequence are left as they are
+ *   out       [total_q, Hq, D] bf16, contiguous, apart from the inputs.  Rows of no sequence
+ *             are left as they are
  *   lse       [Hq, total_q] float or NULL   natural-log log-sum-exp (-inf for a dead row)
  *   causal    1: key j of a sequence is visible to its query i when j <= i + (keys - queries);
  *             0: every key of the sequence is visible
@@ -398,7 +399,9 @@ int gda_small_path_cluster(int64_t pairs, int max_len);
  *  - the stream once each CTA would take >= 3072 positions, or when the longest
  *    sequence is more than 1.25 x the mean.
  * An e4m3 cache streams a position in half the time: its variant of the rule takes
- * 16 S^2 > lmax and moves to the stream from 6144 positions per CTA. */
+ * 16 S^2 > lmax and moves to the stream from 6144 positions per CTA.  So does a 4-bit
+ * cache's, which besides cuts every sequence into as many pieces as fill one wave when
+ * that keeps 95 % of the CTAs busy, at any length. */
 int gda_auto_splits(int B, int heads, int grid, int min_chunk, int lmax, int64_t total);
 
 /* Byte layout of one decode step's inputs packed into a single block, as

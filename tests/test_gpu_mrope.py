@@ -136,3 +136,9 @@ def test_captured(gda):
     rq, _, rk, _ = reference(qgkv, pos + 17, inv, axis, 2, 2, None, None)
     near(q, rq, 64)
     near(k, rk, 64)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,pool", [(4864, 2, 1, "none"), (4865, 1, 1, "bf16"), (7290, 2, 1, "fp4"), (14599, 1, 1, "none")])
+def test_more_tokens_than_warps(gda, T, Hq, Hkv, pool):
+    """Several passes of the grid; in the last one the warps share the tokens that are left."""
+    test_matches_float64(gda, T, Hq, Hkv, 64, 3, True, pool)

@@ -278,3 +278,25 @@ def test_the_gate_alone_on_every_code(gda):
         # sigmoid but 1/2 and those that round to 0 and 1 is a tie
         step = torch.maximum(torch.exp2(torch.floor(torch.log2(want[~nan].clamp(min=1e-45))) - 8), torch.tensor(2.0 ** -134))
         assert bool(((got - want)[~nan].abs() <= step).all())
+
+
+def test_offsets_past_32_bits(gda):
+    """Queries, gate and output whose last rows lie more than 2^32 bytes from the first."""
+    T, Hq, n = 270000, 32, 130
+    rows = torch.zeros(T, 2, Hq, D, dtype=torch.bfloat16, device="cuda")     # 8.8 GB
+    k, v = (torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b = make([n], [n], Hq, 1, seed=31)
+    for big, small in ((rows[:, 0], b["q"]), (rows[:, 1], b["gate"]), (k, b["k"]), (v, b["v"])):
+        big[T - n:] = small[-n:]
+    out = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    c = torch.tensor([T - n, T], dtype=torch.int32, device="cuda")
+    gda.prefill_packed(rows[:, 0], rows[:, 1], k, v, c, out=out, scale=1 / 16)
+    want = gda.prefill_packed(b["q"][-n:], b["gate"][-n:], b["k"][-n:], b["v"][-n:], cu([n]), scale=1 / 16)
+    assert torch.equal(out[T - n:], want) and bool((out[:T - n] == 7.0).all())
+
+
+def test_thousands_of_short_sequences(gda):
+    r = random.Random(5)
+    nq = [r.choice([0, 1, 1, 2, 3]) for _ in range(3000)]
+    nk = [x + r.choice([0, 0, 1, 5]) for x in nq]
+    verify(gda, make(nq, nk, 2, 1, seed=41))

@@ -254,6 +254,18 @@ def _need(name, t, dtype, ndim, device):
         _check_tensor(name, t, dtype, ndim, device)
 
 
+def _need_shape(name, t, dtype, shape, device, what):
+    """As _need, with the sizes ``what`` describes."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check_tensor(name, t, dtype, len(shape), device)
+    if t.shape != shape:
+        raise ValueError("%s must %s" % (name, what))
+
+
 def _cuda_index(name, t, dtype):
     """The device index of the call's first tensor."""
     try:
@@ -292,18 +304,18 @@ def _tokens(name, t, heads=None, dim=None, device=None):
 def _check_fp4(k_pool, v_pool, kv_scales, D=None, device=None):
     """Checks a 4-bit cache; returns (num_slots, Hkv)."""
     torch = _torch()
-    idx = device.index if device is not None else _cuda_index("k_pool", k_pool, torch.uint8)
-    if not _is(k_pool, torch.uint8, 3, idx):
-        _check_tensor("k_pool", k_pool, torch.uint8, 3, device)
-    dev = k_pool.device if device is None else device
-    _need("v_pool", v_pool, torch.uint8, 3, dev)
-    kv_scales = _scale_bytes(kv_scales)
-    _need("kv_scales", kv_scales, torch.uint8, 4, dev)
+    u8 = torch.uint8
+    if device is None:
+        _cuda_index("k_pool", k_pool, u8)
+        device = k_pool.device
+    _need("k_pool", k_pool, u8, 3, device)
     n, h, half = shape = k_pool.shape
-    if v_pool.shape != shape:
-        raise ValueError("k_pool and v_pool must have the same shape")
-    if half % 8 != 0 or kv_scales.shape != (n, h, 2, half // 8):
-        raise ValueError("kv_scales must be [num_slots, Hkv, 2, D / 16] for pools [num_slots, Hkv, D / 2]")
+    _need_shape("v_pool", v_pool, u8, shape, device, "have k_pool's shape")
+    kv_scales = _scale_bytes(kv_scales)
+    what = "be [num_slots, Hkv, 2, D / 16] for pools [num_slots, Hkv, D / 2]"
+    if half % 8 != 0:
+        raise ValueError("kv_scales must " + what)
+    _need_shape("kv_scales", kv_scales, u8, (n, h, 2, half // 8), device, what)
     if D is not None and 2 * half != D:
         raise ValueError("head dims of q and the pools differ")
     return n, h
@@ -345,9 +357,7 @@ def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_sca
         _check_tensor("q", q, bf16, 3)
     dev, shape = q.device, q.shape
     if gate_t is not None:
-        _need("gate", gate_t, bf16, 3, dev)
-        if gate_t.shape != shape:
-            raise ValueError("gate must have q's shape")
+        _need_shape("gate", gate_t, bf16, shape, dev, "have q's shape")
     if kv_scales is not None:
         kv = KV_E2M1
         _check_fp4(k_pool, v_pool, kv_scales, shape[2], dev)
@@ -358,16 +368,12 @@ def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_sca
         _need("v_pool", v_pool, kdt, 3, dev)
         if v_pool.shape != k_pool.shape:
             raise ValueError("k_pool and v_pool must have the same shape")
-    _need("kv_indptr", kv_indptr, i32, 1, dev)
+    _need_shape("kv_indptr", kv_indptr, i32, (shape[0] + 1,), dev, "have B + 1 entries")
     _need("kv_indices", kv_indices, i32, 1, dev)
-    if kv_indptr.numel() != shape[0] + 1:
-        raise ValueError("kv_indptr must have B + 1 entries")
     if kv != KV_E2M1 and k_pool.shape[2] != shape[2]:
         raise ValueError("head dims of q and the pools differ")
     if out is not None:
-        _need("out", out, bf16, 3, dev)
-        if out.shape != shape:
-            raise ValueError("out must have q's shape")
+        _need_shape("out", out, bf16, shape, dev, "have q's shape")
     return kv
 
 
@@ -654,15 +660,11 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
         if cu_seqlens_k.numel() != cu_seqlens.numel():
             raise ValueError("cu_seqlens_k must have B + 1 entries")
     if lse is not None:
-        _need("lse", lse, torch.float32, 2, dev)
-        if lse.shape != (Hq, Tq):
-            raise ValueError("lse must be [Hq, Tq]")
+        _need_shape("lse", lse, torch.float32, (Hq, Tq), dev, "be [Hq, Tq]")
     if out is None:
         out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
     else:
-        _need("out", out, torch.bfloat16, 3, dev)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+        _need_shape("out", out, torch.bfloat16, (Tq, Hq, D), dev, "have q's shape")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
     if error_word is not None and (error_word.get_device() != dev.index or error_word.element_size() != 4
@@ -742,6 +744,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     gate into, or None.  With slots, k_pool and v_pool (bf16, or uint8 codes with kv_scales:
     a 4-bit cache) the K and V rows go into the cache too."""
     torch = _torch()
+    bf16 = torch.bfloat16
     _check_rows("qgkv", qgkv)
     dev = qgkv.device
     T, width = qgkv.shape
@@ -755,33 +758,25 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
         _need("positions", positions, torch.int32, 2, dev)
         if positions.shape[1] != T:
             raise ValueError("positions must be [A, T]")
-        _need("inv_freq", inv_freq, torch.float32, 1, dev)
-        if inv_freq.numel() != len(axis):
-            raise ValueError("inv_freq and pair_axis must have rope_dim / 2 entries")
+        _need_shape("inv_freq", inv_freq, torch.float32, (len(axis),), dev, "have rope_dim / 2 entries, as pair_axis")
         if max(axis) >= positions.shape[0]:
             raise ValueError("pair_axis names an axis that positions lacks")
     for name, t in (("w_q_norm", w_q_norm), ("w_k_norm", w_k_norm)):
         if t is not None:
-            _need(name, t, torch.bfloat16, 1, dev)
-            if t.numel() != D:
-                raise ValueError("%s must have D entries" % name)
+            _need_shape(name, t, bf16, (D,), dev, "have D entries")
     outs = []
     for name, t, h in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("gate_out", gate_out, Hq)):
         if t is not None:
-            _need(name, t, torch.bfloat16, 3, dev)
-            if t.shape != (T, h, D):
-                raise ValueError("%s must be [T, %d, D]" % (name, h))
+            _need_shape(name, t, bf16, (T, h, D), dev, "be [T, %d, D]" % h)
         elif name != "gate_out":
-            t = torch.empty(T, h, D, dtype=torch.bfloat16, device=dev)
+            t = torch.empty_strided((T, h, D), (h * D, D, 1), dtype=bf16, device=dev)
         outs.append(t)
     q_out, k_out, gate_out = outs
     num_slots, kv = 0, KV_BF16
     if k_pool is not None or v_pool is not None or slots is not None or kv_scales is not None:
         if k_pool is None or v_pool is None or slots is None:
             raise ValueError("a cache write needs slots, k_pool and v_pool")
-        _need("slots", slots, torch.int32, 1, dev)
-        if slots.numel() != T:
-            raise ValueError("slots must have T entries")
+        _need_shape("slots", slots, torch.int32, (T,), dev, "have T entries")
         if kv_scales is not None:
             kv = KV_E2M1
             num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
@@ -824,9 +819,7 @@ def kv_write_fp4(k, v, slots, k_pool, v_pool, kv_scales, k_descale: float = 1.0,
     sv = _tokens("v", v, Hkv, D, dev)
     if v.shape[0] != T:
         raise ValueError("k and v must have the same shape")
-    _need("slots", slots, _th.int32, 1, dev)
-    if slots.numel() != T:
-        raise ValueError("slots must have T entries")
+    _need_shape("slots", slots, _th.int32, (T,), dev, "have T entries")
     num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
     if h != Hkv:
         raise ValueError("the pools must have Hkv heads")
@@ -846,13 +839,11 @@ def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_
     N = indices.numel()
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _need(name, t, bf16, 3, dev)
-            if t.shape != (N, Hkv, D):
-                raise ValueError("%s must be [N, Hkv, D]" % name)
+            _need_shape(name, t, bf16, (N, Hkv, D), dev, "be [N, Hkv, D]")
     if k_out is None:
-        k_out = torch.empty((N, Hkv, D), dtype=bf16, device=dev)
+        k_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=dev)
     if v_out is None:
-        v_out = torch.empty((N, Hkv, D), dtype=bf16, device=dev)
+        v_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=dev)
     _launch((_lib or load()).gda_kv_gather_fp4, dev.index, stream, k_pool.data_ptr(), v_pool.data_ptr(),
             kv_scales.data_ptr(), num_slots, indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(),
             v_out.data_ptr(), Hkv, D)

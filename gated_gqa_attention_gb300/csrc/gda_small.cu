@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
   float sl2 = p.scale_log2;
   if (F8) {
     // every warp holds the whole group's Q: its largest magnitude sets 2^e, which puts
-    // it in [2^14, 2^15) (every BF16 value down to 2^-14 below it stays exact in FP16)
+    // it in [2^14, 2^15) (every BF16 value down to 2^-14 below it stays exact in FP16).
+    // 4-bit rows: each head's own, so that an infinite or huge q stays its head's affair
     float mx = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < 16; ++ks)
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
       for (int i = 0; i < 2; ++i)
         mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(qa[ks][i] << 16)), fabsf(__uint_as_float(qa[ks][i] & 0xFFFF0000u))));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    for (int off = KV == 2 ? 2 : 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     const uint32_t qm = __float_as_uint(mx);
     int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);
     e = max(-126, min(127, e));

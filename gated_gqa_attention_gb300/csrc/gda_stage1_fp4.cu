@@ -19,7 +19,7 @@
 //    6.  Of 120 us for 8 x 131072 positions the copies alone take 109 and the arithmetic alone 100.
 //  * A code times its scale is exact in FP16, so cvt.rn.f16x2.e2m1x2 widens a byte (two
 //    codes), one packed multiply applies the scale, and the tiles run as m16n8k16 FP16
-//    MMAs with FP32 accumulation.  Q goes to FP16 with one power of two per piece (its
+//    MMAs with FP32 accumulation.  Q goes to FP16 with one power of two per head (its
 //    largest magnitude lands in [2^14, 2^15)); that factor and k_descale are folded into
 //    the score scale, v_descale into the partial's normalisation.
 //  * QK: S^T[32 tok x 8 heads] = K Q^T, two m-tiles.  Lane (g, t) reads dims 64t .. 64t + 63
@@ -67,7 +67,7 @@ struct Fp4Smem {
   Fp4Stage ring[W][2];            // per-warp rings; stage 0 also holds the merge slice
   float mbuf[W][kG];              // each warp's running max
   float lsum[W][kG];              // each warp's rescaled sum
-  unsigned int qmax[NG];          // largest |q| of each group of the piece (float bits)
+  unsigned int qmax[NG][kG];      // largest |q| of each head of the piece (float bits)
 };
 static_assert(sizeof(float4) * 16 * 32 <= sizeof(Fp4Stage), "merge slice fits a ring stage");
 
@@ -167,7 +167,7 @@ struct Fp4WarpState {
   }
 
   // S^T of the tile's K rows, then the softmax update; nv tokens of the tile are valid
-  __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[16][32], int nv, const float* sl2,
+  __device__ __forceinline__ void qk_softmax(const Fp4Stage& st, const uint2 (*qf)[16][32], int nv, const float (*sl2)[2],
                                              int lane) {
     const int g = lane >> 2, t = lane & 3;
     float acc[NG][4][4];  // [group][m-tile * 2 + k-step parity][4]
@@ -222,8 +222,8 @@ struct Fp4WarpState {
       float s[8];  // s[2j], s[2j + 1]: token g + 8j, heads 2t, 2t + 1 (log2 units)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[i] = (acc[n][0][i] + acc[n][1][i]) * sl2[n];
-        s[4 + i] = (acc[n][2][i] + acc[n][3][i]) * sl2[n];
+        s[i] = (acc[n][0][i] + acc[n][1][i]) * sl2[n][i & 1];
+        s[4 + i] = (acc[n][2][i] + acc[n][3][i]) * sl2[n][i & 1];
       }
       if (nv < kTok4) {
 #pragma unroll
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
   Fp4Smem<NG, W>& sm = *reinterpret_cast<Fp4Smem<NG, W>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x < NG) sm.qmax[threadIdx.x] = 0u;
+  if (threadIdx.x < NG * kG) (&sm.qmax[0][0])[threadIdx.x] = 0u;
   Sched sched;
   sched.begin(p.indptr, p.B, p.Hkv * p.nteam, p.num_splits, gridDim.x, blockIdx.x, p.min_chunk, p.window,
               p.piece_cost, p.rule_kv8);
@@ -418,34 +418,36 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
         mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] << 16)));
         mx = fmaxf(mx, fabsf(__uint_as_float(w2[j] & 0xFFFF0000u)));
       }
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-      if (lane == 0) atomicMax(&sm.qmax[w >> 4], bits);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if ((lane & 3) == 0) atomicMax(&sm.qmax[w >> 4][lane >> 2], __float_as_uint(mx));
     }
     __syncthreads();  // also: the previous piece's merge is done with stage 0 and the Q fragments
     if (!first) issue(ring[0], kv, s1, tile_n(1, len, nmine));
     first = false;
-    // Q into FP16: one power-of-two factor 2^e per group puts its largest magnitude in
-    // [2^14, 2^15)
-    float sl2[NG], qs[NG];
+    // Q into FP16: one power-of-two factor 2^e per head puts its largest magnitude in
+    // [2^14, 2^15) (an infinite or huge q stays its head's affair)
+    auto exponent = [&](int n, int head) -> int {
+      const unsigned int qm = sm.qmax[n][head];
+      const int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);
+      return max(-126, min(127, e));
+    };
+    float sl2[NG][2];
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const unsigned int qm = sm.qmax[n];
-      int e = (qm == 0u) ? 0 : 141 - (int)((qm >> 23) & 0xFFu);
-      e = max(-126, min(127, e));
-      qs[n] = __uint_as_float((uint32_t)(e + 127) << 23);
-      sl2[n] = ldexpf(p.scale_log2, -e);
-    }
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sl2[n][i] = ldexpf(p.scale_log2, -exponent(n, 2 * (lane & 3) + i));
 #pragma unroll
     for (int r = 0; r < kQr; ++r) {
       const int w = warp + r * W;
       if (w >= NG * 16) continue;
       const uint32_t x = qraw[r].x, y = qraw[r].y;
-      const float f = NG == 1 ? qs[0] : (w >> 4) ? qs[NG - 1] : qs[0];
+      const float f = __uint_as_float((uint32_t)(exponent(w >> 4, lane >> 2) + 127) << 23);
       sm.qf[w >> 4][w & 15][lane] = make_uint2(pack_f16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f),
                                                pack_f16(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f));
     }
     __syncthreads();
-    if (threadIdx.x < NG) sm.qmax[threadIdx.x] = 0u;  // every thread has read it; the next write follows a barrier
+    if (threadIdx.x < NG * kG) (&sm.qmax[0][0])[threadIdx.x] = 0u;  // every thread has read it; the next write follows a barrier
 
     for (int k = 0; k < nmine; ++k) {
       Fp4Stage& cur = ring[(k + 1) & 1];

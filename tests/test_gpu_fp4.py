@@ -214,3 +214,26 @@ def test_a_decode_step_from_projection_to_output(gda):
     b["k"], b["v"] = plain64.values(b["kp"], b["sc"][:, :, 0]), plain64.values(b["vp"], b["sc"][:, :, 1])
     b["q"], b["gate"] = q.cpu(), gate.cpu()
     plain64.check(out.cpu(), None, want(b), FP16, 512)
+
+
+@pytest.mark.parametrize("Hq,max_len", [(16, 0), (16, 512), (32, 0), (40, 0)])
+@pytest.mark.parametrize("value", [math.inf, math.nan, 1e30])
+def test_one_query_head_with_extreme_values(gda, Hq, max_len, value):
+    """An infinite, NaN or huge element of one query head leaves every other head as it was."""
+    b = batch([300, 65], Hq, 2, seed=19)
+    out, lse = run(gda, b, max_len=max_len)
+    head = Hq // 2 - 3
+    b["q"][1, head, 100] = value
+    out2, lse2 = run(gda, b, max_len=max_len)
+    others = [h for h in range(Hq) if h != head]
+    assert torch.equal(out2[0], out[0]) and torch.equal(out2[1, others], out[1, others])
+    assert torch.equal(lse2[1, others], lse[1, others])
+    if math.isnan(value):
+        assert torch.isnan(out2[1, head].float()).all() and torch.isnan(lse2[1, head])
+
+
+@pytest.mark.parametrize("max_len,total_len", [(10, 0), (10, 765), (1, 1), (700, 3), (5000, 10 ** 6)])
+def test_wrong_bounds_change_only_the_speed(gda, max_len, total_len):
+    b = batch([700, 65], seed=20)
+    out, lse = run(gda, b, max_len=max_len, total_len=total_len)
+    plain64.check(out, lse, want(b), FP16, 700)

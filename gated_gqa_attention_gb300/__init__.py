@@ -240,44 +240,42 @@ def _torch():
     return _th
 
 
-def _is(t, dtype, ndim, dev):
-    """Whether t is what _check_tensor wants, on device index dev (the quick test before it: these
-    calls take a few microseconds, and the checks of ten tensors have to fit in them)."""
+def _need(name, t, dtype, ndim, dev):
+    """_check_tensor for device index ``dev``, a quick test before it: these calls take a few
+    microseconds, and the checks of ten tensors have to fit in them."""
     try:
-        return t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous()
-    except AttributeError:
-        return False
-
-
-def _need(name, t, dtype, ndim, device):
-    if not _is(t, dtype, ndim, device.index):
-        _check_tensor(name, t, dtype, ndim, device)
-
-
-def _need_shape(name, t, dtype, shape, device, what):
-    """As _need, with the sizes ``what`` describes."""
-    try:
-        if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
             return
     except AttributeError:
         pass
-    _check_tensor(name, t, dtype, len(shape), device)
+    _check_tensor(name, t, dtype, ndim, _torch().device("cuda", dev))
+
+
+def _need_shape(name, t, dtype, shape, dev, what):
+    """As _need, with the sizes ``what`` describes."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check_tensor(name, t, dtype, len(shape), _torch().device("cuda", dev))
     if t.shape != shape:
         raise ValueError("%s must %s" % (name, what))
 
 
-def _cuda_index(name, t, dtype):
-    """The device index of the call's first tensor."""
+def _first(name, t, dtype, ndim):
+    """Checks a call's first tensor; the others have to be on its device, whose index this returns."""
     try:
         i = t.get_device()
+        if i >= 0 and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+            return i
     except AttributeError:
-        i = -1
-    if i < 0 or t.dtype is not dtype:
-        _check_tensor(name, t, dtype)
+        pass
+    _check_tensor(name, t, dtype, ndim)
     return i
 
 
-def _tokens(name, t, heads=None, dim=None, device=None):
+def _tokens(name, t, heads=None, dim=None, dev=None):
     """Checks a [T, H, D] bf16 CUDA tensor whose tokens may be any distance apart (the parts of
     a projection's rows) and returns that distance in elements."""
     torch = _torch()
@@ -287,8 +285,8 @@ def _tokens(name, t, heads=None, dim=None, device=None):
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if dev is not None and t.get_device() != dev:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, dev))
     if t.dim() != 3:
         raise ValueError("%s must have 3 dims" % name)
     T, H, D = t.shape
@@ -301,21 +299,19 @@ def _tokens(name, t, heads=None, dim=None, device=None):
     return st[0] if T > 1 else max(H * D, 8)
 
 
-def _check_fp4(k_pool, v_pool, kv_scales, D=None, device=None):
+def _check_fp4(k_pool, v_pool, kv_scales, D=None, dev=None):
     """Checks a 4-bit cache; returns (num_slots, Hkv)."""
-    torch = _torch()
-    u8 = torch.uint8
-    if device is None:
-        _cuda_index("k_pool", k_pool, u8)
-        device = k_pool.device
-    _need("k_pool", k_pool, u8, 3, device)
+    u8 = _torch().uint8
+    if dev is None:
+        dev = _first("k_pool", k_pool, u8, 3)
+    else:
+        _need("k_pool", k_pool, u8, 3, dev)
     n, h, half = shape = k_pool.shape
-    _need_shape("v_pool", v_pool, u8, shape, device, "have k_pool's shape")
-    kv_scales = _scale_bytes(kv_scales)
+    _need_shape("v_pool", v_pool, u8, shape, dev, "have k_pool's shape")
     what = "be [num_slots, Hkv, 2, D / 16] for pools [num_slots, Hkv, D / 2]"
     if half % 8 != 0:
         raise ValueError("kv_scales must " + what)
-    _need_shape("kv_scales", kv_scales, u8, (n, h, 2, half // 8), device, what)
+    _need_shape("kv_scales", _scale_bytes(kv_scales), u8, (n, h, 2, half // 8), dev, what)
     if D is not None and 2 * half != D:
         raise ValueError("head dims of q and the pools differ")
     return n, h
@@ -353,9 +349,7 @@ def _decode_checks(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out, kv_sca
     """Checks tensor metadata; returns the pools' element type (KV_BF16, KV_E4M3 or KV_E2M1)."""
     torch = _torch()
     bf16, i32 = torch.bfloat16, torch.int32
-    if not _is(q, bf16, 3, _cuda_index("q", q, bf16)):
-        _check_tensor("q", q, bf16, 3)
-    dev, shape = q.device, q.shape
+    dev, shape = _first("q", q, bf16, 3), q.shape
     if gate_t is not None:
         _need_shape("gate", gate_t, bf16, shape, dev, "have q's shape")
     if kv_scales is not None:
@@ -553,7 +547,7 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
     if out is None:
         out = torch.empty_like(q)
     if lse is not None:
-        _need("lse", lse, torch.float32, 2, q.device)
+        _need("lse", lse, torch.float32, 2, q.get_device())
         if kv == KV_E2M1 and lse.shape != (B, Hq):
             raise ValueError("lse must be [B, Hq]")
     if sinks is not None:
@@ -636,7 +630,7 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     [Hq, Tq] float32 or None; error_word as in prefill."""
     torch = _torch()
     sq = _tokens("q", q)
-    dev = q.device
+    dev = q.get_device()
     Tq, Hq, D = q.shape
     sg = 0
     if gate_t is not None:
@@ -662,18 +656,18 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     if lse is not None:
         _need_shape("lse", lse, torch.float32, (Hq, Tq), dev, "be [Hq, Tq]")
     if out is None:
-        out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
+        out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
     else:
         _need_shape("out", out, torch.bfloat16, (Tq, Hq, D), dev, "have q's shape")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
-    if error_word is not None and (error_word.get_device() != dev.index or error_word.element_size() != 4
+    if error_word is not None and (error_word.get_device() != dev or error_word.element_size() != 4
                                    or error_word.numel() < 1):
-        raise ValueError("error_word must be a 32-bit word on %s" % dev)
+        raise ValueError("error_word must be a 32-bit word on cuda:%d" % dev)
     a = _PackedArgs(_ptr(q), _ptr(gate_t), _ptr(k), _ptr(v), sq, sg, sk, sv, _ptr(cu_seqlens), _ptr(cu_seqlens_k),
                     _ptr(out), _ptr(lse), Tq, Tk, cu_seqlens.numel() - 1, Hq, Hkv, D, float(scale),
                     1 if causal else 0, _ptr(error_word))
-    _launch((_lib or load()).gda_prefill_packed, dev.index, stream, a)
+    _launch((_lib or load()).gda_prefill_packed, dev, stream, a)
     return out
 
 
@@ -746,7 +740,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     torch = _torch()
     bf16 = torch.bfloat16
     _check_rows("qgkv", qgkv)
-    dev = qgkv.device
+    dev = qgkv.get_device()
     T, width = qgkv.shape
     Hq, Hkv = int(Hq), int(Hkv)
     if Hq < 1 or Hkv < 1 or width % (2 * Hq + 2 * Hkv) != 0:
@@ -764,12 +758,12 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     for name, t in (("w_q_norm", w_q_norm), ("w_k_norm", w_k_norm)):
         if t is not None:
             _need_shape(name, t, bf16, (D,), dev, "have D entries")
-    outs = []
+    outs, device = [], qgkv.device
     for name, t, h in (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("gate_out", gate_out, Hq)):
         if t is not None:
             _need_shape(name, t, bf16, (T, h, D), dev, "be [T, %d, D]" % h)
         elif name != "gate_out":
-            t = torch.empty_strided((T, h, D), (h * D, D, 1), dtype=bf16, device=dev)
+            t = torch.empty_strided((T, h, D), (h * D, D, 1), dtype=bf16, device=device)
         outs.append(t)
     q_out, k_out, gate_out = outs
     num_slots, kv = 0, KV_BF16
@@ -794,7 +788,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
                    axis, rope_dim, kv, _ptr(q_out), _ptr(gate_out),
                    _ptr(k_out), _ptr(slots), num_slots, _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), float(k_descale),
                    float(v_descale), T, Hq, Hkv, D)
-    _launch((_lib or load()).gda_qk_norm_mrope_kv_write, dev.index, stream, a)
+    _launch((_lib or load()).gda_qk_norm_mrope_kv_write, dev, stream, a)
     return q_out, k_out
 
 
@@ -815,7 +809,7 @@ def kv_write_fp4(k, v, slots, k_pool, v_pool, kv_scales, k_descale: float = 1.0,
     """Quantise the rows of k and v ([T, Hkv, D] bf16, tokens any multiple of 8 elements apart)
     into a 4-bit cache at ``slots`` ([T] int32), through ``gda_kv_write_fp4``."""
     sk = _tokens("k", k)
-    (T, Hkv, D), dev = k.shape, k.device
+    (T, Hkv, D), dev = k.shape, k.get_device()
     sv = _tokens("v", v, Hkv, D, dev)
     if v.shape[0] != T:
         raise ValueError("k and v must have the same shape")
@@ -823,7 +817,7 @@ def kv_write_fp4(k, v, slots, k_pool, v_pool, kv_scales, k_descale: float = 1.0,
     num_slots, h = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
     if h != Hkv:
         raise ValueError("the pools must have Hkv heads")
-    _launch((_lib or load()).gda_kv_write_fp4, dev.index, stream, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(),
+    _launch((_lib or load()).gda_kv_write_fp4, dev, stream, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(),
             num_slots, k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), float(k_descale), float(v_descale),
             T, Hkv, D)
 
@@ -834,17 +828,18 @@ def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_
     (k, v), through ``gda_kv_gather_fp4``; an index outside the pools gives zeros."""
     torch = _torch()
     num_slots, Hkv = _check_fp4(k_pool, v_pool, kv_scales)
-    dev, D, bf16 = k_pool.device, 2 * k_pool.shape[2], torch.bfloat16
+    dev, D, bf16 = k_pool.get_device(), 2 * k_pool.shape[2], torch.bfloat16
     _need("indices", indices, torch.int32, 1, dev)
     N = indices.numel()
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             _need_shape(name, t, bf16, (N, Hkv, D), dev, "be [N, Hkv, D]")
+    device = k_pool.device
     if k_out is None:
-        k_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=dev)
+        k_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=device)
     if v_out is None:
-        v_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=dev)
-    _launch((_lib or load()).gda_kv_gather_fp4, dev.index, stream, k_pool.data_ptr(), v_pool.data_ptr(),
+        v_out = torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=device)
+    _launch((_lib or load()).gda_kv_gather_fp4, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
             kv_scales.data_ptr(), num_slots, indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(),
             v_out.data_ptr(), Hkv, D)
     return k_out, v_out

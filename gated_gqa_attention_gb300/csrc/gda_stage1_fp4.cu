@@ -395,6 +395,13 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
   bool have = sched.next(pc);
   // an idle CTA exits without the trigger, so stage 2 is placed after it has left
   if (have) pdl_launch_dependents();
+  // (a pair of groups loads Q behind its first copies, and so behind those of every CTA: it is
+  // sent to the L2 ahead of them, 51.7 -> 51.1 us for 16 heads per KV head, 8 x 32769)
+  if (NG > 1 && have && threadIdx.x < NG * kG * 4) {
+    const int kvh = pc.kvh / p.nteam, hq = (pc.kvh - kvh * p.nteam) * NG * kG + (int)(threadIdx.x >> 2);
+    const __nv_bfloat16* line = p.q + ((size_t)pc.b * p.Hq + (size_t)kvh * p.G + hq) * kD + 64 * (threadIdx.x & 3);
+    if (hq < p.G) asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+  }
   if (have) piece_head(pc);
   bool first = true;
   while (have) {

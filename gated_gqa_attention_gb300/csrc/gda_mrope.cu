@@ -37,7 +37,6 @@ namespace gda {
 namespace {
 
 constexpr int kMropeWarps = 8;   // per block
-constexpr int kMropeRows = 2;    // rows in flight per warp
 constexpr int kMropeBlocksPerSm = 4;
 
 // eight BF16 values as four FP32 pairs
@@ -181,12 +180,22 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
           for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
           rinv[j] = ss.x + ss.y;
         }
+        auto finish = [&](float sum) -> float { return (w != nullptr) ? rsqrtf(sum * (1.0f / kD) + p.eps) : 1.0f; };
+        if constexpr (N == 2) {
+          // each half warp sums one of the two rows and they swap results: 6 shuffles, not 10
+          const bool up = lane >= 16;
+          float sum = up ? rinv[1] : rinv[0];
+          sum += __shfl_xor_sync(0xffffffffu, up ? rinv[0] : rinv[1], 16);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
+          for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          const float own = finish(sum), other = __shfl_xor_sync(0xffffffffu, own, 16);
+          rinv[0] = up ? other : own;
+          rinv[1] = up ? own : other;
+        } else {
 #pragma unroll
-          for (int j = 0; j < N; ++j) rinv[j] += __shfl_xor_sync(0xffffffffu, rinv[j], off);
-#pragma unroll
-        for (int j = 0; j < N; ++j) rinv[j] = (w != nullptr) ? rsqrtf(rinv[j] * (1.0f / kD) + p.eps) : 1.0f;
+          for (int off = 16; off > 0; off >>= 1) rinv[0] += __shfl_xor_sync(0xffffffffu, rinv[0], off);
+          rinv[0] = finish(rinv[0]);
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           float2 x[4], y[4];
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
         src += N * pitch_h;
         if (dst != nullptr) dst += N * pitch_h;
       };
-      while (h + (kMropeRows - 1) * wpt < heads) rows(std::integral_constant<int, kMropeRows>());
+      while (h + wpt < heads) rows(std::integral_constant<int, 2>());
       while (h < heads) rows(std::integral_constant<int, 1>());
     }
     // v rows into the cache, gate rows out: copies (v quantised for a 4-bit cache)

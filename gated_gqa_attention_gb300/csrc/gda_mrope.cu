@@ -16,17 +16,17 @@
 //
 // Layout.  A warp takes a token's rows, with no block barrier; when fewer tokens than warps
 // are left (a decode step, the end of a prompt) the warps share the tokens' rows evenly (16383
-// tokens on 4864 warps: 71 us; with a last pass of a third of the warps 73.6).  Per token a warp takes cos and sin of every pair once (lanes stride over the
-// pairs) and reads back those of its own dimensions: lane l owns dimensions 8l .. 8l + 7
-// (one 16-byte load and store a row), the partner of a rotated dimension is in lane
-// l +- rope_dim / 16, and the norm weights are folded into cos and sin:
-//   y = rinv (x (w cos) +- x_partner (w_partner sin)),
-// so a row costs four shuffles of packed pairs and two multiply-adds per element.  Two
-// rows are in flight per warp.  FP32 arithmetic, one rounding to BF16; a 4-bit cache
-// quantises that BF16 value, so its rows equal k_out quantised.  Bound by HBM for prompts
-// (every row in once and out once: 16383 tokens of 16 + 2 heads with a BF16 cache at 5.0 TB/s;
-// more rows in flight, by registers or by prefetches into the L2, make it slower: 82 us), by
-// latency for a decode step.
+// tokens on 4864 warps: 71 us; with a last pass of a third of the warps 73.6).  Per token a warp
+// takes cos and sin of every pair once (lanes stride over the pairs) and reads back those of its
+// own dimensions: lane l owns dimensions 8l .. 8l + 7 (one 16-byte load and store a row), the
+// partner of a rotated dimension is in lane l +- rope_dim / 16 and comes by a second load of the
+// same line (69 us; by four shuffles 70), and the norm weights are folded into cos and sin:
+//   y = rinv (x (w cos) +- x_partner (w_partner sin)).
+// Two rows are in flight per warp and share the shuffles of their sums of squares.  FP32
+// arithmetic, one rounding to BF16; a 4-bit cache quantises that BF16 value, so its rows equal
+// k_out quantised.  Bound by HBM for prompts (every row in once and out once: 16383 tokens of 16
+// + 2 heads with a BF16 cache at 5.1 TB/s, 62 us with no arithmetic at all; more rows in flight,
+// by registers or by prefetches into the L2, make it slower: 82 us), by latency for a decode step.
 #include <type_traits>
 
 #include "gda_kernels.h"
@@ -164,13 +164,16 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
       uint4* dst = reinterpret_cast<uint4*>(kind ? p.k_out : p.q_out);
       if (dst != nullptr) dst += (t * heads + h) * (kD / 8) + lane;
       const long long pitch_h = (long long)wpt * (kD / 8);  // from one of the warp's heads to the next
-      // N rows at once: their loads, sums and shuffles overlap
+      // N rows at once: their loads and sums overlap
       auto rows = [&](auto count) {
         constexpr int N = decltype(count)::value;
-        uint4 raw[N];
+        uint4 raw[N], mate[N] = {};
         float rinv[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) raw[j] = __ldcs(src + j * pitch_h);
+        for (int j = 0; j < N; ++j) {
+          raw[j] = __ldcs(src + j * pitch_h);
+          if (rot) mate[j] = __ldcs(src + j * pitch_h + (partner - lane));
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           float2 x[4];
@@ -200,11 +203,7 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
         for (int j = 0; j < N; ++j) {
           float2 x[4], y[4];
           unpack(raw[j], x);
-          uint4 o;
-          o.x = __shfl_sync(0xffffffffu, raw[j].x, partner);
-          o.y = __shfl_sync(0xffffffffu, raw[j].y, partner);
-          o.z = __shfl_sync(0xffffffffu, raw[j].z, partner);
-          o.w = __shfl_sync(0xffffffffu, raw[j].w, partner);
+          const uint4 o = mate[j];
           unpack(o, y);
           uint32_t out[4];
 #pragma unroll

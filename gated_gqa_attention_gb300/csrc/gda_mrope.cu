@@ -217,7 +217,9 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
           if (dst != nullptr) dst[j * pitch_h] = o4;
           if (kind && slot_ok) {
             const size_t r = cache_row + h + j * wpt;
-            if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_pool) + r * kD)[lane] = o4;
+            // (later steps read the cache, the next kernel reads q_out and k_out: these stay in the
+            // L2 longer; 4864 tokens 19.9 -> 19.3 us)
+            if (p.pool == 1) __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_pool) + r * kD) + lane, o4);
             else store_bf16_row4(o4, p.k_factor, p.inv, p.k_pool, p.scales + r * kScalePair, r, lane);
           }
         }
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
       for (int h = (sub - (p.Hq + p.Hkv) % wpt + wpt) % wpt; h < p.Hkv; h += wpt) {
         const uint4 raw = __ldcs(row + (2LL * p.Hq + p.Hkv + h) * (kD / 8));
         const size_t r = cache_row + h;
-        if (p.pool == 1) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pool) + r * kD)[lane] = raw;
+        if (p.pool == 1) __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pool) + r * kD) + lane, raw);
         else store_bf16_row4(raw, p.v_factor, p.inv, p.v_pool, p.scales + r * kScalePair + kScaleBytes, r, lane);
       }
     }

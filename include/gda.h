@@ -500,7 +500,8 @@ int gda_qk_norm_rope_kv_write(const gda_bf16* qgkv, int64_t row_stride, const gd
  *   k_pool, v_pool  both NULL (no cache write; k_out is then required), or [num_slots, Hkv,
  *              D] bf16 (kv_dtype GDA_KV_BF16), or the codes of a 4-bit cache (GDA_KV_E2M1,
  *              with kv_scales and descales as in gda_kv_write_fp4)
- * D = 256, rope_dim a multiple of 16 up to D (0: no rotation).  One kernel, nothing allocated.
+ * The outputs lie apart from the inputs.  D = 256, rope_dim a multiple of 16 up to D (0: no
+ * rotation).  One kernel, nothing allocated.
  */
 typedef struct gda_mrope_args {
     const gda_bf16* qgkv;

@@ -142,3 +142,32 @@ def test_captured(gda):
 def test_more_tokens_than_warps(gda, T, Hq, Hkv, pool):
     """Several passes of the grid; in the last one the warps share the tokens that are left."""
     test_matches_float64(gda, T, Hq, Hkv, 64, 3, True, pool)
+
+
+@pytest.mark.parametrize("side", ["q", "k"])
+def test_one_norm_and_more_kv_heads_than_query_heads(gda, side):
+    T, Hq, Hkv = 37, 2, 5
+    qgkv, pos, inv, axis, wq, wk = make(T, Hq, Hkv, 32, 2, seed=6)
+    wq, wk = (wq, None) if side == "q" else (None, wk)
+    c = lambda t: None if t is None else t.cuda()
+    gate = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q, k = gda.qk_norm_mrope_kv_write(qgkv.cuda(), pos.cuda(), inv.cuda(), axis, Hq, Hkv, w_q_norm=c(wq), w_k_norm=c(wk),
+                                      gate_out=gate)
+    rq, rg, rk, _ = reference(qgkv, pos, inv, axis, Hq, Hkv, wq, wk)
+    near(q, rq, 32)
+    near(k, rk, 32)
+    assert torch.equal(gate.cpu(), rg)
+
+
+def test_many_axes(gda):
+    """Every pair on an axis of its own, the last of 128 axes among them."""
+    T, Hq, Hkv = 9, 1, 1
+    qgkv, _, _, _, wq, wk = make(T, Hq, Hkv, 256, 2, seed=8)
+    g = torch.Generator().manual_seed(9)
+    pos = torch.randint(-1000, 100000, (128, T), generator=g, dtype=torch.int32)
+    inv = (1e4 ** (-torch.arange(0, 256, 2) / 256)).float()
+    axis = list(range(127, -1, -1))
+    q, k = gda.qk_norm_mrope_kv_write(qgkv.cuda(), pos.cuda(), inv.cuda(), axis, Hq, Hkv, w_q_norm=wq.cuda(), w_k_norm=wk.cuda())
+    rq, _, rk, _ = reference(qgkv, pos, inv, axis, Hq, Hkv, wq, wk)
+    near(q, rq, 256)
+    near(k, rk, 256)

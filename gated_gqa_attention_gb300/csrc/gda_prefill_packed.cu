@@ -38,9 +38,10 @@
 //    drains the tensor pipe, so S and PV have threads of their own).
 //  * warps 0-7: softmax.  Warps w and w + 4 share query rows 32 w .. + 31, 64 of a tile's 128
 //    scores each; they agree on the row max through shared memory and keep a running max
-//    (moved lazily, by more than 2^8; O is then rescaled in TMEM) and sum.  P is rounded to
-//    BF16 for the MMA (2^-8 relative, as the values it weighs); the sum adds the FP32
-//    probabilities before that rounding, so lse does not see it.  Before the last tile's PV
+//    (moved lazily, by more than 2^8; O is then rescaled in TMEM) and two sums.  P is rounded
+//    to BF16 for the MMA (2^-8 relative, as the values it weighs); O is divided by the sum of
+//    the rounded probabilities, so that a row's weights add up to 1 and the rounding of its
+//    largest one cancels, and lse takes the sum before the rounding.  Before the last tile's PV
 //    they zero the V rows past the sequence's end (rows of the next sequence: a NaN there
 //    times a probability of 0 would be NaN).
 //  * their epilogue: while the last PV runs, the sigmoids of 16 whole rows per warp (the gate
@@ -78,7 +79,8 @@ constexpr uint32_t kOffK = kOffQ + 4 * kBlk;
 constexpr uint32_t kOffV = kOffK + kKSlots * kHalf;
 constexpr uint32_t kOffX = kOffV + 2 * kHalf;      // row max exchange [parity][half][row]; an item's
                                                    // sums take the parity its last tile did not
-constexpr uint32_t kOffBar = kOffX + 2048;
+constexpr uint32_t kOffE = kOffX + 2048;           // second halves' sums for lse [row]
+constexpr uint32_t kOffBar = kOffE + 512;
 constexpr uint32_t kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   Bars& bars = *reinterpret_cast<Bars*>(sm + kOffBar);
   float* xbuf = reinterpret_cast<float*>(sm + kOffX);
+  float* ebuf = reinterpret_cast<float*>(sm + kOffE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -380,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const __nv_bfloat16* gate_w = p.gate + (long long)(t.s.q0 + i0 + w0) * p.gate_stride + (long long)t.h * kD;
       if (p.fuse_gate && lane < nrow)  // their gate on its way to the L2 while the item is computed
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gate_w + lane * p.gate_stride), "r"(2 * kD) : "memory");
-      float m_run = -INFINITY, l_run = 0.0f;  // running row max (log2 units) and sum
+      // running row max (log2 units), the sum of the probabilities as the MMA multiplies them (the
+      // weights of a row add up to 1), and their sum before that rounding (for lse)
+      float m_run = -INFINITY, l_run = 0.0f, e_run = 0.0f;
 #pragma unroll 1
       for (int j = 0; j < t.ntiles; ++j, ++T) {
         const int sb = T & 1, ph = T >> 1;
@@ -424,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mx > m_run + 8.0f) {
           alpha = (m_run == -INFINITY) ? 0.0f : exp2f(m_run - mx);
           l_run *= alpha;
+          e_run *= alpha;
           m_run = mx;
         }
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -442,21 +448,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        // p = 2^(s * scale_log2 - m): one FFMA and one SFU op per score (a masked score gives
+        // p = 2^(s * scale_log2 - m): half a packed FFMA and one SFU op per score (a masked score gives
         // 2^-inf = 0; a row with no visible key yet uses m = 0); P (BF16 pairs) over the first
         // half of the S buffer: keys 64 h .. at columns 32 h ..
         const float mneg = (m_run == -INFINITY) ? 0.0f : -m_run;
         uint32_t w[32];
-        float la = 0.0f, lb = 0.0f;
+        float2 l2 = make_float2(0.0f, 0.0f), e2 = l2;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float p0 = ex2_approx(fmaf(s[2 * e], p.scale_log2, mneg));
-          const float p1 = ex2_approx(fmaf(s[2 * e + 1], p.scale_log2, mneg));
-          w[e] = bf16x2_rn(p0, p1);
-          la += p0;
-          lb += p1;
+          const float2 a = fma_f32x2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(p.scale_log2, p.scale_log2),
+                                     make_float2(mneg, mneg));
+          const float2 x = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+          w[e] = bf16x2_rn(x.x, x.y);
+          e2 = add_f32x2(e2, x);
+          l2 = add_f32x2(l2, make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
         }
-        l_run += la + lb;
+        l_run += l2.x + l2.y;
+        e_run += e2.x + e2.y;
         tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc, w);
         tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc + 16, w + 16);
         tmem_wait_st();
@@ -504,13 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the row's sum is its two halves' sums: exchanged in the slots of the parity that the
         // last tile did not use (both halves read them before that tile's exchange)
         xbuf[((T & 1) * 2 + hc) * kPM + r] = l_run;
+        if (hc == 1) ebuf[r] = e_run;  // (the first half writes lse)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.pr[rg]);
         ok = __all_sync(0xffffffffu, wait(&bars.pr[rg], 2 * it));
         if (!ok) break;
         const float l = xbuf[(T & 1) * 2 * kPM + r] + xbuf[((T & 1) * 2 + 1) * kPM + r];
-        if (p.lse && hc == 0 && qi < t.s.nq)
-          p.lse[(size_t)t.h * p.Sq + t.s.q0 + qi] = (l == 0.0f) ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
+        if (p.lse && hc == 0 && qi < t.s.nq) {
+          const float e = e_run + ebuf[r];
+          p.lse[(size_t)t.h * p.Sq + t.s.q0 + qi] = (e == 0.0f) ? -INFINITY : (m_run + log2f(e)) * 0.69314718055994530942f;
+        }
         const float inv = (l > 0.0f) ? 1.0f / l : 0.0f;  // (a NaN sum comes with NaN in O)
         ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
         if (!ok) break;

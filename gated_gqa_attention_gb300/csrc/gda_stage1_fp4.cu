@@ -33,9 +33,10 @@
 //    dimension's code of both tokens -- four registers per two selects -- and the scale
 //    pair is (scale of T0, scale of T1).  Row g of m-tile mt is dim 32g + 2mt, row g + 8 the
 //    next one.
-//  * P is rounded to FP16 for the MMA (it lies in [0, 2^8], 2^-11 relative, against the
-//    4-bit V it multiplies) and its sum is kept in FP32 before the rounding, so the LSE
-//    does not see it.
+//  * P is rounded to FP16 for the MMA (it lies in [0, 2^8]: 2^-11 relative, 2^-25 absolute
+//    below 2^-14, against the 4-bit V it multiplies).  O is divided by the FP32 sum of the
+//    rounded values, so that a head's weights add up to 1; the LSE takes the FP32 sum before
+//    the rounding.
 //  * With more than 8 query heads per KV head, pairs of groups share one read of the rows and
 //    one widening of the codes (16 heads, 8 x 32769 positions: 84 -> 58 us).
 //  * Merge: as in the e4m3 kernel -- each warp leaves its rescaled O^T fragments in ring
@@ -66,7 +67,8 @@ struct Fp4Smem {
   uint2 qf[NG][16][32];           // Q^T fragments (FP16, scaled), lane order
   Fp4Stage ring[W][2];            // per-warp rings; stage 0 also holds the merge slice
   float mbuf[W][kG];              // each warp's running max
-  float lsum[W][kG];              // each warp's rescaled sum
+  float lsum[W][kG];              // each warp's rescaled sum of the rounded probabilities
+  float esum[W][kG];              // and of those before the rounding (for the LSE)
   unsigned int qmax[NG][kG];      // largest |q| of each head of the piece (float bits)
 };
 static_assert(sizeof(float4) * 16 * 32 <= sizeof(Fp4Stage), "merge slice fits a ring stage");
@@ -151,7 +153,8 @@ __device__ __forceinline__ void issue_tile(Fp4Stage& st, const KvRows& r, int sl
 template <int NG>
 struct Fp4WarpState {
   float o[NG][16][4];
-  float m[NG][2], l[NG][2];  // heads 2t, 2t + 1 of each group
+  float m[NG][2], l[NG][2], e[NG][2];  // heads 2t, 2t + 1 of each group: maximum, sum after
+                                       // and before the rounding of P
   uint32_t P[NG][4];         // FP16 probabilities, P[.][j] = tokens g + 8j, heads (2t, 2t+1)
 
   __device__ __forceinline__ void reset() {
@@ -162,7 +165,7 @@ struct Fp4WarpState {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
       m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.0f;
+      l[n][0] = l[n][1] = e[n][0] = e[n][1] = 0.0f;
     }
   }
 
@@ -247,6 +250,8 @@ struct Fp4WarpState {
         const float aa = safe_exp2_diff(m[n][0], na), ab = safe_exp2_diff(m[n][1], nb);
         l[n][0] *= aa;
         l[n][1] *= ab;
+        e[n][0] *= aa;
+        e[n][1] *= ab;
         m[n][0] = na;
         m[n][1] = nb;
 #pragma unroll
@@ -263,8 +268,11 @@ struct Fp4WarpState {
       for (int j = 0; j < 4; ++j) {
         const float pa = ex2(s[2 * j] - ra), pb = ex2(s[2 * j + 1] - rb);
         P[n][j] = pack_f16(pa, pb);
-        l[n][0] += pa;
-        l[n][1] += pb;
+        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&P[n][j]));
+        l[n][0] += r.x;
+        l[n][1] += r.y;
+        e[n][0] += pa;
+        e[n][1] += pb;
       }
     }
   }
@@ -484,6 +492,8 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
       for (int off = 4; off < 32; off <<= 1) {
         st.l[n][0] += __shfl_xor_sync(0xffffffffu, st.l[n][0], off);
         st.l[n][1] += __shfl_xor_sync(0xffffffffu, st.l[n][1], off);
+        st.e[n][0] += __shfl_xor_sync(0xffffffffu, st.e[n][0], off);
+        st.e[n][1] += __shfl_xor_sync(0xffffffffu, st.e[n][1], off);
       }
       if (lane < 4) {
         sm.mbuf[warp][ha] = st.m[n][0];
@@ -507,6 +517,8 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
         if (lane < 4) {
           sm.lsum[warp][ha] = st.l[n][0] * fa;
           sm.lsum[warp][hb] = st.l[n][1] * fb;
+          sm.esum[warp][ha] = st.e[n][0] * fa;
+          sm.esum[warp][hb] = st.e[n][1] * fb;
         }
       }
       __syncthreads();
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(W * 32, kFp4CtasPerSm) stage1_fp4_kernel(Stage
 #pragma unroll
         for (int x = 1; x < W; ++x) M = fmaxf(M, sm.mbuf[x][threadIdx.x]);
 #pragma unroll
-        for (int x = 0; x < W; ++x) lt += sm.lsum[x][threadIdx.x];
+        for (int x = 0; x < W; ++x) lt += sm.esum[x][threadIdx.x];
         // (stage 2 takes the largest LSE as its reference: +inf carries a NaN through it)
         p.lse_part[id * kG + threadIdx.x] = (lt > 0.0f) ? M + log2f(lt) : (lt == 0.0f) ? -INFINITY : INFINITY;
       }

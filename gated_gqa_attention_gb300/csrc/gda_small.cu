@@ -38,12 +38,14 @@ struct SmallSmem {
   unsigned char v[2][kChunk][kSmemRow];  // ldmatrix), V rows; two buffers
   uint32_t p[kG][kChunk / 2];            // P of the chunk: BF16 pairs [head][position pair]
   float wmax[kSW][kG];                   // per warp and head: max of the warp's 8 scores
-  float wsum[kSW][kG];                   // per warp and head: sum of its BF16 probabilities
+  float wsum[kSW][kG];                   // per warp and head: sum of its rounded probabilities
+  float wexact[kSW][kG];                 // and of those before the rounding (4-bit rows, for lse)
   // incoming states, slot (g / C) * C + x: CTA x's unnormalised O of query head g of the
   // group (finalised by CTA g % C), its running max (log2 units) and sum
   float o[kG][kD];
   float m[kG];
   float l[kG];
+  float e[kG];                           // the sum before the rounding (4-bit rows)
 };
 constexpr size_t kSmallSmem = sizeof(SmallSmem);
 
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
     if (nch > 1) load_chunk(1);
   }
 
-  float m_run = -INFINITY, l_run = 0.0f;  // head h (identical in every thread of row h)
+  float m_run = -INFINITY, l_run = 0.0f, e_run = 0.0f;  // head h (identical in every thread of row h)
   float oacc[4][4];                        // O of head h, dims 32 warp + 8 nt + 2 qd .. (c0, c1)
 #pragma unroll
   for (int nt = 0; nt < 4; ++nt)
@@ -338,18 +340,28 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
       p0 = safe_exp2_diff(s0, m_new);
       p1 = safe_exp2_diff(s1, m_new);
     }
-    // P rounded to the MMA's type; the sum adds the rounded values the MMA uses
+    // P rounded to the MMA's type; the sum adds the rounded values the MMA uses (4-bit rows:
+    // lse takes a second one, before the rounding)
     const uint32_t pp = F8 ? f16x2_rn(p0, p1) : pack_bf16x2(p0, p1);
     sm.p[h][4 * warp + qd] = pp;
-    const float ws = quad_sum(KV == 2 ? (p0 + p1)  // (4-bit: the sum before the rounding)
-                              : F8 ? (f16_lo(pp) + f16_hi(pp))
+    const float ws = quad_sum(F8 ? (f16_lo(pp) + f16_hi(pp))
                                  : (__uint_as_float(pp << 16) + __uint_as_float(pp & 0xFFFF0000u)));
     if (qd == 0) sm.wsum[warp][h] = ws;
+    if (KV == 2) {
+      const float we = quad_sum(p0 + p1);
+      if (qd == 0) sm.wexact[warp][h] = we;
+    }
     __syncthreads();
     float csum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kSW; ++w) csum += sm.wsum[w][h];
     l_run = l_run * alpha + csum;
+    if (KV == 2) {
+      float cexact = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) cexact += sm.wexact[w][h];
+      e_run = e_run * alpha + cexact;
+    }
     m_run = m_new;
 
     // O += P V over the chunk's 64 positions, this warp's 32 dims (4 n-tiles)
@@ -400,6 +412,7 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
     if (warp == 0 && qd == 0) {
       st_cluster_f32(cluster_addr(&sm.m[slot], dst), m_run);
       st_cluster_f32(cluster_addr(&sm.l[slot], dst), l_run);
+      if (KV == 2) st_cluster_f32(cluster_addr(&sm.e[slot], dst), e_run);
     }
   }
   uint16_t sig[kFin];
@@ -420,22 +433,26 @@ __global__ void __launch_bounds__(kSW * 32, 1) small_decode_kernel(SmallParams p
     float M = sink2;
 #pragma unroll
     for (int x = 0; x < C; ++x) M = fmaxf(M, sm.m[k * C + x]);
-    float acc = 0.0f, W = 0.0f;
+    float acc = 0.0f, W = 0.0f, E = 0.0f;  // (E: W with the sums before the rounding, for lse)
     if (M != -INFINITY) {
 #pragma unroll
       for (int x = 0; x < C; ++x) {
         const float f = safe_exp2_diff(sm.m[k * C + x], M);
         acc = fmaf(sm.o[k * C + x][tid], f, acc);
         W = fmaf(sm.l[k * C + x], f, W);
+        if (KV == 2) E = fmaf(sm.e[k * C + x], f, E);
       }
-      if (sink2 != -INFINITY) W += exp2f(sink2 - M);
+      if (sink2 != -INFINITY) {
+        W += exp2f(sink2 - M);
+        if (KV == 2) E += exp2f(sink2 - M);
+      }
       acc = F8 ? acc * p.v_descale / W : acc / W;
     }
     const uint16_t ob = float_to_bf16_bits(acc);
     const size_t row = ((size_t)b * p.Hq + hf) * kD;
     reinterpret_cast<uint16_t*>(p.out)[row + tid] = p.fuse_gate ? gate_product_bf16(ob, sig[k]) : ob;
     if (p.lse_out != nullptr && tid == 0)
-      p.lse_out[(size_t)b * p.Hq + hf] = (M == -INFINITY) ? -INFINITY : (M + log2f(W)) * 0.69314718055994530942f;
+      p.lse_out[(size_t)b * p.Hq + hf] = (M == -INFINITY) ? -INFINITY : (M + log2f(KV == 2 ? E : W)) * 0.69314718055994530942f;
   }
 }
 

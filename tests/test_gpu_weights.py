@@ -38,6 +38,7 @@ BORDER = 1.0 + 2.0 ** -8
     ([700, 33, 1, 2000], 16, {}),                                  # the split path
     ([700, 33, 1, 2000], 16, dict(num_splits=3)),
     ([700, 33, 1, 2000], 32, {}),                                  # pairs of groups
+    ([700, 33, 1, 600], 16, dict(max_len=700)),                    # one cluster kernel
 ])
 @pytest.mark.parametrize("std", [0.3, 1.0, 3.0])
 def test_decode_over_a_4bit_cache(gda, lens, hq, kw, side, want, std):

@@ -217,8 +217,8 @@ def workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_splits: int = 0) -> i
 
 def workspace_init(workspace, stream=None):
     """Zero a caller-owned workspace's header (its device error word)."""
-    _check(load().gda_workspace_init(ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(),
-                                     _stream(stream)))
+    _launch(load().gda_workspace_init, workspace.get_device(), stream, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
 
 
 def reserve(max_B: int, Hq: int = 16, Hkv: int = 2, D: int = 256, max_splits: int = 0):

@@ -10,9 +10,10 @@
 // The angle.  pos * inv_freq in FP32 is off by up to pos * 2^-24 turns' worth of radians
 // (0.06 at position 10^6), and FP64 runs at a few operations per clock and SM here.  So
 // each frequency is held as a 64-bit fraction of a turn, F = frac(inv_freq / 2 pi) 2^64,
-// taken once per block: (pos * F) mod 2^64 is the position on the circle with every whole
-// turn dropped by the integer wrap, its upper 32 bits go to sincospi, and the error stays
-// below 2^-25 turns at any 32-bit position.
+// taken once per block to the last bit or two: (pos * F) mod 2^64 is the position on the circle
+// with every whole turn dropped by the integer wrap.  Its upper 32 bits, off by 2^-31 turns at
+// most at any 32-bit position, go to sincospi as FP32 half turns, whose rounding is 2^-25 of a
+// half turn at most: the angle is within 2^-23 radians for frequencies below 2^64.
 //
 // Layout.  A warp takes a token's rows, with no block barrier; when fewer tokens than warps
 // are left (a decode step, the end of a prompt) the warps share the tokens' rows evenly (16383
@@ -78,19 +79,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return d;
 }
 
-// frac(f / 2 pi) * 2^64 modulo 2^64, from f = m 2^-s by one 24 x 64 bit product with
-// floor(2^64 / 2 pi) (FP64 arithmetic would cost every warp more than the rest of its start).
+// frac(f / 2 pi) * 2^64 modulo 2^64, from f = m 2^-s by a 24 x 128 bit product with
+// floor(2^128 / 2 pi): the product is off by less than 2^24, and its bits from 2^(64 + s) on are
+// the result, which is therefore off by less than 2 for |f| < 2^64 (s >= -40).  (FP64 arithmetic
+// would cost every warp more than the rest of its start.)
 __device__ __forceinline__ unsigned long long turn_fraction(float f) {
   const uint32_t b = __float_as_uint(f);
   const int e = (int)((b >> 23) & 0xFFu);
   const unsigned long long m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
   const int s = 150 - (e ? e : 1);
-  constexpr unsigned long long kInv2Pi = 0x28BE60DB9391054AULL;
-  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  constexpr unsigned long long kHigh = 0x28BE60DB9391054AULL, kLow = 0x7F09D5F47D4D3770ULL;
+  // words of the product: w0 | w1 | w2, from the lowest
+  const unsigned long long w0 = m * kLow, t = __umul64hi(m, kLow);
+  const unsigned long long w1 = m * kHigh + t, w2 = __umul64hi(m, kHigh) + (w1 < t ? 1ull : 0ull);
   unsigned long long r;
-  if (s <= 0) r = -s < 64 ? lo << -s : 0ull;
-  else if (s < 64) r = (lo >> s) | (hi << (64 - s));
-  else r = s < 128 ? hi >> (s - 64) : 0ull;
+  if (s < 0) r = s > -64 ? (w1 << -s) | (w0 >> (64 + s)) : 0ull;
+  else if (s == 0) r = w1;
+  else if (s < 64) r = (w1 >> s) | (w2 << (64 - s));
+  else r = s < 128 ? w2 >> (s - 64) : 0ull;
   return (b >> 31) ? 0ull - r : r;
 }
 

@@ -490,7 +490,8 @@ int gda_qk_norm_rope_kv_write(const gda_bf16* qgkv, int64_t row_stride, const gd
  * gda_kv_write_fp4 does for GDA_KV_E2M1).  rmsnorm as in gda_qk_norm_rope_kv_write; rope
  * turns pair i = (dimension i, dimension i + rope_dim / 2), 0 <= i < rope_dim / 2, by
  *   positions[pair_axis[i], t] * inv_freq[i]   radians,
- * the angle exact to about 2^-24 at any int32 position.  FP32 arithmetic, one RNE
+ * the angle, less whole turns, within 2^-23 radians at any int32 position for frequencies
+ * below 2^64 in magnitude.  FP32 arithmetic, one RNE
  * rounding to bf16.
  *   qgkv       [T, row_stride] bf16, row_stride >= (2 Hq + 2 Hkv) D, a multiple of 8
  *   positions  [n_axes, T] int32, axis a at positions + a * pos_stride

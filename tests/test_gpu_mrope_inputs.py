@@ -1,0 +1,47 @@
+"""The rotary step: large frequencies at far positions."""
+from fractions import Fraction
+
+import pytest
+import torch
+
+import plain64
+from test_gpu_mrope import make, near
+
+D = 256
+PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679, 10 ** 100)
+
+
+def angles(pos, inv, axis):
+    """positions[axis[i], t] * inv_freq[i] less whole turns, exactly (float64 would lose it): [T, pairs]."""
+    rows = []
+    for t in range(pos.shape[1]):
+        row = []
+        for i, a in enumerate(axis):
+            x = Fraction(int(pos[a, t])) * Fraction(float(inv[i])) / (2 * PI)
+            row.append(float((x - round(x)) * 2 * PI))
+        rows.append(row)
+    return torch.tensor(rows, dtype=torch.float64)
+
+
+def test_the_exact_angle_itself():
+    pos, inv = torch.tensor([[3, -7, 100]], dtype=torch.int32), torch.tensor([0.5, 1.25])
+    want = torch.remainder(pos[0].double()[:, None] * inv.double() + torch.pi, 2 * torch.pi) - torch.pi
+    assert (angles(pos, inv, [0, 0]) - want).abs().max() < 1e-12
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [1.0, 1e3, 1e6, 2.0 ** 24, 3e9, 2.0 ** 45, 1e19])
+def test_large_frequencies_at_far_positions(gda, size):
+    """The angle is a 64-bit fraction of a turn at every frequency, not at those below 1 alone."""
+    T, Hq, Hkv = 10, 4, 1
+    qgkv, _, _, _, wq, wk = make(T, Hq, Hkv, 128, 2, seed=3)
+    g = torch.Generator().manual_seed(5)
+    inv = (size * (0.5 + 0.5 * torch.rand(64, generator=g))).float() * torch.where(torch.arange(64) % 5 == 0, -1.0, 1.0)
+    pos = torch.randint(-2 ** 31, 2 ** 31, (2, T), generator=g).to(torch.int32)
+    pos[0, :4] = torch.tensor([2 ** 31 - 1, -(2 ** 31), 0, 1], dtype=torch.int32)
+    axis = [i % 2 for i in range(64)]
+    q, k = gda.qk_norm_mrope_kv_write(qgkv.cuda(), pos.cuda(), inv.cuda(), axis, Hq, Hkv, w_q_norm=wq.cuda(), w_k_norm=wk.cuda())
+    x = qgkv.reshape(T, 2 * Hq + 2 * Hkv, D)
+    ang = angles(pos, inv, axis)
+    near(q, plain64.norm_rope(x[:, :Hq], wq, 1e-6, ang), 128)
+    near(k, plain64.norm_rope(x[:, 2 * Hq:2 * Hq + Hkv], wk, 1e-6, ang), 128)

@@ -745,6 +745,16 @@ def mrope_pair_axis(sections, interleaved: bool = False):
     return axis
 
 
+def _axis_bytes(pair_axis) -> bytes:
+    """One byte per pair.  (bytes() of a number is that many zeros, and of an array its memory.)"""
+    if isinstance(pair_axis, bytes):
+        return pair_axis
+    try:
+        return bytes(list(pair_axis))
+    except TypeError:
+        raise TypeError("pair_axis must be a sequence of axis numbers") from None
+
+
 def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: int, w_q_norm=None, w_k_norm=None,
                            eps: float = 1e-6, q_out=None, k_out=None, gate_out=None, slots=None, k_pool=None,
                            v_pool=None, kv_scales=None, k_descale: float = 1.0, v_descale: float = 1.0, stream=None):
@@ -765,7 +775,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
     if Hq < 1 or Hkv < 1 or width % (2 * Hq + 2 * Hkv) != 0:
         raise ValueError("qgkv's rows must hold (2 Hq + 2 Hkv) * D elements")
     D = width // (2 * Hq + 2 * Hkv)
-    axis = bytes(pair_axis)
+    axis = _axis_bytes(pair_axis)
     rope_dim = 2 * len(axis)
     if rope_dim:
         _need("positions", positions, torch.int32, 2, dev)

@@ -1,9 +1,10 @@
-"""The rotary step: large frequencies at far positions."""
+"""The rotary step: large frequencies at far positions, the forms of pair_axis."""
 from fractions import Fraction
 
 import pytest
 import torch
 
+import gated_gqa_attention_gb300 as gda_module
 import plain64
 from test_gpu_mrope import make, near
 
@@ -45,3 +46,30 @@ def test_large_frequencies_at_far_positions(gda, size):
     ang = angles(pos, inv, axis)
     near(q, plain64.norm_rope(x[:, :Hq], wq, 1e-6, ang), 128)
     near(k, plain64.norm_rope(x[:, 2 * Hq:2 * Hq + Hkv], wk, 1e-6, ang), 128)
+
+
+def test_the_bytes_of_pair_axis():
+    import numpy as np
+    for form in (b"\x02\x00\x01", [2, 0, 1], (2, 0, 1), np.array([2, 0, 1]), torch.tensor([2, 0, 1]), range(2, -1, -1)):
+        assert sorted(gda_module._axis_bytes(form)) == [0, 1, 2]
+    for bad in (3, 0, None, "012", 1.5):
+        with pytest.raises(TypeError, match="pair_axis must be a sequence"):
+            gda_module._axis_bytes(bad)
+    for bad in ([-1], [256]):
+        with pytest.raises(ValueError):
+            gda_module._axis_bytes(bad)
+
+
+@pytest.mark.gpu
+def test_pair_axis_is_a_sequence_of_axes(gda):
+    """A number is not taken as that many zeros; sequences of any kind of integer are read by their values."""
+    import numpy as np
+    qgkv, pos, inv, axis, _, _ = make(5, 2, 1, 64, 3, seed=7)
+    call = lambda a: gda.qk_norm_mrope_kv_write(qgkv.cuda(), pos.cuda(), inv.cuda(), a, 2, 1)
+    ref = call(axis)
+    for form in (bytes(axis), tuple(axis), np.array(axis), np.array(axis, dtype=np.uint8), torch.tensor(axis)):
+        assert all(torch.equal(a, b) for a, b in zip(call(form), ref))
+    with pytest.raises(TypeError):
+        call(32)
+    with pytest.raises((TypeError, ValueError)):
+        call([-1] * 32)

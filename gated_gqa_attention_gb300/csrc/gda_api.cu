@@ -221,7 +221,9 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
     ps.scale_log2 = codes ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
                         : a->scale * 1.44269504088896340736f;
     ps.kv = a->kv_dtype == GDA_KV_E2M1 ? 2 : codes ? 1 : 0;
-    ps.scales = a->kv_scales;
+    // (the struct's last field is read for the caches that have it: a caller built with a header
+    // before it passes a shorter struct)
+    ps.scales = a->kv_dtype == GDA_KV_E2M1 ? a->kv_scales : nullptr;
     ps.v_descale = codes ? a->v_descale : 1.0f;
     ps.window = a->window;
     ps.fuse_gate = a->fuse_gate ? 1 : 0;
@@ -310,7 +312,7 @@ int enqueue(const gda_args* a, void* ws, cudaStream_t stream) {
   p1.scale_log2 = fp8 || fp4 ? (float)((double)a->scale * (double)a->k_descale * 1.4426950408889634074)
                       : a->scale * 1.44269504088896340736f;
   p1.v_descale = fp8 || fp4 ? a->v_descale : 1.0f;
-  p1.scales = a->kv_scales;
+  p1.scales = fp4 ? a->kv_scales : nullptr;
   p1.num_splits = splits;
   p1.min_chunk = min_chunk;
   // automatic stream schedule with more segments than CTAs: a segment start costs a CTA

@@ -581,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
       // ---------------- items, and the TMA loads of Q and of K's halves: half N of the stream
       // goes into slot N % 3 once the MMAs that read the slot's previous half have completed
-      const int G = (int)gridDim.x, c = (int)blockIdx.x;
+      const uint32_t G = gridDim.x, c = blockIdx.x;
       int it = 0, slot = 0, use = 0, armed[kKSlots] = {}, armed_q = 0;  // slot = N % 3, use = N / 3
       Finder finder;
       const int gsz = p.Hq / p.Hkv;  // query heads per KV head
       bool ok = true;
       auto item_at = [&](int i) -> Item {
         Item t = {-1, 0, {0, 0, 0, 0}, 0, 0};
-        const uint32_t x = (uint32_t)(i * G + ((i & 1) ? G - 1 - c : c));  // (below bound + G < 2^32)
+        const uint32_t x = (uint32_t)i * G + ((i & 1) ? G - 1 - c : c);  // (below bound + 2 G < 2^32)
         if (x < bound) {
           const uint32_t rank = x / (uint32_t)p.Hq;
           t = finder.find(p, (int)rank);

@@ -1,4 +1,5 @@
-"""The rotary step: large frequencies at far positions, the forms of pair_axis."""
+"""The rotary step: large frequencies at far positions, the forms of pair_axis, keys that go only into the cache."""
+import ctypes
 from fractions import Fraction
 
 import pytest
@@ -73,3 +74,28 @@ def test_pair_axis_is_a_sequence_of_axes(gda):
         call(32)
     with pytest.raises((TypeError, ValueError)):
         call([-1] * 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv4", [False, True])
+def test_keys_into_the_cache_alone(gda, kv4):
+    """The C entry without k_out: the same cache rows and queries as with it."""
+    T, Hq, Hkv, n = 21, 4, 2, 30
+    qgkv, pos, inv, axis, wq, wk = (x.cuda() if isinstance(x, torch.Tensor) else x for x in make(T, Hq, Hkv, 64, 3, seed=9))
+    qgkv = qgkv.contiguous()
+    slots = torch.randperm(n)[:T].to(torch.int32).cuda()
+    shape, dt = ((n, Hkv, D // 2), torch.uint8) if kv4 else ((n, Hkv, D), torch.bfloat16)
+    pools = [[torch.zeros(shape, dtype=dt, device="cuda") for _ in range(2)] + [torch.zeros(n, Hkv, 2, 16, dtype=torch.uint8, device="cuda")]
+             for _ in range(2)]
+    kw = dict(kv_scales=pools[0][2]) if kv4 else {}
+    q, _ = gda.qk_norm_mrope_kv_write(qgkv, pos, inv, axis, Hq, Hkv, w_q_norm=wq, w_k_norm=wk, slots=slots, k_pool=pools[0][0],
+                                      v_pool=pools[0][1], **kw)
+    q2 = torch.empty_like(q)
+    a = gda._MropeArgs(qgkv=qgkv.data_ptr(), row_stride=qgkv.shape[1], w_q_norm=wq.data_ptr(), w_k_norm=wk.data_ptr(), eps=1e-6,
+                       n_axes=3, positions=pos.data_ptr(), pos_stride=T, inv_freq=inv.data_ptr(), pair_axis=bytes(axis), rope_dim=64,
+                       kv_dtype=gda.KV_E2M1 if kv4 else gda.KV_BF16, q_out=q2.data_ptr(), slots=slots.data_ptr(), num_slots=n,
+                       k_pool=pools[1][0].data_ptr(), v_pool=pools[1][1].data_ptr(),
+                       kv_scales=pools[1][2].data_ptr() if kv4 else None, k_descale=1.0, v_descale=1.0, T=T, Hq=Hq, Hkv=Hkv, D=D)
+    assert gda.load().gda_qk_norm_mrope_kv_write(a, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(q2, q) and all(torch.equal(x, y) for x, y in zip(*pools))

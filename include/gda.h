@@ -152,7 +152,8 @@ typedef enum gda_status {
  *               below an actual length still gives the right result, only slower.
  *   total_len   0, or the batch's exact number of KV positions (kv_indptr[B]) known on
  *               the host.  With max_len > 0 too, automatic splits and no window, the
- *               split count is chosen on the host (gda_auto_splits with lmax = max_len)
+ *               split count is chosen on the host (gda_auto_splits with lmax = max_len, and
+ *               its variant for an e4m3 or 4-bit cache)
  *               and uniform splits launch as explicit ones: no scan of kv_indptr on the
  *               device and no idle CTAs.  A wrong value changes only the speed.
  *   kv_scales   GDA_KV_E2M1: the pools' scales [num_slots, Hkv, 2, D / 16] (16-byte
@@ -400,8 +401,9 @@ int gda_small_path_cluster(int64_t pairs, int max_len);
  *    sequence is more than 1.25 x the mean.
  * An e4m3 cache streams a position in half the time: its variant of the rule takes
  * 16 S^2 > lmax and moves to the stream from 6144 positions per CTA.  So does a 4-bit
- * cache's, which besides cuts every sequence into as many pieces as fill one wave when
- * that keeps 95 % of the CTAs busy, at any length. */
+ * cache's, whose grid is two CTAs per SM.  Besides, where one wave of equal pieces keeps
+ * 95 % of those CTAs busy and S would be at least that many, S is that many, at any number
+ * of positions per CTA. */
 int gda_auto_splits(int B, int heads, int grid, int min_chunk, int lmax, int64_t total);
 
 /* Byte layout of one decode step's inputs packed into a single block, as

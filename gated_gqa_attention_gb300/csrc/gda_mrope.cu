@@ -32,6 +32,7 @@
 
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
+#include "gda_tc.cuh"
 
 namespace gda {
 
@@ -46,23 +47,6 @@ __device__ __forceinline__ void unpack(const uint4& r, float2* f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-// two FP32 operations in one instruction
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
 // a BF16 row into row r of a pool of codes
 __device__ __forceinline__ void store_bf16_row4(const uint4& v, float factor, int inv, void* pool, unsigned char* scales,
                                                 size_t r, int lane) {
@@ -72,11 +56,6 @@ __device__ __forceinline__ void store_bf16_row4(const uint4& v, float factor, in
   unsigned char* codes = static_cast<unsigned char*>(pool) + r * kCodeBytes;
   if (inv) store_row4<true>(x, factor, codes, scales, lane);
   else store_row4<false>(x, factor, codes, scales, lane);
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 
 // frac(f / 2 pi) * 2^64 modulo 2^64, from f = m 2^-s by a 24 x 128 bit product with
@@ -163,8 +142,8 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
         unpack(__ldg(reinterpret_cast<const uint4*>(w) + partner), b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          cw[i] = mul2(cw[i], a[i]);
-          sw[i] = mul2(sw[i], b[i]);
+          cw[i] = mul_f32x2(cw[i], a[i]);
+          sw[i] = mul_f32x2(sw[i], b[i]);
         }
       }
       uint4* dst = reinterpret_cast<uint4*>(kind ? p.k_out : p.q_out);
@@ -184,9 +163,9 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
         for (int j = 0; j < N; ++j) {
           float2 x[4];
           unpack(raw[j], x);
-          float2 ss = mul2(x[0], x[0]);
+          float2 ss = mul_f32x2(x[0], x[0]);
 #pragma unroll
-          for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+          for (int i = 1; i < 4; ++i) ss = fma_f32x2(x[i], x[i], ss);
           rinv[j] = ss.x + ss.y;
         }
         auto finish = [&](float sum) -> float { return (w != nullptr) ? rsqrtf(sum * (1.0f / kD) + p.eps) : 1.0f; };
@@ -214,10 +193,10 @@ __global__ void __launch_bounds__(kMropeWarps * 32, kMropeBlocksPerSm) mrope_ker
           uint32_t out[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float2 v = mul2(x[i], cw[i]);
-            if (rot) v = fma2(y[i], sw[i], v);  // (other lanes' values never reach an unrotated one)
-            v = mul2(v, make_float2(rinv[j], rinv[j]));
-            out[i] = bf16x2(v.x, v.y);
+            float2 v = mul_f32x2(x[i], cw[i]);
+            if (rot) v = fma_f32x2(y[i], sw[i], v);  // (other lanes' values never reach an unrotated one)
+            v = mul_f32x2(v, make_float2(rinv[j], rinv[j]));
+            out[i] = bf16x2_rn(v.x, v.y);
           }
           const uint4 o4 = make_uint4(out[0], out[1], out[2], out[3]);
           if (dst != nullptr) dst[j * pitch_h] = o4;

@@ -47,6 +47,7 @@
 
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
+#include "gda_tc.cuh"
 
 namespace gda {
 
@@ -84,13 +85,6 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-// 2^x on the SFU (2 ulp; results below the normal range are 0): P is rounded to FP16
-// right after, and 2^-126 against a sum of at least 2^-8 does not count.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
   uint4 v;
@@ -181,8 +175,7 @@ struct Fp4WarpState {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.0f;
     const uint32_t row0 = smem_u32(&st.k[g][0]);  // token g + 8j: + 8 j kRow4
-    // dims 64t + 32 half .. + 31: two scale blocks.  (Rolled: the loop body is what a CTA
-    // first fetches from the instruction cache.)
+    // dims 64t + 32 half .. + 31: two scale blocks
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint4 c[4];
@@ -266,7 +259,9 @@ struct Fp4WarpState {
       const float ra = (m[n][0] == -INFINITY) ? 0.0f : m[n][0], rb = (m[n][1] == -INFINITY) ? 0.0f : m[n][1];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float pa = ex2(s[2 * j] - ra), pb = ex2(s[2 * j + 1] - rb);
+        // (2 ulp, below the normal range 0: FP16's rounding follows, and 2^-126 against a sum of
+        // at least 2^-8 does not count)
+        const float pa = ex2_approx(s[2 * j] - ra), pb = ex2_approx(s[2 * j + 1] - rb);
         P[n][j] = pack_f16(pa, pb);
         const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&P[n][j]));
         l[n][0] += r.x;

@@ -1,5 +1,5 @@
-// gda_tc.cuh -- PTX wrappers of the prefill kernels: tcgen05 (TMEM, MMA, commits), TMA tiles,
-// shared-memory and instruction descriptors, packed FP32 / BF16 arithmetic (sm_103a).
+// gda_tc.cuh -- PTX wrappers: tcgen05 (TMEM, MMA, commits), TMA tiles, shared-memory and
+// instruction descriptors of the prefill kernels; packed FP32 / BF16 arithmetic (sm_103a).
 #pragma once
 
 #include <cuda.h>
@@ -86,7 +86,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 2^x on the SFU (ex2.approx, subnormal results flushed): P is rounded to BF16 right
+// 2^x on the SFU (ex2.approx, subnormal results flushed): P is rounded to BF16 or FP16 right
 // after, far coarser than the instruction's error.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

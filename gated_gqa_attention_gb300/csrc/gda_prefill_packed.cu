@@ -523,6 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.lse[(size_t)t.h * p.Sq + t.s.q0 + qi] = (e == 0.0f) ? -INFINITY : (m_run + log2f(e)) * 0.69314718055994530942f;
         }
         const float inv = (l > 0.0f) ? 1.0f / l : 0.0f;  // (a NaN sum comes with NaN in O)
+        // a dead row is 0 also where a value that its block's other rows see was not finite
+        const uint32_t keep = (l == 0.0f) ? 0u : 0xFFFFFFFFu;
         ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
         if (!ok) break;
         tc_fence_after();
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 v = mul_f32x2(make_float2(o[8 * u + 2 * e], o[8 * u + 2 * e + 1]), make_float2(inv, inv));
-              b4[e] = bf16x2_rn(v.x, v.y);
+              b4[e] = bf16x2_rn(v.x, v.y) & keep;
             }
             *reinterpret_cast<uint4*>(dst + 16 * (u ^ (r & 7))) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
           }

@@ -29,7 +29,6 @@ they are used after a wait for it, and kept until that use is over (or given as 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -330,14 +329,14 @@ def _scale_bytes(kv_scales):
     return kv_scales
 
 
-_SAME = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Context for what a call allocates itself: its memory belongs to the stream that the call runs on.  From the
-    current stream's it could be memory that work queued there still reads, and what the call drops could be handed
-    out there while the call still uses it."""
-    return _SAME if stream is None else _torch().cuda.stream(stream)
+def _alloc(stream, make, *args, **kw):
+    """make(*args, **kw), a tensor that a call allocates itself.  Its memory belongs to the stream that the call runs
+    on: from the current stream's it could be memory that work queued there still reads, and what the call drops
+    could be handed out there while the call still uses it."""
+    if stream is None:
+        return make(*args, **kw)
+    with _torch().cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def _launch(fn, dev, stream, *args):
@@ -399,8 +398,7 @@ def decode(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, scale: Op
     B, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     if out is None:
-        with _on(stream):
-            out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     if scale is None:
         scale = 1.0 / (D ** 0.5)
     if kv == KV_E2M1:
@@ -561,8 +559,7 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
     B, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     if out is None:
-        with _on(stream):
-            out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     if lse is not None:
         _need("lse", lse, torch.float32, 2, q.get_device())
         if kv == KV_E2M1 and lse.shape != (B, Hq):
@@ -575,8 +572,7 @@ def decode_ex(q, gate_t, k_pool, v_pool, kv_indptr, kv_indices, out=None, *, wor
         scale = 1.0 / (D ** 0.5)
     if workspace is None:
         nbytes = workspace_bytes(B, Hq, Hkv, D, num_splits)
-        with _on(stream):
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _alloc(stream, torch.empty, max(nbytes, 256), dtype=torch.uint8, device=q.device)
         workspace_init(workspace, stream)
     a = _Args(_ptr(q), _ptr(gate_t) if fuse_gate else None, _ptr(k_pool), _ptr(v_pool), _ptr(kv_indptr),
               _ptr(kv_indices), _ptr(out), _ptr(lse), int(k_pool.shape[0]), B, Hq, Hkv, D, float(scale),
@@ -674,8 +670,7 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     if lse is not None:
         _need_shape("lse", lse, torch.float32, (Hq, Tq), dev, "be [Hq, Tq]")
     if out is None:
-        with _on(stream):
-            out = torch.zeros(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _alloc(stream, torch.zeros, Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
     else:
         _need_shape("out", out, torch.bfloat16, (Tq, Hq, D), dev, "have q's shape")
     if scale is None:
@@ -747,10 +742,8 @@ def mrope_pair_axis(sections, interleaved: bool = False):
 
 def _axis_bytes(pair_axis) -> bytes:
     """One byte per pair.  (bytes() of a number is that many zeros, and of an array its memory.)"""
-    if isinstance(pair_axis, bytes):
-        return pair_axis
     try:
-        return bytes(list(pair_axis))
+        return bytes(pair_axis if type(pair_axis) in (list, tuple, bytes) else list(pair_axis))
     except TypeError:
         raise TypeError("pair_axis must be a sequence of axis numbers") from None
 
@@ -792,8 +785,7 @@ def qk_norm_mrope_kv_write(qgkv, positions, inv_freq, pair_axis, Hq: int, Hkv: i
         if t is not None:
             _need_shape(name, t, bf16, (T, h, D), dev, "be [T, %d, D]" % h)
         elif name != "gate_out":
-            with _on(stream):
-                t = torch.empty_strided((T, h, D), (h * D, D, 1), dtype=bf16, device=device)
+            t = _alloc(stream, torch.empty_strided, (T, h, D), (h * D, D, 1), dtype=bf16, device=device)
         outs.append(t)
     q_out, k_out, gate_out = outs
     num_slots, kv = 0, KV_BF16
@@ -864,11 +856,11 @@ def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             _need_shape(name, t, bf16, (N, Hkv, D), dev, "be [N, Hkv, D]")
-    if k_out is None or v_out is None:
-        with _on(stream):
-            new = [torch.empty_strided((N, Hkv, D), (Hkv * D, D, 1), dtype=bf16, device=k_pool.device)
-                   if t is None else t for t in (k_out, v_out)]
-        k_out, v_out = new
+    size, strides, device = (N, Hkv, D), (Hkv * D, D, 1), k_pool.device
+    if k_out is None:
+        k_out = _alloc(stream, torch.empty_strided, size, strides, dtype=bf16, device=device)
+    if v_out is None:
+        v_out = _alloc(stream, torch.empty_strided, size, strides, dtype=bf16, device=device)
     _launch((_lib or load()).gda_kv_gather_fp4, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
             kv_scales.data_ptr(), num_slots, indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(),
             v_out.data_ptr(), Hkv, D)

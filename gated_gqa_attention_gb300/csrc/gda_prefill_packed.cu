@@ -17,13 +17,14 @@
 // CTA c takes the items in snake order (c, 2G - 1 - c, 2G + c, ..), heads fastest: equal shares
 // from a descending list, and neighbouring CTAs read the same keys.
 //
-// What bounds it: the tensor pipe for long prompts (a tile takes 1.43 us, 1.31 at the measured
-// BF16 rate), and for short ones what an item costs besides its tiles.  With one CTA per item
+// What bounds it: the tensor pipe for long prompts (a tile takes 1.47 us, 1.31 at the measured
+// BF16 rate; 1.44 with one sum of the probabilities instead of two), and for short ones what an item costs besides its tiles.  With one CTA per item
 // that was 11 us (set-up 1.5, first loads 2.7, last PV 1.0, epilogue 3.6, stores 1.5, the next
 // CTA's launch 0.7).  Here the next item's K and Q arrive and its first S products run during
 // the epilogue, and it is about 5 us (sigmoids and last PV 2.7 to 3, O to shared memory 0.5,
 // products and stores 1, the next S 0.3): 6001 tokens of nine prompts x 32 heads (53 to 56 key
-// tiles in 11 items per SM) 207 -> 148 us; 12288 tokens x 16 heads with prefixes 472 -> 427 us.
+// tiles in 11 items per SM) 207 -> 148 us (151 with both
+// sums); 12288 tokens x 16 heads with prefixes 472 -> 427 us (436).
 // (Measured and dropped: four more warps that run the whole epilogue during the next item's
 // tiles, 210 us, or only its sigmoids, 161 us -- both take from the softmax what they save; the
 // sigmoids as a loop over registers that move up, or with reciprocals by Newton steps in place
@@ -836,7 +837,7 @@ cudaError_t launch_prefill_packed(const PrefillParams& params, const void* q, in
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   // as a programmatic dependent where every item has a CTA and latency counts (300 tokens 12.6 ->
-  // 11.8 us); with more items than CTAs the early CTAs only disturb (12288 tokens 428 -> 438 us)
+  // 11.8 us); with more items than CTAs the early CTAs only disturb (12288 tokens then 428 -> 438 us)
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

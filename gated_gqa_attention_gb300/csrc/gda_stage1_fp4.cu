@@ -16,7 +16,10 @@
 //    144-byte pitch that keeps the 16-byte reads below free of bank conflicts is the row itself.
 //    Two CTAs keep the pipes busy while one merges or waits: a ragged batch of 224 sequences took
 //    125 us with one CTA of 8 warps and three stages, 107 with one of 12 warps, 103 with two of
-//    6.  Of 120 us for 8 x 131072 positions the copies alone take 109 and the arithmetic alone 100.
+//    6.  Of 120 us for 8 x 131072 positions (117 now) the copies alone took 109 and the arithmetic
+//    alone 100.  No pipe is near its limit (b64_l4096: issue 44 %, ALU 37 %, tensor 20 %): a tile's
+//    steps -- scores, maximum, exponentials, transpose, products -- wait for one another in a warp,
+//    and 8 to 12 warps an SM are what the registers allow.
 //  * A code times its scale is exact in FP16, so cvt.rn.f16x2.e2m1x2 widens a byte (two
 //    codes), one packed multiply applies the scale, and the tiles run as m16n8k16 FP16
 //    MMAs with FP32 accumulation.  Q goes to FP16 with one power of two per head (its
@@ -36,9 +39,9 @@
 //  * P is rounded to FP16 for the MMA (it lies in [0, 2^8]: 2^-11 relative, 2^-25 absolute
 //    below 2^-14, against the 4-bit V it multiplies).  O is divided by the FP32 sum of the
 //    rounded values, so that a head's weights add up to 1; the LSE takes the FP32 sum before
-//    the rounding.
+//    the rounding (the second sum: b64_l4096 42.4 -> 42.7 us, 16 heads 51.0 -> 52.4 us).
 //  * With more than 8 query heads per KV head, pairs of groups share one read of the rows and
-//    one widening of the codes (16 heads, 8 x 32769 positions: 84 -> 58 us).
+//    one widening of the codes (16 heads, 8 x 32769 positions: 84 -> 58 us; 52 now).
 //  * Merge: as in the e4m3 kernel -- each warp leaves its rescaled O^T fragments in ring
 //    stage 0, all threads add the slices in a fixed order.  Tile k of a piece lives in stage
 //    (k + 1) % 2, so the next piece's first tile is on its way to stage 1 while stage 0 serves

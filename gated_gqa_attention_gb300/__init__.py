@@ -20,11 +20,13 @@ kernels; their values are ``k_descale * e4m3(code)`` and ``v_descale * e4m3(code
 A 4-bit cache is two uint8 pools of codes [num_slots, Hkv, D / 2] and their scales
 ``kv_scales`` [num_slots, Hkv, 2, D / 16]: passing ``kv_scales`` to ``decode`` or
 ``decode_ex`` selects it.  ``kv_write_fp4`` and ``qk_norm_mrope_kv_write`` write it,
-``kv_gather_fp4`` reads rows back.  A prompt of packed sequences goes
-``qk_norm_mrope_kv_write`` -> ``prefill_packed``.
+``kv_gather_fp4`` reads rows back.  ``kv_write_e4m3`` and ``kv_gather_e4m3`` do the same for an
+e4m3 cache.  A prompt of packed sequences goes ``qk_norm_mrope_kv_write`` -> ``prefill_packed``;
+new tokens behind cached ones (chunks of prompts, drafted tokens, single tokens, any mix) go into
+the cache and then through ``prefill_paged``, over any of the three caches.
 
 Calls run on ``stream`` (default: the current one), and outputs that the decode calls, the
-rotary step, ``kv_gather_fp4`` and ``prefill_packed`` allocate belong to it: on another stream
+rotary step, ``kv_gather_fp4``, ``kv_gather_e4m3``, ``prefill_packed`` and ``prefill_paged`` allocate belong to it: on another stream
 they are used after a wait for it, and kept until that use is over (or given as arguments).
 """
 from __future__ import annotations
@@ -35,8 +37,8 @@ import threading
 from typing import Optional
 
 __all__ = [
-    "load", "decode", "decode_ex", "decode_noalloc", "decode_step_host", "StepHost", "step_layout", "small_path_cluster", "auto_splits", "pack_step", "STEP_MAP_IN", "STEP_MAP_OUT", "prefill", "prefill_read_error", "qk_norm_rope_kv_write", "prefill_packed", "qk_norm_mrope_kv_write", "mrope_pair_axis",
-    "kv_write_fp4", "kv_gather_fp4", "gate", "workspace_bytes", "workspace_init", "reserve",
+    "load", "decode", "decode_ex", "decode_noalloc", "decode_step_host", "StepHost", "step_layout", "small_path_cluster", "auto_splits", "pack_step", "STEP_MAP_IN", "STEP_MAP_OUT", "prefill", "prefill_read_error", "qk_norm_rope_kv_write", "prefill_packed", "prefill_paged", "prefill_paged_workspace_bytes", "qk_norm_mrope_kv_write", "mrope_pair_axis",
+    "kv_write_fp4", "kv_gather_fp4", "kv_write_e4m3", "kv_gather_e4m3", "gate", "workspace_bytes", "workspace_init", "reserve",
     "read_error", "debug_wait_limit", "timing_begin", "timing_end", "status_str", "version", "GdaError", "VARIANT_AUTO", "VARIANT_MMA",
     "VARIANT_SIMT", "VARIANT_TMA", "MAX_SPLITS", "LIB_PATH", "KV_BF16", "KV_E4M3", "KV_E2M1",
 ]
@@ -99,6 +101,20 @@ class _PackedArgs(ctypes.Structure):
     ]
 
 
+class _PagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+        ("gate_stride", ctypes.c_int64), ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+        ("kv_scales", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+        ("kv_indptr", ctypes.c_void_p), ("kv_indices", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("sinks", ctypes.c_void_p), ("total_q", ctypes.c_int64), ("nnz", ctypes.c_int64),
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("scale", ctypes.c_float), ("window", ctypes.c_int), ("keep_first", ctypes.c_int),
+        ("kv_dtype", ctypes.c_int), ("k_descale", ctypes.c_float), ("v_descale", ctypes.c_float),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
 def load(path: Optional[str] = None):
     """Load the C-ABI library (raises when it has not been built)."""
     global _lib
@@ -127,6 +143,14 @@ def load(path: Optional[str] = None):
         lib.gda_kv_write_fp4.restype = i32
         lib.gda_kv_gather_fp4.argtypes = [vp, vp, vp, i64, vp, i64, f32, f32, vp, vp, i32, i32, vp]
         lib.gda_kv_gather_fp4.restype = i32
+        lib.gda_kv_write_e4m3.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, f32, f32, i64, i32, i32, vp]
+        lib.gda_kv_write_e4m3.restype = i32
+        lib.gda_kv_gather_e4m3.argtypes = [vp, vp, i64, vp, i64, f32, f32, vp, vp, i32, i32, vp]
+        lib.gda_kv_gather_e4m3.restype = i32
+        lib.gda_prefill_paged_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        lib.gda_prefill_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.gda_prefill_paged.argtypes = [ctypes.POINTER(_PagedArgs), vp, ctypes.c_size_t, vp]
+        lib.gda_prefill_paged.restype = i32
         lib.gda_qk_norm_mrope_kv_write.argtypes = [ctypes.POINTER(_MropeArgs), vp]
         lib.gda_qk_norm_mrope_kv_write.restype = i32
         lib.gda_prefill_packed.argtypes = [ctypes.POINTER(_PackedArgs), vp]
@@ -685,6 +709,81 @@ def prefill_packed(q, gate_t, k, v, cu_seqlens, cu_seqlens_k=None, *, out=None, 
     return out
 
 
+def prefill_paged_workspace_bytes(total_q: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace prefill_paged needs (0 for invalid sizes)."""
+    return int((_lib or load()).gda_prefill_paged_workspace_bytes(int(total_q), int(B), int(Hq), int(Hkv), int(D)))
+
+
+def prefill_paged(q, gate_t, k_pool, v_pool, cu_seqlens, kv_indptr, kv_indices, *, out=None, lse=None,
+                  scale: Optional[float] = None, window: int = 0, keep_first: int = 0, sinks=None, kv_scales=None,
+                  k_descale: float = 1.0, v_descale: float = 1.0, workspace=None, error_word=None, stream=None):
+    """Gated causal attention of each sequence's newest tokens over its rows of a paged cache, through
+    ``gda_prefill_paged``: chunks of prompts behind a cached prefix, drafted tokens, single tokens.
+
+    q, gate_t: [Tq, Hq, D] bf16 (gate_t None: out = bf16(O)), tokens any multiple of 8 elements apart;
+    cu_seqlens: [B + 1] int32, each sequence's first new token (a decode step: 0, 1, .. B);
+    k_pool, v_pool, kv_scales, kv_indptr, kv_indices: the cache and each sequence's positions as for
+    decode, the new tokens' rows included and last (bf16 pools, e4m3 codes, or a 4-bit cache with
+    kv_scales); a slot outside the pools reads as zeros and sets DEVERR_INDEX in the error word.
+    A query sees the positions up to its own; with ``window`` the last ``window`` of them and the
+    sequence's first ``keep_first``.  sinks: [Hq] float32 sink logits.  out: [Tq, Hq, D] contiguous
+    (rows of no sequence are left as they are: zeros in an ``out`` allocated here); lse: [Hq, Tq] float32
+    or None; workspace: at least prefill_paged_workspace_bytes(...) bytes (None: allocated here), not
+    shared by calls that may overlap; error_word as in prefill."""
+    torch = _torch()
+    sq = _tokens("q", q)
+    dev = q.get_device()
+    Tq, Hq, D = q.shape
+    sg = 0
+    if gate_t is not None:
+        sg = _tokens("gate", gate_t, Hq, D, dev)
+        if gate_t.shape[0] != Tq:
+            raise ValueError("gate must have q's shape")
+    if kv_scales is not None:
+        kv = KV_E2M1
+        num_slots, Hkv = _check_fp4(k_pool, v_pool, kv_scales, D, dev)
+    else:
+        kv = _kv_dtype(k_pool)
+        kdt = k_pool.dtype if kv == KV_E4M3 else torch.bfloat16
+        _need("k_pool", k_pool, kdt, 3, dev)
+        num_slots, Hkv, d = shape = k_pool.shape
+        _need_shape("v_pool", v_pool, kdt, shape, dev, "have k_pool's shape")
+        if d != D:
+            raise ValueError("head dims of q and the pools differ")
+    i32 = torch.int32
+    _need("cu_seqlens", cu_seqlens, i32, 1, dev)
+    B = cu_seqlens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must have B + 1 entries")
+    _need_shape("kv_indptr", kv_indptr, i32, (B + 1,), dev, "have B + 1 entries, as cu_seqlens")
+    _need("kv_indices", kv_indices, i32, 1, dev)
+    if lse is not None:
+        _need_shape("lse", lse, torch.float32, (Hq, Tq), dev, "be [Hq, Tq]")
+    if sinks is not None:
+        _need_shape("sinks", sinks, torch.float32, (Hq,), dev, "have Hq entries")
+    if out is None:
+        out = _alloc(stream, torch.zeros, Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+    else:
+        _need_shape("out", out, torch.bfloat16, (Tq, Hq, D), dev, "have q's shape")
+    if scale is None:
+        scale = 1.0 / (D ** 0.5)
+    if error_word is not None and (error_word.get_device() != dev or error_word.element_size() != 4
+                                   or error_word.numel() < 1):
+        raise ValueError("error_word must be a 32-bit word on cuda:%d" % dev)
+    if workspace is None:
+        n = prefill_paged_workspace_bytes(Tq, B, Hq, Hkv, D)
+        workspace = _alloc(stream, torch.empty, max(n, 256), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on cuda:%d" % dev)
+    a = _PagedArgs(_ptr(q), _ptr(gate_t), sq, sg, _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), num_slots,
+                   _ptr(cu_seqlens), _ptr(kv_indptr), _ptr(kv_indices), _ptr(out), _ptr(lse), _ptr(sinks), Tq,
+                   kv_indices.numel(), B, Hq, Hkv, D, float(scale), int(window), int(keep_first), kv, float(k_descale),
+                   float(v_descale), _ptr(error_word))
+    _launch((_lib or load()).gda_prefill_paged, dev, stream, a, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out
+
+
 def prefill_read_error(clear: bool = True, stream=None) -> int:
     """The library's prefill error word on the current device (synchronises)."""
     w = ctypes.c_uint32(0)
@@ -864,6 +963,58 @@ def kv_gather_fp4(k_pool, v_pool, kv_scales, indices, k_descale: float = 1.0, v_
     _launch((_lib or load()).gda_kv_gather_fp4, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(),
             kv_scales.data_ptr(), num_slots, indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(),
             v_out.data_ptr(), Hkv, D)
+    return k_out, v_out
+
+
+def _check_e4m3(k_pool, v_pool, dev=None):
+    """Checks an e4m3 cache's pools; returns (num_slots, Hkv, D)."""
+    torch = _torch()
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("k_pool must be a torch.float8_e4m3fn or torch.uint8 tensor")
+    if dev is None:
+        dev = _first("k_pool", k_pool, k_pool.dtype, 3)
+    else:
+        _need("k_pool", k_pool, k_pool.dtype, 3, dev)
+    _need_shape("v_pool", v_pool, k_pool.dtype, k_pool.shape, dev, "have k_pool's shape")
+    return k_pool.shape
+
+
+def kv_write_e4m3(k, v, slots, k_pool, v_pool, k_descale: float = 1.0, v_descale: float = 1.0, stream=None):
+    """Quantise the rows of k and v ([T, Hkv, D] bf16, tokens any multiple of 8 elements apart) into an
+    e4m3 cache ([num_slots, Hkv, D] float8_e4m3fn, or uint8 codes) at ``slots`` ([T] int32), through
+    ``gda_kv_write_e4m3``."""
+    sk = _tokens("k", k)
+    (T, Hkv, D), dev = k.shape, k.get_device()
+    sv = _tokens("v", v, Hkv, D, dev)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same shape")
+    _need_shape("slots", slots, _th.int32, (T,), dev, "have T entries")
+    num_slots, h, d = _check_e4m3(k_pool, v_pool, dev)
+    if h != Hkv or d != D:
+        raise ValueError("the pools must be [num_slots, Hkv, D]")
+    _launch((_lib or load()).gda_kv_write_e4m3, dev, stream, k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(),
+            num_slots, k_pool.data_ptr(), v_pool.data_ptr(), float(k_descale), float(v_descale), T, Hkv, D)
+
+
+def kv_gather_e4m3(k_pool, v_pool, indices, k_descale: float = 1.0, v_descale: float = 1.0, k_out=None, v_out=None,
+                   stream=None):
+    """The rows of an e4m3 cache that ``indices`` ([N] int32) name, as bf16 [N, Hkv, D] tensors (k, v),
+    through ``gda_kv_gather_e4m3``; an index outside the pools gives zeros."""
+    torch = _torch()
+    num_slots, Hkv, D = _check_e4m3(k_pool, v_pool)
+    dev, bf16 = k_pool.get_device(), torch.bfloat16
+    _need("indices", indices, torch.int32, 1, dev)
+    N = indices.numel()
+    size, strides, device = (N, Hkv, D), (Hkv * D, D, 1), k_pool.device
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _need_shape(name, t, bf16, size, dev, "be [N, Hkv, D]")
+    if k_out is None:
+        k_out = _alloc(stream, torch.empty_strided, size, strides, dtype=bf16, device=device)
+    if v_out is None:
+        v_out = _alloc(stream, torch.empty_strided, size, strides, dtype=bf16, device=device)
+    _launch((_lib or load()).gda_kv_gather_e4m3, dev, stream, k_pool.data_ptr(), v_pool.data_ptr(), num_slots,
+            indices.data_ptr(), N, float(k_descale), float(v_descale), k_out.data_ptr(), v_out.data_ptr(), Hkv, D)
     return k_out, v_out
 
 

@@ -18,6 +18,7 @@
 #include "gda_device.cuh"
 #include "gda_kernels.h"
 #include "gda_prefill.h"
+#include "gda_prefill_paged.h"
 #include "gda_small.h"
 
 namespace {
@@ -740,6 +741,140 @@ int gda_prefill_packed(const gda_packed_args* a, gda_stream_t stream) {
       p, a->q, a->q_stride, keys ? (const void*)a->k : (const void*)a->q, keys ? a->k_stride : a->q_stride,
       keys ? (const void*)a->v : (const void*)a->q, keys ? a->v_stride : a->q_stride, a->gate,
       reinterpret_cast<cudaStream_t>(stream));
+  if (le == cudaErrorStreamCaptureUnsupported) return GDA_ERR_CAPTURE;  // first use while capturing
+  if (le != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+int gda_kv_write_e4m3(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, int64_t v_stride, const int32_t* slots,
+                      int64_t num_slots, uint8_t* k_pool, uint8_t* v_pool, float k_descale, float v_descale, int64_t T,
+                      int Hkv, int D, gda_stream_t stream) {
+  if (T < 0 || Hkv < 1 || D < 1 || num_slots < 0) return GDA_ERR_SHAPE;
+  if (D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D) return GDA_ERR_SHAPE;
+  if (T > kMaxRows / Hkv) return GDA_ERR_SHAPE;
+  if (!descale_ok(k_descale) || !descale_ok(v_descale)) return GDA_ERR_ARG;
+  if (T == 0) return GDA_OK;
+  if (!k || !v || !slots || !k_pool || !v_pool) return GDA_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(slots, 4) ||
+      !aligned(k_pool, 16) || !aligned(v_pool, 16))
+    return GDA_ERR_ALIGN;
+  gda::Kv8WriteParams p;
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.num_slots = num_slots;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  set_factors(&p, k_descale, v_descale);
+  p.T = T;
+  p.Hkv = Hkv;
+  if (gda::launch_kv8_write(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+int gda_kv_gather_e4m3(const uint8_t* k_pool, const uint8_t* v_pool, int64_t num_slots, const int32_t* indices, int64_t N,
+                       float k_descale, float v_descale, gda_bf16* k_out, gda_bf16* v_out, int Hkv, int D,
+                       gda_stream_t stream) {
+  if (N < 0 || Hkv < 1 || D < 1 || num_slots < 0) return GDA_ERR_SHAPE;
+  if (D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (N > kMaxRows / Hkv) return GDA_ERR_SHAPE;
+  if (!isfinite(k_descale) || !isfinite(v_descale)) return GDA_ERR_ARG;
+  if (N == 0) return GDA_OK;
+  if (!k_pool || !v_pool || !indices || !k_out || !v_out) return GDA_ERR_NULL;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(indices, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return GDA_ERR_ALIGN;
+  gda::Kv8GatherParams p;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.num_slots = num_slots;
+  p.indices = indices;
+  p.N = N;
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  p.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  p.k_descale = k_descale;
+  p.v_descale = v_descale;
+  p.Hkv = Hkv;
+  if (gda::launch_kv8_gather(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;
+  return GDA_OK;
+}
+
+size_t gda_prefill_paged_workspace_bytes(int64_t total_q, int B, int Hq, int Hkv, int D) {
+  if (total_q < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D != gda::kD) return 0;
+  if (total_q > kMaxRows || Hq > kMaxHeads) return 0;
+  return gda::kPagedCutBytes + gda::kPagedMlBytes + gda::kPagedOBytes;
+}
+
+int gda_prefill_paged(const gda_paged_args* a, void* workspace, size_t workspace_bytes, gda_stream_t stream) {
+  if (a == nullptr) return GDA_ERR_NULL;
+  if (a->B < 0 || a->total_q < 0 || a->nnz < 0 || a->num_slots < 0 || a->Hq < 1 || a->Hkv < 1 || a->D < 1 ||
+      a->Hq % a->Hkv != 0 || a->window < 0 || a->keep_first < 0)
+    return GDA_ERR_SHAPE;
+  if (a->D != gda::kD) return GDA_ERR_UNSUPPORTED;
+  if (a->kv_dtype != GDA_KV_BF16 && a->kv_dtype != GDA_KV_E4M3 && a->kv_dtype != GDA_KV_E2M1) return GDA_ERR_UNSUPPORTED;
+  const bool codes = a->kv_dtype != GDA_KV_BF16;
+  if (!isfinite(a->scale) || !(a->scale > 0.0f)) return GDA_ERR_ARG;
+  if (codes && (!descale_ok(a->k_descale) || !descale_ok(a->v_descale))) return GDA_ERR_ARG;
+  // the factor of the scores has to be a normal FP32 value
+  const double factor = (double)a->scale * (codes ? a->k_descale : 1.0f) * 1.44269504088896340736;
+  if (!(factor > 1.2e-38 && factor < 3.4e38)) return GDA_ERR_ARG;
+  if (a->total_q > kMaxRows || a->nnz > kMaxRows || a->Hq > kMaxHeads) return GDA_ERR_SHAPE;
+  const int64_t wq = (int64_t)a->Hq * a->D;
+  if (a->q_stride < wq || (a->gate && a->gate_stride < wq)) return GDA_ERR_SHAPE;
+  if (a->B == 0 || a->total_q == 0) return GDA_OK;
+  if (gda::paged_blocks(a->total_q, a->Hq / a->Hkv, a->B) > 0x7FFFFFFFLL) return GDA_ERR_SHAPE;
+  if (!a->q || !a->out || !a->cu_seqlens || !a->kv_indptr ||
+      (a->nnz > 0 && (!a->kv_indices || !a->k_pool || !a->v_pool || (a->kv_dtype == GDA_KV_E2M1 && !a->kv_scales))))
+    return GDA_ERR_NULL;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || (a->gate && !aligned(a->gate, 16)) ||
+      (a->k_pool && !aligned(a->k_pool, 16)) || (a->v_pool && !aligned(a->v_pool, 16)) ||
+      (a->kv_scales && !aligned(a->kv_scales, 16)) || !aligned(a->cu_seqlens, 4) || !aligned(a->kv_indptr, 4) ||
+      (a->kv_indices && !aligned(a->kv_indices, 4)) || (a->lse && !aligned(a->lse, 4)) ||
+      (a->sinks && !aligned(a->sinks, 4)) || (a->error_word && !aligned(a->error_word, 4)) || a->q_stride % 8 != 0 ||
+      (a->gate && a->gate_stride % 8 != 0))
+    return GDA_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < gda_prefill_paged_workspace_bytes(a->total_q, a->B, a->Hq, a->Hkv, a->D))
+    return GDA_ERR_WORKSPACE;
+  unsigned int* err = a->error_word;
+  if (err == nullptr) {
+    int rc = prefill_error_word(&err);
+    if (rc != GDA_OK) return rc;
+  }
+  gda::PagedParams p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a->q);
+  p.gate = reinterpret_cast<const __nv_bfloat16*>(a->gate);
+  p.q_stride = a->q_stride;
+  p.gate_stride = a->gate_stride;
+  p.k_pool = static_cast<const unsigned char*>(a->k_pool);
+  p.v_pool = static_cast<const unsigned char*>(a->v_pool);
+  p.scales = a->kv_scales;
+  p.num_slots = a->num_slots;
+  p.cu_q = a->cu_seqlens;
+  p.indptr = a->kv_indptr;
+  p.indices = a->kv_indices;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a->out);
+  p.lse = a->lse;
+  p.sinks = a->sinks;
+  p.error = err;
+  p.B = a->B;
+  p.Tq = (int)a->total_q;
+  p.nnz = (int)a->nnz;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.G = a->Hq / a->Hkv;
+  p.window = a->window < a->nnz ? a->window : 0;  // (no sequence is longer than nnz)
+  p.keep = a->keep_first;
+  p.scale_log2 = (float)factor;
+  p.v_descale = codes ? a->v_descale : 1.0f;
+  p.wait_limit = wait_limit();
+  char* ws = static_cast<char*>(workspace);
+  p.cuts = reinterpret_cast<int4*>(ws);
+  p.part_ml = reinterpret_cast<float4*>(ws + gda::kPagedCutBytes);
+  p.part_o = reinterpret_cast<float4*>(ws + gda::kPagedCutBytes + gda::kPagedMlBytes);
+  const cudaError_t le = gda::launch_prefill_paged(p, a->kv_dtype, reinterpret_cast<cudaStream_t>(stream));
   if (le == cudaErrorStreamCaptureUnsupported) return GDA_ERR_CAPTURE;  // first use while capturing
   if (le != cudaSuccess) return GDA_ERR_CUDA;
   return GDA_OK;

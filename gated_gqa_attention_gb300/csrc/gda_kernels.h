@@ -117,6 +117,34 @@ struct Kv4GatherParams {
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_gather(const Kv4GatherParams& p, cudaStream_t stream);
 
+// 8-bit (e4m3) cache rows: write and read back.
+struct Kv8WriteParams {
+  const __nv_bfloat16* k;      // [T, Hkv, D], token t at t * k_stride
+  const __nv_bfloat16* v;
+  long long k_stride, v_stride;
+  const int* slots;            // [T]
+  long long num_slots;
+  unsigned char* k_pool;       // [num_slots, Hkv, D] codes
+  unsigned char* v_pool;
+  float k_factor, v_factor;    // inv: exact reciprocals of the descales, else the descales
+  int inv;
+  long long T;
+  int Hkv;
+};
+struct Kv8GatherParams {
+  const unsigned char* k_pool;
+  const unsigned char* v_pool;
+  long long num_slots;
+  const int* indices;          // [N]
+  long long N;
+  __nv_bfloat16* k_out;        // [N, Hkv, D]
+  __nv_bfloat16* v_out;
+  float k_descale, v_descale;
+  int Hkv;
+};
+cudaError_t launch_kv8_write(const Kv8WriteParams& p, cudaStream_t stream);
+cudaError_t launch_kv8_gather(const Kv8GatherParams& p, cudaStream_t stream);
+
 // The step before attention for any tokens, with positions on several axes.
 constexpr int kMropeMaxPairs = 128;
 struct MropeParams {

@@ -47,6 +47,7 @@
 
 #include "gda_kernels.h"
 #include "gda_prefill.h"
+#include "gda_prefill_paged.h"
 #include "gda_tc.cuh"
 
 namespace gda {
@@ -665,6 +666,7 @@ cudaError_t prefill_init(int dev, cudaStream_t stream) {
   e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   e = packed_init();
+  if (e == cudaSuccess) e = paged_init();
   if (e != cudaSuccess) return e;
   cudaStream_t own = nullptr;
   e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);

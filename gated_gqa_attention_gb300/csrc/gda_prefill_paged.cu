@@ -1,0 +1,1169 @@
+// gda_prefill_paged.cu -- gated attention of each sequence's newest tokens over its rows of a paged
+// cache (sm_103a): tcgen05 MMAs, TMEM operands and accumulators, rows gathered by slot.
+//
+// Sequence b has nq new tokens and L positions, the new ones last; its query i is at position
+// p = L - nq + i and sees, of the keys j <= p, the last `window` ones and the first `keep` ones
+// (all without a window).  Per query head h, with the cache row of position j at slot indices[j]:
+//   O   = sum_j e^(s_j) v_j / (e^(sink_h) + sum_j e^(s_j)),  s_j = scale * q . k_j   (no key: O = 0)
+//   out = RNE_bf16(RNE_bf16(O) * RNE_bf16(sigmoid(gate))),  lse = log of the divisor
+//
+// Rows.  The G query heads of a KV head read the same keys, so an item is 128 rows of (token, head)
+// pairs of one KV head, token after token: one token of 8 heads fills 8 rows, 16 tokens all 128.
+// Its keys come in tiles of 128 positions; tiles that no row of the item sees are left out.
+//
+// Shares.  The lengths are on the device.  The items, by sequence, KV head and block, form one
+// stream in which an item costs its tiles and a constant; each CTA takes an equal share of it.  An
+// item that a share's end cuts is computed in parts: each CTA leaves its part (row max, sum,
+// unnormalised O in FP32) in the workspace, at most two per CTA, and a second kernel joins them in
+// the order of the shares, so a result does not depend on which CTA ends first.  What an item costs
+// is taken as linear in its number within the sequence, so that sums over items have a closed form.
+#include "gda.h"
+#include "gda_kernels.h"
+#include "gda_kv4.cuh"
+#include "gda_prefill.h"
+#include "gda_prefill_dev.cuh"
+#include "gda_prefill_paged.h"
+
+namespace gda {
+
+namespace {
+
+constexpr int kPM = 128;            // rows per item (MMA M)
+constexpr int kPN = 128;            // keys per tile (MMA N of S)
+constexpr int kSoftmaxWarps = 8;    // warps 0-7
+constexpr int kPlanWarp = 8, kMmaWarp = 9, kPvWarp = 11;
+constexpr int kGatherWarp = 12;     // warps 12, 13: Q and K; 14, 15: V
+constexpr int kThreads = 16 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
+// registers of a thread: softmax, issuers and planner, gatherers (4 x 128 at the launch)
+constexpr int kRegsSoftmax = 176, kRegsIssue = 56, kRegsGather = 104;
+static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsGather <= 4 * 128, "register shares");
+
+constexpr int kItemCost = 4;        // of an item besides its tiles, in half tiles
+
+constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
+constexpr uint32_t kHalf = 2 * kBlk;               // a half tile: 2 column blocks, 32 KiB
+
+template <int KV>
+struct Layout {
+  static constexpr int kKSlots = KV == GDA_KV_BF16 ? 3 : 2;
+  static constexpr uint32_t kOffQ = 0;                          // [4 blocks][128 rows][128 B]
+  static constexpr uint32_t kOffK = kOffQ + 4 * kBlk;
+  static constexpr uint32_t kOffV = kOffK + kKSlots * kHalf;
+  static constexpr uint32_t kOffX = kOffV + 2 * kHalf;          // row max exchange [parity][half][row]
+  static constexpr uint32_t kOffE = kOffX + 2048;               // second halves' sums for lse [row]
+  static constexpr uint32_t kOffBar = kOffE + 512;
+  static constexpr uint32_t kOffScale = kOffBar + 512;          // [4 items][row]: the row's score factor
+  static constexpr uint32_t kBytes = kOffScale + (KV == GDA_KV_BF16 ? 0 : 2048);
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+struct Item {
+  int b;               // sequence (-1: no more items)
+  int q0, nq;          // its first new token, their number
+  int kb, L;           // first entry of `indices`, positions
+  int h, i;            // KV head, block of 128 rows
+  int ta, tb;          // this CTA's tiles of the item's
+  int f, tl;           // tile t holds positions from 128 t (t < f) or 128 (t - f + tl) on
+  int lo, hi;          // positions that any row sees: [lo, hi) and those below p.keep
+  int part;            // -1: the whole item, else where its part goes
+};
+struct Cut {           // a place in the stream: block i of KV head h of sequence b, before its tile t
+  int b, h, i, t;
+};
+struct Bars {
+  uint64_t qf, q_empty;                             // Q landed; the item's S products have read it
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], p_empty[2];        // per S / P buffer
+  uint64_t xm[4][2];                                // per row quarter and tile parity: both maxima stored
+  uint64_t pr[4];                                   // per row quarter: both halves' epilogues are here
+  uint64_t o_full, o_empty, v_free;                 // the item's O complete; read; its staging read
+  uint64_t i_full[2], i_empty[2];                   // item slots
+  Item item[2];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+constexpr int kGatherWarps = 4;                     // 2 each
+constexpr int kItemReaders = 2 + kGatherWarps + kSoftmaxWarps;  // both issuers, gatherers, softmax
+
+// ---- the stream of items
+
+struct Seq {
+  int q0, nq, kb, L;   // (clamped to the tensors)
+};
+__device__ __forceinline__ Seq seq_of(const PagedParams& p, int b) {
+  Seq s;
+  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+  const int k0 = __ldg(p.indptr + b), k1 = __ldg(p.indptr + b + 1);
+  s.q0 = min(max(q0, 0), p.Tq);
+  s.nq = max(min(q1, p.Tq) - s.q0, 0);
+  s.kb = min(max(k0, 0), p.nnz);
+  s.L = max(min(k1, p.nnz) - s.kb, 0);
+  return s;
+}
+__device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) {
+  return (int)(((long long)s.nq * p.G + kPM - 1) >> 7);
+}
+// block i of a sequence: what its rows see, and its tiles
+struct Range {
+  int lo, hi, f, tl, n;
+};
+__device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, int i) {
+  Range r;
+  const int ta = (int)(((long long)i * kPM) / p.G);                              // first and last token
+  const int tb = (int)min((long long)s.nq - 1, ((long long)i * kPM + kPM - 1) / p.G);
+  const int off = s.L - s.nq;
+  r.hi = max(off + tb + 1, 0);
+  r.lo = p.window > 0 ? (int)min(max((long long)off + ta - p.window + 1, 0LL), (long long)r.hi) : 0;
+  const int th = (r.hi + kPN - 1) >> 7;
+  r.tl = r.lo >> 7;
+  r.f = min((min(p.keep, r.lo) + kPN - 1) >> 7, r.tl);
+  r.n = r.f + th - r.tl;
+  return r;
+}
+// Costs of a sequence's blocks, per KV head: linear from its first to its last block.
+struct Costs {
+  int mt;              // blocks
+  long long first, rise;
+  __device__ __forceinline__ Costs(const PagedParams& p, const Seq& s) {
+    mt = blocks_of(p, s);
+    first = rise = 0;
+    if (mt > 0) {
+      first = 2LL * range_of(p, s, 0).n + kItemCost;
+      if (mt > 1) rise = 2LL * range_of(p, s, mt - 1).n + kItemCost - first;
+    }
+  }
+  // of the blocks before block i
+  __device__ __forceinline__ long long before(int i) const {
+    long long c = first * i;
+    if (rise != 0) {
+      const long long m = (rise > 0 ? rise : -rise) * ((long long)i * (i - 1) / 2) / (mt - 1);
+      c += rise > 0 ? m : -m;
+    }
+    return c;
+  }
+};
+// the place at x within a sequence's costs (0 <= x < Hkv * c.before(c.mt))
+__device__ __noinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, long long x) {
+  const Costs c(p, s);
+  const long long per_head = c.before(c.mt);
+  Cut r;
+  r.b = b;
+  r.h = (int)(x / per_head);
+  x -= r.h * per_head;
+  int lo = 0, hi = c.mt - 1;   // the last block that starts at or before x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.before(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  r.i = lo;
+  const long long at = c.before(lo), cost = c.before(lo + 1) - at;
+  r.t = cost > 0 ? (int)((long long)range_of(p, s, lo).n * (x - at) / cost) : 0;
+  return r;
+}
+
+// One KV row's worth of codes to FP16, 16-byte chunks of 8 values.
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b) {
+  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16));
+}
+__device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w, uint32_t scale2) {
+  uint32_t f[4];
+  e2m1x8_to_f16x2x4(w, f);
+  return make_uint4(f16x2_mul(f[0], scale2), f16x2_mul(f[1], scale2), f16x2_mul(f[2], scale2), f16x2_mul(f[3], scale2));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// a pair of probabilities rounded for the MMA, and the values they stand for
+template <int KV>
+__device__ __forceinline__ uint32_t round_pair(float2 x) {
+  return KV == GDA_KV_BF16 ? bf16x2_rn(x.x, x.y) : f16x2_rn(x.x, x.y);
+}
+template <int KV>
+__device__ __forceinline__ float2 pair_values(uint32_t w) {
+  if (KV == GDA_KV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// kind::f16 instruction descriptor with BF16 or FP16 operands (their type is a bit in each field)
+template <int KV>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, int b_mn) {
+  return idesc_bf16(M, N, b_mn) & (KV == GDA_KV_BF16 ? 0xFFFFFFFFu : ~((1u << 7) | (1u << 10)));
+}
+
+// log2-domain sink of a row joined to (m, l, e): its weight goes into the sums, m may rise
+__device__ __forceinline__ void join_sink(const PagedParams& p, int head, float& m, float& l, float& e, float& w) {
+  const float s = __ldg(p.sinks + head) * 1.44269504088896340736f;
+  w = 1.0f;  // what O is multiplied by
+  if (s > m) {
+    w = (m == -INFINITY) ? 0.0f : exp2f(m - s);
+    l = l * w + 1.0f;
+    e = e * w + 1.0f;
+    m = s;
+  } else if (s > -INFINITY) {
+    const float t = exp2f(s - m);
+    l += t;
+    e += t;
+  }
+}
+__device__ __forceinline__ float lse_of(float m, float e) {
+  return (e == 0.0f) ? -INFINITY : (m + log2f(e)) * 0.69314718055994530942f;
+}
+
+}  // namespace
+
+template <int KV>
+__global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid_constant__ PagedParams p) {
+  using Lay = Layout<KV>;
+  constexpr int kKSlots = Lay::kKSlots;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  // the 128-byte swizzled tiles need a 1024-byte aligned base: a misaligned one is reported,
+  // not used (the same for every CTA)
+  if ((smem_u32(sm) & 1023u) != 0) {
+    if (threadIdx.x == 0) {
+      atomicOr(p.error, kErrTimeout);
+      p.cuts[0] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  Bars& bars = *reinterpret_cast<Bars*>(sm + Lay::kOffBar);
+  float* xbuf = reinterpret_cast<float*>(sm + Lay::kOffX);
+  float* ebuf = reinterpret_cast<float*>(sm + Lay::kOffE);
+  float* qscale = reinterpret_cast<float*>(sm + Lay::kOffScale);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(&bars.qf, 2);
+    mbar_init(&bars.q_empty, 1);
+    for (int x = 0; x < kKSlots; ++x) {
+      mbar_init(&bars.k_full[x], 2);
+      mbar_init(&bars.k_empty[x], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars.v_full[x], 2);
+      mbar_init(&bars.v_empty[x], 1);
+      mbar_init(&bars.s_full[x], 1);
+      mbar_init(&bars.p_full[x], kSoftmaxWarps);
+      mbar_init(&bars.p_empty[x], 1);
+      mbar_init(&bars.i_full[x], 1);
+      mbar_init(&bars.i_empty[x], kItemReaders);
+    }
+    for (int q4 = 0; q4 < 4; ++q4) {
+      mbar_init(&bars.xm[q4][0], 2);
+      mbar_init(&bars.xm[q4][1], 2);
+      mbar_init(&bars.pr[q4], 2);
+    }
+    mbar_init(&bars.o_full, 1);
+    mbar_init(&bars.o_empty, kSoftmaxWarps);
+    mbar_init(&bars.v_free, kSoftmaxWarps);
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  // (as a programmatic dependent: the set-up above ran during the previous kernel's end, whose
+  // results are visible from here on)
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+
+  // ---- this CTA's share [start, end) of the stream: a thread per sequence (512 at a time); the sums
+  // and the two places are exchanged in shared memory that the roles use later
+  long long* wsum = reinterpret_cast<long long*>(sm + Lay::kOffX);       // [16]
+  Cut* place = reinterpret_cast<Cut*>(sm + Lay::kOffX + 256);            // start, end
+  int ctas = 0;
+  {
+    long long total = 0, x0 = 0, x1 = 0;
+    Seq s = {0, 0, 0, 0};
+    long long cost = 0, upto = 0;  // the thread's sequence's, and of all up to it
+    if (tid < 2) place[tid] = {p.B, 0, 0, 0};
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      long long sum = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        if (pass == 0 || p.B > kThreads) {
+          cost = 0;
+          if (b < p.B) {
+            s = seq_of(p, b);
+            const Costs c(p, s);
+            cost = p.Hkv * c.before(c.mt);
+          }
+          upto = cost;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
+          }
+          __syncthreads();
+          if (lane == 31) wsum[warp] = upto;
+          __syncthreads();
+          long long all = 0;
+          for (int w = 0; w < 16; ++w) {
+            if (w == warp) upto += sum + all;
+            all += wsum[w];
+          }
+          sum += all;
+        }
+        if (pass == 1 && cost > 0) {
+          const long long from = upto - cost;
+          if (x0 >= from && x0 < upto) place[0] = cut_at(p, s, b, x0 - from);
+          if (x1 >= from && x1 < upto) place[1] = cut_at(p, s, b, x1 - from);
+        }
+      }
+      if (pass == 0) {
+        total = sum;
+        // no CTA gets less than a tile's worth
+        ctas = (int)max(1LL, min((long long)gridDim.x, total / 2));
+        const int c = blockIdx.x;
+        x0 = c < ctas ? total * c / ctas : total;
+        x1 = c + 1 < ctas ? total * (c + 1) / ctas : total;
+      }
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const Cut start = place[0], end = place[1];
+  __syncthreads();
+  if (tid == 0) {
+    if (blockIdx.x == 0) p.cuts[0] = make_int4(ctas, 0, 0, 0);
+    p.cuts[1 + blockIdx.x] = make_int4(start.b, start.h, start.i, start.t);
+  }
+
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort_flag = &bars.abort;
+  auto fail = [&]() {
+    if (bars.abort == 0) atomicOr(p.error, kErrTimeout);
+    bars.abort = 1;
+  };
+  // (short: the roles' code shares one instruction cache, and this is in it many times.  A
+  // limit below the default is the failure-path test's: polls then hardly suspend.)
+  const long long limit = p.wait_limit;
+  const uint32_t hint = limit < kWaitLimitCycles ? 0u : 10000u;  // ns
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    if (mbar_try_wait_for(bar, parity & 1, hint)) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    do {
+      if (*abort_flag || clock64() - t0 > limit) return false;
+    } while (!mbar_try_wait_for(bar, parity & 1, hint));
+    return true;
+  };
+  // what a role started is waited for with the default limit, whatever the abort flag says
+  auto drain = [&](uint64_t* bar, int parity) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity & 1) && clock64() - t0 < kWaitLimitCycles) {
+    }
+  };
+  // item i (in slot i % 2) of this CTA; its readers release the slot
+  auto get_item = [&](int i, Item* t) -> bool {
+    if (!wait(&bars.i_full[i & 1], i >> 1)) return false;
+    *t = bars.item[i & 1];
+    return true;
+  };
+
+  // Every role walks the same items.  `it` counts those with tiles, T the tiles and N = 2 T the
+  // half tiles so far: the phases of the barriers follow from them.
+  if (warp < kSoftmaxWarps) {
+    regs_grow<kRegsSoftmax>();
+    // ---------------- softmax: warp w owns rows 32 (w % 4) .. + 31 (its TMEM lane quarter) and
+    // keys [64 hc, 64 hc + 64) of each tile, hc = w / 4
+    const int rg = warp & 3, hc = warp >> 2;
+    const int r = 32 * rg + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(rg * 32) << 16);
+    bool ok = true;
+    int it = 0, T = 0;
+    for (int n = 0;; ++n) {
+      Item t;
+      ok = __all_sync(0xffffffffu, get_item(n, &t));
+      __syncwarp();
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
+      if (t.b < 0) break;
+      const long long rows = (long long)t.nq * p.G - (long long)t.i * kPM;  // of the item (128 at most count)
+      const long long flat = (long long)t.i * kPM + r;
+      const int tok = (int)(flat / p.G), head = t.h * p.G + (int)(flat - (long long)tok * p.G);
+      // keys that this row sees: below k_hi, and from k_lo on or below p.keep
+      const int pos = t.L - t.nq + tok;
+      const int k_hi = max(pos + 1, 0), k_lo = p.window > 0 ? (int)max((long long)pos - p.window + 1, 0LL) : 0;
+      const bool some = 32 * rg < rows;   // (rows of the warp)
+      // for the epilogue this warp takes 16 rows, w0 .. of the item; lane y < 16 knows row y's place
+      const int w0 = 32 * rg + 16 * hc, nrow = (int)min(16LL, rows - w0);
+      long long o_at = 0, g_at = 0;       // in 16-byte words
+      if (lane < nrow) {
+        const long long fl = (long long)t.i * kPM + w0 + lane;
+        const int tk = (int)(fl / p.G), hd = t.h * p.G + (int)(fl - (long long)tk * p.G);
+        o_at = ((long long)(t.q0 + tk) * p.Hq + hd) * (kD / 8);
+        g_at = ((t.q0 + tk) * p.gate_stride) / 8 + hd * (kD / 8);
+        if (p.gate && t.part < 0)         // the gate on its way to the L2 while the item is computed
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint4*>(p.gate) + g_at),
+                       "r"(2 * kD) : "memory");
+      }
+      // running row max (log2 units), the sum of the probabilities as the MMA multiplies them (the
+      // weights of a row add up to 1), and their sum before that rounding (for lse)
+      float m_run = -INFINITY, l_run = 0.0f, e_run = 0.0f;
+      float factor = p.scale_log2;
+#pragma unroll 1
+      for (int j = t.ta; j < t.tb; ++j, ++T) {
+        const int sb = T & 1, ph = T >> 1;
+        ok = __all_sync(0xffffffffu, wait(&bars.s_full[sb], ph));
+        if (!ok) break;
+        tc_fence_after();
+        // (Q's copy was over before the S product began)
+        if (KV != GDA_KV_BF16 && j == t.ta) factor = qscale[(it & 3) * kPM + r];
+        float hm = -INFINITY;
+        float s[64];
+        if (some) {
+          tmem_ld32(t_row + kTmemS + sb * kPN + 64 * hc, s);
+          tmem_ld32(t_row + kTmemS + sb * kPN + 64 * hc + 32, s + 32);
+          tmem_wait_ld();
+          const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of s[0]
+          if (__any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep))) {
+            const int nh = k_hi - k0, nl = k_lo - k0, nf = p.keep - k0;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= nh || (c < nl && c >= nf)) s[c] = -INFINITY;
+          }
+          float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) e4[c & 3] = fmaxf(e4[c & 3], s[c]);
+          hm = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
+        }
+        // the two halves of the row agree on the tile max (parity-buffered slots); after this
+        // both have read their S, so P may overwrite it
+        xbuf[(sb * 2 + hc) * kPM + r] = hm;
+        tc_fence_before();  // this warp's S reads are ordered before the partner's P writes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.xm[rg][sb]);
+        ok = __all_sync(0xffffffffu, wait(&bars.xm[rg][sb], ph));
+        if (!ok) break;
+        tc_fence_after();
+        if (some) {
+          const float mx = fmaxf(hm, xbuf[(sb * 2 + (1 - hc)) * kPM + r]) * factor;
+          // lazy max: it moves only by more than 2^8, so probabilities stay below 2^8 (both
+          // halves of a row take the same decisions from the same values)
+          float alpha = 1.0f;
+          if (mx > m_run + 8.0f) {
+            alpha = (m_run == -INFINITY) ? 0.0f : exp2f(m_run - mx);
+            l_run *= alpha;
+            e_run *= alpha;
+            m_run = mx;
+          }
+          if (j > t.ta && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            // O must hold PV of the tile before it is rescaled; this warp rescales its half of O
+            ok = __all_sync(0xffffffffu, wait(&bars.p_empty[(T - 1) & 1], (T - 1) >> 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 32) {
+              float o[32];
+              tmem_ld32(t_row + kTmemO + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32(t_row + kTmemO + c0, o);
+            }
+            tmem_wait_st();
+          }
+          // p = 2^(s * factor - m): half a packed FFMA and one SFU op per score (a masked score gives
+          // 2^-inf = 0; a row with no visible key yet uses m = 0); P (16-bit pairs) over the first
+          // half of the S buffer: keys 64 h .. at columns 32 h ..
+          const float mneg = (m_run == -INFINITY) ? 0.0f : -m_run;
+          float f = factor;
+          if (__any_sync(0xffffffffu, fabsf(m_run) > 262144.0f && m_run != -INFINITY)) {
+            // huge scores: the product is rounded first, as in the row max, or its rounding error alone
+            // could be a large exponent
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] *= factor;
+            f = 1.0f;
+          }
+          uint32_t w[32];
+          float2 l2 = make_float2(0.0f, 0.0f), e2 = l2;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 a = fma_f32x2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(f, f),
+                                       make_float2(mneg, mneg));
+            const float2 x = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            w[e] = round_pair<KV>(x);
+            e2 = add_f32x2(e2, x);
+            l2 = add_f32x2(l2, pair_values<KV>(w[e]));
+          }
+          l_run += l2.x + l2.y;
+          e_run += e2.x + e2.y;
+          tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc, w);
+          tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc + 16, w + 16);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[sb]);
+      }
+      if (!ok) break;
+      const bool tiles = t.tb > t.ta;
+      float l = 0.0f, e = 0.0f;
+      if (tiles) {
+        // the row's sums are its two halves' sums: exchanged in the slots of the parity that the
+        // last tile did not use (both halves read them before that tile's exchange)
+        xbuf[((T & 1) * 2 + hc) * kPM + r] = l_run;
+        if (hc == 1) ebuf[r] = e_run;  // (the first half uses it)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.pr[rg]);
+        ok = __all_sync(0xffffffffu, wait(&bars.pr[rg], 2 * it));
+        if (!ok) break;
+        l = xbuf[(T & 1) * 2 * kPM + r] + xbuf[((T & 1) * 2 + 1) * kPM + r];
+        if (hc == 0) e = e_run + ebuf[r];
+      }
+      if (t.part >= 0) {
+        // ---- a part of an item: sums and O as they are, for the joining kernel
+        if (hc == 0 && r < rows) p.part_ml[(size_t)t.part * kPM + r] = make_float4(m_run, l, e, 0.0f);
+        ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
+        if (!ok) break;
+        tc_fence_after();
+        if (some) {
+          float4* dst = p.part_o + (size_t)t.part * 64 * kPM + r;
+#pragma unroll 1
+          for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 32) {
+            float o[32];
+            tmem_ld32(t_row + kTmemO + c0, o);
+            tmem_wait_ld();
+            if (r < rows) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                dst[(size_t)((c0 >> 2) + u) * kPM] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.o_empty);
+          mbar_arrive(&bars.pr[rg]);
+          mbar_arrive(&bars.v_free);
+        }
+        ok = __all_sync(0xffffffffu, wait(&bars.pr[rg], 2 * it + 1));
+        if (!ok) break;
+        ++it;
+        continue;
+      }
+      // ---- epilogue of a whole item.  While the last products run: the sigmoids of this warp's 16
+      // rows, lane l dimensions 8l .. 8l + 7 of each (1 without a gate)
+      constexpr int kRows = 16;
+      uint32_t sg[4 * kRows];
+#pragma unroll
+      for (int y = 0; y < kRows; ++y) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (p.gate) {
+          const long long at = __shfl_sync(0xffffffffu, g_at, y);
+          if (y < nrow) v = __ldcs(reinterpret_cast<const uint4*>(p.gate) + at + lane);
+        }
+        sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
+      }
+      if (p.gate) {
+#pragma unroll
+        for (int y = 0; y < kRows; y += 4) sigmoids<4>(sg + 4 * y, p.table);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4 * kRows; ++x) sg[x] = 0x3F803F80u;
+      }
+      float m = m_run, wo = 1.0f;
+      if (p.sinks && r < rows) join_sink(p, head, m, l, e, wo);
+      if (p.lse && hc == 0 && r < rows) p.lse[(size_t)head * p.Tq + t.q0 + tok] = lse_of(m, e);
+      unsigned char* stage = sm + Lay::kOffV;
+      if (tiles) {
+        const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;  // (a NaN sum comes with NaN in O)
+        // a dead row is 0 also where a value that its block's other rows see was not finite
+        const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
+        ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
+        if (!ok) break;
+        tc_fence_after();
+        // O / l as BF16 into the V buffers (free: the last PV has completed), this warp's 128
+        // columns of its 32 rows: [64-column block][row][128 B], 16-byte chunks swizzled by row
+#pragma unroll 1
+        for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 64) {
+          float o[64];
+          tmem_ld32(t_row + kTmemO + c0, o);
+          tmem_ld32(t_row + kTmemO + c0 + 32, o + 32);
+          tmem_wait_ld();
+          unsigned char* dst = stage + (c0 >> 6) * kBlk + r * 128;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t b4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 v = mul_f32x2(make_float2(o[8 * u + 2 * x], o[8 * u + 2 * x + 1]), make_float2(inv, inv));
+              b4[x] = bf16x2_rn(v.x, v.y) & keep;
+            }
+            *reinterpret_cast<uint4*>(dst + 16 * (u ^ (r & 7))) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.o_empty);  // the next item's PV may start
+          mbar_arrive(&bars.pr[rg]);
+        }
+        ok = __all_sync(0xffffffffu, wait(&bars.pr[rg], 2 * it + 1));  // both halves of these rows are staged
+        if (!ok) break;
+        ++it;
+      }
+#pragma unroll
+      for (int y = 0; y < kRows; ++y) {
+        const int row = w0 + y;
+        const long long at = __shfl_sync(0xffffffffu, o_at, y);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (tiles)
+          v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+        // (a product of two BF16 values, correctly rounded by one instruction)
+        v.x = mul_bf16x2(v.x, sg[4 * y]), v.y = mul_bf16x2(v.y, sg[4 * y + 1]);
+        v.z = mul_bf16x2(v.z, sg[4 * y + 2]), v.w = mul_bf16x2(v.w, sg[4 * y + 3]);
+        if (y < nrow) reinterpret_cast<uint4*>(p.out)[at + lane] = v;
+      }
+      // (generic accesses to the V buffers before the next rows go into them)
+      fence_async_shared();
+      __syncwarp();
+      if (tiles && lane == 0) mbar_arrive(&bars.v_free);
+    }
+    if (!ok) fail();
+  } else if (warp < kGatherWarp) {
+    regs_shrink<kRegsIssue>();
+    if (warp == kPlanWarp) {
+      // ---------------- the share's items, one after the other
+      bool ok = true;
+      Cut at = start;
+      Seq s = {0, 0, 0, 0};
+      int mt = 0;
+      if (at.b < p.B) {
+        s = seq_of(p, at.b);
+        mt = blocks_of(p, s);
+      }
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        Item t = {};
+        t.b = -1;
+        const bool last = at.b == end.b && at.h == end.h && at.i == end.i;  // the share ends in this item
+        if (at.b < p.B && !(last && end.t <= at.t)) {
+          const Range r = range_of(p, s, at.i);
+          t.b = at.b;
+          t.q0 = s.q0, t.nq = s.nq, t.kb = s.kb, t.L = s.L;
+          t.h = at.h, t.i = at.i;
+          t.ta = at.t, t.tb = last ? end.t : r.n;
+          t.f = r.f, t.tl = r.tl, t.lo = r.lo, t.hi = r.hi;
+          t.part = (t.ta > 0) ? 2 * (int)blockIdx.x : (t.tb < r.n) ? 2 * (int)blockIdx.x + 1 : -1;
+        }
+        if (lane == 0) {
+          if (n >= 2) ok = wait(&bars.i_empty[n & 1], (n >> 1) - 1);
+          if (ok) {
+            bars.item[n & 1] = t;
+            mbar_arrive(&bars.i_full[n & 1]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok || t.b < 0) break;
+        if (last) {
+          at = end;
+          at.b = p.B;
+          continue;
+        }
+        at.t = 0;
+        if (++at.i < mt) continue;
+        at.i = 0;
+        if (++at.h < p.Hkv) continue;
+        at.h = 0;
+        // the next sequence with new tokens
+        ++at.b;
+#pragma unroll 1
+        for (bool found = false; at.b < p.B && !found;) {
+          const int b = at.b + lane;
+          int nq = 0;
+          if (b < p.B) nq = seq_of(p, b).nq;
+          const unsigned any = __ballot_sync(0xffffffffu, nq > 0);
+          found = any != 0u;
+          at.b += found ? __ffs(any) - 1 : 32;
+        }
+        at.b = min(at.b, p.B);
+        if (at.b < p.B) {
+          s = seq_of(p, at.b);
+          mt = blocks_of(p, s);
+        }
+      }
+      if (!ok && lane == 0) fail();
+    } else if (lane == 0 && warp == kMmaWarp) {
+      // ---------------- S issuer: S(T) = Q K(T)^T into S buffer T % 2, which P(T - 2) occupied
+      const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK);
+      constexpr uint32_t idS = idesc_of<KV>(kPM, kPN, 0);
+      int it = 0, T = 0, slot = 0, use = 0;
+      int done = -1;  // the tile of the last commit to s_full
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        Item t;
+        ok = get_item(n, &t);
+        if (!ok) break;
+        mbar_arrive(&bars.i_empty[n & 1]);
+        if (t.b < 0) break;
+        if (t.tb == t.ta) continue;
+        ok = wait(&bars.qf, it);
+#pragma unroll 1
+        for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
+          const int sb = T & 1;
+          const int x0 = slot, u0 = use;
+          const int x1 = slot + 1 == kKSlots ? 0 : slot + 1, u1 = slot + 1 == kKSlots ? use + 1 : use;
+          ok = wait(&bars.k_full[x0], u0) && wait(&bars.k_full[x1], u1);
+          if (ok && T >= 2) ok = wait(&bars.p_empty[sb], (T >> 1) - 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t kb = sK + (hh ? x1 : x0) * kHalf;
+#pragma unroll
+            for (int k8 = 0; k8 < 8; ++k8) {
+              const int kk = 8 * hh + k8;  // k-step: head dimensions 16 kk .. 16 kk + 15
+              const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+              const uint64_t bd = sdesc_sw128(kb + ((kk >> 2) & 1) * kBlk + (kk & 3) * 32, 16, 1024);
+              umma_bf16_ss(tmem + kTmemS + sb * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars.k_empty[hh ? x1 : x0]);
+          }
+          umma_commit(&bars.s_full[sb]);
+          done = T;
+          slot = x1 + 1 == kKSlots ? 0 : x1 + 1;
+          use = x1 + 1 == kKSlots ? u1 + 1 : u1;
+        }
+        if (!ok) break;
+        umma_commit(&bars.q_empty);  // (every S product of the item)
+        ++it;
+      }
+      if (!ok) {
+        fail();
+        // the last commit covers every MMA issued before it
+        if (done >= 0) drain(&bars.s_full[done & 1], done >> 1);
+      }
+    } else if (lane == 0 && warp == kPvWarp) {
+      // ---------------- PV issuer: O += P(T) V(T), per 128-dimension half of O
+      const uint32_t sV = smem_u32(sm + Lay::kOffV);
+      constexpr uint32_t idO = idesc_of<KV>(kPM, 128, 1);
+      int it = 0, T = 0, done = -1;
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        Item t;
+        ok = get_item(n, &t);
+        if (!ok) break;
+        mbar_arrive(&bars.i_empty[n & 1]);
+        if (t.b < 0) break;
+        if (t.tb == t.ta) continue;
+        if (it > 0) ok = wait(&bars.o_empty, it - 1);  // the epilogue has read the previous item's O
+#pragma unroll 1
+        for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
+          const int pb = T & 1;
+          ok = wait(&bars.p_full[pb], T >> 1) && wait(&bars.v_full[0], T) && wait(&bars.v_full[1], T);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              // V half hh is MN-major (dims contiguous): LBO = stride between its two 64-dim
+              // blocks, SBO = 8 key rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in
+              // columns 8 kk .. 8 kk + 7 of the S buffer
+              const uint64_t bd = sdesc_sw128(sV + hh * kHalf + kk * 16 * 128, kBlk, 1024);
+              umma_bf16_ts(tmem + kTmemO + 128 * hh, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO,
+                           (j > t.ta || kk > 0) ? 1u : 0u);
+            }
+            umma_commit(&bars.v_empty[hh]);
+          }
+          umma_commit(&bars.p_empty[pb]);
+          done = T;
+        }
+        if (!ok) break;
+        umma_commit(&bars.o_full);
+        ++it;
+      }
+      if (!ok) {
+        fail();
+        if (done >= 0) drain(&bars.p_empty[done & 1], done >> 1);
+      }
+    }
+  } else {
+    regs_shrink<kRegsGather>();
+    // ---------------- gatherers: warps 12, 13 take Q and K, 14, 15 V; each 64 of a tile's 128 rows.
+    // A half tile (128 dimensions of every key) goes into the next slot of its ring once the MMAs
+    // that read the slot's previous half have completed.  BF16 rows are copied asynchronously
+    // (cp.async), and a half's barrier is arrived at when a later one has been started or there is
+    // nothing else to do; codes go through registers, widened to FP16.
+    const bool is_v = warp >= kGatherWarp + 2;
+    const int r64 = 64 * (warp & 1);                 // this warp's first row of a tile
+    const int slots = is_v ? 2 : kKSlots;
+    unsigned char* ring = sm + (is_v ? Lay::kOffV : Lay::kOffK);
+    uint64_t* full = is_v ? bars.v_full : bars.k_full;
+    uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+    const unsigned char* pool = is_v ? p.v_pool : p.k_pool;
+    int it = 0, slot = 0, use = 0;
+    bool ok = true;
+    int pend = 0;                                    // copies started whose barrier was not arrived at
+    uint64_t *pb0 = nullptr, *pb1 = nullptr, *pb2 = nullptr;
+    auto signal_oldest = [&]() {
+      if (pend == 1) cp_async_wait<0>();
+      else if (pend == 2) cp_async_wait<1>();
+      else cp_async_wait<2>();
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pb0);
+      pb0 = pb1;
+      pb1 = pb2;
+      --pend;
+    };
+    auto started = [&](uint64_t* bar) {
+      if (KV == GDA_KV_BF16) {
+        cp_async_commit();
+        if (pend == 0) pb0 = bar;
+        else if (pend == 1) pb1 = bar;
+        else pb2 = bar;
+        ++pend;
+      } else {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      }
+    };
+    // waits, arriving at what is complete meanwhile
+    auto acquire = [&](uint64_t* bar, int parity) -> bool {
+      if (KV == GDA_KV_BF16) {
+        while (pend > 0) {
+          if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
+          signal_oldest();
+        }
+      }
+      return __all_sync(0xffffffffu, wait(bar, parity));
+    };
+    for (int n = 0;; ++n) {
+      ok = acquire(&bars.i_full[n & 1], n >> 1);
+      if (!ok) break;
+      const Item t = bars.item[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
+      if (t.b < 0) break;
+      if (t.tb == t.ta) continue;
+      if (is_v && it > 0) ok = acquire(&bars.v_free, it - 1);  // the previous item's outputs have left the buffers
+      // the slots of rows r64 + lane and r64 + 32 + lane of tile j: -1 where no row of the item
+      // sees the position (zeros then)
+      int nx[2];
+      auto look_up = [&](int j) {
+        const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + r64 + lane;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int pos = base + 32 * x;
+          int sl = -1;
+          if (pos < t.hi && (pos >= t.lo || pos < p.keep)) {
+            sl = __ldg(p.indices + t.kb + pos);
+            if (sl < 0 || (long long)sl >= p.num_slots) {  // a row outside the pools reads as zeros
+              atomicOr(p.error, kErrIndex);
+              sl = -1;
+            }
+          }
+          nx[x] = sl;
+        }
+      };
+      if (ok) look_up(t.ta);
+#pragma unroll 1
+      for (int j = t.ta; j < t.tb && ok; ++j) {
+        const int sl0 = nx[0], sl1 = nx[1];
+        if (j + 1 < t.tb) look_up(j + 1);
+#pragma unroll 1
+        for (int hh = 0; hh < 2 && ok; ++hh) {
+          unsigned char* dst = ring + slot * kHalf;
+          if (KV == GDA_KV_BF16) {
+            if (pend == 3) signal_oldest();
+            if (use > 0) ok = acquire(&empty[slot], use - 1);
+            if (!ok) break;
+            // two rows (256 bytes each) per step
+            const uint32_t d0 = smem_u32(dst) + ((lane & 15) >> 3) * kBlk + (r64 + (lane >> 4)) * 128;
+#pragma unroll 8
+            for (int x = 0; x < 32; ++x) {
+              const int sl = __shfl_sync(0xffffffffu, x < 16 ? sl0 : sl1, (2 * x + (lane >> 4)) & 31);
+              const unsigned char* src =
+                  pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + hh * kD + (lane & 15) * 16;
+              cp_async16(d0 + x * 256 + (((lane & 7) ^ ((2 * x + (lane >> 4)) & 7)) << 4), src, sl >= 0 ? 16 : 0);
+            }
+          } else if (KV == GDA_KV_E4M3) {
+            // four rows (128 codes each) per step, eight steps' loads in flight
+#pragma unroll 1
+            for (int y = 0; y < 2 && ok; ++y) {
+              uint4 raw[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int sl = __shfl_sync(0xffffffffu, y ? sl1 : sl0, 4 * x + (lane >> 3));
+                raw[x] = make_uint4(0u, 0u, 0u, 0u);
+                if (sl >= 0)
+                  raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + ((size_t)sl * p.Hkv + t.h) * kD + hh * 128) + (lane & 7));
+              }
+              if (y == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
+              if (!ok) break;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int row = r64 + 32 * y + 4 * x + (lane >> 3), c = 2 * (lane & 7);
+                unsigned char* at = dst + (c >> 3) * kBlk + row * 128;
+                *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
+                *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
+              }
+            }
+          } else {
+            // eight rows (64 bytes of codes, 8 scales) per step
+            uint4 raw[8];
+            uint32_t sc[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int sl = __shfl_sync(0xffffffffu, x < 4 ? sl0 : sl1, (8 * x + (lane >> 2)) & 31);
+              raw[x] = make_uint4(0u, 0u, 0u, 0u);
+              sc[x] = 0u;
+              if (sl >= 0) {
+                const size_t row = (size_t)sl * p.Hkv + t.h;
+                raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + row * kCodeBytes + hh * 64) + (lane & 3));
+                sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + row * kScalePair + (is_v ? kScaleBytes : 0) + hh * 8) +
+                              (lane & 3));
+              }
+            }
+            if (use > 0) ok = acquire(&empty[slot], use - 1);
+            if (!ok) break;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int row = r64 + 8 * x + (lane >> 2), c = 4 * (lane & 3);
+              const uint32_t f = e4m3x2_to_f16x2(sc[x]);
+              const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+              unsigned char* at = dst + (c >> 3) * kBlk + row * 128;
+              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
+              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
+              *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
+              *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
+            }
+          }
+          if (!ok) break;
+          started(&full[slot]);
+          if (++slot == slots) {
+            slot = 0;
+            ++use;
+          }
+        }
+        if (ok && !is_v && j == t.ta) {
+          // Q behind the first K tile (it needs the previous item's last S product): a row per step,
+          // zeros in rows past the item's last
+          if (it > 0) ok = acquire(&bars.q_empty, it - 1);
+          if (KV == GDA_KV_BF16 && pend == 3) signal_oldest();
+          if (!ok) break;
+          const long long flat0 = (long long)t.i * kPM + r64, rows = (long long)t.nq * p.G;
+          int tok = (int)(flat0 / p.G), g = (int)(flat0 - (long long)tok * p.G);
+          unsigned char* dq = sm + Lay::kOffQ + (lane >> 3) * kBlk + r64 * 128;
+#pragma unroll 1
+          for (int x0 = 0; x0 < 64; x0 += 8) {
+            uint4 raw[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const bool in = flat0 + x0 + x < rows;
+              const __nv_bfloat16* src =
+                  p.q + (in ? (long long)(t.q0 + tok) * p.q_stride + (long long)(t.h * p.G + g) * kD : 0) + lane * 8;
+              if (KV == GDA_KV_BF16)
+                cp_async16(smem_u32(dq + (x0 + x) * 128 + (((lane & 7) ^ x) << 4)), src, in ? 16 : 0);
+              else
+                raw[x] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+              if (++g == p.G) {
+                g = 0;
+                ++tok;
+              }
+            }
+            if (KV != GDA_KV_BF16) {
+              // in FP16, each row times a power of two that brings its largest element to [1, 2): exact but
+              // for elements 2^-14 of that and less, which lose bits below 2^-24 of it
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const uint32_t w4[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+                uint32_t top = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7FFF0000u, w4[e] & 0x7FFF0000u));
+                top = __reduce_max_sync(0xffffffffu, top) >> 23;      // its exponent
+                // (0 and subnormals, and infinities and NaNs, stay as they are)
+                const int ex = (top == 0u || top == 255u) ? 127 : min(max((int)top, 30), 250);
+                const float up = __uint_as_float((uint32_t)(254 - ex) << 23);   // 2^(127 - ex)
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  o[e] = f16x2_rn(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xFFFF0000u) * up);
+                *reinterpret_cast<uint4*>(dq + (x0 + x) * 128 + (((lane & 7) ^ x) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (lane == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
+                  qscale[(it & 3) * kPM + r64 + x0 + x] =
+                      fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
+              }
+            }
+          }
+          started(&bars.qf);
+        }
+      }
+      if (!ok) break;
+      ++it;
+    }
+    if (KV == GDA_KV_BF16) {
+      while (ok && pend > 0) signal_oldest();
+      cp_async_wait<0>();
+    }
+    if (!ok) fail();
+  }
+
+  // ---- teardown: every role is done (or gave up and waited for what it started)
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the item that the start of share c = blockIdx.x + 1 cuts first:
+//   m = max m_k, w_k = 2^(m_k - m), O = sum w_k O_k / (sum w_k l_k + sink)
+// in the order of the shares.  blockIdx.y takes an eighth of the dimensions; a thread has four
+// dimensions of a row, neighbouring threads neighbouring rows (as the parts are laid out).
+constexpr int kJoinThreads = 256, kJoinY = 8;
+__global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ int part[kPagedMaxCtas + 1];
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int c = blockIdx.x + 1, tid = threadIdx.x;
+  const int ctas = p.cuts[0].x;
+  if (c >= ctas) return;
+  const int4 me = p.cuts[1 + c], before = p.cuts[c];
+  auto same = [&](const int4& a) { return a.x == me.x && a.y == me.y && a.z == me.z; };
+  if (me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
+  // the parts: share c - 1's last one, then the first ones of the shares that start in the item
+  int mine = -1;
+  bool in = false;
+  if (c + tid < ctas) {
+    const int4 a = p.cuts[1 + c + tid];
+    in = same(a);
+    if (in) {
+      const int4 z = c + tid + 1 < ctas ? p.cuts[2 + c + tid] : make_int4(p.B, 0, 0, 0);
+      if (!same(z) || z.w > a.w) mine = 2 * (c + tid);   // (else the share is empty)
+    }
+  }
+  if (in) part[1 + tid] = mine;
+  if (tid == 0) part[0] = 2 * (c - 1) + 1;
+  const int parts = 1 + __syncthreads_count(in);
+  const Seq s = seq_of(p, me.x);
+  const long long flat0 = (long long)me.z * kPM;
+  const int rows = (int)min((long long)kPM, (long long)s.nq * p.G - flat0);
+  constexpr int kCols = 64 / kJoinY;
+  for (int x = tid; x < rows * kCols; x += kJoinThreads) {
+    const int r = x % rows, c4 = blockIdx.y * kCols + x / rows;
+    const int tok = (int)((flat0 + r) / p.G), head = me.y * p.G + (int)((flat0 + r) - (long long)tok * p.G);
+    float m = -INFINITY;
+    for (int k = 0; k < parts; ++k)
+      if (part[k] >= 0) {
+        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kPM + r);
+        if (!(a.x <= m)) m = a.x;   // (a NaN stays)
+      }
+    float l = 0.0f, e = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < parts; ++k)
+      if (part[k] >= 0) {
+        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kPM + r);
+        if (a.y == 0.0f) continue;  // no visible key in this part
+        const float w = exp2f(a.x - m);
+        const float4 v = __ldcg(p.part_o + ((size_t)part[k] * 64 + c4) * kPM + r);
+        l += w * a.y;
+        e += w * a.z;
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+    float wo = 1.0f;
+    if (p.sinks) join_sink(p, head, m, l, e, wo);
+    if (p.lse && c4 == 0) p.lse[(size_t)head * p.Tq + s.q0 + tok] = lse_of(m, e);
+    const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;
+    const bool dead = l == 0.0f || wo == 0.0f;
+    uint32_t lo = dead ? 0u : bf16x2_rn(o.x * inv, o.y * inv), hi = dead ? 0u : bf16x2_rn(o.z * inv, o.w * inv);
+    if (p.gate) {
+      const uint2 g = __ldg(reinterpret_cast<const uint2*>(p.gate + (long long)(s.q0 + tok) * p.gate_stride +
+                                                           (long long)head * kD) + c4);
+      const uint32_t slo = (uint32_t)sigmoid_bf16((uint16_t)g.x) | ((uint32_t)sigmoid_bf16((uint16_t)(g.x >> 16)) << 16);
+      const uint32_t shi = (uint32_t)sigmoid_bf16((uint16_t)g.y) | ((uint32_t)sigmoid_bf16((uint16_t)(g.y >> 16)) << 16);
+      lo = mul_bf16x2(lo, slo);
+      hi = mul_bf16x2(hi, shi);
+    }
+    reinterpret_cast<uint2*>(p.out + ((size_t)(s.q0 + tok) * p.Hq + head) * kD)[c4] = make_uint2(lo, hi);
+  }
+}
+
+namespace {
+
+template <int KV>
+cudaError_t launch(const PagedParams& p, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<KV>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_paged_kernel<KV>, p);
+}
+template <int KV>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(prefill_paged_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Layout<KV>::kBytes);
+}
+
+}  // namespace
+
+cudaError_t paged_init() {
+  cudaError_t e = allow_smem<GDA_KV_BF16>();
+  if (e == cudaSuccess) e = allow_smem<GDA_KV_E4M3>();
+  if (e == cudaSuccess) e = allow_smem<GDA_KV_E2M1>();
+  return e;
+}
+
+cudaError_t launch_prefill_paged(const PagedParams& params, int kv_dtype, cudaStream_t stream) {
+  PagedParams p = params;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  e = prefill_init(dev, stream);
+  if (e == cudaSuccess) e = sigmoid_table(&p.table);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
+  if (kv_dtype == GDA_KV_BF16) e = launch<GDA_KV_BF16>(p, grid, stream);
+  else if (kv_dtype == GDA_KV_E4M3) e = launch<GDA_KV_E4M3>(p, grid, stream);
+  else e = launch<GDA_KV_E2M1>(p, grid, stream);
+  if (e != cudaSuccess || grid < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(grid - 1), kJoinY);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_paged_join_kernel, p);
+}
+
+}  // namespace gda

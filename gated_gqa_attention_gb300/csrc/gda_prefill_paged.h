@@ -1,0 +1,56 @@
+// gda_prefill_paged.h -- launch interface between the C ABI (gda_api.cu) and the attention of new
+// tokens over a paged cache.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gda {
+
+struct PagedParams {
+  const __nv_bfloat16* q;      // [Tq, Hq, 256], token t at t * q_stride elements
+  const __nv_bfloat16* gate;   // likewise, or nullptr
+  long long q_stride, gate_stride;
+  const unsigned char* k_pool; // [num_slots, Hkv, row] of the cache's type
+  const unsigned char* v_pool;
+  const unsigned char* scales; // 4-bit: [num_slots, Hkv, 2, 16]
+  long long num_slots;
+  const int* cu_q;             // [B + 1] first new token of each sequence
+  const int* indptr;           // [B + 1] first entry of `indices` of each sequence
+  const int* indices;          // [nnz] slot of every position
+  __nv_bfloat16* out;          // [Tq, Hq, 256]
+  float* lse;                  // [Hq, Tq] natural log, or nullptr
+  const float* sinks;          // [Hq] sink logits (natural units), or nullptr
+  unsigned int* error;         // device error word
+  int B, Tq, nnz, Hq, Hkv, G;
+  int window, keep;            // window > 0: the last `window` positions and the first `keep`
+  float scale_log2;            // scale * k_descale * log2(e)
+  float v_descale;
+  long long wait_limit;
+  const uint16_t* table;       // BF16 sigmoid of every BF16 code
+  // workspace: where the CTAs' shares start, and what shares that cut an item leave of it
+  int4* cuts;                  // [kPagedMaxCtas + 1]: {CTAs with a share, -, -, -}, then each CTA's start
+  float4* part_ml;             // [2 kPagedMaxCtas][128] {row max (log2), sum, unrounded sum, -}
+  float4* part_o;              // [2 kPagedMaxCtas][64][128]: four dimensions of a row
+};
+
+constexpr int kPagedMaxCtas = 160;
+// bytes of each part of the workspace
+constexpr size_t kPagedCutBytes = 4096;
+constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxCtas * 128 * 16;
+constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxCtas * 64 * 128 * 16;
+static_assert((kPagedMaxCtas + 1) * 16 <= kPagedCutBytes, "cut table");
+
+// The most 128-row blocks (rows: a token's query heads of one KV head, token after token) that B
+// sequences of `tokens` tokens in all can have.
+inline long long paged_blocks(long long tokens, long long G, long long B) {
+  const long long n = tokens * G / 128 + B;
+  return n < tokens * G ? n : tokens * G;
+}
+
+// kv_dtype: GDA_KV_* of the pools
+cudaError_t launch_prefill_paged(const PagedParams& p, int kv_dtype, cudaStream_t stream);
+cudaError_t paged_init();  // the kernels' attributes on the current device
+
+}  // namespace gda

@@ -268,6 +268,26 @@ int gda_kv_gather_fp4(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_
                       const int32_t* indices, int64_t N, float k_descale, float v_descale, gda_bf16* k_out,
                       gda_bf16* v_out, int Hkv, int D, gda_stream_t stream);
 
+/* Quantise the K and V rows of T tokens into an 8-bit cache (GDA_KV_E4M3 above), which gda_decode_e4m3,
+ * gda_decode_ex and gda_prefill_paged attend over:
+ *   code = nearest e4m3 to x / descale, the quotient taken in FP32 (IEEE), ties to even, beyond 448
+ *   (infinities too) 448; a NaN keeps as a NaN
+ *   k, v       [T, Hkv, D] bf16 with token strides, slots [T] int32: as gda_kv_write_fp4
+ *   k_pool, v_pool  [num_slots, Hkv, D] bytes (16-byte aligned)
+ * Descales have to be finite and > 0 (GDA_ERR_ARG).  D = 256 (else GDA_ERR_UNSUPPORTED).
+ * Enqueues one kernel; T = 0 enqueues nothing. */
+int gda_kv_write_e4m3(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, int64_t v_stride, const int32_t* slots,
+                      int64_t num_slots, uint8_t* k_pool, uint8_t* v_pool, float k_descale, float v_descale, int64_t T,
+                      int Hkv, int D, gda_stream_t stream);
+
+/* Read rows of an 8-bit cache back as BF16:
+ *   k_out[n, h, :] = RNE_bf16(k_descale * e4m3(K codes of slot indices[n])), v_out likewise,
+ * [N, Hkv, D] bf16.  An index outside [0, num_slots) gives zeros; indices may repeat.
+ * Descales have to be finite.  D = 256.  Enqueues one kernel; N = 0 enqueues nothing. */
+int gda_kv_gather_e4m3(const uint8_t* k_pool, const uint8_t* v_pool, int64_t num_slots, const int32_t* indices, int64_t N,
+                       float k_descale, float v_descale, gda_bf16* k_out, gda_bf16* v_out, int Hkv, int D,
+                       gda_stream_t stream);
+
 /* Prefill / extend gated SDPA (cuDNN FE-OSS "Gated Attention Block (SM107)", Overview
  * stages (4) SDPA with GQA H_q / H_kv and (5) the gate; Fusion knobs: fuse_gate puts
  * O *= sigmoid(GATE) in the SDPA epilogue, after the dead-row select; Forward:
@@ -339,6 +359,74 @@ typedef struct gda_packed_args {
 } gda_packed_args;
 
 int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
+
+/*
+ * Gated attention of each sequence's newest tokens over its rows of a paged cache: a chunk of a
+ * prompt behind a cached prefix, drafted tokens behind a user's last one, a decode step's single
+ * tokens, or a batch of all of these.  The new tokens' own rows are in the cache already.
+ * Sequence b has the tokens [cu_seqlens[b], cu_seqlens[b + 1]) of q and L = kv_indptr[b + 1] -
+ * kv_indptr[b] positions, the new tokens last: its query i is at position p = L - tokens + i and
+ * sees key j <= p, with window > 0 only where j > p - window or j < keep_first:
+ *   s_j = scale * q . K[slot_j, h / G],  slot_j = kv_indices[kv_indptr[b] + j]
+ *   O   = sum_j e^{s_j} V[slot_j, h / G] / (e^{sinks[h]} + sum_j e^{s_j})     (sinks NULL: no term)
+ *   out = RNE_bf16(RNE_bf16(O) * RNE_bf16(sigmoid(gate)))
+ *   q, gate   [total_q, Hq, D] bf16, token t at t * q_stride and t * gate_stride elements (multiples of
+ *             8; heads and dimensions of a token contiguous); gate NULL: out = RNE_bf16(O)
+ *   k_pool, v_pool, kv_scales, kv_dtype, k_descale, v_descale  the cache, as in gda_args (a BF16, an
+ *             e4m3 or a 4-bit one); descales have to be finite and > 0 (GDA_ERR_ARG)
+ *   num_slots rows in the pools.  A position that some query sees and whose slot is outside
+ *             [0, num_slots) reads as a row of zeros, and GDA_DEVERR_INDEX is set in the error word
+ *   cu_seqlens  [B + 1] int32, device, non-decreasing; sequences may be empty, and rows may lie before
+ *             the first or behind the last one.  kv_indptr  [B + 1] int32, device, non-decreasing.
+ *             Their contents are not checked: values are clamped to the tensors (total_q tokens,
+ *             nnz positions), so nothing outside them is read or written
+ *   kv_indices  [nnz] int32; a slot may be named any number of times
+ *   out       [total_q, Hq, D] bf16, contiguous, apart from the inputs.  Rows of no sequence are left
+ *             as they are
+ *   lse       [Hq, total_q] float or NULL: natural log of the divisor above
+ *   sinks     [Hq] float sink logits or NULL
+ *   window    0: all positions up to the query's own; else its last `window` ones and the sequence's
+ *             first keep_first (keep_first without a window has no effect)
+ *   error_word  as gda_prefill; gda_prefill_read_error reads the library's
+ * A query that sees no key (more tokens than positions) gives out = 0, lse = -inf or its sink.
+ * Positions that no query of the 128 rows computed together (the query heads of neighbouring tokens)
+ * sees are not read.  Within these a non-finite V row that one query sees may also reach another
+ * that does not see it (its probability there is 0, and 0 times it is NaN); other sequences' rows and
+ * those behind a sequence's end never do.
+ * scale must be finite and > 0, and scale * k_descale a normal FP32 value (GDA_ERR_ARG).  D = 256.
+ * The workspace (gda_prefill_paged_workspace_bytes, 256-byte aligned, contents free before and after
+ * the call) must not be shared by calls that may overlap.  The first call on a device and stream
+ * capture are as for gda_prefill.  The lengths are read on the device: two kernels, no read back,
+ * no plan to keep, and a captured call follows cu_seqlens, kv_indptr and kv_indices as they are at
+ * each replay.  Results do not depend on timing: the same call gives the same bits.
+ */
+typedef struct gda_paged_args {
+    const gda_bf16* q;
+    const gda_bf16* gate;
+    int64_t q_stride, gate_stride;
+    const void* k_pool;
+    const void* v_pool;
+    const uint8_t* kv_scales;
+    int64_t num_slots;
+    const int32_t* cu_seqlens;
+    const int32_t* kv_indptr;
+    const int32_t* kv_indices;
+    gda_bf16* out;
+    float* lse;
+    const float* sinks;
+    int64_t total_q, nnz;
+    int B, Hq, Hkv, D;
+    float scale;
+    int window, keep_first;
+    int kv_dtype;
+    float k_descale, v_descale;
+    uint32_t* error_word;
+} gda_paged_args;
+
+/* Bytes of workspace gda_prefill_paged needs for these sizes (0 for invalid ones). */
+size_t gda_prefill_paged_workspace_bytes(int64_t total_q, int B, int Hq, int Hkv, int D);
+
+int gda_prefill_paged(const gda_paged_args* args, void* workspace, size_t workspace_bytes, gda_stream_t stream);
 
 /* The library's prefill error word (used when gda_prefill gets error_word == NULL) on
  * the current device: synchronises `stream`, stores the bits in *error_word, clears

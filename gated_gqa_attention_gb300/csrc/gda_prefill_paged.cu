@@ -7,16 +7,20 @@
 //   O   = sum_j e^(s_j) v_j / (e^(sink_h) + sum_j e^(s_j)),  s_j = scale * q . k_j   (no key: O = 0)
 //   out = RNE_bf16(RNE_bf16(O) * RNE_bf16(sigmoid(gate))),  lse = log of the divisor
 //
-// Rows.  The G query heads of a KV head read the same keys, so an item is 128 rows of (token, head)
-// pairs of one KV head, token after token: one token of 8 heads fills 8 rows, 16 tokens all 128.
+// Rows.  The G query heads of a KV head read the same keys, so an item is 256 rows of (token, head)
+// pairs of one KV head, token after token: one token of 8 heads fills 8 rows, 32 tokens all 256.
 // Its keys come in tiles of 128 positions; tiles that no row of the item sees are left out.
 //
+// Pairs.  A cluster of two CTAs computes an item, 128 rows in each, by MMAs of the pair (M = 256):
+// every gathered row is read once per 256 rows, a CTA gathers half of it (64 keys of K, half the
+// dimensions of V) and its shared memory holds three K tiles and two V tiles that way.
+//
 // Shares.  The lengths are on the device.  The items, by sequence, KV head and block, form one
-// stream in which an item costs its tiles and a constant; each CTA takes an equal share of it.  An
-// item that a share's end cuts is computed in parts: each CTA leaves its part (row max, sum,
-// unnormalised O in FP32) in the workspace, at most two per CTA, and a second kernel joins them in
-// the order of the shares, so a result does not depend on which CTA ends first.  What an item costs
-// is taken as linear in its number within the sequence, so that sums over items have a closed form.
+// stream in which an item costs its tiles and a constant; each pair takes an equal share of it.  An
+// item that a share's end cuts is computed in parts: each pair leaves its part (row max, sum,
+// unnormalised O in FP32) in the workspace, at most two per pair, and a second kernel joins them in
+// the order of the shares, so a result does not depend on which ends first.  What an item costs is
+// taken as linear in its number within the sequence, so that sums over items have a closed form.
 #include "gda.h"
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
@@ -28,7 +32,8 @@ namespace gda {
 
 namespace {
 
-constexpr int kPM = 128;            // rows per item (MMA M)
+constexpr int kPM = 128;            // rows of an item per CTA (half the MMA's M)
+constexpr int kRowsI = kPagedRows;  // rows of an item
 constexpr int kPN = 128;            // keys per tile (MMA N of S)
 constexpr int kSoftmaxWarps = 8;    // warps 0-7
 constexpr int kPlanWarp = 8, kMmaWarp = 9, kPvWarp = 11;
@@ -43,7 +48,8 @@ static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsGather <= 4 * 128, "register 
 constexpr int kItemCost = 4;        // of an item besides its tiles, in half tiles
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
-constexpr uint32_t kHalf = 2 * kBlk;               // a half tile: 2 column blocks, 32 KiB
+constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
+constexpr uint32_t kKBlk = kBlk / 2;               // K: a 64-column block of its 64 keys
 
 template <int KV>
 struct Layout {
@@ -63,8 +69,8 @@ struct Item {
   int b;               // sequence (-1: no more items)
   int q0, nq;          // its first new token, their number
   int kb, L;           // first entry of `indices`, positions
-  int h, i;            // KV head, block of 128 rows
-  int ta, tb;          // this CTA's tiles of the item's
+  int h, i;            // KV head, block of 256 rows
+  int ta, tb;          // this share's tiles of the item's
   int f, tl;           // tile t holds positions from 128 t (t < f) or 128 (t - f + tl) on
   int lo, hi;          // positions that any row sees: [lo, hi) and those below p.keep
   int part;            // -1: the whole item, else where its part goes
@@ -73,8 +79,10 @@ struct Cut {           // a place in the stream: block i of KV head h of sequenc
   int b, h, i, t;
 };
 struct Bars {
-  uint64_t qf, q_empty;                             // Q landed; the item's S products have read it
-  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  // *_land: this CTA's part of Q, K, V has landed (every gathering thread arrives); *_peer, in rank 0:
+  // rank 1's has; p_full and o_empty, in rank 0, count both CTAs' warps; commits arrive in both
+  uint64_t q_land, q_peer, q_empty;                 // (q_empty: the item's S products have read it)
+  uint64_t k_land[3], k_peer[3], k_empty[3], v_land[2], v_peer[2], v_empty[2];
   uint64_t s_full[2], p_full[2], p_empty[2];        // per S / P buffer
   uint64_t xm[4][2];                                // per row quarter and tile parity: both maxima stored
   uint64_t pr[4];                                   // per row quarter: both halves' epilogues are here
@@ -86,7 +94,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 constexpr int kGatherWarps = 4;                     // 2 each
-constexpr int kItemReaders = 2 + kGatherWarps + kSoftmaxWarps;  // both issuers, gatherers, softmax
+constexpr int kItemReaders = 2 + kGatherWarps + kSoftmaxWarps;  // issuers (rank 1: their relays), gatherers, softmax
 
 // ---- the stream of items
 
@@ -104,7 +112,7 @@ __device__ __forceinline__ Seq seq_of(const PagedParams& p, int b) {
   return s;
 }
 __device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) {
-  return (int)(((long long)s.nq * p.G + kPM - 1) >> 7);
+  return (int)(((long long)s.nq * p.G + kRowsI - 1) / kRowsI);
 }
 // block i of a sequence: what its rows see, and its tiles
 struct Range {
@@ -112,8 +120,8 @@ struct Range {
 };
 __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, int i) {
   Range r;
-  const int ta = (int)(((long long)i * kPM) / p.G);                              // first and last token
-  const int tb = (int)min((long long)s.nq - 1, ((long long)i * kPM + kPM - 1) / p.G);
+  const int ta = (int)(((long long)i * kRowsI) / p.G);                              // first and last token
+  const int tb = (int)min((long long)s.nq - 1, ((long long)i * kRowsI + kRowsI - 1) / p.G);
   const int off = s.L - s.nq;
   r.hi = max(off + tb + 1, 0);
   r.lo = p.window > 0 ? (int)min(max((long long)off + ta - p.window + 1, 0LL), (long long)r.hi) : 0;
@@ -178,9 +186,7 @@ __device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w, uint32_t scale2) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -230,7 +236,7 @@ __device__ __forceinline__ float lse_of(float m, float e) {
 }  // namespace
 
 template <int KV>
-__global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid_constant__ PagedParams p) {
   using Lay = Layout<KV>;
   constexpr int kKSlots = Lay::kKSlots;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -248,19 +254,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
   float* ebuf = reinterpret_cast<float*>(sm + Lay::kOffE);
   float* qscale = reinterpret_cast<float*>(sm + Lay::kOffScale);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), share = blockIdx.x >> 1, shares = gridDim.x >> 1;
 
   if (tid == 0) {
-    mbar_init(&bars.qf, 2);
+    mbar_init(&bars.q_land, 64);
+    mbar_init(&bars.q_peer, 1);
     mbar_init(&bars.q_empty, 1);
     for (int x = 0; x < kKSlots; ++x) {
-      mbar_init(&bars.k_full[x], 2);
+      mbar_init(&bars.k_land[x], 64);
+      mbar_init(&bars.k_peer[x], 1);
       mbar_init(&bars.k_empty[x], 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars.v_full[x], 2);
+      mbar_init(&bars.v_land[x], 64);
+      mbar_init(&bars.v_peer[x], 1);
       mbar_init(&bars.v_empty[x], 1);
       mbar_init(&bars.s_full[x], 1);
-      mbar_init(&bars.p_full[x], kSoftmaxWarps);
+      mbar_init(&bars.p_full[x], 2 * kSoftmaxWarps);
       mbar_init(&bars.p_empty[x], 1);
       mbar_init(&bars.i_full[x], 1);
       mbar_init(&bars.i_empty[x], kItemReaders);
@@ -271,14 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       mbar_init(&bars.pr[q4], 2);
     }
     mbar_init(&bars.o_full, 1);
-    mbar_init(&bars.o_empty, kSoftmaxWarps);
+    mbar_init(&bars.o_empty, 2 * kSoftmaxWarps);
     mbar_init(&bars.v_free, kSoftmaxWarps);
     bars.abort = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&bars.tmem, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&bars.tmem, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   // (as a programmatic dependent: the set-up above ran during the previous kernel's end, whose
@@ -286,11 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // ---- this CTA's share [start, end) of the stream: a thread per sequence (512 at a time); the sums
+  // ---- this pair's share [start, end) of the stream: a thread per sequence (512 at a time); the sums
   // and the two places are exchanged in shared memory that the roles use later
   long long* wsum = reinterpret_cast<long long*>(sm + Lay::kOffX);       // [16]
   Cut* place = reinterpret_cast<Cut*>(sm + Lay::kOffX + 256);            // start, end
-  int ctas = 0;
+  int used = 0;   // shares
   {
     long long total = 0, x0 = 0, x1 = 0;
     Seq s = {0, 0, 0, 0};
@@ -333,21 +343,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       }
       if (pass == 0) {
         total = sum;
-        // no CTA gets less than a tile's worth
-        ctas = (int)max(1LL, min((long long)gridDim.x, total / 2));
-        const int c = blockIdx.x;
-        x0 = c < ctas ? total * c / ctas : total;
-        x1 = c + 1 < ctas ? total * (c + 1) / ctas : total;
+        // none is less than a tile's worth
+        used = (int)max(1LL, min((long long)shares, total / 2));
+        x0 = share < used ? total * share / used : total;
+        x1 = share + 1 < used ? total * (share + 1) / used : total;
       }
     }
   }
   __syncthreads();
-  tc_fence_after();
   const Cut start = place[0], end = place[1];
-  __syncthreads();
-  if (tid == 0) {
-    if (blockIdx.x == 0) p.cuts[0] = make_int4(ctas, 0, 0, 0);
-    p.cuts[1 + blockIdx.x] = make_int4(start.b, start.h, start.i, start.t);
+  __syncwarp();
+  // both CTAs' barriers are set up, and `place` has been read
+  cluster_sync_all();
+  tc_fence_after();
+  if (tid == 0 && rank == 0) {
+    if (share == 0) p.cuts[0] = make_int4(used, 0, 0, 0);
+    p.cuts[1 + share] = make_int4(start.b, start.h, start.i, start.t);
   }
 
   const uint32_t tmem = bars.tmem;
@@ -355,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
   auto fail = [&]() {
     if (bars.abort == 0) atomicOr(p.error, kErrTimeout);
     bars.abort = 1;
+    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(cluster_addr(&bars.abort, rank ^ 1)) : "memory");  // (alive until the end)
   };
   // (short: the roles' code shares one instruction cache, and this is in it many times.  A
   // limit below the default is the failure-path test's: polls then hardly suspend.)
@@ -369,6 +381,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
     } while (!mbar_try_wait_for(bar, parity & 1, hint));
     return true;
   };
+  // of the issuers, in rank 0: barriers that both CTAs arrive on
+  auto wait_both = [&](uint64_t* bar, int parity) -> bool {
+    if (mbar_try_wait_cluster(bar, parity & 1, hint)) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    do {
+      if (*abort_flag || clock64() - t0 > limit) return false;
+    } while (!mbar_try_wait_cluster(bar, parity & 1, hint));
+    return true;
+  };
+  auto arrive_first = [&](uint64_t* bar) { mbar_arrive_cluster(cluster_addr(bar, 0)); };  // rank 0's barrier
   // what a role started is waited for with the default limit, whatever the abort flag says
   auto drain = [&](uint64_t* bar, int parity) {
     const long long t0 = clock64();
@@ -401,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       if (!ok) break;
       if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
       if (t.b < 0) break;
-      const long long rows = (long long)t.nq * p.G - (long long)t.i * kPM;  // of the item (128 at most count)
-      const long long flat = (long long)t.i * kPM + r;
+      const long long flat0 = (long long)t.i * kRowsI + rank * kPM;         // this CTA's first row
+      const long long rows = (long long)t.nq * p.G - flat0;                 // (128 at most count)
+      const long long flat = flat0 + r;
       const int tok = (int)(flat / p.G), head = t.h * p.G + (int)(flat - (long long)tok * p.G);
       // keys that this row sees: below k_hi, and from k_lo on or below p.keep
       const int pos = t.L - t.nq + tok;
@@ -412,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       const int w0 = 32 * rg + 16 * hc, nrow = (int)min(16LL, rows - w0);
       long long o_at = 0, g_at = 0;       // in 16-byte words
       if (lane < nrow) {
-        const long long fl = (long long)t.i * kPM + w0 + lane;
+        const long long fl = flat0 + w0 + lane;
         const int tk = (int)(fl / p.G), hd = t.h * p.G + (int)(fl - (long long)tk * p.G);
         o_at = ((long long)(t.q0 + tk) * p.Hq + hd) * (kD / 8);
         g_at = ((t.q0 + tk) * p.gate_stride) / 8 + hd * (kD / 8);
@@ -517,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[sb]);
+        if (lane == 0) arrive_first(&bars.p_full[sb]);
       }
       if (!ok) break;
       const bool tiles = t.tb > t.ta;
@@ -536,12 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       }
       if (t.part >= 0) {
         // ---- a part of an item: sums and O as they are, for the joining kernel
-        if (hc == 0 && r < rows) p.part_ml[(size_t)t.part * kPM + r] = make_float4(m_run, l, e, 0.0f);
+        const int rr = rank * kPM + r;
+        if (hc == 0 && r < rows) p.part_ml[(size_t)t.part * kRowsI + rr] = make_float4(m_run, l, e, 0.0f);
         ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
         if (!ok) break;
         tc_fence_after();
         if (some) {
-          float4* dst = p.part_o + (size_t)t.part * 64 * kPM + r;
+          float4* dst = p.part_o + (size_t)t.part * 64 * kRowsI + rr;
 #pragma unroll 1
           for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 32) {
             float o[32];
@@ -550,14 +575,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
             if (r < rows) {
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                dst[(size_t)((c0 >> 2) + u) * kPM] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                dst[(size_t)((c0 >> 2) + u) * kRowsI] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars.o_empty);
+          arrive_first(&bars.o_empty);
           mbar_arrive(&bars.pr[rg]);
           mbar_arrive(&bars.v_free);
         }
@@ -620,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars.o_empty);  // the next item's PV may start
+          arrive_first(&bars.o_empty);  // the next item's PV may start
           mbar_arrive(&bars.pr[rg]);
         }
         ok = __all_sync(0xffffffffu, wait(&bars.pr[rg], 2 * it + 1));  // both halves of these rows are staged
@@ -669,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
           t.h = at.h, t.i = at.i;
           t.ta = at.t, t.tb = last ? end.t : r.n;
           t.f = r.f, t.tl = r.tl, t.lo = r.lo, t.hi = r.hi;
-          t.part = (t.ta > 0) ? 2 * (int)blockIdx.x : (t.tb < r.n) ? 2 * (int)blockIdx.x + 1 : -1;
+          t.part = (t.ta > 0) ? 2 * share : (t.tb < r.n) ? 2 * share + 1 : -1;
         }
         if (lane == 0) {
           if (n >= 2) ok = wait(&bars.i_empty[n & 1], (n >> 1) - 1);
@@ -708,10 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         }
       }
       if (!ok && lane == 0) fail();
-    } else if (lane == 0 && warp == kMmaWarp) {
+    } else if (rank == 0 && lane == 0 && warp == kMmaWarp) {
       // ---------------- S issuer: S(T) = Q K(T)^T into S buffer T % 2, which P(T - 2) occupied
       const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK);
-      constexpr uint32_t idS = idesc_of<KV>(kPM, kPN, 0);
+      constexpr uint32_t idS = idesc_of<KV>(kRowsI, kPN, 0);
       int it = 0, T = 0, slot = 0, use = 0;
       int done = -1;  // the tile of the last commit to s_full
       bool ok = true;
@@ -722,35 +747,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
-        ok = wait(&bars.qf, it);
+        ok = wait(&bars.q_land, it) && wait_both(&bars.q_peer, it);
 #pragma unroll 1
         for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
           const int sb = T & 1;
-          const int x0 = slot, u0 = use;
-          const int x1 = slot + 1 == kKSlots ? 0 : slot + 1, u1 = slot + 1 == kKSlots ? use + 1 : use;
-          ok = wait(&bars.k_full[x0], u0) && wait(&bars.k_full[x1], u1);
+          ok = wait(&bars.k_land[slot], use) && wait_both(&bars.k_peer[slot], use);
           if (ok && T >= 2) ok = wait(&bars.p_empty[sb], (T >> 1) - 1);
           if (!ok) break;
+          fence_async_shared();   // (the rows were written by threads, the MMAs read through the async proxy)
           tc_fence_after();
+          const uint32_t kb = sK + slot * kHalf;
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t kb = sK + (hh ? x1 : x0) * kHalf;
-#pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) {
-              const int kk = 8 * hh + k8;  // k-step: head dimensions 16 kk .. 16 kk + 15
-              const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
-              const uint64_t bd = sdesc_sw128(kb + ((kk >> 2) & 1) * kBlk + (kk & 3) * 32, 16, 1024);
-              umma_bf16_ss(tmem + kTmemS + sb * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&bars.k_empty[hh ? x1 : x0]);
+          for (int kk = 0; kk < 16; ++kk) {  // head dimensions 16 kk .. 16 kk + 15
+            const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+            const uint64_t bd = sdesc_sw128(kb + (kk >> 2) * kKBlk + (kk & 3) * 32, 16, 1024);
+            umma_pair_ss(tmem + kTmemS + sb * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
           }
-          umma_commit(&bars.s_full[sb]);
+          umma_commit_pair(&bars.k_empty[slot]);
+          umma_commit_pair(&bars.s_full[sb]);
           done = T;
-          slot = x1 + 1 == kKSlots ? 0 : x1 + 1;
-          use = x1 + 1 == kKSlots ? u1 + 1 : u1;
+          if (++slot == kKSlots) {
+            slot = 0;
+            ++use;
+          }
         }
         if (!ok) break;
-        umma_commit(&bars.q_empty);  // (every S product of the item)
+        umma_commit_pair(&bars.q_empty);  // (every S product of the item)
         ++it;
       }
       if (!ok) {
@@ -758,10 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         // the last commit covers every MMA issued before it
         if (done >= 0) drain(&bars.s_full[done & 1], done >> 1);
       }
-    } else if (lane == 0 && warp == kPvWarp) {
-      // ---------------- PV issuer: O += P(T) V(T), per 128-dimension half of O
+    } else if (rank == 0 && lane == 0 && warp == kPvWarp) {
+      // ---------------- PV issuer: O += P(T) V(T)
       const uint32_t sV = smem_u32(sm + Lay::kOffV);
-      constexpr uint32_t idO = idesc_of<KV>(kPM, 128, 1);
+      constexpr uint32_t idO = idesc_of<KV>(kRowsI, kD, 1);
       int it = 0, T = 0, done = -1;
       bool ok = true;
       for (int n = 0;; ++n) {
@@ -771,90 +793,95 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
-        if (it > 0) ok = wait(&bars.o_empty, it - 1);  // the epilogue has read the previous item's O
+        if (it > 0) ok = wait_both(&bars.o_empty, it - 1);  // the epilogues have read the previous item's O
 #pragma unroll 1
         for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
           const int pb = T & 1;
-          ok = wait(&bars.p_full[pb], T >> 1) && wait(&bars.v_full[0], T) && wait(&bars.v_full[1], T);
+          ok = wait(&bars.v_land[pb], T >> 1) && wait_both(&bars.v_peer[pb], T >> 1) && wait_both(&bars.p_full[pb], T >> 1);
           if (!ok) break;
+          fence_async_shared();
           tc_fence_after();
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              // V half hh is MN-major (dims contiguous): LBO = stride between its two 64-dim
-              // blocks, SBO = 8 key rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in
-              // columns 8 kk .. 8 kk + 7 of the S buffer
-              const uint64_t bd = sdesc_sw128(sV + hh * kHalf + kk * 16 * 128, kBlk, 1024);
-              umma_bf16_ts(tmem + kTmemO + 128 * hh, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO,
-                           (j > t.ta || kk > 0) ? 1u : 0u);
-            }
-            umma_commit(&bars.v_empty[hh]);
+          for (int kk = 0; kk < 8; ++kk) {
+            // V is MN-major (dims contiguous): LBO = stride between a CTA's two 64-dim blocks, SBO = 8 key
+            // rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in columns 8 kk .. 8 kk + 7 of the S buffer
+            const uint64_t bd = sdesc_sw128(sV + pb * kHalf + kk * 16 * 128, kBlk, 1024);
+            umma_pair_ts(tmem + kTmemO, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO, (j > t.ta || kk > 0) ? 1u : 0u);
           }
-          umma_commit(&bars.p_empty[pb]);
+          umma_commit_pair(&bars.v_empty[pb]);
+          umma_commit_pair(&bars.p_empty[pb]);
           done = T;
         }
         if (!ok) break;
-        umma_commit(&bars.o_full);
+        umma_commit_pair(&bars.o_full);
         ++it;
       }
       if (!ok) {
         fail();
         if (done >= 0) drain(&bars.p_empty[done & 1], done >> 1);
       }
+    } else if (rank == 1 && lane == 0 && (warp == kMmaWarp || warp == kPvWarp)) {
+      // ---------------- rank 1: what has landed here is passed on to rank 0's issuer
+      const bool is_v = warp == kPvWarp;
+      const int slots = is_v ? 2 : kKSlots;
+      uint64_t* land = is_v ? bars.v_land : bars.k_land;
+      uint64_t* peer = is_v ? bars.v_peer : bars.k_peer;
+      int it = 0, slot = 0, use = 0;
+      bool ok = true;
+      auto pass = [&](uint64_t* from, uint64_t* to, int parity) {
+        ok = wait(from, parity);
+        if (!ok) return;
+        fence_async_shared();
+        arrive_first(to);
+      };
+      for (int n = 0;; ++n) {
+        Item t;
+        ok = get_item(n, &t);
+        if (!ok) break;
+        mbar_arrive(&bars.i_empty[n & 1]);
+        if (t.b < 0) break;
+        if (t.tb == t.ta) continue;
+#pragma unroll 1
+        for (int j = t.ta; j < t.tb && ok; ++j) {
+          pass(&land[slot], &peer[slot], use);
+          if (++slot == slots) {
+            slot = 0;
+            ++use;
+          }
+          if (ok && !is_v && j == t.ta) pass(&bars.q_land, &bars.q_peer, it);
+        }
+        if (!ok) break;
+        ++it;
+      }
+      if (!ok) fail();
     }
   } else {
     regs_shrink<kRegsGather>();
-    // ---------------- gatherers: warps 12, 13 take Q and K, 14, 15 V; each 64 of a tile's 128 rows.
-    // A half tile (128 dimensions of every key) goes into the next slot of its ring once the MMAs
-    // that read the slot's previous half have completed.  BF16 rows are copied asynchronously
-    // (cp.async), and a half's barrier is arrived at when a later one has been started or there is
-    // nothing else to do; codes go through registers, widened to FP16.
+    // ---------------- gatherers: warps 12, 13 take Q and K (32 of this CTA's 64 keys of a tile each), 14,
+    // 15 V (64 of the 128 keys each, this CTA's 128 dimensions).  A tile goes into the next slot of its
+    // ring once the MMAs that read the slot's previous tile have completed.  BF16 rows are copied
+    // asynchronously (cp.async, whose completion arrives at the slot's barrier); codes go through
+    // registers, widened to FP16.
     const bool is_v = warp >= kGatherWarp + 2;
-    const int r64 = 64 * (warp & 1);                 // this warp's first row of a tile
+    const int r64 = (is_v ? 64 : 32) * (warp & 1);   // this warp's first row of the CTA's part of a tile
+    const int key0 = is_v ? r64 : 64 * rank + r64;   // that row's key
     const int slots = is_v ? 2 : kKSlots;
     unsigned char* ring = sm + (is_v ? Lay::kOffV : Lay::kOffK);
-    uint64_t* full = is_v ? bars.v_full : bars.k_full;
+    uint64_t* land = is_v ? bars.v_land : bars.k_land;
     uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
     const unsigned char* pool = is_v ? p.v_pool : p.k_pool;
     int it = 0, slot = 0, use = 0;
     bool ok = true;
-    int pend = 0;                                    // copies started whose barrier was not arrived at
-    uint64_t *pb0 = nullptr, *pb1 = nullptr, *pb2 = nullptr;
-    auto signal_oldest = [&]() {
-      if (pend == 1) cp_async_wait<0>();
-      else if (pend == 2) cp_async_wait<1>();
-      else cp_async_wait<2>();
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pb0);
-      pb0 = pb1;
-      pb1 = pb2;
-      --pend;
-    };
-    auto started = [&](uint64_t* bar) {
+    // this thread's part of what `bar` counts is on its way, or written
+    auto landed = [&](uint64_t* bar) {
       if (KV == GDA_KV_BF16) {
-        cp_async_commit();
-        if (pend == 0) pb0 = bar;
-        else if (pend == 1) pb1 = bar;
-        else pb2 = bar;
-        ++pend;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
       } else {
         fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+        mbar_arrive(bar);
       }
     };
-    // waits, arriving at what is complete meanwhile
-    auto acquire = [&](uint64_t* bar, int parity) -> bool {
-      if (KV == GDA_KV_BF16) {
-        while (pend > 0) {
-          if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1))) return true;
-          signal_oldest();
-        }
-      }
-      return __all_sync(0xffffffffu, wait(bar, parity));
-    };
+    auto acquire = [&](uint64_t* bar, int parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
     for (int n = 0;; ++n) {
       ok = acquire(&bars.i_full[n & 1], n >> 1);
       if (!ok) break;
@@ -864,114 +891,125 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
       if (t.b < 0) break;
       if (t.tb == t.ta) continue;
       if (is_v && it > 0) ok = acquire(&bars.v_free, it - 1);  // the previous item's outputs have left the buffers
-      // the slots of rows r64 + lane and r64 + 32 + lane of tile j: -1 where no row of the item
-      // sees the position (zeros then)
-      int nx[2];
+      // the slots of keys key0 + lane and (V) key0 + 32 + lane of tile j, loaded a tile ahead and looked
+      // at when used; `seen`: where some row of the item sees the position
+      int nx[2] = {-1, -1};
+      bool seen[2] = {false, false};
       auto look_up = [&](int j) {
-        const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + r64 + lane;
+        const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + key0 + lane;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int pos = base + 32 * x;
-          int sl = -1;
-          if (pos < t.hi && (pos >= t.lo || pos < p.keep)) {
-            sl = __ldg(p.indices + t.kb + pos);
-            if (sl < 0 || (long long)sl >= p.num_slots) {  // a row outside the pools reads as zeros
-              atomicOr(p.error, kErrIndex);
-              sl = -1;
-            }
-          }
-          nx[x] = sl;
+          seen[x] = (x == 0 || is_v) && pos < t.hi && (pos >= t.lo || pos < p.keep);
+          if (seen[x]) nx[x] = __ldg(p.indices + t.kb + pos);
         }
       };
       if (ok) look_up(t.ta);
 #pragma unroll 1
       for (int j = t.ta; j < t.tb && ok; ++j) {
-        const int sl0 = nx[0], sl1 = nx[1];
+        // -1: zeros.  A row outside the pools reads as zeros and is reported
+        const bool in0 = nx[0] >= 0 && (long long)nx[0] < p.num_slots, in1 = nx[1] >= 0 && (long long)nx[1] < p.num_slots;
+        if ((seen[0] && !in0) || (seen[1] && !in1)) atomicOr(p.error, kErrIndex);
+        const int sl0 = seen[0] && in0 ? nx[0] : -1, sl1 = seen[1] && in1 ? nx[1] : -1;
         if (j + 1 < t.tb) look_up(j + 1);
-#pragma unroll 1
-        for (int hh = 0; hh < 2 && ok; ++hh) {
-          unsigned char* dst = ring + slot * kHalf;
-          if (KV == GDA_KV_BF16) {
-            if (pend == 3) signal_oldest();
-            if (use > 0) ok = acquire(&empty[slot], use - 1);
-            if (!ok) break;
-            // two rows (256 bytes each) per step
+        unsigned char* dst = ring + slot * kHalf;
+        if (KV == GDA_KV_BF16) {
+          if (use > 0) ok = acquire(&empty[slot], use - 1);
+          if (!ok) break;
+          if (!is_v) {
+            // a row (512 bytes) per step
+            const uint32_t d0 = smem_u32(dst) + (lane >> 3) * kKBlk + r64 * 128;
+#pragma unroll 8
+            for (int x = 0; x < 32; ++x) {
+              const int sl = __shfl_sync(0xffffffffu, sl0, x);
+              const unsigned char* src = pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + lane * 16;
+              cp_async16(d0 + x * 128 + (((lane & 7) ^ (x & 7)) << 4), src, sl >= 0 ? 16 : 0);
+            }
+          } else {
+            // two half rows (256 bytes) per step
             const uint32_t d0 = smem_u32(dst) + ((lane & 15) >> 3) * kBlk + (r64 + (lane >> 4)) * 128;
 #pragma unroll 8
             for (int x = 0; x < 32; ++x) {
               const int sl = __shfl_sync(0xffffffffu, x < 16 ? sl0 : sl1, (2 * x + (lane >> 4)) & 31);
               const unsigned char* src =
-                  pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + hh * kD + (lane & 15) * 16;
+                  pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + rank * kD + (lane & 15) * 16;
               cp_async16(d0 + x * 256 + (((lane & 7) ^ ((2 * x + (lane >> 4)) & 7)) << 4), src, sl >= 0 ? 16 : 0);
             }
-          } else if (KV == GDA_KV_E4M3) {
-            // four rows (128 codes each) per step, eight steps' loads in flight
+          }
+        } else if (KV == GDA_KV_E4M3) {
+          // K: two rows of 256 codes per step, V: four half rows of 128; eight steps' loads in flight
+          const int lanes = is_v ? 8 : 16, part = lane & (lanes - 1), sub = is_v ? lane >> 3 : lane >> 4;
+          const uint32_t blk = is_v ? kBlk : kKBlk;
 #pragma unroll 1
-            for (int y = 0; y < 2 && ok; ++y) {
-              uint4 raw[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int sl = __shfl_sync(0xffffffffu, y ? sl1 : sl0, 4 * x + (lane >> 3));
-                raw[x] = make_uint4(0u, 0u, 0u, 0u);
-                if (sl >= 0)
-                  raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + ((size_t)sl * p.Hkv + t.h) * kD + hh * 128) + (lane & 7));
-              }
-              if (y == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
-              if (!ok) break;
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int row = r64 + 32 * y + 4 * x + (lane >> 3), c = 2 * (lane & 7);
-                unsigned char* at = dst + (c >> 3) * kBlk + row * 128;
-                *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
-                *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
-              }
-            }
-          } else {
-            // eight rows (64 bytes of codes, 8 scales) per step
+          for (int y = 0; y < 2 && ok; ++y) {
             uint4 raw[8];
-            uint32_t sc[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-              const int sl = __shfl_sync(0xffffffffu, x < 4 ? sl0 : sl1, (8 * x + (lane >> 2)) & 31);
+              const int row = is_v ? 4 * x + sub : 16 * y + 2 * x + sub;   // (V: of the warp's half y)
+              const int sl = __shfl_sync(0xffffffffu, is_v && y ? sl1 : sl0, row);
               raw[x] = make_uint4(0u, 0u, 0u, 0u);
-              sc[x] = 0u;
-              if (sl >= 0) {
-                const size_t row = (size_t)sl * p.Hkv + t.h;
-                raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + row * kCodeBytes + hh * 64) + (lane & 3));
-                sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + row * kScalePair + (is_v ? kScaleBytes : 0) + hh * 8) +
-                              (lane & 3));
-              }
+              if (sl >= 0)
+                raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + ((size_t)sl * p.Hkv + t.h) * kD + (is_v ? rank * 128 : 0)) + part);
             }
-            if (use > 0) ok = acquire(&empty[slot], use - 1);
+            if (y == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
             if (!ok) break;
+            const int c = 2 * part;                                        // the first of two 8-dimension chunks
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-              const int row = r64 + 8 * x + (lane >> 2), c = 4 * (lane & 3);
-              const uint32_t f = e4m3x2_to_f16x2(sc[x]);
-              const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-              unsigned char* at = dst + (c >> 3) * kBlk + row * 128;
-              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
-              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
-              *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
-              *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
+              const int row = r64 + (is_v ? 32 * y + 4 * x + sub : 16 * y + 2 * x + sub);
+              unsigned char* at = dst + (c >> 3) * blk + row * 128;
+              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
+              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
             }
           }
+        } else {
+          // K: four rows of 128 bytes of codes and 16 scales per step, V: eight half rows
+          const int lanes = is_v ? 4 : 8, part = lane & (lanes - 1), sub = is_v ? lane >> 2 : lane >> 3;
+          const uint32_t blk = is_v ? kBlk : kKBlk;
+          uint4 raw[8];
+          uint32_t sc[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int row = is_v ? 8 * x + sub : 4 * x + sub;
+            const int sl = __shfl_sync(0xffffffffu, row < 32 ? sl0 : sl1, row & 31);
+            raw[x] = make_uint4(0u, 0u, 0u, 0u);
+            sc[x] = 0u;
+            if (sl >= 0) {
+              const size_t at = (size_t)sl * p.Hkv + t.h;
+              raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kCodeBytes + (is_v ? rank * 64 : 0)) + part);
+              sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + at * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0)) + part);
+            }
+          }
+          if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
-          started(&full[slot]);
-          if (++slot == slots) {
-            slot = 0;
-            ++use;
+          const int c = 4 * part;                                          // the first of four 8-dimension chunks
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int row = r64 + (is_v ? 8 * x + sub : 4 * x + sub);
+            const uint32_t f = e4m3x2_to_f16x2(sc[x]);
+            const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+            unsigned char* at = dst + (c >> 3) * blk + row * 128;
+            *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
+            *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
+            *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
+            *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
           }
         }
-        if (ok && !is_v && j == t.ta) {
+        if (!ok) break;
+        landed(&land[slot]);
+        if (++slot == slots) {
+          slot = 0;
+          ++use;
+        }
+        if (!is_v && j == t.ta) {
           // Q behind the first K tile (it needs the previous item's last S product): a row per step,
           // zeros in rows past the item's last
           if (it > 0) ok = acquire(&bars.q_empty, it - 1);
-          if (KV == GDA_KV_BF16 && pend == 3) signal_oldest();
           if (!ok) break;
-          const long long flat0 = (long long)t.i * kPM + r64, rows = (long long)t.nq * p.G;
+          const int q64 = 64 * (warp & 1);
+          const long long flat0 = (long long)t.i * kRowsI + rank * kPM + q64, rows = (long long)t.nq * p.G;
           int tok = (int)(flat0 / p.G), g = (int)(flat0 - (long long)tok * p.G);
-          unsigned char* dq = sm + Lay::kOffQ + (lane >> 3) * kBlk + r64 * 128;
+          unsigned char* dq = sm + Lay::kOffQ + (lane >> 3) * kBlk + q64 * 128;
 #pragma unroll 1
           for (int x0 = 0; x0 < 64; x0 += 8) {
             uint4 raw[8];
@@ -1008,31 +1046,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
                   o[e] = f16x2_rn(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xFFFF0000u) * up);
                 *reinterpret_cast<uint4*>(dq + (x0 + x) * 128 + (((lane & 7) ^ x) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 if (lane == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
-                  qscale[(it & 3) * kPM + r64 + x0 + x] =
+                  qscale[(it & 3) * kPM + q64 + x0 + x] =
                       fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
               }
             }
           }
-          started(&bars.qf);
+          landed(&bars.q_land);
         }
       }
       if (!ok) break;
       ++it;
     }
-    if (KV == GDA_KV_BF16) {
-      while (ok && pend > 0) signal_oldest();
-      cp_async_wait<0>();
-    }
+    if (KV == GDA_KV_BF16) cp_async_wait_all();
     if (!ok) fail();
   }
 
-  // ---- teardown: every role is done (or gave up and waited for what it started)
+  // ---- teardown: every role of both CTAs is done (or gave up and waited for what it started)
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -1042,23 +1077,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid
 // dimensions of a row, neighbouring threads neighbouring rows (as the parts are laid out).
 constexpr int kJoinThreads = 256, kJoinY = 8;
 __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ int part[kPagedMaxCtas + 1];
+  __shared__ int part[kPagedMaxShares + 1];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int c = blockIdx.x + 1, tid = threadIdx.x;
-  const int ctas = p.cuts[0].x;
-  if (c >= ctas) return;
+  const int used = p.cuts[0].x;
+  if (c >= used) return;
   const int4 me = p.cuts[1 + c], before = p.cuts[c];
   auto same = [&](const int4& a) { return a.x == me.x && a.y == me.y && a.z == me.z; };
   if (me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
   // the parts: share c - 1's last one, then the first ones of the shares that start in the item
   int mine = -1;
   bool in = false;
-  if (c + tid < ctas) {
+  if (c + tid < used) {
     const int4 a = p.cuts[1 + c + tid];
     in = same(a);
     if (in) {
-      const int4 z = c + tid + 1 < ctas ? p.cuts[2 + c + tid] : make_int4(p.B, 0, 0, 0);
+      const int4 z = c + tid + 1 < used ? p.cuts[2 + c + tid] : make_int4(p.B, 0, 0, 0);
       if (!same(z) || z.w > a.w) mine = 2 * (c + tid);   // (else the share is empty)
     }
   }
@@ -1066,8 +1101,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   if (tid == 0) part[0] = 2 * (c - 1) + 1;
   const int parts = 1 + __syncthreads_count(in);
   const Seq s = seq_of(p, me.x);
-  const long long flat0 = (long long)me.z * kPM;
-  const int rows = (int)min((long long)kPM, (long long)s.nq * p.G - flat0);
+  const long long flat0 = (long long)me.z * kRowsI;
+  const int rows = (int)min((long long)kRowsI, (long long)s.nq * p.G - flat0);
   constexpr int kCols = 64 / kJoinY;
   for (int x = tid; x < rows * kCols; x += kJoinThreads) {
     const int r = x % rows, c4 = blockIdx.y * kCols + x / rows;
@@ -1075,17 +1110,17 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
     float m = -INFINITY;
     for (int k = 0; k < parts; ++k)
       if (part[k] >= 0) {
-        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kPM + r);
+        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
         if (!(a.x <= m)) m = a.x;   // (a NaN stays)
       }
     float l = 0.0f, e = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int k = 0; k < parts; ++k)
       if (part[k] >= 0) {
-        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kPM + r);
+        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
         if (a.y == 0.0f) continue;  // no visible key in this part
         const float w = exp2f(a.x - m);
-        const float4 v = __ldcg(p.part_o + ((size_t)part[k] * 64 + c4) * kPM + r);
+        const float4 v = __ldcg(p.part_o + ((size_t)part[k] * 64 + c4) * kRowsI + r);
         l += w * a.y;
         e += w * a.z;
         o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
@@ -1149,13 +1184,14 @@ cudaError_t launch_prefill_paged(const PagedParams& params, int kv_dtype, cudaSt
   if (e == cudaSuccess) e = sigmoid_table(&p.table);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
-  if (kv_dtype == GDA_KV_BF16) e = launch<GDA_KV_BF16>(p, grid, stream);
-  else if (kv_dtype == GDA_KV_E4M3) e = launch<GDA_KV_E4M3>(p, grid, stream);
-  else e = launch<GDA_KV_E2M1>(p, grid, stream);
-  if (e != cudaSuccess || grid < 2) return e;
+  const int shares = sms / 2 < kPagedMaxShares ? sms / 2 : kPagedMaxShares;
+  if (shares < 1) return cudaErrorInvalidDevice;
+  if (kv_dtype == GDA_KV_BF16) e = launch<GDA_KV_BF16>(p, 2 * shares, stream);
+  else if (kv_dtype == GDA_KV_E4M3) e = launch<GDA_KV_E4M3>(p, 2 * shares, stream);
+  else e = launch<GDA_KV_E2M1>(p, 2 * shares, stream);
+  if (e != cudaSuccess || shares < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid - 1), kJoinY);
+  cfg.gridDim = dim3((unsigned)(shares - 1), kJoinY);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

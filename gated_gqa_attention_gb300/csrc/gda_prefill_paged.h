@@ -29,23 +29,24 @@ struct PagedParams {
   float v_descale;
   long long wait_limit;
   const uint16_t* table;       // BF16 sigmoid of every BF16 code
-  // workspace: where the CTAs' shares start, and what shares that cut an item leave of it
-  int4* cuts;                  // [kPagedMaxCtas + 1]: {CTAs with a share, -, -, -}, then each CTA's start
-  float4* part_ml;             // [2 kPagedMaxCtas][128] {row max (log2), sum, unrounded sum, -}
-  float4* part_o;              // [2 kPagedMaxCtas][64][128]: four dimensions of a row
+  // workspace: where the shares of the work start, and what shares that cut an item leave of it
+  int4* cuts;                  // {number of shares, -, -, -}, then each share's start
+  float4* part_ml;             // [2 kPagedMaxShares][256] {row max (log2), sum, unrounded sum, -}
+  float4* part_o;              // [2 kPagedMaxShares][64][256]: four dimensions of a row
 };
 
-constexpr int kPagedMaxCtas = 160;
+constexpr int kPagedRows = 256;       // rows of an item: 128 in each CTA of a pair
+constexpr int kPagedMaxShares = 80;   // pairs of CTAs
 // bytes of each part of the workspace
 constexpr size_t kPagedCutBytes = 4096;
-constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxCtas * 128 * 16;
-constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxCtas * 64 * 128 * 16;
-static_assert((kPagedMaxCtas + 1) * 16 <= kPagedCutBytes, "cut table");
+constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxShares * kPagedRows * 16;
+constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxShares * 64 * kPagedRows * 16;
+static_assert((kPagedMaxShares + 1) * 16 <= kPagedCutBytes, "cut table");
 
-// The most 128-row blocks (rows: a token's query heads of one KV head, token after token) that B
+// The most blocks of rows (rows: a token's query heads of one KV head, token after token) that B
 // sequences of `tokens` tokens in all can have.
 inline long long paged_blocks(long long tokens, long long G, long long B) {
-  const long long n = tokens * G / 128 + B;
+  const long long n = tokens * G / kPagedRows + B;
   return n < tokens * G ? n : tokens * G;
 }
 

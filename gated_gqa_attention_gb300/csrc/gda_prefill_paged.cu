@@ -21,6 +21,8 @@
 // unnormalised O in FP32) in the workspace, at most two per pair, and a second kernel joins them in
 // the order of the shares, so a result does not depend on which ends first.  What an item costs is
 // taken as linear in its number within the sequence, so that sums over items have a closed form.
+#include <limits.h>
+
 #include "gda.h"
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
@@ -891,49 +893,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (t.b < 0) break;
       if (t.tb == t.ta) continue;
       if (is_v && it > 0) ok = acquire(&bars.v_free, it - 1);  // the previous item's outputs have left the buffers
-      // the slots of keys key0 + lane and (V) key0 + 32 + lane of tile j, loaded a tile ahead and looked
-      // at when used; `seen`: where some row of the item sees the position
-      int nx[2] = {-1, -1};
-      bool seen[2] = {false, false};
-      auto look_up = [&](int j) {
+      // the slots of keys key0 + lane and (V) key0 + 32 + lane of tile j: loaded two tiles ahead, looked at
+      // when used; kUnseen where no row of the item sees the position
+      constexpr int kUnseen = INT_MIN;
+      int n0[2], n1[2], n2[2];
+      auto look_up = [&](int j, int* to) {
         const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + key0 + lane;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int pos = base + 32 * x;
-          seen[x] = (x == 0 || is_v) && pos < t.hi && (pos >= t.lo || pos < p.keep);
-          if (seen[x]) nx[x] = __ldg(p.indices + t.kb + pos);
+          to[x] = kUnseen;
+          if ((x == 0 || is_v) && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep)) to[x] = __ldg(p.indices + t.kb + pos);
         }
       };
-      if (ok) look_up(t.ta);
+      // -1: zeros.  A row outside the pools reads as zeros and is reported
+      auto slot_of = [&](int v) -> int {
+        if (v >= 0 && (long long)v < p.num_slots) return v;
+        if (v != kUnseen) atomicOr(p.error, kErrIndex);
+        return -1;
+      };
+      look_up(t.ta, n0);
+      look_up(t.ta + 1, n1);
 #pragma unroll 1
       for (int j = t.ta; j < t.tb && ok; ++j) {
-        // -1: zeros.  A row outside the pools reads as zeros and is reported
-        const bool in0 = nx[0] >= 0 && (long long)nx[0] < p.num_slots, in1 = nx[1] >= 0 && (long long)nx[1] < p.num_slots;
-        if ((seen[0] && !in0) || (seen[1] && !in1)) atomicOr(p.error, kErrIndex);
-        const int sl0 = seen[0] && in0 ? nx[0] : -1, sl1 = seen[1] && in1 ? nx[1] : -1;
-        if (j + 1 < t.tb) look_up(j + 1);
+        look_up(j + 2, n2);
+        const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
+        n0[0] = n1[0], n0[1] = n1[1], n1[0] = n2[0], n1[1] = n2[1];
         unsigned char* dst = ring + slot * kHalf;
+        // four rows per step, eight lanes each: lane l8 of row 4 q + g8 takes 16 bytes of every 128
+        const int g8 = lane >> 3, l8 = lane & 7;
         if (KV == GDA_KV_BF16) {
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
+          const uint32_t d0 = smem_u32(dst) + (r64 + g8) * 128;
+          const uint32_t sw[2] = {(uint32_t)(l8 ^ g8) << 4, (uint32_t)(l8 ^ (4 + g8)) << 4};
+          const unsigned char* base = pool + (size_t)t.h * (2 * kD) + (is_v ? rank * kD : 0) + l8 * 16;
+          const uint32_t pitch = (uint32_t)p.Hkv * (2 * kD);
           if (!is_v) {
-            // a row (512 bytes) per step
-            const uint32_t d0 = smem_u32(dst) + (lane >> 3) * kKBlk + r64 * 128;
-#pragma unroll 8
-            for (int x = 0; x < 32; ++x) {
-              const int sl = __shfl_sync(0xffffffffu, sl0, x);
-              const unsigned char* src = pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + lane * 16;
-              cp_async16(d0 + x * 128 + (((lane & 7) ^ (x & 7)) << 4), src, sl >= 0 ? 16 : 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int sl = __shfl_sync(0xffffffffu, sl0, 4 * q + g8);
+              const unsigned char* src = base + (size_t)(uint32_t)max(sl, 0) * pitch;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kKBlk, src + 128 * c, sl >= 0 ? 16 : 0);
             }
           } else {
-            // two half rows (256 bytes) per step
-            const uint32_t d0 = smem_u32(dst) + ((lane & 15) >> 3) * kBlk + (r64 + (lane >> 4)) * 128;
-#pragma unroll 8
-            for (int x = 0; x < 32; ++x) {
-              const int sl = __shfl_sync(0xffffffffu, x < 16 ? sl0 : sl1, (2 * x + (lane >> 4)) & 31);
-              const unsigned char* src =
-                  pool + ((size_t)max(sl, 0) * p.Hkv + t.h) * (2 * kD) + rank * kD + (lane & 15) * 16;
-              cp_async16(d0 + x * 256 + (((lane & 7) ^ ((2 * x + (lane >> 4)) & 7)) << 4), src, sl >= 0 ? 16 : 0);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int sl = __shfl_sync(0xffffffffu, q < 8 ? sl0 : sl1, (4 * q + g8) & 31);
+              const unsigned char* src = base + (size_t)(uint32_t)max(sl, 0) * pitch;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kBlk, src + 128 * c, sl >= 0 ? 16 : 0);
             }
           }
         } else if (KV == GDA_KV_E4M3) {

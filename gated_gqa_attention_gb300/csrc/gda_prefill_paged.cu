@@ -38,7 +38,7 @@ constexpr int kPM = 128;            // rows of an item per CTA (half the MMA's M
 constexpr int kRowsI = kPagedRows;  // rows of an item
 constexpr int kPN = 128;            // keys per tile (MMA N of S)
 constexpr int kSoftmaxWarps = 8;    // warps 0-7
-constexpr int kPlanWarp = 8, kMmaWarp = 9, kPvWarp = 11;
+constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 11;
 constexpr int kGatherWarp = 12;     // warps 12, 13: Q and K; 14, 15: V
 constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512;
@@ -96,7 +96,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 constexpr int kGatherWarps = 4;                     // 2 each
-constexpr int kItemReaders = 2 + kGatherWarps + kSoftmaxWarps;  // issuers (rank 1: their relays), gatherers, softmax
+constexpr int kItemReaders = kGatherWarps + kSoftmaxWarps;  // and the issuer, or rank 1's two relays
 
 // ---- the stream of items
 
@@ -275,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       mbar_init(&bars.p_full[x], 2 * kSoftmaxWarps);
       mbar_init(&bars.p_empty[x], 1);
       mbar_init(&bars.i_full[x], 1);
-      mbar_init(&bars.i_empty[x], kItemReaders);
+      mbar_init(&bars.i_empty[x], kItemReaders + 1 + rank);
     }
     for (int q4 = 0; q4 < 4; ++q4) {
       mbar_init(&bars.xm[q4][0], 2);
@@ -593,26 +593,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         ++it;
         continue;
       }
-      // ---- epilogue of a whole item.  While the last products run: the sigmoids of this warp's 16
-      // rows, lane l dimensions 8l .. 8l + 7 of each (1 without a gate)
-      constexpr int kRows = 16;
+      // ---- epilogue of a whole item, eight rows at a time: their sigmoids (lane l has dimensions 8l ..
+      // 8l + 7 of each; 1 without a gate), the first eight's while the last products run
+      constexpr int kRows = 8;
       uint32_t sg[4 * kRows];
-#pragma unroll
-      for (int y = 0; y < kRows; ++y) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      auto gate_rows = [&](int y0) {
         if (p.gate) {
-          const long long at = __shfl_sync(0xffffffffu, g_at, y);
-          if (y < nrow) v = __ldcs(reinterpret_cast<const uint4*>(p.gate) + at + lane);
+#pragma unroll
+          for (int y = 0; y < kRows; ++y) {
+            const long long at = __shfl_sync(0xffffffffu, g_at, y0 + y);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (y0 + y < nrow) v = __ldcs(reinterpret_cast<const uint4*>(p.gate) + at + lane);
+            sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
+          }
+#pragma unroll
+          for (int y = 0; y < kRows; y += 4) sigmoids<4>(sg + 4 * y, p.table);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4 * kRows; ++x) sg[x] = 0x3F803F80u;
         }
-        sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
-      }
-      if (p.gate) {
-#pragma unroll
-        for (int y = 0; y < kRows; y += 4) sigmoids<4>(sg + 4 * y, p.table);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4 * kRows; ++x) sg[x] = 0x3F803F80u;
-      }
+      };
+      if (nrow > 0) gate_rows(0);
       float m = m_run, wo = 1.0f;
       if (p.sinks && r < rows) join_sink(p, head, m, l, e, wo);
       if (p.lse && hc == 0 && r < rows) p.lse[(size_t)head * p.Tq + t.q0 + tok] = lse_of(m, e);
@@ -654,17 +655,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         if (!ok) break;
         ++it;
       }
+#pragma unroll 1
+      for (int y0 = 0; y0 < nrow; y0 += kRows) {
+        if (y0 > 0) gate_rows(y0);
 #pragma unroll
-      for (int y = 0; y < kRows; ++y) {
-        const int row = w0 + y;
-        const long long at = __shfl_sync(0xffffffffu, o_at, y);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (tiles)
-          v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
-        // (a product of two BF16 values, correctly rounded by one instruction)
-        v.x = mul_bf16x2(v.x, sg[4 * y]), v.y = mul_bf16x2(v.y, sg[4 * y + 1]);
-        v.z = mul_bf16x2(v.z, sg[4 * y + 2]), v.w = mul_bf16x2(v.w, sg[4 * y + 3]);
-        if (y < nrow) reinterpret_cast<uint4*>(p.out)[at + lane] = v;
+        for (int y = 0; y < kRows; ++y) {
+          const int row = w0 + y0 + y;
+          const long long at = __shfl_sync(0xffffffffu, o_at, y0 + y);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (tiles)
+            v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+          // (a product of two BF16 values, correctly rounded by one instruction)
+          v.x = mul_bf16x2(v.x, sg[4 * y]), v.y = mul_bf16x2(v.y, sg[4 * y + 1]);
+          v.z = mul_bf16x2(v.z, sg[4 * y + 2]), v.w = mul_bf16x2(v.w, sg[4 * y + 3]);
+          if (y0 + y < nrow) reinterpret_cast<uint4*>(p.out)[at + lane] = v;
+        }
       }
       // (generic accesses to the V buffers before the next rows go into them)
       fence_async_shared();
@@ -736,58 +741,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       }
       if (!ok && lane == 0) fail();
     } else if (rank == 0 && lane == 0 && warp == kMmaWarp) {
-      // ---------------- S issuer: S(T) = Q K(T)^T into S buffer T % 2, which P(T - 2) occupied
-      const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK);
-      constexpr uint32_t idS = idesc_of<KV>(kRowsI, kPN, 0);
+      // ---------------- issuer: S(T) = Q K(T)^T into S buffer T % 2, O += P(T) V(T), in the order S(T + 1),
+      // PV(T): one thread's MMAs run in order, so S(T + 2) follows PV(T), whose P its scores replace,
+      // without a wait between them
+      const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK), sV = smem_u32(sm + Lay::kOffV);
+      constexpr uint32_t idS = idesc_of<KV>(kRowsI, kPN, 0), idO = idesc_of<KV>(kRowsI, kD, 1);
       int it = 0, T = 0, slot = 0, use = 0;
-      int done = -1;  // the tile of the last commit to s_full
+      int done_s = -1, done_o = -1;  // tiles of the last commits
       bool ok = true;
-      for (int n = 0;; ++n) {
-        Item t;
-        ok = get_item(n, &t);
-        if (!ok) break;
-        mbar_arrive(&bars.i_empty[n & 1]);
-        if (t.b < 0) break;
-        if (t.tb == t.ta) continue;
-        ok = wait(&bars.q_land, it) && wait_both(&bars.q_peer, it);
-#pragma unroll 1
-        for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
-          const int sb = T & 1;
-          ok = wait(&bars.k_land[slot], use) && wait_both(&bars.k_peer[slot], use);
-          if (ok && T >= 2) ok = wait(&bars.p_empty[sb], (T >> 1) - 1);
-          if (!ok) break;
-          fence_async_shared();   // (the rows were written by threads, the MMAs read through the async proxy)
-          tc_fence_after();
-          const uint32_t kb = sK + slot * kHalf;
+      auto issue_s = [&](int x) -> bool {
+        if (!wait(&bars.k_land[slot], use) || !wait_both(&bars.k_peer[slot], use)) return false;
+        fence_async_shared();   // (the rows were written by threads, the MMAs read through the async proxy)
+        tc_fence_after();
+        const uint32_t kb = sK + slot * kHalf;
 #pragma unroll
-          for (int kk = 0; kk < 16; ++kk) {  // head dimensions 16 kk .. 16 kk + 15
-            const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = sdesc_sw128(kb + (kk >> 2) * kKBlk + (kk & 3) * 32, 16, 1024);
-            umma_pair_ss(tmem + kTmemS + sb * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
-          }
-          umma_commit_pair(&bars.k_empty[slot]);
-          umma_commit_pair(&bars.s_full[sb]);
-          done = T;
-          if (++slot == kKSlots) {
-            slot = 0;
-            ++use;
-          }
+        for (int kk = 0; kk < 16; ++kk) {  // head dimensions 16 kk .. 16 kk + 15
+          const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+          const uint64_t bd = sdesc_sw128(kb + (kk >> 2) * kKBlk + (kk & 3) * 32, 16, 1024);
+          umma_pair_ss(tmem + kTmemS + (x & 1) * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
         }
-        if (!ok) break;
-        umma_commit_pair(&bars.q_empty);  // (every S product of the item)
-        ++it;
-      }
-      if (!ok) {
-        fail();
-        // the last commit covers every MMA issued before it
-        if (done >= 0) drain(&bars.s_full[done & 1], done >> 1);
-      }
-    } else if (rank == 0 && lane == 0 && warp == kPvWarp) {
-      // ---------------- PV issuer: O += P(T) V(T)
-      const uint32_t sV = smem_u32(sm + Lay::kOffV);
-      constexpr uint32_t idO = idesc_of<KV>(kRowsI, kD, 1);
-      int it = 0, T = 0, done = -1;
-      bool ok = true;
+        umma_commit_pair(&bars.k_empty[slot]);
+        umma_commit_pair(&bars.s_full[x & 1]);
+        done_s = x;
+        if (++slot == kKSlots) {
+          slot = 0;
+          ++use;
+        }
+        return true;
+      };
       for (int n = 0;; ++n) {
         Item t;
         ok = get_item(n, &t);
@@ -795,11 +776,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
-        if (it > 0) ok = wait_both(&bars.o_empty, it - 1);  // the epilogues have read the previous item's O
+        ok = wait(&bars.q_land, it) && wait_both(&bars.q_peer, it) && issue_s(T);
 #pragma unroll 1
         for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
+          if (j + 1 < t.tb) ok = issue_s(T + 1);
+          else umma_commit_pair(&bars.q_empty);               // (every S product of the item)
+          if (ok && j == t.ta && it > 0) ok = wait_both(&bars.o_empty, it - 1);  // the epilogues have read the previous O
           const int pb = T & 1;
-          ok = wait(&bars.v_land[pb], T >> 1) && wait_both(&bars.v_peer[pb], T >> 1) && wait_both(&bars.p_full[pb], T >> 1);
+          ok = ok && wait(&bars.v_land[pb], T >> 1) && wait_both(&bars.v_peer[pb], T >> 1) && wait_both(&bars.p_full[pb], T >> 1);
           if (!ok) break;
           fence_async_shared();
           tc_fence_after();
@@ -812,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
           umma_commit_pair(&bars.v_empty[pb]);
           umma_commit_pair(&bars.p_empty[pb]);
-          done = T;
+          done_o = T;
         }
         if (!ok) break;
         umma_commit_pair(&bars.o_full);
@@ -820,11 +804,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       }
       if (!ok) {
         fail();
-        if (done >= 0) drain(&bars.p_empty[done & 1], done >> 1);
+        // the last commits cover every MMA issued before them
+        if (done_s >= 0) drain(&bars.s_full[done_s & 1], done_s >> 1);
+        if (done_o >= 0) drain(&bars.p_empty[done_o & 1], done_o >> 1);
       }
-    } else if (rank == 1 && lane == 0 && (warp == kMmaWarp || warp == kPvWarp)) {
+    } else if (rank == 1 && lane == 0 && (warp == kMmaWarp || warp == kRelayWarp)) {
       // ---------------- rank 1: what has landed here is passed on to rank 0's issuer
-      const bool is_v = warp == kPvWarp;
+      const bool is_v = warp == kRelayWarp;
       const int slots = is_v ? 2 : kKSlots;
       uint64_t* land = is_v ? bars.v_land : bars.k_land;
       uint64_t* peer = is_v ? bars.v_peer : bars.k_peer;
@@ -1083,19 +1069,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
 
 // Joins the parts of the item that the start of share c = blockIdx.x + 1 cuts first:
 //   m = max m_k, w_k = 2^(m_k - m), O = sum w_k O_k / (sum w_k l_k + sink)
-// in the order of the shares.  blockIdx.y takes an eighth of the dimensions; a thread has four
-// dimensions of a row, neighbouring threads neighbouring rows (as the parts are laid out).
-constexpr int kJoinThreads = 256, kJoinY = 8;
+// in the order of the shares.  A thread has eight dimensions of a row, neighbouring threads
+// neighbouring rows (as the parts are laid out); blocks blockIdx.y take 256 such pieces each, as many
+// as the item's rows make.
+constexpr int kJoinThreads = 256, kJoinY = kPagedRows * (kD / 8) / kJoinThreads;
 __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const __grid_constant__ PagedParams p) {
   __shared__ int part[kPagedMaxShares + 1];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int c = blockIdx.x + 1, tid = threadIdx.x;
   const int used = p.cuts[0].x;
-  if (c >= used) return;
   const int4 me = p.cuts[1 + c], before = p.cuts[c];
   auto same = [&](const int4& a) { return a.x == me.x && a.y == me.y && a.z == me.z; };
-  if (me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
+  if (c >= used || me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
+  const Seq s = seq_of(p, me.x);
+  const long long flat0 = (long long)me.z * kRowsI;
+  const int rows = (int)min((long long)kRowsI, (long long)s.nq * p.G - flat0);
+  const int x = blockIdx.y * kJoinThreads + tid;
+  if ((int)(blockIdx.y * kJoinThreads) >= rows * (kD / 8)) return;
   // the parts: share c - 1's last one, then the first ones of the shares that start in the item
   int mine = -1;
   bool in = false;
@@ -1107,50 +1098,64 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
       if (!same(z) || z.w > a.w) mine = 2 * (c + tid);   // (else the share is empty)
     }
   }
-  if (in) part[1 + tid] = mine;
-  if (tid == 0) part[0] = 2 * (c - 1) + 1;
-  const int parts = 1 + __syncthreads_count(in);
-  const Seq s = seq_of(p, me.x);
-  const long long flat0 = (long long)me.z * kRowsI;
-  const int rows = (int)min((long long)kRowsI, (long long)s.nq * p.G - flat0);
-  constexpr int kCols = 64 / kJoinY;
-  for (int x = tid; x < rows * kCols; x += kJoinThreads) {
-    const int r = x % rows, c4 = blockIdx.y * kCols + x / rows;
-    const int tok = (int)((flat0 + r) / p.G), head = me.y * p.G + (int)((flat0 + r) - (long long)tok * p.G);
-    float m = -INFINITY;
-    for (int k = 0; k < parts; ++k)
-      if (part[k] >= 0) {
-        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
-        if (!(a.x <= m)) m = a.x;   // (a NaN stays)
-      }
-    float l = 0.0f, e = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = 0; k < parts; ++k)
-      if (part[k] >= 0) {
-        const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
-        if (a.y == 0.0f) continue;  // no visible key in this part
-        const float w = exp2f(a.x - m);
-        const float4 v = __ldcg(p.part_o + ((size_t)part[k] * 64 + c4) * kRowsI + r);
-        l += w * a.y;
-        e += w * a.z;
-        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
-      }
-    float wo = 1.0f;
-    if (p.sinks) join_sink(p, head, m, l, e, wo);
-    if (p.lse && c4 == 0) p.lse[(size_t)head * p.Tq + s.q0 + tok] = lse_of(m, e);
-    const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;
-    const bool dead = l == 0.0f || wo == 0.0f;
-    uint32_t lo = dead ? 0u : bf16x2_rn(o.x * inv, o.y * inv), hi = dead ? 0u : bf16x2_rn(o.z * inv, o.w * inv);
-    if (p.gate) {
-      const uint2 g = __ldg(reinterpret_cast<const uint2*>(p.gate + (long long)(s.q0 + tok) * p.gate_stride +
-                                                           (long long)head * kD) + c4);
-      const uint32_t slo = (uint32_t)sigmoid_bf16((uint16_t)g.x) | ((uint32_t)sigmoid_bf16((uint16_t)(g.x >> 16)) << 16);
-      const uint32_t shi = (uint32_t)sigmoid_bf16((uint16_t)g.y) | ((uint32_t)sigmoid_bf16((uint16_t)(g.y >> 16)) << 16);
-      lo = mul_bf16x2(lo, slo);
-      hi = mul_bf16x2(hi, shi);
-    }
-    reinterpret_cast<uint2*>(p.out + ((size_t)(s.q0 + tok) * p.Hq + head) * kD)[c4] = make_uint2(lo, hi);
+  // (empty shares are left out: the list is in order, by ballots within the first warps)
+  __shared__ int count[kJoinThreads / 32];
+  const unsigned ball = __ballot_sync(0xffffffffu, mine >= 0);
+  if ((tid & 31) == 0) count[tid >> 5] = __popc(ball);
+  __syncthreads();
+  int at = 1, parts = 1;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < (tid >> 5)) at += count[w];
+    parts += count[w];
   }
+  if (mine >= 0) part[at + __popc(ball & ((1u << (tid & 31)) - 1u))] = mine;
+  if (tid == 0) part[0] = 2 * (c - 1) + 1;
+  __syncthreads();
+  const int r = x % rows, c8 = x / rows;
+  if (c8 >= kD / 8) return;
+  const int tok = (int)((flat0 + r) / p.G), head = me.y * p.G + (int)((flat0 + r) - (long long)tok * p.G);
+  const uint4* gate = nullptr;
+  uint4 g = make_uint4(0u, 0u, 0u, 0u);
+  if (p.gate) {
+    gate = reinterpret_cast<const uint4*>(p.gate + (long long)(s.q0 + tok) * p.gate_stride + (long long)head * kD) + c8;
+    g = __ldg(gate);
+  }
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) {
+    const float a = __ldcg(&p.part_ml[(size_t)part[k] * kRowsI + r].x);
+    if (!(a <= m)) m = a;   // (a NaN stays)
+  }
+  float l = 0.0f, e = 0.0f;
+  float o[8] = {};
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
+    const float4* src = p.part_o + ((size_t)part[k] * 64 + 2 * c8) * kRowsI + r;
+    const float4 u = __ldcg(src), v = __ldcg(src + kRowsI);
+    if (a.y != 0.0f) {  // (0: no visible key in this part)
+      const float w = exp2f(a.x - m);
+      l += w * a.y;
+      e += w * a.z;
+      o[0] += w * u.x, o[1] += w * u.y, o[2] += w * u.z, o[3] += w * u.w;
+      o[4] += w * v.x, o[5] += w * v.y, o[6] += w * v.z, o[7] += w * v.w;
+    }
+  }
+  float wo = 1.0f;
+  if (p.sinks) join_sink(p, head, m, l, e, wo);
+  if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + s.q0 + tok] = lse_of(m, e);
+  const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;
+  const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = bf16x2_rn(o[2 * i] * inv, o[2 * i + 1] * inv) & keep;
+  if (p.gate) {
+    uint32_t sg[4] = {g.x, g.y, g.z, g.w};
+    sigmoids<1>(sg, p.table);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = mul_bf16x2(b[i], sg[i]);
+  }
+  reinterpret_cast<uint4*>(p.out + ((size_t)(s.q0 + tok) * p.Hq + head) * kD)[c8] = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 namespace {

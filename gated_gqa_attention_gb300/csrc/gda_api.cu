@@ -824,7 +824,8 @@ int gda_prefill_paged(const gda_paged_args* a, void* workspace, size_t workspace
   const int64_t wq = (int64_t)a->Hq * a->D;
   if (a->q_stride < wq || (a->gate && a->gate_stride < wq)) return GDA_ERR_SHAPE;
   if (a->B == 0 || a->total_q == 0) return GDA_OK;
-  if (gda::paged_blocks(a->total_q, a->Hq / a->Hkv, a->B) > 0x7FFFFFFFLL) return GDA_ERR_SHAPE;
+  // a sequence's rows of one KV head (and a block past them) are counted in 31 bits
+  if (a->total_q * (a->Hq / a->Hkv) > 0x7FFFFC00LL) return GDA_ERR_SHAPE;
   if (!a->q || !a->out || !a->cu_seqlens || !a->kv_indptr ||
       (a->nnz > 0 && (!a->kv_indices || !a->k_pool || !a->v_pool || (a->kv_dtype == GDA_KV_E2M1 && !a->kv_scales))))
     return GDA_ERR_NULL;

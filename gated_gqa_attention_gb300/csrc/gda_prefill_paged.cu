@@ -39,12 +39,12 @@ constexpr int kRowsI = kPagedRows;  // rows of an item
 constexpr int kPN = 128;            // keys per tile (MMA N of S)
 constexpr int kSoftmaxWarps = 8;    // warps 0-7
 constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 11;
-constexpr int kGatherWarp = 12;     // warps 12, 13: Q and K; 14, 15: V
+constexpr int kGatherWarp = 12;     // warps 12, 13: K; 14, 15: Q and V
 constexpr int kThreads = 16 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 // registers of a thread: softmax, issuers and planner, gatherers (4 x 128 at the launch)
-constexpr int kRegsSoftmax = 176, kRegsIssue = 56, kRegsGather = 104;
+constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsGather <= 4 * 128, "register shares");
 
 constexpr int kItemCost = 4;        // of an item besides its tiles, in half tiles
@@ -113,17 +113,16 @@ __device__ __forceinline__ Seq seq_of(const PagedParams& p, int b) {
   s.L = max(min(k1, p.nnz) - s.kb, 0);
   return s;
 }
-__device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) {
-  return (int)(((long long)s.nq * p.G + kRowsI - 1) / kRowsI);
-}
+// (a sequence's rows, tokens times G, fit 31 bits with two blocks to spare: the host checks it)
+__device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) { return (s.nq * p.G + kRowsI - 1) / kRowsI; }
 // block i of a sequence: what its rows see, and its tiles
 struct Range {
   int lo, hi, f, tl, n;
 };
 __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, int i) {
   Range r;
-  const int ta = (int)(((long long)i * kRowsI) / p.G);                              // first and last token
-  const int tb = (int)min((long long)s.nq - 1, ((long long)i * kRowsI + kRowsI - 1) / p.G);
+  const int ta = (int)((unsigned)(i * kRowsI) / (unsigned)p.G);                              // first and last token
+  const int tb = min(s.nq - 1, (int)((unsigned)(i * kRowsI + kRowsI - 1) / (unsigned)p.G));
   const int off = s.L - s.nq;
   r.hi = max(off + tb + 1, 0);
   r.lo = p.window > 0 ? (int)min(max((long long)off + ta - p.window + 1, 0LL), (long long)r.hi) : 0;
@@ -136,32 +135,26 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, in
 // Costs of a sequence's blocks, per KV head: linear from its first to its last block.
 struct Costs {
   int mt;              // blocks
-  long long first, rise;
+  long long first, rise;   // the first one's, and 2^16 times what the next one costs more
   __device__ __forceinline__ Costs(const PagedParams& p, const Seq& s) {
     mt = blocks_of(p, s);
     first = rise = 0;
     if (mt > 0) {
-      first = 2LL * range_of(p, s, 0).n + kItemCost;
-      if (mt > 1) rise = 2LL * range_of(p, s, mt - 1).n + kItemCost - first;
+      const int n0 = range_of(p, s, 0).n;
+      first = 2LL * n0 + kItemCost;
+      if (mt > 1) rise = ((2LL * (range_of(p, s, mt - 1).n - n0)) << 16) / (mt - 1);
     }
   }
   // of the blocks before block i
-  __device__ __forceinline__ long long before(int i) const {
-    long long c = first * i;
-    if (rise != 0) {
-      const long long m = (rise > 0 ? rise : -rise) * ((long long)i * (i - 1) / 2) / (mt - 1);
-      c += rise > 0 ? m : -m;
-    }
-    return c;
-  }
+  __device__ __forceinline__ long long before(int i) const { return first * i + ((rise * ((long long)i * (i - 1) / 2)) >> 16); }
 };
 // the place at x within a sequence's costs (0 <= x < Hkv * c.before(c.mt))
-__device__ __noinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, long long x) {
+__device__ __forceinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, long long x) {
   const Costs c(p, s);
   const long long per_head = c.before(c.mt);
   Cut r;
   r.b = b;
-  r.h = (int)(x / per_head);
+  r.h = (int)((unsigned long long)x / (unsigned long long)per_head);
   x -= r.h * per_head;
   int lo = 0, hi = c.mt - 1;   // the last block that starts at or before x
   while (lo < hi) {
@@ -171,7 +164,80 @@ __device__ __noinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, lo
   }
   r.i = lo;
   const long long at = c.before(lo), cost = c.before(lo + 1) - at;
-  r.t = cost > 0 ? (int)((long long)range_of(p, s, lo).n * (x - at) / cost) : 0;
+  r.t = cost > 0 ? (int)((unsigned long long)(range_of(p, s, lo).n * (x - at)) / (unsigned long long)cost) : 0;
+  return r;
+}
+// Where share x of `shares` starts and ends, and how many shares there are.  A whole warp calls it.
+struct Share {
+  Cut start, end;
+  int used;
+};
+__device__ __forceinline__ Share share_of(const PagedParams& p, int x, int shares) {
+  const int lane = threadIdx.x & 31;
+  Seq s = {0, 0, 0, 0};
+  long long cost = 0, total = 0;
+#pragma unroll 4
+  for (int b = lane; b < p.B; b += 32) {
+    s = seq_of(p, b);
+    const Costs c(p, s);
+    cost = p.Hkv * c.before(c.mt);
+    total += cost;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  Share r;
+  // none is less than a tile's worth
+  r.used = (int)max(1LL, min((long long)shares, total / 2));
+  // lanes below 16 find the start, the others the end
+  const int y = x + (lane >> 4);
+  const long long at = y < r.used ? total * y / r.used : total;
+  Seq mine = s;
+  int mine_b = p.B;
+  long long mine_x = 0, sum = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    if (p.B > 32) {
+      cost = 0;
+      if (b0 + lane < p.B) {
+        s = seq_of(p, b0 + lane);
+        const Costs c(p, s);
+        cost = p.Hkv * c.before(c.mt);
+      }
+    }
+    long long upto = cost;  // of the sequences up to the lane's
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    upto += sum;
+    const long long at0 = __shfl_sync(0xffffffffu, at, 0), at1 = __shfl_sync(0xffffffffu, at, 16);
+    // (costs of 0 hold no place: from <= at < upto)
+    const unsigned hit0 = __ballot_sync(0xffffffffu, at0 >= upto - cost && at0 < upto);
+    const unsigned hit1 = __ballot_sync(0xffffffffu, at1 >= upto - cost && at1 < upto);
+    const unsigned hit = lane < 16 ? hit0 : hit1;
+    const int src = hit ? __ffs(hit) - 1 : 0;
+    Seq t;
+    t.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+    t.nq = __shfl_sync(0xffffffffu, s.nq, src);
+    t.kb = __shfl_sync(0xffffffffu, s.kb, src);
+    t.L = __shfl_sync(0xffffffffu, s.L, src);
+    const long long from = __shfl_sync(0xffffffffu, upto - cost, src);
+    if (hit) {
+      mine = t;
+      mine_b = b0 + src;
+      mine_x = at - from;
+    }
+    sum = __shfl_sync(0xffffffffu, upto, 31);
+    if (sum > at1) break;   // (both are found)
+  }
+  Cut c = {p.B, 0, 0, 0};
+  if (mine_b < p.B) c = cut_at(p, mine, mine_b, mine_x);
+  __syncwarp();
+  r.start = {__shfl_sync(0xffffffffu, c.b, 0), __shfl_sync(0xffffffffu, c.h, 0), __shfl_sync(0xffffffffu, c.i, 0),
+             __shfl_sync(0xffffffffu, c.t, 0)};
+  r.end = {__shfl_sync(0xffffffffu, c.b, 16), __shfl_sync(0xffffffffu, c.h, 16), __shfl_sync(0xffffffffu, c.i, 16),
+           __shfl_sync(0xffffffffu, c.t, 16)};
   return r;
 }
 
@@ -298,71 +364,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // ---- this pair's share [start, end) of the stream: a thread per sequence (512 at a time); the sums
-  // and the two places are exchanged in shared memory that the roles use later
-  long long* wsum = reinterpret_cast<long long*>(sm + Lay::kOffX);       // [16]
-  Cut* place = reinterpret_cast<Cut*>(sm + Lay::kOffX + 256);            // start, end
-  int used = 0;   // shares
-  {
-    long long total = 0, x0 = 0, x1 = 0;
-    Seq s = {0, 0, 0, 0};
-    long long cost = 0, upto = 0;  // the thread's sequence's, and of all up to it
-    if (tid < 2) place[tid] = {p.B, 0, 0, 0};
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      long long sum = 0;
-#pragma unroll 1
-      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        if (pass == 0 || p.B > kThreads) {
-          cost = 0;
-          if (b < p.B) {
-            s = seq_of(p, b);
-            const Costs c(p, s);
-            cost = p.Hkv * c.before(c.mt);
-          }
-          upto = cost;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += v;
-          }
-          __syncthreads();
-          if (lane == 31) wsum[warp] = upto;
-          __syncthreads();
-          long long all = 0;
-          for (int w = 0; w < 16; ++w) {
-            if (w == warp) upto += sum + all;
-            all += wsum[w];
-          }
-          sum += all;
-        }
-        if (pass == 1 && cost > 0) {
-          const long long from = upto - cost;
-          if (x0 >= from && x0 < upto) place[0] = cut_at(p, s, b, x0 - from);
-          if (x1 >= from && x1 < upto) place[1] = cut_at(p, s, b, x1 - from);
-        }
-      }
-      if (pass == 0) {
-        total = sum;
-        // none is less than a tile's worth
-        used = (int)max(1LL, min((long long)shares, total / 2));
-        x0 = share < used ? total * share / used : total;
-        x1 = share + 1 < used ? total * (share + 1) / used : total;
-      }
-    }
-  }
-  __syncthreads();
-  const Cut start = place[0], end = place[1];
+  // both CTAs' barriers are set up before anything arrives at them (the planner's share is found meanwhile)
   __syncwarp();
-  // both CTAs' barriers are set up, and `place` has been read
-  cluster_sync_all();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  Share mine = {};
+  if (warp == kPlanWarp) mine = share_of(p, share, shares);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
-  if (tid == 0 && rank == 0) {
-    if (share == 0) p.cuts[0] = make_int4(used, 0, 0, 0);
-    p.cuts[1 + share] = make_int4(start.b, start.h, start.i, start.t);
-  }
-
   const uint32_t tmem = bars.tmem;
   volatile int* abort_flag = &bars.abort;
   auto fail = [&]() {
@@ -426,20 +435,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (!ok) break;
       if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
       if (t.b < 0) break;
-      const long long flat0 = (long long)t.i * kRowsI + rank * kPM;         // this CTA's first row
-      const long long rows = (long long)t.nq * p.G - flat0;                 // (128 at most count)
-      const long long flat = flat0 + r;
-      const int tok = (int)(flat / p.G), head = t.h * p.G + (int)(flat - (long long)tok * p.G);
+      const int flat0 = t.i * kRowsI + rank * kPM;                          // this CTA's first row
+      const int rows = t.nq * p.G - flat0;                                  // (128 at most count)
+      const int tok = (int)((unsigned)(flat0 + r) / (unsigned)p.G), head = t.h * p.G + (flat0 + r - tok * p.G);
       // keys that this row sees: below k_hi, and from k_lo on or below p.keep
       const int pos = t.L - t.nq + tok;
       const int k_hi = max(pos + 1, 0), k_lo = p.window > 0 ? (int)max((long long)pos - p.window + 1, 0LL) : 0;
       const bool some = 32 * rg < rows;   // (rows of the warp)
       // for the epilogue this warp takes 16 rows, w0 .. of the item; lane y < 16 knows row y's place
-      const int w0 = 32 * rg + 16 * hc, nrow = (int)min(16LL, rows - w0);
+      const int w0 = 32 * rg + 16 * hc, nrow = min(16, rows - w0);
       long long o_at = 0, g_at = 0;       // in 16-byte words
       if (lane < nrow) {
-        const long long fl = flat0 + w0 + lane;
-        const int tk = (int)(fl / p.G), hd = t.h * p.G + (int)(fl - (long long)tk * p.G);
+        const int fl = flat0 + w0 + lane;
+        const int tk = (int)((unsigned)fl / (unsigned)p.G), hd = t.h * p.G + (fl - tk * p.G);
         o_at = ((long long)(t.q0 + tk) * p.Hq + hd) * (kD / 8);
         g_at = ((t.q0 + tk) * p.gate_stride) / 8 + hd * (kD / 8);
         if (p.gate && t.part < 0)         // the gate on its way to the L2 while the item is computed
@@ -457,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         if (!ok) break;
         tc_fence_after();
         // (Q's copy was over before the S product began)
-        if (KV != GDA_KV_BF16 && j == t.ta) factor = qscale[(it & 3) * kPM + r];
+        if (KV != GDA_KV_BF16 && j == t.ta && r < rows) factor = qscale[(it & 3) * kPM + r];
         float hm = -INFINITY;
         float s[64];
         if (some) {
@@ -474,7 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 64; ++c) e4[c & 3] = fmaxf(e4[c & 3], s[c]);
-          hm = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
+          // (a row past the item's last holds anything: its max stays -inf, so that it decides nothing below)
+          if (r < rows) hm = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
         }
         // the two halves of the row agree on the tile max (parity-buffered slots); after this
         // both have read their S, so P may overwrite it
@@ -681,8 +690,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     regs_shrink<kRegsIssue>();
     if (warp == kPlanWarp) {
       // ---------------- the share's items, one after the other
+      if (lane == 0 && rank == 0) {
+        if (share == 0) p.cuts[0] = make_int4(mine.used, 0, 0, 0);
+        p.cuts[1 + share] = make_int4(mine.start.b, mine.start.h, mine.start.i, mine.start.t);
+      }
+      const Cut end = mine.end;
       bool ok = true;
-      Cut at = start;
+      Cut at = mine.start;
       Seq s = {0, 0, 0, 0};
       int mt = 0;
       if (at.b < p.B) {
@@ -829,6 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
+        if (is_v) pass(&bars.q_land, &bars.q_peer, it);
 #pragma unroll 1
         for (int j = t.ta; j < t.tb && ok; ++j) {
           pass(&land[slot], &peer[slot], use);
@@ -836,7 +851,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
             slot = 0;
             ++use;
           }
-          if (ok && !is_v && j == t.ta) pass(&bars.q_land, &bars.q_peer, it);
         }
         if (!ok) break;
         ++it;
@@ -845,8 +859,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     }
   } else {
     regs_shrink<kRegsGather>();
-    // ---------------- gatherers: warps 12, 13 take Q and K (32 of this CTA's 64 keys of a tile each), 14,
-    // 15 V (64 of the 128 keys each, this CTA's 128 dimensions).  A tile goes into the next slot of its
+    // ---------------- gatherers: warps 12, 13 take K (32 of this CTA's 64 keys of a tile each), 14, 15
+    // Q and V (64 of the 128 keys each, this CTA's 128 dimensions).  A tile goes into the next slot of its
     // ring once the MMAs that read the slot's previous tile have completed.  BF16 rows are copied
     // asynchronously (cp.async, whose completion arrives at the slot's barrier); codes go through
     // registers, widened to FP16.
@@ -878,7 +892,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
       if (t.b < 0) break;
       if (t.tb == t.ta) continue;
-      if (is_v && it > 0) ok = acquire(&bars.v_free, it - 1);  // the previous item's outputs have left the buffers
+      // four rows per step, eight lanes each: lane l8 of row 4 q + g8 takes 16 bytes of every 128
+      const int g8 = lane >> 3, l8 = lane & 7;
       // the slots of keys key0 + lane and (V) key0 + 32 + lane of tile j: loaded two tiles ahead, looked at
       // when used; kUnseen where no row of the item sees the position
       constexpr int kUnseen = INT_MIN;
@@ -892,29 +907,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           if ((x == 0 || is_v) && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep)) to[x] = __ldg(p.indices + t.kb + pos);
         }
       };
+      look_up(t.ta, n0);
+      look_up(t.ta + 1, n1);
       // -1: zeros.  A row outside the pools reads as zeros and is reported
       auto slot_of = [&](int v) -> int {
         if (v >= 0 && (long long)v < p.num_slots) return v;
         if (v != kUnseen) atomicOr(p.error, kErrIndex);
         return -1;
       };
-      look_up(t.ta, n0);
-      look_up(t.ta + 1, n1);
+      if (is_v && ok) {
+        // Q (the previous item's last S product has read it): the item's rows, 64 per warp, four rows per
+        // step as below; rows past its last stay what they are, and what comes of them goes nowhere
+        if (it > 0) ok = acquire(&bars.q_empty, it - 1);
+        if (!ok) break;
+        const int q64 = 64 * (warp & 1), flat0 = t.i * kRowsI + rank * kPM + q64;
+        const int rows = min(64, t.nq * p.G - flat0);
+        const int dt = 4 / p.G, dg = 4 - dt * p.G;     // four rows on
+        int tok = (int)((unsigned)(flat0 + g8) / (unsigned)p.G), g = flat0 + g8 - tok * p.G;
+        unsigned char* dq = sm + Lay::kOffQ + (q64 + g8) * 128;
+#pragma unroll 2
+        for (int q = 0; 4 * q < rows; ++q) {
+          const bool in = 4 * q + g8 < rows;
+          const __nv_bfloat16* src = p.q + (in ? (long long)(t.q0 + tok) * p.q_stride + (long long)(t.h * p.G + g) * kD : 0) + l8 * 8;
+          const uint32_t to = smem_u32(dq) + q * 512 + ((l8 ^ ((4 * q + g8) & 7)) << 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) cp_async16(to + c * kBlk, src + 64 * c, in ? 16 : 0);
+          tok += dt;
+          g += dg;
+          if (g >= p.G) {
+            g -= p.G;
+            ++tok;
+          }
+        }
+        if (KV != GDA_KV_BF16) {
+          // to FP16 in place (each thread what it copied), each row times a power of two that brings its
+          // largest element to [1, 2): exact but for elements 2^-14 of that and less, which lose bits
+          // below 2^-24 of it
+          cp_async_wait_all();
 #pragma unroll 1
-      for (int j = t.ta; j < t.tb && ok; ++j) {
-        look_up(j + 2, n2);
-        const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
-        n0[0] = n1[0], n0[1] = n1[1], n1[0] = n2[0], n1[1] = n2[1];
-        unsigned char* dst = ring + slot * kHalf;
-        // four rows per step, eight lanes each: lane l8 of row 4 q + g8 takes 16 bytes of every 128
-        const int g8 = lane >> 3, l8 = lane & 7;
-        if (KV == GDA_KV_BF16) {
+          for (int q = 0; 4 * q < rows; ++q) {
+            unsigned char* at = dq + q * 512 + ((l8 ^ ((4 * q + g8) & 7)) << 4);
+            uint4 raw[4];
+            uint32_t top = 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              raw[c] = *reinterpret_cast<const uint4*>(at + c * kBlk);
+              const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7FFF0000u, w4[e] & 0x7FFF0000u));
+            }
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top >>= 23;                                             // its exponent
+            // (0 and subnormals, and infinities and NaNs, stay as they are)
+            const int ex = (top == 0u || top == 255u) ? 127 : min(max((int)top, 30), 250);
+            const float up = __uint_as_float((uint32_t)(254 - ex) << 23);   // 2^(127 - ex)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = f16x2_rn(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xFFFF0000u) * up);
+              *reinterpret_cast<uint4*>(at + c * kBlk) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (l8 == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
+              qscale[(it & 3) * kPM + q64 + 4 * q + g8] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
+          }
+        }
+        landed(&bars.q_land);
+        if (it > 0) ok = acquire(&bars.v_free, it - 1);  // the previous item's outputs have left V's slots
+        if (!ok) break;
+      }
+      if (KV == GDA_KV_BF16) {
+        const uint32_t sw[2] = {(uint32_t)(l8 ^ g8) << 4, (uint32_t)(l8 ^ (4 + g8)) << 4};
+        const unsigned char* base = pool + (size_t)t.h * (2 * kD) + (is_v ? rank * kD : 0) + l8 * 16;
+        const uint32_t pitch = (uint32_t)p.Hkv * (2 * kD);
+#pragma unroll 1
+        for (int j = t.ta; j < t.tb; ++j) {
+          look_up(j + 2, n2);
+          const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
+          n0[0] = n1[0], n0[1] = n1[1], n1[0] = n2[0], n1[1] = n2[1];
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
-          const uint32_t d0 = smem_u32(dst) + (r64 + g8) * 128;
-          const uint32_t sw[2] = {(uint32_t)(l8 ^ g8) << 4, (uint32_t)(l8 ^ (4 + g8)) << 4};
-          const unsigned char* base = pool + (size_t)t.h * (2 * kD) + (is_v ? rank * kD : 0) + l8 * 16;
-          const uint32_t pitch = (uint32_t)p.Hkv * (2 * kD);
+          const uint32_t d0 = smem_u32(ring + slot * kHalf) + (r64 + g8) * 128;
           if (!is_v) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -932,122 +1008,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
               for (int c = 0; c < 2; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kBlk, src + 128 * c, sl >= 0 ? 16 : 0);
             }
           }
-        } else if (KV == GDA_KV_E4M3) {
-          // K: two rows of 256 codes per step, V: four half rows of 128; eight steps' loads in flight
-          const int lanes = is_v ? 8 : 16, part = lane & (lanes - 1), sub = is_v ? lane >> 3 : lane >> 4;
-          const uint32_t blk = is_v ? kBlk : kKBlk;
+          landed(&land[slot]);
+          if (++slot == slots) {
+            slot = 0;
+            ++use;
+          }
+        }
+      } else {
+        // codes: kSteps 16-byte loads per lane and tile, the next tile's on their way while one is widened.
+        // e4m3: K has two steps per four rows (128 codes each), V one; 4 bits: one per four rows, V one per eight
+        constexpr int kSteps = KV == GDA_KV_E4M3 ? 16 : 8;
+        uint4 raw[kSteps];
+        uint32_t sc[KV == GDA_KV_E2M1 ? kSteps : 1];
+        const int part = (KV == GDA_KV_E2M1 && is_v) ? lane & 3 : l8, sub = (KV == GDA_KV_E2M1 && is_v) ? lane >> 2 : g8;
+        auto row_of = [&](int x) -> int {   // of the warp's part of a tile
+          if (KV == GDA_KV_E4M3) return is_v ? 4 * x + sub : 4 * (x >> 1) + sub;
+          return is_v ? 8 * x + sub : 4 * x + sub;
+        };
+        auto load = [&](int x, int sl0, int sl1) {
+          const int row = row_of(x);
+          const int sl = __shfl_sync(0xffffffffu, row < 32 ? sl0 : sl1, row & 31);
+          raw[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (KV == GDA_KV_E2M1) sc[x] = 0u;
+          if (sl < 0) return;
+          const size_t at = (size_t)sl * p.Hkv + t.h;
+          if (KV == GDA_KV_E4M3) {
+            raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kD + (is_v ? rank * 128 : 128 * (x & 1))) + part);
+          } else {
+            raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kCodeBytes + (is_v ? rank * 64 : 0)) + part);
+            sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + at * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0)) + part);
+          }
+        };
+        {
+          const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
+#pragma unroll
+          for (int x = 0; x < kSteps; ++x) load(x, sl0, sl1);
+        }
 #pragma unroll 1
-          for (int y = 0; y < 2 && ok; ++y) {
-            uint4 raw[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const int row = is_v ? 4 * x + sub : 16 * y + 2 * x + sub;   // (V: of the warp's half y)
-              const int sl = __shfl_sync(0xffffffffu, is_v && y ? sl1 : sl0, row);
-              raw[x] = make_uint4(0u, 0u, 0u, 0u);
-              if (sl >= 0)
-                raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + ((size_t)sl * p.Hkv + t.h) * kD + (is_v ? rank * 128 : 0)) + part);
-            }
-            if (y == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
-            if (!ok) break;
-            const int c = 2 * part;                                        // the first of two 8-dimension chunks
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const int row = r64 + (is_v ? 32 * y + 4 * x + sub : 16 * y + 2 * x + sub);
-              unsigned char* at = dst + (c >> 3) * blk + row * 128;
-              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
-              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
-            }
-          }
-        } else {
-          // K: four rows of 128 bytes of codes and 16 scales per step, V: eight half rows
-          const int lanes = is_v ? 4 : 8, part = lane & (lanes - 1), sub = is_v ? lane >> 2 : lane >> 3;
-          const uint32_t blk = is_v ? kBlk : kKBlk;
-          uint4 raw[8];
-          uint32_t sc[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int row = is_v ? 8 * x + sub : 4 * x + sub;
-            const int sl = __shfl_sync(0xffffffffu, row < 32 ? sl0 : sl1, row & 31);
-            raw[x] = make_uint4(0u, 0u, 0u, 0u);
-            sc[x] = 0u;
-            if (sl >= 0) {
-              const size_t at = (size_t)sl * p.Hkv + t.h;
-              raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kCodeBytes + (is_v ? rank * 64 : 0)) + part);
-              sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + at * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0)) + part);
-            }
-          }
+        for (int j = t.ta; j < t.tb; ++j) {
+          look_up(j + 2, n2);
+          const int sl0 = slot_of(n1[0]), sl1 = is_v ? slot_of(n1[1]) : -1;   // of the next tile
+          n1[0] = n2[0], n1[1] = n2[1];
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
-          const int c = 4 * part;                                          // the first of four 8-dimension chunks
+          unsigned char* dst = ring + slot * kHalf + r64 * 128;
+          const uint32_t blk = is_v ? kBlk : kKBlk;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int row = r64 + (is_v ? 8 * x + sub : 4 * x + sub);
-            const uint32_t f = e4m3x2_to_f16x2(sc[x]);
-            const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-            unsigned char* at = dst + (c >> 3) * blk + row * 128;
-            *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
-            *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
-            *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
-            *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
-          }
-        }
-        if (!ok) break;
-        landed(&land[slot]);
-        if (++slot == slots) {
-          slot = 0;
-          ++use;
-        }
-        if (!is_v && j == t.ta) {
-          // Q behind the first K tile (it needs the previous item's last S product): a row per step,
-          // zeros in rows past the item's last
-          if (it > 0) ok = acquire(&bars.q_empty, it - 1);
-          if (!ok) break;
-          const int q64 = 64 * (warp & 1);
-          const long long flat0 = (long long)t.i * kRowsI + rank * kPM + q64, rows = (long long)t.nq * p.G;
-          int tok = (int)(flat0 / p.G), g = (int)(flat0 - (long long)tok * p.G);
-          unsigned char* dq = sm + Lay::kOffQ + (lane >> 3) * kBlk + q64 * 128;
-#pragma unroll 1
-          for (int x0 = 0; x0 < 64; x0 += 8) {
-            uint4 raw[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const bool in = flat0 + x0 + x < rows;
-              const __nv_bfloat16* src =
-                  p.q + (in ? (long long)(t.q0 + tok) * p.q_stride + (long long)(t.h * p.G + g) * kD : 0) + lane * 8;
-              if (KV == GDA_KV_BF16)
-                cp_async16(smem_u32(dq + (x0 + x) * 128 + (((lane & 7) ^ x) << 4)), src, in ? 16 : 0);
-              else
-                raw[x] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
-              if (++g == p.G) {
-                g = 0;
-                ++tok;
-              }
+          for (int x = 0; x < kSteps; ++x) {
+            const int row = row_of(x);
+            if (KV == GDA_KV_E4M3) {
+              const int c = 2 * part;                  // the first of two 8-dimension chunks (of 128 dimensions)
+              unsigned char* at = dst + ((c >> 3) + (is_v ? 0 : 2 * (x & 1))) * blk + row * 128;
+              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
+              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
+            } else {
+              const int c = 4 * part;                  // the first of four
+              const uint32_t f = e4m3x2_to_f16x2(sc[x]);
+              const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+              unsigned char* at = dst + (c >> 3) * blk + row * 128;
+              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
+              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
+              *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
+              *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
             }
-            if (KV != GDA_KV_BF16) {
-              // in FP16, each row times a power of two that brings its largest element to [1, 2): exact but
-              // for elements 2^-14 of that and less, which lose bits below 2^-24 of it
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const uint32_t w4[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-                uint32_t top = 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7FFF0000u, w4[e] & 0x7FFF0000u));
-                top = __reduce_max_sync(0xffffffffu, top) >> 23;      // its exponent
-                // (0 and subnormals, and infinities and NaNs, stay as they are)
-                const int ex = (top == 0u || top == 255u) ? 127 : min(max((int)top, 30), 250);
-                const float up = __uint_as_float((uint32_t)(254 - ex) << 23);   // 2^(127 - ex)
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  o[e] = f16x2_rn(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xFFFF0000u) * up);
-                *reinterpret_cast<uint4*>(dq + (x0 + x) * 128 + (((lane & 7) ^ x) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                if (lane == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
-                  qscale[(it & 3) * kPM + q64 + x0 + x] =
-                      fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
-              }
-            }
+            if (j + 1 < t.tb) load(x, sl0, sl1);
           }
-          landed(&bars.q_land);
+          landed(&land[slot]);
+          if (++slot == slots) {
+            slot = 0;
+            ++use;
+          }
         }
       }
       if (!ok) break;

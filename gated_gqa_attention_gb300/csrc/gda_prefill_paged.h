@@ -43,13 +43,6 @@ constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxShares * kPagedRows * 16;
 constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxShares * 64 * kPagedRows * 16;
 static_assert((kPagedMaxShares + 1) * 16 <= kPagedCutBytes, "cut table");
 
-// The most blocks of rows (rows: a token's query heads of one KV head, token after token) that B
-// sequences of `tokens` tokens in all can have.
-inline long long paged_blocks(long long tokens, long long G, long long B) {
-  const long long n = tokens * G / kPagedRows + B;
-  return n < tokens * G ? n : tokens * G;
-}
-
 // kv_dtype: GDA_KV_* of the pools
 cudaError_t launch_prefill_paged(const PagedParams& p, int kv_dtype, cudaStream_t stream);
 cudaError_t paged_init();  // the kernels' attributes on the current device

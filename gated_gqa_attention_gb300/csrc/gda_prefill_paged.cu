@@ -38,16 +38,22 @@ constexpr int kPM = 128;            // rows of an item per CTA (half the MMA's M
 constexpr int kRowsI = kPagedRows;  // rows of an item
 constexpr int kPN = 128;            // keys per tile (MMA N of S)
 constexpr int kSoftmaxWarps = 8;    // warps 0-7
-constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 11;
-constexpr int kGatherWarp = 12;     // warps 12, 13: K; 14, 15: Q and V
-constexpr int kThreads = 16 * 32;
+constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 10;  // relays: 10 for K, 11 for Q and V
+constexpr int kGatherWarp = 12;     // the gatherers: the first half of them for K, the others for Q and V
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
-// registers of a thread: softmax, issuers and planner, gatherers (4 x 128 at the launch)
+constexpr int kGatherers = 4;       // half of them for K, half for Q and V
+constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
+// registers of a thread: softmax, planner and issuer, gatherers share out what the block has at its
+// launch (128 each).  Spills are dear here: shared memory leaves the L1 little room
 constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
-static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsGather <= 4 * 128, "register shares");
+static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + 32 * kGatherers * kRegsGather <= kThreads * 128, "register shares");
+constexpr int kRowsK = 64 / (kGatherers / 2), kRowsV = 128 / (kGatherers / 2);  // of a tile per gathering warp
+// arrivals that make a CTA's part of a tile complete: every copying thread's, or one of each widening warp
+template <int KV>
+constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
 
-constexpr int kItemCost = 4;        // of an item besides its tiles, in half tiles
+constexpr int kItemCost = 14;        // of an item besides its tiles, in half tiles
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
 constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
@@ -81,11 +87,12 @@ struct Cut {           // a place in the stream: block i of KV head h of sequenc
   int b, h, i, t;
 };
 struct Bars {
-  // *_land: this CTA's part of Q, K, V has landed (every gathering thread arrives); *_peer, in rank 0:
-  // rank 1's has; p_full and o_empty, in rank 0, count both CTAs' warps; commits arrive in both
-  uint64_t q_land, q_peer, q_empty;                 // (q_empty: the item's S products have read it)
-  uint64_t k_land[3], k_peer[3], k_empty[3], v_land[2], v_peer[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], p_empty[2];        // per S / P buffer
+  // *_land: this CTA's part of Q, K, V has landed (every gathering thread arrives).  In rank 0, where
+  // both CTAs arrive: q_full and k_full (both parts have), pv_full (P written and both parts of V),
+  // o_empty (O read).  Commits arrive in both CTAs
+  uint64_t q_land, q_full, q_empty;                 // (q_empty: the item's S products have read it)
+  uint64_t k_land[3], k_full[3], k_empty[3], v_land[2], v_empty[2];
+  uint64_t s_full[2], pv_full[2], p_empty[2];       // per S / P buffer
   uint64_t xm[4][2];                                // per row quarter and tile parity: both maxima stored
   uint64_t pr[4];                                   // per row quarter: both halves' epilogues are here
   uint64_t o_full, o_empty, v_free;                 // the item's O complete; read; its staging read
@@ -95,9 +102,6 @@ struct Bars {
   int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
-constexpr int kGatherWarps = 4;                     // 2 each
-constexpr int kItemReaders = kGatherWarps + kSoftmaxWarps;  // and the issuer, or rank 1's two relays
-
 // ---- the stream of items
 
 struct Seq {
@@ -297,6 +301,8 @@ __device__ __forceinline__ void join_sink(const PagedParams& p, int head, float&
     e += t;
   }
 }
+// the lowest n bits (none for n <= 0, all from 64 on)
+__device__ __forceinline__ unsigned long long below(int n) { return n <= 0 ? 0ull : ~0ull >> (64 - min(n, 64)); }
 __device__ __forceinline__ float lse_of(float m, float e) {
   return (e == 0.0f) ? -INFINITY : (m + log2f(e)) * 0.69314718055994530942f;
 }
@@ -325,23 +331,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   const int rank = (int)cluster_rank(), share = blockIdx.x >> 1, shares = gridDim.x >> 1;
 
   if (tid == 0) {
-    mbar_init(&bars.q_land, 64);
-    mbar_init(&bars.q_peer, 1);
+    mbar_init(&bars.q_land, kLandings<KV>);
+    mbar_init(&bars.q_full, 2);
     mbar_init(&bars.q_empty, 1);
     for (int x = 0; x < kKSlots; ++x) {
-      mbar_init(&bars.k_land[x], 64);
-      mbar_init(&bars.k_peer[x], 1);
+      mbar_init(&bars.k_land[x], kLandings<KV>);
+      mbar_init(&bars.k_full[x], 2);
       mbar_init(&bars.k_empty[x], 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars.v_land[x], 64);
-      mbar_init(&bars.v_peer[x], 1);
+      mbar_init(&bars.v_land[x], kLandings<KV>);
       mbar_init(&bars.v_empty[x], 1);
       mbar_init(&bars.s_full[x], 1);
-      mbar_init(&bars.p_full[x], 2 * kSoftmaxWarps);
+      mbar_init(&bars.pv_full[x], 2 * kSoftmaxWarps + 2);
       mbar_init(&bars.p_empty[x], 1);
       mbar_init(&bars.i_full[x], 1);
-      mbar_init(&bars.i_empty[x], kItemReaders + 1 + rank);
+      mbar_init(&bars.i_empty[x], 2 + kGatherers + kSoftmaxWarps + (rank == 0 ? 1 : 0));  // relays, gatherers, softmax, issuer
     }
     for (int q4 = 0; q4 < 4; ++q4) {
       mbar_init(&bars.xm[q4][0], 2);
@@ -390,16 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     do {
       if (*abort_flag || clock64() - t0 > limit) return false;
     } while (!mbar_try_wait_for(bar, parity & 1, hint));
-    return true;
-  };
-  // of the issuers, in rank 0: barriers that both CTAs arrive on
-  auto wait_both = [&](uint64_t* bar, int parity) -> bool {
-    if (mbar_try_wait_cluster(bar, parity & 1, hint)) return true;
-    const long long t0 = clock64();
-#pragma unroll 1
-    do {
-      if (*abort_flag || clock64() - t0 > limit) return false;
-    } while (!mbar_try_wait_cluster(bar, parity & 1, hint));
     return true;
   };
   auto arrive_first = [&](uint64_t* bar) { mbar_arrive_cluster(cluster_addr(bar, 0)); };  // rank 0's barrier
@@ -474,10 +469,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           tmem_wait_ld();
           const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of s[0]
           if (__any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep))) {
-            const int nh = k_hi - k0, nl = k_lo - k0, nf = p.keep - k0;
+            const unsigned long long seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
+            const uint32_t seen2[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (c >= nh || (c < nl && c >= nf)) s[c] = -INFINITY;
+              if (!(seen2[c >> 5] & (1u << (c & 31)))) s[c] = -INFINITY;
           }
           float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -552,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(&bars.p_full[sb]);
+        if (lane == 0) arrive_first(&bars.pv_full[sb]);
       }
       if (!ok) break;
       const bool tiles = t.tb > t.ta;
@@ -602,27 +598,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         ++it;
         continue;
       }
-      // ---- epilogue of a whole item, eight rows at a time: their sigmoids (lane l has dimensions 8l ..
-      // 8l + 7 of each; 1 without a gate), the first eight's while the last products run
-      constexpr int kRows = 8;
+      // ---- epilogue of a whole item, four rows at a time (lane l has dimensions 8l .. 8l + 7 of each), the
+      // gate of the next four on its way.  Rolled: this code runs once per item, and unrolled its
+      // instructions came from the L2 each time (8 rows of a single token: 5 us)
+      constexpr int kRows = 4;
       uint32_t sg[4 * kRows];
       auto gate_rows = [&](int y0) {
-        if (p.gate) {
 #pragma unroll
-          for (int y = 0; y < kRows; ++y) {
-            const long long at = __shfl_sync(0xffffffffu, g_at, y0 + y);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (y0 + y < nrow) v = __ldcs(reinterpret_cast<const uint4*>(p.gate) + at + lane);
-            sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
-          }
-#pragma unroll
-          for (int y = 0; y < kRows; y += 4) sigmoids<4>(sg + 4 * y, p.table);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4 * kRows; ++x) sg[x] = 0x3F803F80u;
+        for (int y = 0; y < kRows; ++y) {
+          const long long at = __shfl_sync(0xffffffffu, g_at, (y0 + y) & 31);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (p.gate && y0 + y < nrow) v = __ldcs(reinterpret_cast<const uint4*>(p.gate) + at + lane);
+          sg[4 * y] = v.x, sg[4 * y + 1] = v.y, sg[4 * y + 2] = v.z, sg[4 * y + 3] = v.w;
         }
       };
-      if (nrow > 0) gate_rows(0);
+      gate_rows(0);
       float m = m_run, wo = 1.0f;
       if (p.sinks && r < rows) join_sink(p, head, m, l, e, wo);
       if (p.lse && hc == 0 && r < rows) p.lse[(size_t)head * p.Tq + t.q0 + tok] = lse_of(m, e);
@@ -666,7 +656,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       }
 #pragma unroll 1
       for (int y0 = 0; y0 < nrow; y0 += kRows) {
-        if (y0 > 0) gate_rows(y0);
+        uint32_t now[4 * kRows];
+#pragma unroll
+        for (int x = 0; x < 4 * kRows; ++x) now[x] = sg[x];
+        gate_rows(y0 + kRows);
+        if (p.gate) {
+          sigmoids<kRows>(now, p.table);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4 * kRows; ++x) now[x] = 0x3F803F80u;
+        }
 #pragma unroll
         for (int y = 0; y < kRows; ++y) {
           const int row = w0 + y0 + y;
@@ -675,8 +674,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           if (tiles)
             v = *reinterpret_cast<const uint4*>(stage + (lane >> 3) * kBlk + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
           // (a product of two BF16 values, correctly rounded by one instruction)
-          v.x = mul_bf16x2(v.x, sg[4 * y]), v.y = mul_bf16x2(v.y, sg[4 * y + 1]);
-          v.z = mul_bf16x2(v.z, sg[4 * y + 2]), v.w = mul_bf16x2(v.w, sg[4 * y + 3]);
+          v.x = mul_bf16x2(v.x, now[4 * y]), v.y = mul_bf16x2(v.y, now[4 * y + 1]);
+          v.z = mul_bf16x2(v.z, now[4 * y + 2]), v.w = mul_bf16x2(v.w, now[4 * y + 3]);
           if (y0 + y < nrow) reinterpret_cast<uint4*>(p.out)[at + lane] = v;
         }
       }
@@ -755,18 +754,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       }
       if (!ok && lane == 0) fail();
     } else if (rank == 0 && lane == 0 && warp == kMmaWarp) {
-      // ---------------- issuer: S(T) = Q K(T)^T into S buffer T % 2, O += P(T) V(T), in the order S(T + 1),
-      // PV(T): one thread's MMAs run in order, so S(T + 2) follows PV(T), whose P its scores replace,
+      // ---------------- issuer: S(T) = Q K(T)^T into S buffer T % 2, O += P(T) V(T).  A wait in the issuing
+      // thread lets the tensor pipe run empty, so there are few, all before a group of MMAs: PV(T) and
+      // S(T + 2).  One thread's MMAs run in order: S(T + 2) follows PV(T), whose P its scores replace,
       // without a wait between them
       const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK), sV = smem_u32(sm + Lay::kOffV);
       constexpr uint32_t idS = idesc_of<KV>(kRowsI, kPN, 0), idO = idesc_of<KV>(kRowsI, kD, 1);
       int it = 0, T = 0, slot = 0, use = 0;
       int done_s = -1, done_o = -1;  // tiles of the last commits
       bool ok = true;
-      auto issue_s = [&](int x) -> bool {
-        if (!wait(&bars.k_land[slot], use) || !wait_both(&bars.k_peer[slot], use)) return false;
-        fence_async_shared();   // (the rows were written by threads, the MMAs read through the async proxy)
-        tc_fence_after();
+      auto issue_s = [&](int x) {
         const uint32_t kb = sK + slot * kHalf;
 #pragma unroll
         for (int kk = 0; kk < 16; ++kk) {  // head dimensions 16 kk .. 16 kk + 15
@@ -774,14 +771,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           const uint64_t bd = sdesc_sw128(kb + (kk >> 2) * kKBlk + (kk & 3) * 32, 16, 1024);
           umma_pair_ss(tmem + kTmemS + (x & 1) * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
         }
-        umma_commit_pair(&bars.k_empty[slot]);
         umma_commit_pair(&bars.s_full[x & 1]);
+        umma_commit_pair(&bars.k_empty[slot]);
         done_s = x;
         if (++slot == kKSlots) {
           slot = 0;
           ++use;
         }
-        return true;
       };
       for (int n = 0;; ++n) {
         Item t;
@@ -790,27 +786,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
-        ok = wait(&bars.q_land, it) && wait_both(&bars.q_peer, it) && issue_s(T);
+        // (S product x, two tiles ahead of PV product T)
+        ok = wait(&bars.q_full, it);
+        int x = T;
 #pragma unroll 1
-        for (int j = t.ta; j < t.tb && ok; ++j, ++T) {
-          if (j + 1 < t.tb) ok = issue_s(T + 1);
-          else umma_commit_pair(&bars.q_empty);               // (every S product of the item)
-          if (ok && j == t.ta && it > 0) ok = wait_both(&bars.o_empty, it - 1);  // the epilogues have read the previous O
+        for (int j = t.ta; j < t.tb + 2 && ok; ++j) {
+          const bool more = j < t.tb;   // S product j of the item, after PV of tile j - 2
+          if (more) ok = wait(&bars.k_full[slot], use);
           const int pb = T & 1;
-          ok = ok && wait(&bars.v_land[pb], T >> 1) && wait_both(&bars.v_peer[pb], T >> 1) && wait_both(&bars.p_full[pb], T >> 1);
-          if (!ok) break;
-          fence_async_shared();
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            // V is MN-major (dims contiguous): LBO = stride between a CTA's two 64-dim blocks, SBO = 8 key
-            // rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in columns 8 kk .. 8 kk + 7 of the S buffer
-            const uint64_t bd = sdesc_sw128(sV + pb * kHalf + kk * 16 * 128, kBlk, 1024);
-            umma_pair_ts(tmem + kTmemO, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO, (j > t.ta || kk > 0) ? 1u : 0u);
+          if (j >= t.ta + 2) {
+            if (ok && j == t.ta + 2 && it > 0) ok = wait(&bars.o_empty, it - 1);  // the epilogues have read the previous O
+            ok = ok && wait(&bars.pv_full[pb], T >> 1);
           }
-          umma_commit_pair(&bars.v_empty[pb]);
-          umma_commit_pair(&bars.p_empty[pb]);
-          done_o = T;
+          if (!ok) break;
+          tc_fence_after();
+          if (j >= t.ta + 2) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              // V is MN-major (dims contiguous): LBO = stride between a CTA's two 64-dim blocks, SBO = 8 key
+              // rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in columns 8 kk .. 8 kk + 7 of the S buffer
+              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + kk * 16 * 128, kBlk, 1024);
+              umma_pair_ts(tmem + kTmemO, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO, (j > t.ta + 2 || kk > 0) ? 1u : 0u);
+            }
+            umma_commit_pair(&bars.v_empty[pb]);
+            umma_commit_pair(&bars.p_empty[pb]);
+            done_o = T++;
+          }
+          if (more) {
+            issue_s(x++);
+            if (j + 1 == t.tb) umma_commit_pair(&bars.q_empty);   // (every S product of the item)
+          }
         }
         if (!ok) break;
         umma_commit_pair(&bars.o_full);
@@ -822,12 +827,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         if (done_s >= 0) drain(&bars.s_full[done_s & 1], done_s >> 1);
         if (done_o >= 0) drain(&bars.p_empty[done_o & 1], done_o >> 1);
       }
-    } else if (rank == 1 && lane == 0 && (warp == kMmaWarp || warp == kRelayWarp)) {
-      // ---------------- rank 1: what has landed here is passed on to rank 0's issuer
-      const bool is_v = warp == kRelayWarp;
+    } else if (lane == 0 && warp >= kRelayWarp) {
+      // ---------------- relays: what has landed in this CTA is passed on to the issuer's barriers (and to
+      // the proxy by which the MMAs read it)
+      const bool is_v = warp > kRelayWarp;
       const int slots = is_v ? 2 : kKSlots;
       uint64_t* land = is_v ? bars.v_land : bars.k_land;
-      uint64_t* peer = is_v ? bars.v_peer : bars.k_peer;
+      uint64_t* full = is_v ? bars.pv_full : bars.k_full;
       int it = 0, slot = 0, use = 0;
       bool ok = true;
       auto pass = [&](uint64_t* from, uint64_t* to, int parity) {
@@ -843,10 +849,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         mbar_arrive(&bars.i_empty[n & 1]);
         if (t.b < 0) break;
         if (t.tb == t.ta) continue;
-        if (is_v) pass(&bars.q_land, &bars.q_peer, it);
+        if (is_v) pass(&bars.q_land, &bars.q_full, it);
 #pragma unroll 1
         for (int j = t.ta; j < t.tb && ok; ++j) {
-          pass(&land[slot], &peer[slot], use);
+          pass(&land[slot], &full[slot], use);
           if (++slot == slots) {
             slot = 0;
             ++use;
@@ -859,14 +865,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     }
   } else {
     regs_shrink<kRegsGather>();
-    // ---------------- gatherers: warps 12, 13 take K (32 of this CTA's 64 keys of a tile each), 14, 15
-    // Q and V (64 of the 128 keys each, this CTA's 128 dimensions).  A tile goes into the next slot of its
-    // ring once the MMAs that read the slot's previous tile have completed.  BF16 rows are copied
-    // asynchronously (cp.async, whose completion arrives at the slot's barrier); codes go through
-    // registers, widened to FP16.
-    const bool is_v = warp >= kGatherWarp + 2;
-    const int r64 = (is_v ? 64 : 32) * (warp & 1);   // this warp's first row of the CTA's part of a tile
-    const int key0 = is_v ? r64 : 64 * rank + r64;   // that row's key
+    // ---------------- gatherers, for K (this CTA's 64 keys of a tile) or for Q and V (128 keys, this CTA's
+    // 128 dimensions).  A tile goes into the next slot of its ring once the MMAs that read the slot's
+    // previous tile have completed.  BF16 rows are copied asynchronously (cp.async, whose completion
+    // arrives at the slot's barrier); codes go through registers, widened to FP16.
+    constexpr int kHalfTeam = kGatherers / 2;
+    const int gw = (warp - kGatherWarp) % kHalfTeam;
+    const bool is_v = warp >= kGatherWarp + kHalfTeam;
+    const int row0 = is_v ? gw * kRowsV : gw * kRowsK;   // this warp's first row of the CTA's part of a tile
+    const int key0 = is_v ? row0 : 64 * rank + row0;             // that row's key
     const int slots = is_v ? 2 : kKSlots;
     unsigned char* ring = sm + (is_v ? Lay::kOffV : Lay::kOffK);
     uint64_t* land = is_v ? bars.v_land : bars.k_land;
@@ -879,8 +886,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (KV == GDA_KV_BF16) {
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
       } else {
-        fence_async_shared();
-        mbar_arrive(bar);
+        __syncwarp();       // (one arrival per warp: each thread's would take its turn at the barrier.  A
+        if (lane == 0) mbar_arrive(bar);  // fence here would wait for the next tile's loads: the relay has it)
       }
     };
     auto acquire = [&](uint64_t* bar, int parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
@@ -894,17 +901,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (t.tb == t.ta) continue;
       // four rows per step, eight lanes each: lane l8 of row 4 q + g8 takes 16 bytes of every 128
       const int g8 = lane >> 3, l8 = lane & 7;
-      // the slots of keys key0 + lane and (V) key0 + 32 + lane of tile j: loaded two tiles ahead, looked at
-      // when used; kUnseen where no row of the item sees the position
-      constexpr int kUnseen = INT_MIN;
-      int n0[2], n1[2], n2[2];
+      // the slots of this warp's keys of tile j, key0 + lane and (two of them) key0 + 32 + lane: loaded two
+      // tiles ahead, looked at when used; kUnseen where no row of the item sees the position
+      constexpr int kUnseen = INT_MIN, kPer = kRowsV / 32;
+      int n0[kPer], n1[kPer], n2[kPer];
       auto look_up = [&](int j, int* to) {
         const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + key0 + lane;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kPer; ++x) {
           const int pos = base + 32 * x;
+          const bool own = is_v || 32 * x + lane < kRowsK;
           to[x] = kUnseen;
-          if ((x == 0 || is_v) && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep)) to[x] = __ldg(p.indices + t.kb + pos);
+          if (own && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep)) to[x] = __ldg(p.indices + t.kb + pos);
         }
       };
       look_up(t.ta, n0);
@@ -916,15 +924,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         return -1;
       };
       if (is_v && ok) {
-        // Q (the previous item's last S product has read it): the item's rows, 64 per warp, four rows per
+        // Q (the previous item's last S product has read it): the item's rows, four rows per
         // step as below; rows past its last stay what they are, and what comes of them goes nowhere
         if (it > 0) ok = acquire(&bars.q_empty, it - 1);
         if (!ok) break;
-        const int q64 = 64 * (warp & 1), flat0 = t.i * kRowsI + rank * kPM + q64;
-        const int rows = min(64, t.nq * p.G - flat0);
+        const int q0 = gw * kRowsV, flat0 = t.i * kRowsI + rank * kPM + q0;
+        const int rows = min(kRowsV, t.nq * p.G - flat0);
         const int dt = 4 / p.G, dg = 4 - dt * p.G;     // four rows on
         int tok = (int)((unsigned)(flat0 + g8) / (unsigned)p.G), g = flat0 + g8 - tok * p.G;
-        unsigned char* dq = sm + Lay::kOffQ + (q64 + g8) * 128;
+        unsigned char* dq = sm + Lay::kOffQ + (q0 + g8) * 128;
 #pragma unroll 2
         for (int q = 0; 4 * q < rows; ++q) {
           const bool in = 4 * q + g8 < rows;
@@ -972,7 +980,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
               *reinterpret_cast<uint4*>(at + c * kBlk) = make_uint4(o[0], o[1], o[2], o[3]);
             }
             if (l8 == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
-              qscale[(it & 3) * kPM + q64 + 4 * q + g8] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
+              qscale[(it & 3) * kPM + q0 + 4 * q + g8] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
           }
         }
         landed(&bars.q_land);
@@ -986,26 +994,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
 #pragma unroll 1
         for (int j = t.ta; j < t.tb; ++j) {
           look_up(j + 2, n2);
-          const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
-          n0[0] = n1[0], n0[1] = n1[1], n1[0] = n2[0], n1[1] = n2[1];
+          int sl[kPer];
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n0[x]), n0[x] = n1[x], n1[x] = n2[x];
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
-          const uint32_t d0 = smem_u32(ring + slot * kHalf) + (r64 + g8) * 128;
+          const uint32_t d0 = smem_u32(ring + slot * kHalf) + (row0 + g8) * 128;
           if (!is_v) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const int sl = __shfl_sync(0xffffffffu, sl0, 4 * q + g8);
-              const unsigned char* src = base + (size_t)(uint32_t)max(sl, 0) * pitch;
+              const int at = __shfl_sync(0xffffffffu, sl[0], 4 * q + g8);
+              const unsigned char* src = base + (size_t)(uint32_t)max(at, 0) * pitch;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kKBlk, src + 128 * c, sl >= 0 ? 16 : 0);
+              for (int c = 0; c < 4; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kKBlk, src + 128 * c, at >= 0 ? 16 : 0);
             }
           } else {
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const int sl = __shfl_sync(0xffffffffu, q < 8 ? sl0 : sl1, (4 * q + g8) & 31);
-              const unsigned char* src = base + (size_t)(uint32_t)max(sl, 0) * pitch;
+              const int at = __shfl_sync(0xffffffffu, sl[(q >> 3) % kPer], (4 * q + g8) & 31);
+              const unsigned char* src = base + (size_t)(uint32_t)max(at, 0) * pitch;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kBlk, src + 128 * c, sl >= 0 ? 16 : 0);
+              for (int c = 0; c < 2; ++c) cp_async16(d0 + q * 512 + sw[q & 1] + c * kBlk, src + 128 * c, at >= 0 ? 16 : 0);
             }
           }
           landed(&land[slot]);
@@ -1015,63 +1024,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
         }
       } else {
-        // codes: kSteps 16-byte loads per lane and tile, the next tile's on their way while one is widened.
-        // e4m3: K has two steps per four rows (128 codes each), V one; 4 bits: one per four rows, V one per eight
-        constexpr int kSteps = KV == GDA_KV_E4M3 ? 16 : 8;
+        // codes: a few 16-byte loads per lane and tile, the next tile's on their way while one is widened.
+        // A group of rows (kRowsPer) per step: four of 128 bytes by eight lanes each, or the eight half rows
+        // of a 4-bit V by four; an e4m3 K row has two parts of 128 bytes
+        constexpr bool k8 = KV == GDA_KV_E4M3;
+        constexpr int kSteps = k8 ? 16 : 8;
         uint4 raw[kSteps];
-        uint32_t sc[KV == GDA_KV_E2M1 ? kSteps : 1];
-        const int part = (KV == GDA_KV_E2M1 && is_v) ? lane & 3 : l8, sub = (KV == GDA_KV_E2M1 && is_v) ? lane >> 2 : g8;
-        auto row_of = [&](int x) -> int {   // of the warp's part of a tile
-          if (KV == GDA_KV_E4M3) return is_v ? 4 * x + sub : 4 * (x >> 1) + sub;
-          return is_v ? 8 * x + sub : 4 * x + sub;
-        };
-        auto load = [&](int x, int sl0, int sl1) {
+        uint32_t sc[k8 ? 1 : kSteps];
+        const int part = !k8 && is_v ? lane & 3 : l8, sub = !k8 && is_v ? lane >> 2 : g8;
+        const unsigned char* base;
+        uint32_t pitch;
+        if (k8) {
+          base = pool + (size_t)t.h * kD + (is_v ? rank * 128 : 0) + part * 16;
+          pitch = (uint32_t)p.Hkv * kD;
+        } else {
+          base = pool + (size_t)t.h * kCodeBytes + (is_v ? rank * 64 : 0) + part * 16;
+          pitch = (uint32_t)p.Hkv * kCodeBytes;
+        }
+        const unsigned char* sbase = k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0) + part * 2;
+        const uint32_t spitch = (uint32_t)p.Hkv * kScalePair;
+        // the row of step x in the warp's part of a tile, and its part (e4m3 K)
+        auto row_of = [&](int x) -> int { return k8 ? 4 * (is_v ? x : x >> 1) + sub : (is_v ? 8 : 4) * x + sub; };
+        auto load = [&](int x, const int* sl) {
           const int row = row_of(x);
-          const int sl = __shfl_sync(0xffffffffu, row < 32 ? sl0 : sl1, row & 31);
+          const int at = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
           raw[x] = make_uint4(0u, 0u, 0u, 0u);
-          if (KV == GDA_KV_E2M1) sc[x] = 0u;
-          if (sl < 0) return;
-          const size_t at = (size_t)sl * p.Hkv + t.h;
-          if (KV == GDA_KV_E4M3) {
-            raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kD + (is_v ? rank * 128 : 128 * (x & 1))) + part);
-          } else {
-            raw[x] = __ldg(reinterpret_cast<const uint4*>(pool + at * kCodeBytes + (is_v ? rank * 64 : 0)) + part);
-            sc[x] = __ldg(reinterpret_cast<const unsigned short*>(p.scales + at * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0)) + part);
+          if (at >= 0) raw[x] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)(uint32_t)at * pitch + (k8 && !is_v ? 128 * (x & 1) : 0)));
+          if (!k8) {
+            sc[x] = 0u;
+            if (at >= 0) sc[x] = __ldg(reinterpret_cast<const unsigned short*>(sbase + (size_t)(uint32_t)at * spitch));
           }
         };
         {
-          const int sl0 = slot_of(n0[0]), sl1 = is_v ? slot_of(n0[1]) : -1;
+          int sl[kPer];
 #pragma unroll
-          for (int x = 0; x < kSteps; ++x) load(x, sl0, sl1);
+          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n0[x]);
+#pragma unroll
+          for (int x = 0; x < kSteps; ++x) load(x, sl);
         }
+        const uint32_t blk = is_v ? kBlk : kKBlk;
+        const int c = k8 ? 2 * part : 4 * part;   // the first of a step's two (4 bits: four) 8-dimension chunks
 #pragma unroll 1
         for (int j = t.ta; j < t.tb; ++j) {
           look_up(j + 2, n2);
-          const int sl0 = slot_of(n1[0]), sl1 = is_v ? slot_of(n1[1]) : -1;   // of the next tile
-          n1[0] = n2[0], n1[1] = n2[1];
+          int sl[kPer];                            // of the next tile
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n1[x]), n1[x] = n2[x];
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
-          unsigned char* dst = ring + slot * kHalf + r64 * 128;
-          const uint32_t blk = is_v ? kBlk : kKBlk;
+          unsigned char* dst = ring + slot * kHalf + row0 * 128 + (c >> 3) * blk;
 #pragma unroll
           for (int x = 0; x < kSteps; ++x) {
             const int row = row_of(x);
-            if (KV == GDA_KV_E4M3) {
-              const int c = 2 * part;                  // the first of two 8-dimension chunks (of 128 dimensions)
-              unsigned char* at = dst + ((c >> 3) + (is_v ? 0 : 2 * (x & 1))) * blk + row * 128;
+            unsigned char* at = dst + row * 128 + (k8 && !is_v ? 2 * (x & 1) * blk : 0);
+            if (k8) {
               *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
               *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
             } else {
-              const int c = 4 * part;                  // the first of four
               const uint32_t f = e4m3x2_to_f16x2(sc[x]);
               const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-              unsigned char* at = dst + (c >> 3) * blk + row * 128;
               *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
               *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
               *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
               *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
             }
-            if (j + 1 < t.tb) load(x, sl0, sl1);
+            if (j + 1 < t.tb) load(x, sl);
           }
           landed(&land[slot]);
           if (++slot == slots) {

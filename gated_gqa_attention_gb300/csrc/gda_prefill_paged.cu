@@ -59,6 +59,7 @@ constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128
 constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
 constexpr uint32_t kKBlk = kBlk / 2;               // K: a 64-column block of its 64 keys
 
+constexpr int kStages = 3;          // steps of codes that a gathering warp has under way
 template <int KV>
 struct Layout {
   static constexpr int kKSlots = KV == GDA_KV_BF16 ? 3 : 2;
@@ -68,8 +69,10 @@ struct Layout {
   static constexpr uint32_t kOffX = kOffV + 2 * kHalf;          // row max exchange [parity][half][row]
   static constexpr uint32_t kOffE = kOffX + 2048;               // second halves' sums for lse [row]
   static constexpr uint32_t kOffBar = kOffE + 512;
-  static constexpr uint32_t kOffScale = kOffBar + 512;          // [4 items][row]: the row's score factor
-  static constexpr uint32_t kBytes = kOffScale + (KV == GDA_KV_BF16 ? 0 : 2048);
+  static constexpr uint32_t kOffScale = kOffBar + 512;          // codes: [4 items][row] the row's score factor
+  static constexpr uint32_t kOffStage = kOffScale + 2048;       // and [gathering warp][step] codes (and scales, 4 bytes each)
+  static constexpr uint32_t kStageBytes = 2048 + (KV == GDA_KV_E2M1 ? 512 : 0), kStageWarp = kStages * kStageBytes;
+  static constexpr uint32_t kBytes = KV == GDA_KV_BF16 ? kOffScale : kOffStage + kGatherers * kStageWarp;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -917,6 +920,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       };
       look_up(t.ta, n0);
       look_up(t.ta + 1, n1);
+      if (KV != GDA_KV_BF16) look_up(t.ta + 2, n2);
       // -1: zeros.  A row outside the pools reads as zeros and is reported
       auto slot_of = [&](int v) -> int {
         if (v >= 0 && (long long)v < p.num_slots) return v;
@@ -1024,83 +1028,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
         }
       } else {
-        // codes: a few 16-byte loads per lane and tile, the next tile's on their way while one is widened.
-        // A group of rows (kRowsPer) per step: four of 128 bytes by eight lanes each, or the eight half rows
-        // of a 4-bit V by four; an e4m3 K row has two parts of 128 bytes
+        // codes.  A tile goes in kSubs steps of 2 KiB per warp: copied (cp.async) into a small ring of the
+        // warp's own, kStages steps ahead, and widened from there by the thread that copied it, 16 bytes at
+        // four places.  The next tile's lines are sent to the L2 when its slots are known.  (Held in
+        // registers instead, a tile's steps have to be unrolled: 2.7 us a tile, bound by instruction fetches.)
         constexpr bool k8 = KV == GDA_KV_E4M3;
-        constexpr int kSteps = k8 ? 16 : 8;
-        uint4 raw[kSteps];
-        uint32_t sc[k8 ? 1 : kSteps];
-        const int part = !k8 && is_v ? lane & 3 : l8, sub = !k8 && is_v ? lane >> 2 : g8;
-        const unsigned char* base;
-        uint32_t pitch;
-        if (k8) {
-          base = pool + (size_t)t.h * kD + (is_v ? rank * 128 : 0) + part * 16;
-          pitch = (uint32_t)p.Hkv * kD;
-        } else {
-          base = pool + (size_t)t.h * kCodeBytes + (is_v ? rank * 64 : 0) + part * 16;
-          pitch = (uint32_t)p.Hkv * kCodeBytes;
-        }
-        const unsigned char* sbase = k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0) + part * 2;
-        const uint32_t spitch = (uint32_t)p.Hkv * kScalePair;
-        // the row of step x in the warp's part of a tile, and its part (e4m3 K)
-        auto row_of = [&](int x) -> int { return k8 ? 4 * (is_v ? x : x >> 1) + sub : (is_v ? 8 : 4) * x + sub; };
-        auto load = [&](int x, const int* sl) {
-          const int row = row_of(x);
-          const int at = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
-          raw[x] = make_uint4(0u, 0u, 0u, 0u);
-          if (at >= 0) raw[x] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)(uint32_t)at * pitch + (k8 && !is_v ? 128 * (x & 1) : 0)));
-          if (!k8) {
-            sc[x] = 0u;
-            if (at >= 0) sc[x] = __ldg(reinterpret_cast<const unsigned short*>(sbase + (size_t)(uint32_t)at * spitch));
+        constexpr int kSubs = k8 ? 4 : 2;
+        const int part = !k8 && is_v ? lane & 3 : l8, sub_row = !k8 && is_v ? lane >> 2 : g8;
+        const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
+        const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (is_v ? rank * (k8 ? 128 : 64) : 0);
+        const unsigned char* sbase =
+            k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0) + ((part * 2) & ~3);
+        unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * (Lay::kStageWarp) + lane * 16;
+        // step `sub`, place u: the row in the warp's part of a tile (e4m3 K has two places a row)
+        auto row_of = [&](int sub, int u) -> int {
+          if (k8) return is_v ? 16 * sub + 4 * u + sub_row : 8 * sub + 4 * (u >> 1) + sub_row;
+          return is_v ? 32 * sub + 8 * u + sub_row : 16 * sub + 4 * u + sub_row;
+        };
+        int sl[kPer];        // the slots of the tile that is being copied, ij
+        int ij = t.ta, isub = 0, islot = 0, wslot = 0;
+        auto next_slots = [&](int* from) {
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) {
+            sl[x] = slot_of(from[x]);
           }
         };
-        {
-          int sl[kPer];
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n0[x]);
-#pragma unroll
-          for (int x = 0; x < kSteps; ++x) load(x, sl);
-        }
+        next_slots(n0);
         const uint32_t blk = is_v ? kBlk : kKBlk;
-        const int c = k8 ? 2 * part : 4 * part;   // the first of a step's two (4 bits: four) 8-dimension chunks
+        const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
+        const int turn = k8 ? (l8 ^ (l8 >> 2)) & 1 : is_v ? 2 * (part >> 1) : l8 >> 1;   // XORed to a place's chunks
+        const int total = (t.tb - t.ta) * kSubs;
+        int sub = 0;
 #pragma unroll 1
-        for (int j = t.ta; j < t.tb; ++j) {
-          look_up(j + 2, n2);
-          int sl[kPer];                            // of the next tile
+        for (int s = -kStages; s < total; ++s) {
+          if (s >= 0) {
+            if (sub == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
+            if (!ok) break;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            unsigned char* dst = ring + slot * kHalf + row0 * 128 + (c >> 3) * blk;
+            const unsigned char* from = stage + wslot * Lay::kStageBytes;
+            // (all of the step's loads first; the eight lanes that share a store's bank cycle take their
+            // chunks in different orders, so that they meet eight different banks)
+            uint4 raw[4];
+            uint32_t s4[4];
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n1[x]), n1[x] = n2[x];
-          if (use > 0) ok = acquire(&empty[slot], use - 1);
-          if (!ok) break;
-          unsigned char* dst = ring + slot * kHalf + row0 * 128 + (c >> 3) * blk;
-#pragma unroll
-          for (int x = 0; x < kSteps; ++x) {
-            const int row = row_of(x);
-            unsigned char* at = dst + row * 128 + (k8 && !is_v ? 2 * (x & 1) * blk : 0);
-            if (k8) {
-              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].x, raw[x].y);
-              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e4m3x8_to_f16(raw[x].z, raw[x].w);
-            } else {
-              const uint32_t f = e4m3x2_to_f16x2(sc[x]);
-              const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-              *reinterpret_cast<uint4*>(at + (((c & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].x, s_lo);
-              *reinterpret_cast<uint4*>(at + ((((c + 1) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].y, s_lo);
-              *reinterpret_cast<uint4*>(at + ((((c + 2) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].z, s_hi);
-              *reinterpret_cast<uint4*>(at + ((((c + 3) & 7) ^ (row & 7)) << 4)) = e2m1x8_to_f16(raw[x].w, s_hi);
+            for (int u = 0; u < 4; ++u) {
+              raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
+              if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + 2048 + u * 128);
             }
-            if (j + 1 < t.tb) load(x, sl);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = row_of(sub, u);
+              unsigned char* at = dst + row * 128 + (k8 && !is_v ? 2 * (u & 1) * blk : 0);
+              const int x7 = (c & 7) ^ (row & 7) ^ turn;
+              if (k8) {
+                const uint32_t w0 = turn ? raw[u].z : raw[u].x, w1 = turn ? raw[u].w : raw[u].y;
+                const uint32_t w2 = turn ? raw[u].x : raw[u].z, w3 = turn ? raw[u].y : raw[u].w;
+                *reinterpret_cast<uint4*>(at + (x7 << 4)) = e4m3x8_to_f16(w0, w1);
+                *reinterpret_cast<uint4*>(at + ((x7 ^ 1) << 4)) = e4m3x8_to_f16(w2, w3);
+              } else {
+                const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
+                uint32_t w0 = raw[u].x, w1 = raw[u].y, w2 = raw[u].z, w3 = raw[u].w, t0;
+                if (turn & 1) t0 = w0, w0 = w1, w1 = t0, t0 = w2, w2 = w3, w3 = t0;
+                if (turn & 2) t0 = w0, w0 = w2, w2 = t0, t0 = w1, w1 = w3, w3 = t0;
+                const uint32_t s_lo = __byte_perm(f, f, turn & 2 ? 0x3232 : 0x1010), s_hi = __byte_perm(f, f, turn & 2 ? 0x1010 : 0x3232);
+                *reinterpret_cast<uint4*>(at + (x7 << 4)) = e2m1x8_to_f16(w0, s_lo);
+                *reinterpret_cast<uint4*>(at + ((x7 ^ 1) << 4)) = e2m1x8_to_f16(w1, s_lo);
+                *reinterpret_cast<uint4*>(at + ((x7 ^ 2) << 4)) = e2m1x8_to_f16(w2, s_hi);
+                *reinterpret_cast<uint4*>(at + ((x7 ^ 3) << 4)) = e2m1x8_to_f16(w3, s_hi);
+              }
+            }
+            wslot = wslot + 1 == kStages ? 0 : wslot + 1;
+            if (++sub == kSubs) {
+              sub = 0;
+              landed(&land[slot]);
+              if (++slot == slots) {
+                slot = 0;
+                ++use;
+              }
+            }
           }
-          landed(&land[slot]);
-          if (++slot == slots) {
-            slot = 0;
-            ++use;
+          if (ij < t.tb) {
+            const uint32_t to = smem_u32(stage) + islot * Lay::kStageBytes;
+            int at[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = row_of(isub, u);
+              at[u] = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const size_t o = (size_t)(uint32_t)max(at[u], 0);
+              cp_async16(to + u * 512, base + o * pitch + (k8 && !is_v ? 128 * (u & 1) : 0) + part * 16, at[u] >= 0 ? 16 : 0);
+              if (!k8)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + 2048 + u * 128),
+                             "l"(sbase + o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
+            }
+            islot = islot + 1 == kStages ? 0 : islot + 1;
+            if (++isub == kSubs) {
+              isub = 0;
+              ++ij;
+              next_slots(n1);
+#pragma unroll
+              for (int x = 0; x < kPer; ++x) {
+                n1[x] = n2[x];
+                // the tile after next: to the L2, a row per lane
+                if (n1[x] >= 0 && (long long)n1[x] < p.num_slots) {
+                  const unsigned char* line = base + (size_t)(uint32_t)n1[x] * pitch;
+                  asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+                  if (k8 && !is_v) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128));
+                }
+              }
+              look_up(ij + 2, n2);
+            }
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        cp_async_wait_all();
       }
       if (!ok) break;
       ++it;
     }
-    if (KV == GDA_KV_BF16) cp_async_wait_all();
+    cp_async_wait_all();
     if (!ok) fail();
   }
 

@@ -42,16 +42,17 @@ constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 10;  // relays: 10 for K
 constexpr int kGatherWarp = 12;     // the gatherers: the first half of them for K, the others for Q and V
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
-constexpr int kGatherers = 4;       // half of them for K, half for Q and V
+constexpr int kGatherers = 4;       // half of them for K, half for Q and V (with eight, codes are no faster)
 constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
-// registers of a thread: softmax, planner and issuer, gatherers share out what the block has at its
-// launch (128 each).  Spills are dear here: shared memory leaves the L1 little room
+// registers of a thread (softmax, planner and issuer, gatherers) share out what the block has at its
+// launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room
 constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
 static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + 32 * kGatherers * kRegsGather <= kThreads * 128, "register shares");
 constexpr int kRowsK = 64 / (kGatherers / 2), kRowsV = 128 / (kGatherers / 2);  // of a tile per gathering warp
 // arrivals that make a CTA's part of a tile complete: every copying thread's, or one of each widening warp
 template <int KV>
 constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
+constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per thread
 
 constexpr int kItemCost = 14;        // of an item besides its tiles, in half tiles
 
@@ -71,7 +72,8 @@ struct Layout {
   static constexpr uint32_t kOffBar = kOffE + 512;
   static constexpr uint32_t kOffScale = kOffBar + 512;          // codes: [4 items][row] the row's score factor
   static constexpr uint32_t kOffStage = kOffScale + 2048;       // and [gathering warp][step] codes (and scales, 4 bytes each)
-  static constexpr uint32_t kStageBytes = 2048 + (KV == GDA_KV_E2M1 ? 512 : 0), kStageWarp = kStages * kStageBytes;
+  static constexpr uint32_t kStageCodes = 512 * kPlaces;  // of a step, per warp
+  static constexpr uint32_t kStageBytes = kStageCodes + (KV == GDA_KV_E2M1 ? kStageCodes / 4 : 0), kStageWarp = kStages * kStageBytes;
   static constexpr uint32_t kBytes = KV == GDA_KV_BF16 ? kOffScale : kOffStage + kGatherers * kStageWarp;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -630,21 +632,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         // O / l as BF16 into the V buffers (free: the last PV has completed), this warp's 128
         // columns of its 32 rows: [64-column block][row][128 B], 16-byte chunks swizzled by row
 #pragma unroll 1
-        for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 64) {
-          float o[64];
+        for (int c0 = 128 * hc; c0 < 128 * hc + 128; c0 += 32) {
+          float o[32];
           tmem_ld32(t_row + kTmemO + c0, o);
-          tmem_ld32(t_row + kTmemO + c0 + 32, o + 32);
           tmem_wait_ld();
           unsigned char* dst = stage + (c0 >> 6) * kBlk + r * 128;
+          const int x7 = ((c0 >> 3) & 7) ^ (r & 7);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
+          for (int u = 0; u < 4; ++u) {
             uint32_t b4[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const float2 v = mul_f32x2(make_float2(o[8 * u + 2 * x], o[8 * u + 2 * x + 1]), make_float2(inv, inv));
               b4[x] = bf16x2_rn(v.x, v.y) & keep;
             }
-            *reinterpret_cast<uint4*>(dst + 16 * (u ^ (r & 7))) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+            *reinterpret_cast<uint4*>(dst + 16 * (x7 ^ u)) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
           }
         }
         tc_fence_before();
@@ -1028,12 +1030,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
         }
       } else {
-        // codes.  A tile goes in kSubs steps of 2 KiB per warp: copied (cp.async) into a small ring of the
-        // warp's own, kStages steps ahead, and widened from there by the thread that copied it, 16 bytes at
-        // four places.  The next tile's lines are sent to the L2 when its slots are known.  (Held in
+        // codes.  A tile goes in kSubs steps per warp: copied (cp.async) into a small ring of the warp's own,
+        // kStages steps ahead, and widened from there by the thread that copied it, 16 bytes at kU places.  The next tile's lines are sent to the L2 when its slots are known.  (Held in
         // registers instead, a tile's steps have to be unrolled: 2.7 us a tile, bound by instruction fetches.)
         constexpr bool k8 = KV == GDA_KV_E4M3;
-        constexpr int kSubs = k8 ? 4 : 2;
+        constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
         const int part = !k8 && is_v ? lane & 3 : l8, sub_row = !k8 && is_v ? lane >> 2 : g8;
         const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
         const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (is_v ? rank * (k8 ? 128 : 64) : 0);
@@ -1042,8 +1043,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * (Lay::kStageWarp) + lane * 16;
         // step `sub`, place u: the row in the warp's part of a tile (e4m3 K has two places a row)
         auto row_of = [&](int sub, int u) -> int {
-          if (k8) return is_v ? 16 * sub + 4 * u + sub_row : 8 * sub + 4 * (u >> 1) + sub_row;
-          return is_v ? 32 * sub + 8 * u + sub_row : 16 * sub + 4 * u + sub_row;
+          if (k8) return is_v ? 4 * (kU * sub + u) + sub_row : 4 * ((kU / 2) * sub + (u >> 1)) + sub_row;
+          return (is_v ? 8 : 4) * (kU * sub + u) + sub_row;
         };
         int sl[kPer];        // the slots of the tile that is being copied, ij
         int ij = t.ta, isub = 0, islot = 0, wslot = 0;
@@ -1069,15 +1070,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
             const unsigned char* from = stage + wslot * Lay::kStageBytes;
             // (all of the step's loads first; the eight lanes that share a store's bank cycle take their
             // chunks in different orders, so that they meet eight different banks)
-            uint4 raw[4];
-            uint32_t s4[4];
+            uint4 raw[kU];
+            uint32_t s4[kU];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kU; ++u) {
               raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
-              if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + 2048 + u * 128);
+              if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + Lay::kStageCodes + u * 128);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kU; ++u) {
               const int row = row_of(sub, u);
               unsigned char* at = dst + row * 128 + (k8 && !is_v ? 2 * (u & 1) * blk : 0);
               const int x7 = (c & 7) ^ (row & 7) ^ turn;
@@ -1110,18 +1111,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
           if (ij < t.tb) {
             const uint32_t to = smem_u32(stage) + islot * Lay::kStageBytes;
-            int at[4];
+            int at[kU];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kU; ++u) {
               const int row = row_of(isub, u);
               at[u] = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kU; ++u) {
               const size_t o = (size_t)(uint32_t)max(at[u], 0);
               cp_async16(to + u * 512, base + o * pitch + (k8 && !is_v ? 128 * (u & 1) : 0) + part * 16, at[u] >= 0 ? 16 : 0);
               if (!k8)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + 2048 + u * 128),
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + Lay::kStageCodes + u * 128),
                              "l"(sbase + o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
             }
             islot = islot + 1 == kStages ? 0 : islot + 1;

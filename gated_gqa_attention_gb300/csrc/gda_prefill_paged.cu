@@ -467,34 +467,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         // (Q's copy was over before the S product began)
         if (KV != GDA_KV_BF16 && j == t.ta && r < rows) factor = qscale[(it & 3) * kPM + r];
         float hm = -INFINITY;
-        float s[64];
+        // (two rolled passes over the scores in TMEM: unrolled over 64 scores in registers, this loop is
+        // bound by the fetching of its instructions)
+        const uint32_t t_s = t_row + kTmemS + sb * kPN + 64 * hc;       // this warp's 64 scores, then their P
+        const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of the first
+        const bool masked = __any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep));
+        const unsigned long long seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
         if (some) {
-          tmem_ld32(t_row + kTmemS + sb * kPN + 64 * hc, s);
-          tmem_ld32(t_row + kTmemS + sb * kPN + 64 * hc + 32, s + 32);
-          tmem_wait_ld();
-          const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of s[0]
-          if (__any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep))) {
-            const unsigned long long seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
-            const uint32_t seen2[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+#pragma unroll 1
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float s[32];
+            tmem_ld32(t_s + c0, s);
+            tmem_wait_ld();
+            if (masked) {
+              const uint32_t m = (uint32_t)(seen >> c0);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(seen2[c >> 5] & (1u << (c & 31)))) s[c] = -INFINITY;
+              for (int c = 0; c < 32; ++c)
+                if (!(m & (1u << c))) s[c] = -INFINITY;
+            }
+            float e4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 32; ++c) e4[c & 3] = fmaxf(e4[c & 3], s[c]);
+            hm = fmaxf(hm, fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])));
           }
-          float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 64; ++c) e4[c & 3] = fmaxf(e4[c & 3], s[c]);
           // (a row past the item's last holds anything: its max stays -inf, so that it decides nothing below)
-          if (r < rows) hm = fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]));
+          if (r >= rows) hm = -INFINITY;
         }
-        // the two halves of the row agree on the tile max (parity-buffered slots); after this
-        // both have read their S, so P may overwrite it
+        // the two halves of the row agree on the tile max (parity-buffered slots)
         xbuf[(sb * 2 + hc) * kPM + r] = hm;
-        tc_fence_before();  // this warp's S reads are ordered before the partner's P writes
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.xm[rg][sb]);
         ok = __all_sync(0xffffffffu, wait(&bars.xm[rg][sb], ph));
         if (!ok) break;
-        tc_fence_after();
         if (some) {
           const float mx = fmaxf(hm, xbuf[(sb * 2 + (1 - hc)) * kPM + r]) * factor;
           // lazy max: it moves only by more than 2^8, so probabilities stay below 2^8 (both
@@ -524,31 +528,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
           // p = 2^(s * factor - m): half a packed FFMA and one SFU op per score (a masked score gives
           // 2^-inf = 0; a row with no visible key yet uses m = 0); P (16-bit pairs) over the first
-          // half of the S buffer: keys 64 h .. at columns 32 h ..
+          // half of this warp's scores
           const float mneg = (m_run == -INFINITY) ? 0.0f : -m_run;
-          float f = factor;
-          if (__any_sync(0xffffffffu, fabsf(m_run) > 262144.0f && m_run != -INFINITY)) {
-            // huge scores: the product is rounded first, as in the row max, or its rounding error alone
-            // could be a large exponent
-#pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] *= factor;
-            f = 1.0f;
-          }
-          uint32_t w[32];
+          // huge scores: the product is rounded first, as in the row max, or its rounding error alone
+          // could be a large exponent
+          const bool huge = __any_sync(0xffffffffu, fabsf(m_run) > 262144.0f && m_run != -INFINITY);
           float2 l2 = make_float2(0.0f, 0.0f), e2 = l2;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            float s[16];
+            tmem_ld16(t_s + c0, s);
+            tmem_wait_ld();
+            if (masked) {
+              const uint32_t m = (uint32_t)(seen >> c0);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 a = fma_f32x2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(f, f),
-                                       make_float2(mneg, mneg));
-            const float2 x = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            w[e] = round_pair<KV>(x);
-            e2 = add_f32x2(e2, x);
-            l2 = add_f32x2(l2, pair_values<KV>(w[e]));
+              for (int c = 0; c < 16; ++c)
+                if (!(m & (1u << c))) s[c] = -INFINITY;
+            }
+            float f = factor;
+            if (huge) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) s[c] *= factor;
+              f = 1.0f;
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 a = fma_f32x2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(f, f), make_float2(mneg, mneg));
+              const float2 x = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+              w[e] = round_pair<KV>(x);
+              e2 = add_f32x2(e2, x);
+              l2 = add_f32x2(l2, pair_values<KV>(w[e]));
+            }
+            tmem_st8(t_s + c0 / 2, w);
           }
           l_run += l2.x + l2.y;
           e_run += e2.x + e2.y;
-          tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc, w);
-          tmem_st16(t_row + kTmemS + sb * kPN + 32 * hc + 16, w + 16);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -770,11 +785,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       bool ok = true;
       auto issue_s = [&](int x) {
         const uint32_t kb = sK + slot * kHalf;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {  // 64 head dimensions
+          const uint64_t ad = sdesc_sw128(sQ + c * kBlk, 16, 1024), bd = sdesc_sw128(kb + c * kKBlk, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 16; ++kk) {  // head dimensions 16 kk .. 16 kk + 15
-          const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = sdesc_sw128(kb + (kk >> 2) * kKBlk + (kk & 3) * 32, 16, 1024);
-          umma_pair_ss(tmem + kTmemS + (x & 1) * kPN, ad, bd, idS, kk > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)  // 16 each (32 bytes; descriptors count 16)
+            umma_pair_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
         }
         umma_commit_pair(&bars.s_full[x & 1]);
         umma_commit_pair(&bars.k_empty[slot]);
@@ -806,12 +822,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           if (!ok) break;
           tc_fence_after();
           if (j >= t.ta + 2) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {  // 64 keys; V is MN-major (dims contiguous): LBO = stride between a CTA's two
+              // 64-dim blocks, SBO = 8 key rows
+              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + c * 64 * 128, kBlk, 1024);
+              const uint32_t a = tmem + kTmemS + pb * kPN + 64 * c;  // (P over the first half of these keys' scores)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              // V is MN-major (dims contiguous): LBO = stride between a CTA's two 64-dim blocks, SBO = 8 key
-              // rows; k-step kk = keys 16 kk .. 16 kk + 15, whose P is in columns 8 kk .. 8 kk + 7 of the S buffer
-              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + kk * 16 * 128, kBlk, 1024);
-              umma_pair_ts(tmem + kTmemO, tmem + kTmemS + pb * kPN + 8 * kk, bd, idO, (j > t.ta + 2 || kk > 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k)  // 16 keys each
+                umma_pair_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > t.ta + 2 || c > 0 || k > 0) ? 1u : 0u);
             }
             umma_commit_pair(&bars.v_empty[pb]);
             umma_commit_pair(&bars.p_empty[pb]);

@@ -250,9 +250,19 @@ __device__ __forceinline__ Share share_of(const PagedParams& p, int x, int share
   return r;
 }
 
-// One KV row's worth of codes to FP16, 16-byte chunks of 8 values.
+// Eight codes to FP16, a 16-byte chunk.
 __device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b) {
-  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16));
+  uint4 f;
+  asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\t"
+      "mov.b32 {a0, a1}, %4;\n\t"
+      "mov.b32 {b0, b1}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, a1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, b0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, b1;\n\t}"
+      : "=r"(f.x), "=r"(f.y), "=r"(f.z), "=r"(f.w)
+      : "r"(a), "r"(b));
+  return f;
 }
 __device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w, uint32_t scale2) {
   uint32_t f[4];
@@ -1049,21 +1059,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         }
       } else {
         // codes.  A tile goes in kSubs steps per warp: copied (cp.async) into a small ring of the warp's own,
-        // kStages steps ahead, and widened from there by the thread that copied it, 16 bytes at kU places.  The next tile's lines are sent to the L2 when its slots are known.  (Held in
-        // registers instead, a tile's steps have to be unrolled: 2.7 us a tile, bound by instruction fetches.)
+        // kStages steps ahead, and widened from there by the thread that copied it, 16 bytes at kU places.
+        // The next tile's lines are sent to the L2 when its slots are known.
+        // A place is four rows of 128 bytes (e4m3 K: half rows), or a 4-bit V's eight rows of 64.  The lanes
+        // of a row's later parts take a neighbouring row's (sub_row), so that the eight 16-byte chunks that
+        // are stored at a time lie in eight different banks
         constexpr bool k8 = KV == GDA_KV_E4M3;
         constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
-        const int part = !k8 && is_v ? lane & 3 : l8, sub_row = !k8 && is_v ? lane >> 2 : g8;
+        const int part = !k8 && is_v ? lane & 3 : l8;
+        const int sub_row = k8 ? g8 ^ (l8 >> 2) : is_v ? (lane >> 2) ^ (part & 2) : g8 ^ (l8 >> 1);
         const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
-        const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (is_v ? rank * (k8 ? 128 : 64) : 0);
+        const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (is_v ? rank * (k8 ? 128 : 64) : 0) + part * 16;
         const unsigned char* sbase =
             k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0) + ((part * 2) & ~3);
         unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * (Lay::kStageWarp) + lane * 16;
-        // step `sub`, place u: the row in the warp's part of a tile (e4m3 K has two places a row)
-        auto row_of = [&](int sub, int u) -> int {
-          if (k8) return is_v ? 4 * (kU * sub + u) + sub_row : 4 * ((kU / 2) * sub + (u >> 1)) + sub_row;
-          return (is_v ? 8 : 4) * (kU * sub + u) + sub_row;
-        };
+        // rows from one place to the next, and from one step to the next
+        const int place_rows = k8 ? 4 : is_v ? 8 : 4, step_rows = k8 && !is_v ? 2 * kU : kU * place_rows;
+        const bool halves = k8 && !is_v;
+        // the row of place u in a step (an e4m3 K row has two places)
+        auto row_of = [&](int u) -> int { return place_rows * (halves ? u >> 1 : u) + sub_row; };
+        const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
+        const uint32_t blk = is_v ? kBlk : kKBlk;
+        unsigned char* dst0 = ring + row0 * 128 + (c >> 3) * blk;
         int sl[kPer];        // the slots of the tile that is being copied, ij
         int ij = t.ta, isub = 0, islot = 0, wslot = 0;
         auto next_slots = [&](int* from) {
@@ -1073,9 +1090,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
         };
         next_slots(n0);
-        const uint32_t blk = is_v ? kBlk : kKBlk;
-        const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
-        const int turn = k8 ? (l8 ^ (l8 >> 2)) & 1 : is_v ? 2 * (part >> 1) : l8 >> 1;   // XORed to a place's chunks
         const int total = (t.tb - t.ta) * kSubs;
         int sub = 0;
 #pragma unroll 1
@@ -1084,11 +1098,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
             if (sub == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
             if (!ok) break;
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-            unsigned char* dst = ring + slot * kHalf + row0 * 128 + (c >> 3) * blk;
+            unsigned char* dst = dst0 + slot * kHalf + sub * step_rows * 128;
             const unsigned char* from = stage + wslot * Lay::kStageBytes;
-            // (all of the step's loads first; the eight lanes that share a store's bank cycle take their
-            // chunks in different orders, so that they meet eight different banks)
-            uint4 raw[kU];
+            uint4 raw[kU];    // (all of the step's loads first)
             uint32_t s4[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
@@ -1097,24 +1109,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-              const int row = row_of(sub, u);
-              unsigned char* at = dst + row * 128 + (k8 && !is_v ? 2 * (u & 1) * blk : 0);
-              const int x7 = (c & 7) ^ (row & 7) ^ turn;
+              const int row = row_of(u);
+              // (steps are multiples of eight rows, or of four and the row's swizzle follows the step)
+              unsigned char* at = dst + row * 128 + (halves ? (u & 1) * 2 * blk : 0);
+              const int x7 = ((c & 7) ^ ((row + sub * step_rows) & 7)) << 4;
               if (k8) {
-                const uint32_t w0 = turn ? raw[u].z : raw[u].x, w1 = turn ? raw[u].w : raw[u].y;
-                const uint32_t w2 = turn ? raw[u].x : raw[u].z, w3 = turn ? raw[u].y : raw[u].w;
-                *reinterpret_cast<uint4*>(at + (x7 << 4)) = e4m3x8_to_f16(w0, w1);
-                *reinterpret_cast<uint4*>(at + ((x7 ^ 1) << 4)) = e4m3x8_to_f16(w2, w3);
+                *reinterpret_cast<uint4*>(at + x7) = e4m3x8_to_f16(raw[u].x, raw[u].y);
+                *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e4m3x8_to_f16(raw[u].z, raw[u].w);
               } else {
                 const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
-                uint32_t w0 = raw[u].x, w1 = raw[u].y, w2 = raw[u].z, w3 = raw[u].w, t0;
-                if (turn & 1) t0 = w0, w0 = w1, w1 = t0, t0 = w2, w2 = w3, w3 = t0;
-                if (turn & 2) t0 = w0, w0 = w2, w2 = t0, t0 = w1, w1 = w3, w3 = t0;
-                const uint32_t s_lo = __byte_perm(f, f, turn & 2 ? 0x3232 : 0x1010), s_hi = __byte_perm(f, f, turn & 2 ? 0x1010 : 0x3232);
-                *reinterpret_cast<uint4*>(at + (x7 << 4)) = e2m1x8_to_f16(w0, s_lo);
-                *reinterpret_cast<uint4*>(at + ((x7 ^ 1) << 4)) = e2m1x8_to_f16(w1, s_lo);
-                *reinterpret_cast<uint4*>(at + ((x7 ^ 2) << 4)) = e2m1x8_to_f16(w2, s_hi);
-                *reinterpret_cast<uint4*>(at + ((x7 ^ 3) << 4)) = e2m1x8_to_f16(w3, s_hi);
+                const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+                *reinterpret_cast<uint4*>(at + x7) = e2m1x8_to_f16(raw[u].x, s_lo);
+                *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e2m1x8_to_f16(raw[u].y, s_lo);
+                *reinterpret_cast<uint4*>(at + (x7 ^ 32)) = e2m1x8_to_f16(raw[u].z, s_hi);
+                *reinterpret_cast<uint4*>(at + (x7 ^ 48)) = e2m1x8_to_f16(raw[u].w, s_hi);
               }
             }
             wslot = wslot + 1 == kStages ? 0 : wslot + 1;
@@ -1132,13 +1140,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
             int at[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-              const int row = row_of(isub, u);
+              const int row = row_of(u) + isub * step_rows;
               at[u] = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
               const size_t o = (size_t)(uint32_t)max(at[u], 0);
-              cp_async16(to + u * 512, base + o * pitch + (k8 && !is_v ? 128 * (u & 1) : 0) + part * 16, at[u] >= 0 ? 16 : 0);
+              cp_async16(to + u * 512, base + o * pitch + (halves ? 128 * (u & 1) : 0), at[u] >= 0 ? 16 : 0);
               if (!k8)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + Lay::kStageCodes + u * 128),
                              "l"(sbase + o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
@@ -1153,7 +1161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
                 n1[x] = n2[x];
                 // the tile after next: to the L2, a row per lane
                 if (n1[x] >= 0 && (long long)n1[x] < p.num_slots) {
-                  const unsigned char* line = base + (size_t)(uint32_t)n1[x] * pitch;
+                  const unsigned char* line = base - part * 16 + (size_t)(uint32_t)n1[x] * pitch;
                   asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
                   if (k8 && !is_v) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128));
                 }

@@ -54,7 +54,7 @@ template <int KV>
 constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
 constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per thread
 
-constexpr int kItemCost = 14;        // of an item besides its tiles, in half tiles
+constexpr int kItemCost = 10;        // of an item besides its tiles, in half tiles
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
 constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
@@ -141,21 +141,31 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, in
   r.n = r.f + th - r.tl;
   return r;
 }
-// Costs of a sequence's blocks, per KV head: linear from its first to its last block.
+// Costs of a sequence's blocks, per KV head: linear up to block `knee`, constant from there.  (Tiles
+// grow with the positions up to the last block, or to the first one whose window leaves positions out.)
 struct Costs {
-  int mt;              // blocks
+  int mt, knee;            // blocks
   long long first, rise;   // the first one's, and 2^16 times what the next one costs more
   __device__ __forceinline__ Costs(const PagedParams& p, const Seq& s) {
     mt = blocks_of(p, s);
+    knee = 0;
     first = rise = 0;
     if (mt > 0) {
       const int n0 = range_of(p, s, 0).n;
       first = 2LL * n0 + kItemCost;
-      if (mt > 1) rise = ((2LL * (range_of(p, s, mt - 1).n - n0)) << 16) / (mt - 1);
+      if (mt > 1) {
+        knee = mt - 1;
+        if (p.window > 0)  // the block of the token whose position is the window's length
+          knee = (int)min((long long)knee, max(0LL, (long long)p.window - s.L + s.nq) * p.G / kRowsI + 1);
+        rise = ((2LL * (range_of(p, s, knee).n - n0)) << 16) / knee;
+      }
     }
   }
   // of the blocks before block i
-  __device__ __forceinline__ long long before(int i) const { return first * i + ((rise * ((long long)i * (i - 1) / 2)) >> 16); }
+  __device__ __forceinline__ long long before(int i) const {
+    const long long k = min(i, knee);
+    return first * i + ((rise * (k * (k - 1) / 2 + (i - k) * knee)) >> 16);
+  }
 };
 // the place at x within a sequence's costs (0 <= x < Hkv * c.before(c.mt))
 __device__ __forceinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, long long x) {

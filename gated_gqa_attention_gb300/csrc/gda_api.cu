@@ -74,6 +74,13 @@ void set_factors(P* p, float k_descale, float v_descale) {
   p->v_factor = p->inv ? 1.0f / v_descale : v_descale;
 }
 
+// The factor of an 8-bit cache write.
+gda::Kv8Factor kv8_factor(float d) {
+  const float r = 1.0f / d;
+  const bool normal = r >= 1.17549435e-38f && isfinite(r);
+  return {d, r, power_of_two(d) ? gda::kKv8Exact : normal ? gda::kKv8Near : gda::kKv8Divide};
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int check_sizes(int B, int Hq, int Hkv, int D, int num_splits) {
@@ -768,7 +775,8 @@ int gda_kv_write_e4m3(const gda_bf16* k, int64_t k_stride, const gda_bf16* v, in
   p.num_slots = num_slots;
   p.k_pool = k_pool;
   p.v_pool = v_pool;
-  set_factors(&p, k_descale, v_descale);
+  p.k_factor = kv8_factor(k_descale);
+  p.v_factor = kv8_factor(v_descale);
   p.T = T;
   p.Hkv = Hkv;
   if (gda::launch_kv8_write(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GDA_ERR_CUDA;

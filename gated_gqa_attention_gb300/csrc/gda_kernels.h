@@ -118,6 +118,13 @@ cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_gather(const Kv4GatherParams& p, cudaStream_t stream);
 
 // 8-bit (e4m3) cache rows: write and read back.
+constexpr int kKv8Exact = 0;   // the reciprocal is exact
+constexpr int kKv8Near = 1;    // it is a normal number
+constexpr int kKv8Divide = 2;
+struct Kv8Factor {
+  float descale, reciprocal;
+  int mode;
+};
 struct Kv8WriteParams {
   const __nv_bfloat16* k;      // [T, Hkv, D], token t at t * k_stride
   const __nv_bfloat16* v;
@@ -126,8 +133,7 @@ struct Kv8WriteParams {
   long long num_slots;
   unsigned char* k_pool;       // [num_slots, Hkv, D] codes
   unsigned char* v_pool;
-  float k_factor, v_factor;    // inv: exact reciprocals of the descales, else the descales
-  int inv;
+  Kv8Factor k_factor, v_factor;
   long long T;
   int Hkv;
 };

@@ -23,6 +23,8 @@
 // taken as linear in its number within the sequence, so that sums over items have a closed form.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "gda.h"
 #include "gda_kernels.h"
 #include "gda_kv4.cuh"
@@ -1074,114 +1076,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         // A place is four rows of 128 bytes (e4m3 K: half rows), or a 4-bit V's eight rows of 64.  The lanes
         // of a row's later parts take a neighbouring row's (sub_row), so that the eight 16-byte chunks that
         // are stored at a time lie in eight different banks
-        constexpr bool k8 = KV == GDA_KV_E4M3;
-        constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
-        const int part = !k8 && is_v ? lane & 3 : l8;
-        const int sub_row = k8 ? g8 ^ (l8 >> 2) : is_v ? (lane >> 2) ^ (part & 2) : g8 ^ (l8 >> 1);
-        const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
-        const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (is_v ? rank * (k8 ? 128 : 64) : 0) + part * 16;
-        const unsigned char* sbase =
-            k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes + rank * 8 : 0) + ((part * 2) & ~3);
-        unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * (Lay::kStageWarp) + lane * 16;
-        // rows from one place to the next, and from one step to the next
-        const int place_rows = k8 ? 4 : is_v ? 8 : 4, step_rows = k8 && !is_v ? 2 * kU : kU * place_rows;
-        const bool halves = k8 && !is_v;
-        // the row of place u in a step (an e4m3 K row has two places)
-        auto row_of = [&](int u) -> int { return place_rows * (halves ? u >> 1 : u) + sub_row; };
-        const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
-        const uint32_t blk = is_v ? kBlk : kKBlk;
-        unsigned char* dst0 = ring + row0 * 128 + (c >> 3) * blk;
-        int sl[kPer];        // the slots of the tile that is being copied, ij
-        int ij = t.ta, isub = 0, islot = 0, wslot = 0;
-        auto next_slots = [&](int* from) {
+        auto gather = [&](auto of_v) {
+          constexpr bool k8 = KV == GDA_KV_E4M3, kV = decltype(of_v)::value;
+          constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
+          constexpr bool kHalves = k8 && !kV;                      // an e4m3 K row has two places
+          constexpr int kPlaceRows = !k8 && kV ? 8 : 4;            // rows from one place to the next
+          constexpr int kStepRows = (kHalves ? kU / 2 : kU) * kPlaceRows;
+          static_assert(kStepRows % 8 == 0, "a row's swizzle does not depend on the step");
+          const int part = !k8 && kV ? lane & 3 : l8;
+          const int sub_row = k8 ? g8 ^ (l8 >> 2) : kV ? (lane >> 2) ^ (part & 2) : g8 ^ (l8 >> 1);
+          auto row_of = [](int u) -> int { return kPlaceRows * (kHalves ? u >> 1 : u); };   // and sub_row
+          const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
+          const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (kV ? rank * (k8 ? 128 : 64) : 0) + part * 16;
+          const unsigned char* sbase =
+              k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (kV ? kScaleBytes + rank * 8 : 0) + ((part * 2) & ~3);
+          unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * Lay::kStageWarp + lane * 16;
+          const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
+          constexpr uint32_t kColBlk = kV ? kBlk : kKBlk;
+          unsigned char* dst0 = ring + (row0 + sub_row) * 128 + (c >> 3) * kColBlk;
+          const int sw[2] = {((c & 7) ^ (sub_row & 7)) << 4, ((c & 7) ^ ((4 + sub_row) & 7)) << 4};  // of rows 8 n, 8 n + 4
+          int sl[kPer];        // the slots of the tile that is being copied, ij
+          int ij = t.ta, isub = 0, islot = 0, wslot = 0;
+          auto next_slots = [&](int* from) {
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) {
-            sl[x] = slot_of(from[x]);
-          }
-        };
-        next_slots(n0);
-        const int total = (t.tb - t.ta) * kSubs;
-        int sub = 0;
+            for (int x = 0; x < kPer; ++x) sl[x] = slot_of(from[x]);
+          };
+          next_slots(n0);
+          const int total = (t.tb - t.ta) * kSubs;
+          int sub = 0;
 #pragma unroll 1
-        for (int s = -kStages; s < total; ++s) {
-          if (s >= 0) {
-            if (sub == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
-            if (!ok) break;
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-            unsigned char* dst = dst0 + slot * kHalf + sub * step_rows * 128;
-            const unsigned char* from = stage + wslot * Lay::kStageBytes;
-            uint4 raw[kU];    // (all of the step's loads first)
-            uint32_t s4[kU];
+          for (int s = -kStages; s < total; ++s) {
+            if (s >= 0) {
+              if (sub == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
+              if (!ok) break;
+              asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+              unsigned char* dst = dst0 + slot * kHalf + sub * kStepRows * 128;
+              const unsigned char* from = stage + wslot * Lay::kStageBytes;
+              uint4 raw[kU];    // (all of the step's loads first)
+              uint32_t s4[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
-              if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + Lay::kStageCodes + u * 128);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              const int row = row_of(u);
-              // (steps are multiples of eight rows, or of four and the row's swizzle follows the step)
-              unsigned char* at = dst + row * 128 + (halves ? (u & 1) * 2 * blk : 0);
-              const int x7 = ((c & 7) ^ ((row + sub * step_rows) & 7)) << 4;
-              if (k8) {
-                *reinterpret_cast<uint4*>(at + x7) = e4m3x8_to_f16(raw[u].x, raw[u].y);
-                *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e4m3x8_to_f16(raw[u].z, raw[u].w);
-              } else {
-                const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
-                const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-                *reinterpret_cast<uint4*>(at + x7) = e2m1x8_to_f16(raw[u].x, s_lo);
-                *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e2m1x8_to_f16(raw[u].y, s_lo);
-                *reinterpret_cast<uint4*>(at + (x7 ^ 32)) = e2m1x8_to_f16(raw[u].z, s_hi);
-                *reinterpret_cast<uint4*>(at + (x7 ^ 48)) = e2m1x8_to_f16(raw[u].w, s_hi);
+              for (int u = 0; u < kU; ++u) {
+                raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
+                if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + Lay::kStageCodes + u * 128);
               }
-            }
-            wslot = wslot + 1 == kStages ? 0 : wslot + 1;
-            if (++sub == kSubs) {
-              sub = 0;
-              landed(&land[slot]);
-              if (++slot == slots) {
-                slot = 0;
-                ++use;
-              }
-            }
-          }
-          if (ij < t.tb) {
-            const uint32_t to = smem_u32(stage) + islot * Lay::kStageBytes;
-            int at[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              const int row = row_of(u) + isub * step_rows;
-              at[u] = __shfl_sync(0xffffffffu, row < 32 ? sl[0] : sl[kPer - 1], row & 31);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              const size_t o = (size_t)(uint32_t)max(at[u], 0);
-              cp_async16(to + u * 512, base + o * pitch + (halves ? 128 * (u & 1) : 0), at[u] >= 0 ? 16 : 0);
-              if (!k8)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + Lay::kStageCodes + u * 128),
-                             "l"(sbase + o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
-            }
-            islot = islot + 1 == kStages ? 0 : islot + 1;
-            if (++isub == kSubs) {
-              isub = 0;
-              ++ij;
-              next_slots(n1);
-#pragma unroll
-              for (int x = 0; x < kPer; ++x) {
-                n1[x] = n2[x];
-                // the tile after next: to the L2, a row per lane
-                if (n1[x] >= 0 && (long long)n1[x] < p.num_slots) {
-                  const unsigned char* line = base - part * 16 + (size_t)(uint32_t)n1[x] * pitch;
-                  asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-                  if (k8 && !is_v) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128));
+              for (int u = 0; u < kU; ++u) {
+                unsigned char* at = dst + row_of(u) * 128 + (kHalves ? (u & 1) * 2 * kColBlk : 0);
+                const int x7 = sw[(row_of(u) >> 2) & 1];
+                if (k8) {
+                  *reinterpret_cast<uint4*>(at + x7) = e4m3x8_to_f16(raw[u].x, raw[u].y);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e4m3x8_to_f16(raw[u].z, raw[u].w);
+                } else {
+                  const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
+                  const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+                  *reinterpret_cast<uint4*>(at + x7) = e2m1x8_to_f16(raw[u].x, s_lo);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e2m1x8_to_f16(raw[u].y, s_lo);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 32)) = e2m1x8_to_f16(raw[u].z, s_hi);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 48)) = e2m1x8_to_f16(raw[u].w, s_hi);
                 }
               }
-              look_up(ij + 2, n2);
+              wslot = wslot + 1 == kStages ? 0 : wslot + 1;
+              if (++sub == kSubs) {
+                sub = 0;
+                landed(&land[slot]);
+                if (++slot == slots) {
+                  slot = 0;
+                  ++use;
+                }
+              }
             }
+            if (ij < t.tb) {
+              const uint32_t to = smem_u32(stage) + islot * Lay::kStageBytes;
+              const int first = isub * kStepRows;   // (a step's rows lie in one of the two registers of slots)
+              const int mine = first < 32 ? sl[0] : sl[kPer - 1];
+              int at[kU];
+#pragma unroll
+              for (int u = 0; u < kU; ++u) at[u] = __shfl_sync(0xffffffffu, mine, (first + row_of(u) + sub_row) & 31);
+#pragma unroll
+              for (int u = 0; u < kU; ++u) {
+                const uint32_t o = (uint32_t)max(at[u], 0);
+                cp_async16(to + u * 512, base + (size_t)o * pitch + (kHalves ? 128 * (u & 1) : 0), at[u] >= 0 ? 16 : 0);
+                if (!k8)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to - lane * 12 + Lay::kStageCodes + u * 128),
+                               "l"(sbase + (size_t)o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
+              }
+              islot = islot + 1 == kStages ? 0 : islot + 1;
+              if (++isub == kSubs) {
+                isub = 0;
+                ++ij;
+                next_slots(n1);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+                  n1[x] = n2[x];
+                  // the tile after next: to the L2, a row per lane
+                  if (n1[x] >= 0 && (long long)n1[x] < p.num_slots) {
+                    const unsigned char* line = base - part * 16 + (size_t)(uint32_t)n1[x] * pitch;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+                    if (kHalves) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128));
+                  }
+                }
+                look_up(ij + 2, n2);
+              }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        cp_async_wait_all();
+          cp_async_wait_all();
+        };
+        if (is_v) gather(std::true_type());
+        else gather(std::false_type());
       }
       if (!ok) break;
       ++it;

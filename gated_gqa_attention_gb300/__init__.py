@@ -767,6 +767,8 @@ def prefill_paged(q, gate_t, k_pool, v_pool, cu_seqlens, kv_indptr, kv_indices, 
         _need_shape("out", out, torch.bfloat16, (Tq, Hq, D), dev, "have q's shape")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
+    if not (0 <= window < 1 << 31 and 0 <= keep_first < 1 << 31):
+        raise ValueError("window and keep_first must be numbers of positions")
     if error_word is not None and (error_word.get_device() != dev or error_word.element_size() != 4
                                    or error_word.numel() < 1):
         raise ValueError("error_word must be a 32-bit word on cuda:%d" % dev)

@@ -322,7 +322,7 @@ __device__ __forceinline__ void join_sink(const PagedParams& p, int head, float&
     l = l * w + 1.0f;
     e = e * w + 1.0f;
     m = s;
-  } else if (s > -INFINITY) {
+  } else if (s != -INFINITY) {  // (a NaN too)
     const float t = exp2f(s - m);
     l += t;
     e += t;
@@ -494,7 +494,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         const uint32_t t_s = t_row + kTmemS + sb * kPN + 64 * hc;       // this warp's 64 scores, then their P
         const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of the first
         const bool masked = __any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep));
-        const unsigned long long seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
+        unsigned long long seen = ~0ull;
+        if (masked) seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
         if (some) {
 #pragma unroll 1
           for (int c0 = 0; c0 < 64; c0 += 32) {
@@ -660,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       if (p.lse && hc == 0 && r < rows) p.lse[(size_t)head * p.Tq + t.q0 + tok] = lse_of(m, e);
       unsigned char* stage = sm + Lay::kOffV;
       if (tiles) {
-        const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;  // (a NaN sum comes with NaN in O)
+        const float inv = (l == 0.0f) ? 0.0f : wo * p.v_descale / l;
         // a dead row is 0 also where a value that its block's other rows see was not finite
         const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
         ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
@@ -1279,7 +1280,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   float wo = 1.0f;
   if (p.sinks) join_sink(p, head, m, l, e, wo);
   if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + s.q0 + tok] = lse_of(m, e);
-  const float inv = (l > 0.0f) ? wo * p.v_descale / l : 0.0f;
+  const float inv = (l == 0.0f) ? 0.0f : wo * p.v_descale / l;
   const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
   uint32_t b[4];
 #pragma unroll

@@ -105,7 +105,14 @@ def test_sinks(gda, kv, window, first):
     b.sinks += torch.where(torch.arange(16, device="cuda") % 3 == 0, 90.0, -90.0)   # far above and far below the scores
     b.check(gda, window, first)
     b.sinks[::2] = -math.inf                                                        # no sink
-    b.check(gda, window, first)
+    o, lse = b.check(gda, window, first)
+    # a sink that is no number, or infinite: its head alone
+    b.sinks[5], b.sinks[6] = math.nan, math.inf
+    o2, lse2 = b.call(gda, window, first)
+    rest = [h for h in range(16) if h not in (5, 6)]
+    seen = b.want(window, first).sabs > 0                                           # rows with keys
+    assert bool(o2[:, 5][seen[:, 5]].isnan().all()) and bool((o2[:, 6] == 0).all())
+    assert torch.equal(o[:, rest], o2[:, rest]) and torch.equal(lse[rest], lse2[rest])
 
 
 @pytest.mark.parametrize("kv", KV)
@@ -440,10 +447,12 @@ def test_refusals(gda):
         ok(workspace=torch.empty(1 << 26, dtype=torch.uint8))
     with pytest.raises(gda.GdaError):
         ok(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
-    with pytest.raises(gda.GdaError):
-        ok(window=-1)
-    with pytest.raises(gda.GdaError):
-        ok(keep_first=-1)
+    for bad in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="window"):
+            ok(window=bad)
+        with pytest.raises(ValueError, match="window"):
+            ok(keep_first=bad)
+    ok(window=(1 << 31) - 1, keep_first=(1 << 31) - 1)
     with pytest.raises(gda.GdaError):
         ok(scale=math.inf)
     with pytest.raises(ValueError, match="out must"):
@@ -462,3 +471,24 @@ def test_refusals(gda):
     b.sinks = torch.zeros(8, device="cuda")
     with pytest.raises(ValueError, match="sinks"):
         ok()
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_values_that_are_no_numbers(gda, kv):
+    """A NaN in a query, or in a row that it sees, is in its results; tokens of other sequences keep their bits."""
+    b = Batch([(3, 700), (40, 300), (1, 2000)], kv=kv, seed=29)
+    o, lse = b.call(gda)
+    first = b.indices[700 + 5].long()                # seen by every token of the second sequence
+    v = b.v_pool.clone()
+    if kv == "fp4":
+        b.kw["kv_scales"] = b.kw["kv_scales"].clone()
+        b.kw["kv_scales"][first, :, 1] = 0x7F
+    else:
+        v.view(torch.uint8)[first] = 0x7F if kv == "e4m3" else 0xFF
+    b.v_pool = v
+    b.q[1, 4, 7] = math.nan
+    o2, lse2 = b.call(gda)
+    assert bool(o2[3:43].isnan().all()) and bool(o2[1, 4].isnan().all()) and bool(lse2[4, 1].isnan())
+    rest = torch.ones(44, 16, dtype=torch.bool, device="cuda")
+    rest[3:43], rest[1, 4] = False, False
+    assert torch.equal(o[rest], o2[rest])

@@ -745,6 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         s = seq_of(p, at.b);
         mt = blocks_of(p, s);
       }
+      if (lane == 0 && rank == 0) p.cuts[1 + shares + share] = make_int4(s.q0, s.nq, 0, 0);
 #pragma unroll 1
       for (int n = 0;; ++n) {
         Item t = {};
@@ -1211,31 +1212,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
 constexpr int kJoinThreads = 256, kJoinY = kPagedRows * (kD / 8) / kJoinThreads;
 __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const __grid_constant__ PagedParams p) {
   __shared__ int part[kPagedMaxShares + 1];
+  __shared__ int count[kJoinThreads / 32];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const int c = blockIdx.x + 1, tid = threadIdx.x;
+  // (all that the cuts table has to say in one trip to memory; places past the last share end the table)
+  const int c = blockIdx.x + 1, tid = threadIdx.x, shares = gridDim.x + 1;
+  const int4 end = make_int4(p.B, 0, 0, 0);
   const int used = p.cuts[0].x;
-  const int4 me = p.cuts[1 + c], before = p.cuts[c];
-  auto same = [&](const int4& a) { return a.x == me.x && a.y == me.y && a.z == me.z; };
+  const int4 me = p.cuts[1 + c], before = p.cuts[c], seq = p.cuts[1 + shares + c];
+  const int4 a = c + tid < shares ? p.cuts[1 + c + tid] : end, z = c + tid + 1 < shares ? p.cuts[2 + c + tid] : end;
+  auto same = [&](const int4& x) { return x.x == me.x && x.y == me.y && x.z == me.z; };
   if (c >= used || me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
-  const Seq s = seq_of(p, me.x);
-  const long long flat0 = (long long)me.z * kRowsI;
-  const int rows = (int)min((long long)kRowsI, (long long)s.nq * p.G - flat0);
+  const int q0 = seq.x, flat0 = me.z * kRowsI;
+  const int rows = min(kRowsI, seq.y * p.G - flat0);
   const int x = blockIdx.y * kJoinThreads + tid;
   if ((int)(blockIdx.y * kJoinThreads) >= rows * (kD / 8)) return;
-  // the parts: share c - 1's last one, then the first ones of the shares that start in the item
+  // the parts: share c - 1's last one, then the first ones of the shares that start in the item; empty
+  // shares are left out, the list in order by ballots
   int mine = -1;
-  bool in = false;
-  if (c + tid < used) {
-    const int4 a = p.cuts[1 + c + tid];
-    in = same(a);
-    if (in) {
-      const int4 z = c + tid + 1 < used ? p.cuts[2 + c + tid] : make_int4(p.B, 0, 0, 0);
-      if (!same(z) || z.w > a.w) mine = 2 * (c + tid);   // (else the share is empty)
-    }
-  }
-  // (empty shares are left out: the list is in order, by ballots within the first warps)
-  __shared__ int count[kJoinThreads / 32];
+  if (c + tid < used && same(a) && (c + tid + 1 >= used || !same(z) || z.w > a.w)) mine = 2 * (c + tid);
   const unsigned ball = __ballot_sync(0xffffffffu, mine >= 0);
   if ((tid & 31) == 0) count[tid >> 5] = __popc(ball);
   __syncthreads();
@@ -1249,37 +1244,30 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   __syncthreads();
   const int r = x % rows, c8 = x / rows;
   if (c8 >= kD / 8) return;
-  const int tok = (int)((flat0 + r) / p.G), head = me.y * p.G + (int)((flat0 + r) - (long long)tok * p.G);
-  const uint4* gate = nullptr;
+  const int tok = (int)((unsigned)(flat0 + r) / (unsigned)p.G), head = me.y * p.G + (flat0 + r - tok * p.G);
   uint4 g = make_uint4(0u, 0u, 0u, 0u);
-  if (p.gate) {
-    gate = reinterpret_cast<const uint4*>(p.gate + (long long)(s.q0 + tok) * p.gate_stride + (long long)head * kD) + c8;
-    g = __ldg(gate);
-  }
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int k = 0; k < parts; ++k) {
-    const float a = __ldcg(&p.part_ml[(size_t)part[k] * kRowsI + r].x);
-    if (!(a <= m)) m = a;   // (a NaN stays)
-  }
-  float l = 0.0f, e = 0.0f;
+  if (p.gate)
+    g = __ldg(reinterpret_cast<const uint4*>(p.gate + (long long)(q0 + tok) * p.gate_stride + (long long)head * kD) + c8);
+  // running max, so that a part's sums and values come in one trip
+  float m = -INFINITY, l = 0.0f, e = 0.0f;
   float o[8] = {};
 #pragma unroll 4
   for (int k = 0; k < parts; ++k) {
-    const float4 a = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
+    const float4 s = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
     const float4* src = p.part_o + ((size_t)part[k] * 64 + 2 * c8) * kRowsI + r;
     const float4 u = __ldcg(src), v = __ldcg(src + kRowsI);
-    if (a.y != 0.0f) {  // (0: no visible key in this part)
-      const float w = exp2f(a.x - m);
-      l += w * a.y;
-      e += w * a.z;
-      o[0] += w * u.x, o[1] += w * u.y, o[2] += w * u.z, o[3] += w * u.w;
-      o[4] += w * v.x, o[5] += w * v.y, o[6] += w * v.z, o[7] += w * v.w;
+    if (s.y != 0.0f) {  // (0: no visible key in this part)
+      const float top = fmaxf(m, s.x), w = exp2f(s.x - top), old = exp2f(m - top);
+      m = top;
+      l = l * old + w * s.y;
+      e = e * old + w * s.z;
+      o[0] = o[0] * old + w * u.x, o[1] = o[1] * old + w * u.y, o[2] = o[2] * old + w * u.z, o[3] = o[3] * old + w * u.w;
+      o[4] = o[4] * old + w * v.x, o[5] = o[5] * old + w * v.y, o[6] = o[6] * old + w * v.z, o[7] = o[7] * old + w * v.w;
     }
   }
   float wo = 1.0f;
   if (p.sinks) join_sink(p, head, m, l, e, wo);
-  if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + s.q0 + tok] = lse_of(m, e);
+  if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + q0 + tok] = lse_of(m, e);
   const float inv = (l == 0.0f) ? 0.0f : wo * p.v_descale / l;
   const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
   uint32_t b[4];
@@ -1291,7 +1279,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = mul_bf16x2(b[i], sg[i]);
   }
-  reinterpret_cast<uint4*>(p.out + ((size_t)(s.q0 + tok) * p.Hq + head) * kD)[c8] = make_uint4(b[0], b[1], b[2], b[3]);
+  reinterpret_cast<uint4*>(p.out + ((size_t)(q0 + tok) * p.Hq + head) * kD)[c8] = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 namespace {

@@ -30,7 +30,7 @@ struct PagedParams {
   long long wait_limit;
   const uint16_t* table;       // BF16 sigmoid of every BF16 code
   // workspace: where the shares of the work start, and what shares that cut an item leave of it
-  int4* cuts;                  // {number of shares, -, -, -}, then each share's start
+  int4* cuts;                  // {number of shares, -, -, -}, each share's start, each one's first sequence {row, tokens, -, -}
   float4* part_ml;             // [2 kPagedMaxShares][256] {row max (log2), sum, unrounded sum, -}
   float4* part_o;              // [2 kPagedMaxShares][64][256]: four dimensions of a row
 };
@@ -41,7 +41,7 @@ constexpr int kPagedMaxShares = 80;   // pairs of CTAs
 constexpr size_t kPagedCutBytes = 4096;
 constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxShares * kPagedRows * 16;
 constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxShares * 64 * kPagedRows * 16;
-static_assert((kPagedMaxShares + 1) * 16 <= kPagedCutBytes, "cut table");
+static_assert((2 * kPagedMaxShares + 1) * 16 <= kPagedCutBytes, "cut table");
 
 // kv_dtype: GDA_KV_* of the pools
 cudaError_t launch_prefill_paged(const PagedParams& p, int kv_dtype, cudaStream_t stream);

@@ -828,7 +828,7 @@ int gda_prefill_paged(const gda_paged_args* a, void* workspace, size_t workspace
   // the factor of the scores has to be a normal FP32 value
   const double factor = (double)a->scale * (codes ? a->k_descale : 1.0f) * 1.44269504088896340736;
   if (!(factor > 1.2e-38 && factor < 3.4e38)) return GDA_ERR_ARG;
-  if (a->total_q > kMaxRows || a->nnz > kMaxRows || a->Hq > kMaxHeads) return GDA_ERR_SHAPE;
+  if (a->total_q > kMaxRows || a->nnz > kMaxRows || a->B > kMaxRows || a->Hq > kMaxHeads) return GDA_ERR_SHAPE;
   const int64_t wq = (int64_t)a->Hq * a->D;
   if (a->q_stride < wq || (a->gate && a->gate_stride < wq)) return GDA_ERR_SHAPE;
   if (a->B == 0 || a->total_q == 0) return GDA_OK;

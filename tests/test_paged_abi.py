@@ -64,6 +64,7 @@ def paged_args(**kw):
     (dict(scale=1e-30, k_descale=1e-30), ARG), (dict(scale=1e30, k_descale=1e30), ARG), (dict(Hq=15), SHAPE),
     (dict(Hkv=0), SHAPE), (dict(D=128), UNSUPPORTED), (dict(kv_dtype=2), UNSUPPORTED), (dict(kv_dtype=-1), UNSUPPORTED),
     (dict(B=-1), SHAPE), (dict(total_q=-1), SHAPE), (dict(nnz=-1), SHAPE), (dict(num_slots=-1), SHAPE),
+    (dict(B=(1 << 31) - 1), SHAPE), (dict(total_q=1 << 28), SHAPE),   # (8 heads a group: 2^31 rows)
     (dict(total_q=1 << 31), SHAPE), (dict(nnz=1 << 31), SHAPE), (dict(window=-1), SHAPE), (dict(keep_first=-1), SHAPE),
     (dict(B=0), OK), (dict(total_q=0), OK), (dict(total_q=0, q=None, out=None), OK)])
 def test_paged_refusals(lib, change, status):

@@ -20,7 +20,38 @@
 // item that a share's end cuts is computed in parts: each pair leaves its part (row max, sum,
 // unnormalised O in FP32) in the workspace, at most two per pair, and a second kernel joins them in
 // the order of the shares, so a result does not depend on which ends first.  What an item costs is
-// taken as linear in its number within the sequence, so that sums over items have a closed form.
+// taken as linear in its number within the sequence, and as constant from the block on whose window
+// is full, so that sums over items have a closed form (linear to the last block, the prompts under a
+// window took 195 us instead of 167).
+//
+// Roles of a CTA's 16 warps, tied by mbarriers whose every wait is bounded:
+//   0-7    softmax and epilogue (row quarter warp % 4, keys or dimensions half warp / 4)
+//   8      planner: the share's items, one ahead
+//   9      issuer (in rank 0 alone, one thread): PV of tile T, then S of tile T + 2
+//   10, 11 relays: what landed in the CTA -> proxy fence -> rank 0's barriers
+//   12-13  gather K;  14-15 gather Q and V
+// BF16 rows are copied by cp.async whose completion arrives at the ring's barrier; codes are copied
+// into a ring of each warp's own and widened from there to FP16, which holds every code exactly.
+// P stays in TMEM, over the first half of each warp's own scores, so PV reads no shared memory for
+// it (P in shared memory with a K ring of two: 869 instead of 814 us for 2048 tokens at 34816).
+//
+// Roundings to fewer bits: P to the MMA's type, BF16 or FP16 (2^-8 or 2^-11 of a weight; the
+// divisor sums the rounded weights, so a row's weights add up to 1; lse sums them unrounded); for
+// codes Q to FP16, scaled by a power of two per row; O to BF16 as the formula has it.  Scores, row
+// maxima, sums, O and the parts are FP32.
+//
+// What bounds it (GPU time, without the host's):
+//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 690 us, 1640 TFLOP/s, tensor pipe 73 %
+//     busy.  A tile's chain is softmax 1.1 us, MMAs 1.05 us and the hops between the two CTAs, with
+//     two tiles under way: 1.33-1.55 us a tile
+//   few rows, BF16 (64 sequences, a window of 1024): 101 us for 540 MB, 5.3 TB/s with both kernels,
+//     of which the first reads 5.6 TB/s.  An item ends with about 6 us that read nothing
+//   few rows, codes (64 sequences of 4 tokens, e4m3): 125 us, 2.3 TB/s: the four widening warps,
+//     1.5-1.7 us a tile (eight of them: no faster; codes widened from registers: 2.7 us a tile)
+//   one short sequence: 12.8 us, of which a share is found and the first rows come in 7-8 us and the
+//     parts are joined in 3-4 us
+// A TMA gather of four rows a time (tile::gather4) brought 3.95 us a 64 KiB tile, 2.5 TB/s in all,
+// against 1.36 us of the cp.async here.
 #include <limits.h>
 
 #include <type_traits>
@@ -44,7 +75,7 @@ constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 10;  // relays: 10 for K
 constexpr int kGatherWarp = 12;     // the gatherers: the first half of them for K, the others for Q and V
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
-constexpr int kGatherers = 4;       // half of them for K, half for Q and V (with eight, codes are no faster)
+constexpr int kGatherers = 4;       // half of them for K, half for Q and V
 constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
 // registers of a thread (softmax, planner and issuer, gatherers) share out what the block has at its
 // launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room
@@ -56,7 +87,10 @@ template <int KV>
 constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
 constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per thread
 
-constexpr int kItemCost = 10;        // of an item besides its tiles, in half tiles
+// What an item costs besides its tiles, in half tiles (about 6 us: its last softmax and PV, the epilogue,
+// the next one's first S).  With 4, 10, 14 and 18: mixed batch of 4-bit rows 488, 395, 402, 410 us; 64
+// sequences of 4 tokens, e4m3, 130, 125, 125, 127; single tokens and prompts within 2 %.
+constexpr int kItemCost = 10;
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
 constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
@@ -94,7 +128,7 @@ struct Cut {           // a place in the stream: block i of KV head h of sequenc
   int b, h, i, t;
 };
 struct Bars {
-  // *_land: this CTA's part of Q, K, V has landed (every gathering thread arrives).  In rank 0, where
+  // *_land: this CTA's part of Q, K, V has landed (kLandings arrivals).  In rank 0, where
   // both CTAs arrive: q_full and k_full (both parts have), pv_full (P written and both parts of V),
   // o_empty (O read).  Commits arrive in both CTAs
   uint64_t q_land, q_full, q_empty;                 // (q_empty: the item's S products have read it)
@@ -109,6 +143,7 @@ struct Bars {
   int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+
 // ---- the stream of items
 
 struct Seq {
@@ -344,6 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   // the 128-byte swizzled tiles need a 1024-byte aligned base: a misaligned one is reported,
   // not used (the same for every CTA)
   if ((smem_u32(sm) & 1023u) != 0) {
+    pdl_wait_prior_grid();   // (the joining kernel starts when this one is over)
     if (threadIdx.x == 0) {
       atomicOr(p.error, kErrTimeout);
       p.cuts[0] = make_int4(0, 0, 0, 0);
@@ -439,8 +475,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     return true;
   };
 
-  // Every role walks the same items.  `it` counts those with tiles, T the tiles and N = 2 T the
-  // half tiles so far: the phases of the barriers follow from them.
+  // Every role walks the same items.  `it` counts those with tiles, T the tiles so far, (slot, use) the
+  // places of a ring: the phases of the barriers follow from them.
   if (warp < kSoftmaxWarps) {
     regs_grow<kRegsSoftmax>();
     // ---------------- softmax: warp w owns rows 32 (w % 4) .. + 31 (its TMEM lane quarter) and
@@ -915,7 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     // ---------------- gatherers, for K (this CTA's 64 keys of a tile) or for Q and V (128 keys, this CTA's
     // 128 dimensions).  A tile goes into the next slot of its ring once the MMAs that read the slot's
     // previous tile have completed.  BF16 rows are copied asynchronously (cp.async, whose completion
-    // arrives at the slot's barrier); codes go through registers, widened to FP16.
+    // arrives at the slot's barrier); codes are copied to a small ring of the warp's and widened from it.
     constexpr int kHalfTeam = kGatherers / 2;
     const int gw = (warp - kGatherWarp) % kHalfTeam;
     const bool is_v = warp >= kGatherWarp + kHalfTeam;

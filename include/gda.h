@@ -389,7 +389,7 @@ int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
  *             first keep_first (keep_first without a window has no effect)
  *   error_word  as gda_prefill; gda_prefill_read_error reads the library's
  * A query that sees no key (more tokens than positions) gives out = 0, lse = -inf or its sink.
- * Positions that no query of the 128 rows computed together (the query heads of neighbouring tokens)
+ * Positions that no query of the 256 rows computed together (the query heads of neighbouring tokens)
  * sees are not read.  Within these a non-finite V row that one query sees may also reach another
  * that does not see it (its probability there is 0, and 0 times it is NaN); other sequences' rows and
  * those behind a sequence's end never do.
@@ -645,8 +645,8 @@ int gda_read_error(const void* workspace, gda_stream_t stream, int clear, uint32
 int gda_timing_begin(int max_calls);
 int gda_timing_end(int* n_timed, double* total_ms);
 
-/* Failure-path testing.  The kernels that wait on mbarriers (gda_prefill, and the
- * GDA_VARIANT_TMA stage 1 of the decode) give up a wait after a limit of SM cycles
+/* Failure-path testing.  The kernels that wait on mbarriers (gda_prefill,
+ * gda_prefill_packed, gda_prefill_paged and the GDA_VARIANT_TMA stage 1 of the decode) give up a wait after a limit of SM cycles
  * (about two seconds by default), set GDA_DEVERR_TIMEOUT in their error word (the
  * workspace's, or gda_prefill's), wait with the default limit for the copies and MMAs
  * they already started, and return, so the context stays usable and the host reads a

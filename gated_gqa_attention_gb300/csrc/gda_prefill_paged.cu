@@ -13,12 +13,13 @@
 //
 // Pairs.  A cluster of two CTAs computes an item, 128 rows in each, by MMAs of the pair (M = 256):
 // every gathered row is read once per 256 rows, a CTA gathers half of it (64 keys of K, half the
-// dimensions of V) and its shared memory holds three K tiles and two V tiles that way.
+// dimensions of V) and its shared memory holds three K tiles and two V tiles that way.  Batches
+// whose sequences have few rows go by a CTA to an item: 128 rows, tiles of 64 keys (kFewRows).
 //
 // Shares.  The lengths are on the device.  The items, by sequence, KV head and block, form one
-// stream in which an item costs its tiles and a constant; each pair takes an equal share of it.  An
-// item that a share's end cuts is computed in parts: each pair leaves its part (row max, sum,
-// unnormalised O in FP32) in the workspace, at most two per pair, and a second kernel joins them in
+// stream in which an item costs its tiles and a constant; each pair, or lone CTA, takes an equal
+// share of it.  An item that a share's end cuts is computed in parts: each share leaves its part (row
+// max, sum, unnormalised O in FP32) in the workspace, at most two, and a second kernel joins them in
 // the order of the shares, so a result does not depend on which ends first.  What an item costs is
 // taken as linear in its number within the sequence, and as constant from the block on whose window
 // is full, so that sums over items have a closed form (linear to the last block, the prompts under a
@@ -67,9 +68,14 @@ namespace gda {
 
 namespace {
 
-constexpr int kPM = 128;            // rows of an item per CTA (half the MMA's M)
-constexpr int kRowsI = kPagedRows;  // rows of an item
-constexpr int kPN = 128;            // keys per tile (MMA N of S)
+constexpr int kPM = 128;            // rows of an item per CTA
+// An item's rows (the MMAs' M), its tiles' keys (N of S) and how many CTAs compute it
+template <bool PAIR>
+struct Geo {
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kRows = kPM * kCtas;
+  static constexpr int kKeys = 64 * kCtas;
+};
 constexpr int kSoftmaxWarps = 8;    // warps 0-7
 constexpr int kPlanWarp = 8, kMmaWarp = 9, kRelayWarp = 10;  // relays: 10 for K, 11 for Q and V
 constexpr int kGatherWarp = 12;     // the gatherers: the first half of them for K, the others for Q and V
@@ -81,7 +87,7 @@ constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
 // launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room
 constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
 static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + 32 * kGatherers * kRegsGather <= kThreads * 128, "register shares");
-constexpr int kRowsK = 64 / (kGatherers / 2), kRowsV = 128 / (kGatherers / 2);  // of a tile per gathering warp
+constexpr int kRowsK = 64 / (kGatherers / 2), kRowsQ = kPM / (kGatherers / 2);  // of a tile and of Q per gathering warp
 // arrivals that make a CTA's part of a tile complete: every copying thread's, or one of each widening warp
 template <int KV>
 constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
@@ -91,6 +97,14 @@ constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per
 // the next one's first S).  With 4, 10, 14 and 18: mixed batch of 4-bit rows 488, 395, 402, 410 us; 64
 // sequences of 4 tokens, e4m3, 130, 125, 125, 127; single tokens and prompts within 2 %.
 constexpr int kItemCost = 10;
+
+// The batch's kernel: a CTA to an item (128 rows, tiles of 64 keys) where a sequence has no more than
+// kFewRows rows (tokens times G) on average, else a pair (256 rows, 128 keys).  The pair's MMAs take the
+// same time for any number of rows, a lone CTA's are half of a tile's; its items end side by side.
+// 48 sequences at 3000 to 5000 positions, 8 heads a group, lone against pair: single tokens BF16 78 and
+// 83 us, e4m3 86 and 92, 4-bit 79 and 90; 16 tokens 96 and 100, 109 and 116, 101 and 114; 24 tokens
+// (two blocks of 128) 155 and 107, 186 and 122, 174 and 120.  One sequence of one token: within 5 %.
+constexpr int kFewRows = 128;
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB
 constexpr uint32_t kHalf = 2 * kBlk;               // a CTA's half of a K or V tile: 32 KiB
@@ -160,41 +174,47 @@ __device__ __forceinline__ Seq seq_of(const PagedParams& p, int b) {
   return s;
 }
 // (a sequence's rows, tokens times G, fit 31 bits with two blocks to spare: the host checks it)
-__device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) { return (s.nq * p.G + kRowsI - 1) / kRowsI; }
+template <bool PAIR>
+__device__ __forceinline__ int blocks_of(const PagedParams& p, const Seq& s) {
+  return (s.nq * p.G + Geo<PAIR>::kRows - 1) / Geo<PAIR>::kRows;
+}
 // block i of a sequence: what its rows see, and its tiles
 struct Range {
   int lo, hi, f, tl, n;
 };
+template <bool PAIR>
 __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, int i) {
+  constexpr int kRowsI = Geo<PAIR>::kRows, kPN = Geo<PAIR>::kKeys;
   Range r;
   const int ta = (int)((unsigned)(i * kRowsI) / (unsigned)p.G);                              // first and last token
   const int tb = min(s.nq - 1, (int)((unsigned)(i * kRowsI + kRowsI - 1) / (unsigned)p.G));
   const int off = s.L - s.nq;
   r.hi = max(off + tb + 1, 0);
   r.lo = p.window > 0 ? (int)min(max((long long)off + ta - p.window + 1, 0LL), (long long)r.hi) : 0;
-  const int th = (r.hi + kPN - 1) >> 7;
-  r.tl = r.lo >> 7;
-  r.f = min((min(p.keep, r.lo) + kPN - 1) >> 7, r.tl);
+  const int th = (int)(((unsigned)r.hi + kPN - 1) / kPN);
+  r.tl = r.lo / kPN;
+  r.f = min((int)(((unsigned)min(p.keep, r.lo) + kPN - 1) / kPN), r.tl);
   r.n = r.f + th - r.tl;
   return r;
 }
 // Costs of a sequence's blocks, per KV head: linear up to block `knee`, constant from there.  (Tiles
 // grow with the positions up to the last block, or to the first one whose window leaves positions out.)
+template <bool PAIR>
 struct Costs {
   int mt, knee;            // blocks
   long long first, rise;   // the first one's, and 2^16 times what the next one costs more
   __device__ __forceinline__ Costs(const PagedParams& p, const Seq& s) {
-    mt = blocks_of(p, s);
+    mt = blocks_of<PAIR>(p, s);
     knee = 0;
     first = rise = 0;
     if (mt > 0) {
-      const int n0 = range_of(p, s, 0).n;
+      const int n0 = range_of<PAIR>(p, s, 0).n;
       first = 2LL * n0 + kItemCost;
       if (mt > 1) {
         knee = mt - 1;
         if (p.window > 0)  // the block of the token whose position is the window's length
-          knee = (int)min((long long)knee, max(0LL, (long long)p.window - s.L + s.nq) * p.G / kRowsI + 1);
-        rise = ((2LL * (range_of(p, s, knee).n - n0)) << 16) / knee;
+          knee = (int)min((long long)knee, max(0LL, (long long)p.window - s.L + s.nq) * p.G / Geo<PAIR>::kRows + 1);
+        rise = ((2LL * (range_of<PAIR>(p, s, knee).n - n0)) << 16) / knee;
       }
     }
   }
@@ -205,8 +225,9 @@ struct Costs {
   }
 };
 // the place at x within a sequence's costs (0 <= x < Hkv * c.before(c.mt))
+template <bool PAIR>
 __device__ __forceinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b, long long x) {
-  const Costs c(p, s);
+  const Costs<PAIR> c(p, s);
   const long long per_head = c.before(c.mt);
   Cut r;
   r.b = b;
@@ -220,7 +241,7 @@ __device__ __forceinline__ Cut cut_at(const PagedParams& p, const Seq& s, int b,
   }
   r.i = lo;
   const long long at = c.before(lo), cost = c.before(lo + 1) - at;
-  r.t = cost > 0 ? (int)((unsigned long long)(range_of(p, s, lo).n * (x - at)) / (unsigned long long)cost) : 0;
+  r.t = cost > 0 ? (int)((unsigned long long)(range_of<PAIR>(p, s, lo).n * (x - at)) / (unsigned long long)cost) : 0;
   return r;
 }
 // Where share x of `shares` starts and ends, and how many shares there are.  A whole warp calls it.
@@ -228,6 +249,7 @@ struct Share {
   Cut start, end;
   int used;
 };
+template <bool PAIR>
 __device__ __forceinline__ Share share_of(const PagedParams& p, int x, int shares) {
   const int lane = threadIdx.x & 31;
   Seq s = {0, 0, 0, 0};
@@ -235,15 +257,15 @@ __device__ __forceinline__ Share share_of(const PagedParams& p, int x, int share
 #pragma unroll 4
   for (int b = lane; b < p.B; b += 32) {
     s = seq_of(p, b);
-    const Costs c(p, s);
+    const Costs<PAIR> c(p, s);
     cost = p.Hkv * c.before(c.mt);
     total += cost;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   Share r;
-  // none is less than a tile's worth
-  r.used = (int)max(1LL, min((long long)shares, total / 2));
+  // none is less than 128 keys' worth
+  r.used = (int)max(1LL, min((long long)shares, total * Geo<PAIR>::kKeys / 256));
   // lanes below 16 find the start, the others the end
   const int y = x + (lane >> 4);
   const long long at = y < r.used ? total * y / r.used : total;
@@ -256,7 +278,7 @@ __device__ __forceinline__ Share share_of(const PagedParams& p, int x, int share
       cost = 0;
       if (b0 + lane < p.B) {
         s = seq_of(p, b0 + lane);
-        const Costs c(p, s);
+        const Costs<PAIR> c(p, s);
         cost = p.Hkv * c.before(c.mt);
       }
     }
@@ -288,7 +310,7 @@ __device__ __forceinline__ Share share_of(const PagedParams& p, int x, int share
     if (sum > at1) break;   // (both are found)
   }
   Cut c = {p.B, 0, 0, 0};
-  if (mine_b < p.B) c = cut_at(p, mine, mine_b, mine_x);
+  if (mine_b < p.B) c = cut_at<PAIR>(p, mine, mine_b, mine_x);
   __syncwarp();
   r.start = {__shfl_sync(0xffffffffu, c.b, 0), __shfl_sync(0xffffffffu, c.h, 0), __shfl_sync(0xffffffffu, c.i, 0),
              __shfl_sync(0xffffffffu, c.t, 0)};
@@ -369,11 +391,11 @@ __device__ __forceinline__ float lse_of(float m, float e) {
   return (e == 0.0f) ? -INFINITY : (m + log2f(e)) * 0.69314718055994530942f;
 }
 
-}  // namespace
-
-template <int KV>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid_constant__ PagedParams p) {
+template <int KV, bool PAIR>
+__device__ __forceinline__ void paged_body(const PagedParams& p) {
   using Lay = Layout<KV>;
+  constexpr int kCtas = Geo<PAIR>::kCtas, kRowsI = Geo<PAIR>::kRows, kPN = Geo<PAIR>::kKeys, kHK = kPN / 2;
+  constexpr int kRowsV = kPN / (kGatherers / 2);   // of a V tile per gathering warp
   constexpr int kKSlots = Lay::kKSlots;
   extern __shared__ __align__(1024) unsigned char sm[];
   // the 128-byte swizzled tiles need a 1024-byte aligned base: a misaligned one is reported,
@@ -391,22 +413,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   float* ebuf = reinterpret_cast<float*>(sm + Lay::kOffE);
   float* qscale = reinterpret_cast<float*>(sm + Lay::kOffScale);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_rank(), share = blockIdx.x >> 1, shares = gridDim.x >> 1;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int share = (int)blockIdx.x / kCtas, shares = (int)gridDim.x / kCtas;
 
   if (tid == 0) {
     mbar_init(&bars.q_land, kLandings<KV>);
-    mbar_init(&bars.q_full, 2);
+    mbar_init(&bars.q_full, kCtas);
     mbar_init(&bars.q_empty, 1);
     for (int x = 0; x < kKSlots; ++x) {
       mbar_init(&bars.k_land[x], kLandings<KV>);
-      mbar_init(&bars.k_full[x], 2);
+      mbar_init(&bars.k_full[x], kCtas);
       mbar_init(&bars.k_empty[x], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars.v_land[x], kLandings<KV>);
       mbar_init(&bars.v_empty[x], 1);
       mbar_init(&bars.s_full[x], 1);
-      mbar_init(&bars.pv_full[x], 2 * kSoftmaxWarps + 2);
+      mbar_init(&bars.pv_full[x], kCtas * (kSoftmaxWarps + 1));
       mbar_init(&bars.p_empty[x], 1);
       mbar_init(&bars.i_full[x], 1);
       mbar_init(&bars.i_empty[x], 2 + kGatherers + kSoftmaxWarps + (rank == 0 ? 1 : 0));  // relays, gatherers, softmax, issuer
@@ -417,14 +440,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       mbar_init(&bars.pr[q4], 2);
     }
     mbar_init(&bars.o_full, 1);
-    mbar_init(&bars.o_empty, 2 * kSoftmaxWarps);
+    mbar_init(&bars.o_empty, kCtas * kSoftmaxWarps);
     mbar_init(&bars.v_free, kSoftmaxWarps);
     bars.abort = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc_pair(&bars.tmem, kTmemCols);
-    tmem_relinquish_pair();
+    if (PAIR) {
+      tmem_alloc_pair(&bars.tmem, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&bars.tmem, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   // (as a programmatic dependent: the set-up above ran during the previous kernel's end, whose
@@ -432,20 +460,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // both CTAs' barriers are set up before anything arrives at them (the planner's share is found meanwhile)
+  // all barriers are set up before anything arrives at them (the planner's share is found meanwhile)
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (PAIR) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else __syncthreads();
   Share mine = {};
-  if (warp == kPlanWarp) mine = share_of(p, share, shares);
+  if (warp == kPlanWarp) mine = share_of<PAIR>(p, share, shares);
   __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (PAIR) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
   volatile int* abort_flag = &bars.abort;
   auto fail = [&]() {
     if (bars.abort == 0) atomicOr(p.error, kErrTimeout);
     bars.abort = 1;
-    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(cluster_addr(&bars.abort, rank ^ 1)) : "memory");  // (alive until the end)
+    if (PAIR)   // (alive until the end)
+      asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(cluster_addr(&bars.abort, rank ^ 1)) : "memory");
   };
   // (short: the roles' code shares one instruction cache, and this is in it many times.  A
   // limit below the default is the failure-path test's: polls then hardly suspend.)
@@ -460,7 +490,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
     } while (!mbar_try_wait_for(bar, parity & 1, hint));
     return true;
   };
-  auto arrive_first = [&](uint64_t* bar) { mbar_arrive_cluster(cluster_addr(bar, 0)); };  // rank 0's barrier
+  auto arrive_first = [&](uint64_t* bar) {   // rank 0's barrier
+    if (PAIR) mbar_arrive_cluster(cluster_addr(bar, 0));
+    else mbar_arrive(bar);
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (PAIR) umma_commit_pair(bar);
+    else umma_commit(bar);
+  };
   // what a role started is waited for with the default limit, whatever the abort flag says
   auto drain = [&](uint64_t* bar, int parity) {
     const long long t0 = clock64();
@@ -480,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   if (warp < kSoftmaxWarps) {
     regs_grow<kRegsSoftmax>();
     // ---------------- softmax: warp w owns rows 32 (w % 4) .. + 31 (its TMEM lane quarter) and
-    // keys [64 hc, 64 hc + 64) of each tile, hc = w / 4
+    // half hc = w / 4 of each tile's keys
     const int rg = warp & 3, hc = warp >> 2;
     const int r = 32 * rg + lane;
     const uint32_t t_row = tmem + ((uint32_t)(rg * 32) << 16);
@@ -527,14 +564,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         float hm = -INFINITY;
         // (two rolled passes over the scores in TMEM: unrolled over 64 scores in registers, this loop is
         // bound by the fetching of its instructions)
-        const uint32_t t_s = t_row + kTmemS + sb * kPN + 64 * hc;       // this warp's 64 scores, then their P
-        const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + 64 * hc;  // key of the first
-        const bool masked = __any_sync(0xffffffffu, k0 + 64 > k_hi || (k0 < k_lo && k0 + 64 > p.keep));
+        const uint32_t t_s = t_row + kTmemS + sb * kPN + kHK * hc;      // this warp's scores, then their P
+        const int k0 = (j < t.f ? j : j - t.f + t.tl) * kPN + kHK * hc;  // key of the first
+        const bool masked = __any_sync(0xffffffffu, k0 + kHK > k_hi || (k0 < k_lo && k0 + kHK > p.keep));
         unsigned long long seen = ~0ull;
         if (masked) seen = below(k_hi - k0) & (~below(k_lo - k0) | below(p.keep - k0));
         if (some) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 32) {
+          for (int c0 = 0; c0 < kHK; c0 += 32) {
             float s[32];
             tmem_ld32(t_s + c0, s);
             tmem_wait_ld();
@@ -594,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           const bool huge = __any_sync(0xffffffffu, fabsf(m_run) > 262144.0f && m_run != -INFINITY);
           float2 l2 = make_float2(0.0f, 0.0f), e2 = l2;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 16) {
+          for (int c0 = 0; c0 < kHK; c0 += 16) {
             float s[16];
             tmem_ld16(t_s + c0, s);
             tmem_wait_ld();
@@ -779,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       int mt = 0;
       if (at.b < p.B) {
         s = seq_of(p, at.b);
-        mt = blocks_of(p, s);
+        mt = blocks_of<PAIR>(p, s);
       }
       if (lane == 0 && rank == 0) p.cuts[1 + shares + share] = make_int4(s.q0, s.nq, 0, 0);
 #pragma unroll 1
@@ -788,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         t.b = -1;
         const bool last = at.b == end.b && at.h == end.h && at.i == end.i;  // the share ends in this item
         if (at.b < p.B && !(last && end.t <= at.t)) {
-          const Range r = range_of(p, s, at.i);
+          const Range r = range_of<PAIR>(p, s, at.i);
           t.b = at.b;
           t.q0 = s.q0, t.nq = s.nq, t.kb = s.kb, t.L = s.L;
           t.h = at.h, t.i = at.i;
@@ -829,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         at.b = min(at.b, p.B);
         if (at.b < p.B) {
           s = seq_of(p, at.b);
-          mt = blocks_of(p, s);
+          mt = blocks_of<PAIR>(p, s);
         }
       }
       if (!ok && lane == 0) fail();
@@ -843,6 +880,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
       int it = 0, T = 0, slot = 0, use = 0;
       int done_s = -1, done_o = -1;  // tiles of the last commits
       bool ok = true;
+      auto mma_ss = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        if (PAIR) umma_pair_ss(d, a, b, id, acc);
+        else umma_bf16_ss(d, a, b, id, acc);
+      };
+      auto mma_ts = [](uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        if (PAIR) umma_pair_ts(d, a, b, id, acc);
+        else umma_bf16_ts(d, a, b, id, acc);
+      };
       auto issue_s = [&](int x) {
         const uint32_t kb = sK + slot * kHalf;
 #pragma unroll 1
@@ -850,10 +895,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           const uint64_t ad = sdesc_sw128(sQ + c * kBlk, 16, 1024), bd = sdesc_sw128(kb + c * kKBlk, 16, 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 16 each (32 bytes; descriptors count 16)
-            umma_pair_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
+            mma_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
         }
-        umma_commit_pair(&bars.s_full[x & 1]);
-        umma_commit_pair(&bars.k_empty[slot]);
+        commit(&bars.s_full[x & 1]);
+        commit(&bars.k_empty[slot]);
         done_s = x;
         if (++slot == kKSlots) {
           slot = 0;
@@ -883,25 +928,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           tc_fence_after();
           if (j >= t.ta + 2) {
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {  // 64 keys; V is MN-major (dims contiguous): LBO = stride between a CTA's two
-              // 64-dim blocks, SBO = 8 key rows
-              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + c * 64 * 128, kBlk, 1024);
-              const uint32_t a = tmem + kTmemS + pb * kPN + 64 * c;  // (P over the first half of these keys' scores)
+            for (int c = 0; c < 2; ++c) {  // a half's keys; V is MN-major (dims contiguous): LBO = stride between a
+              // CTA's 64-dim blocks, SBO = 8 key rows
+              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + c * kHK * 128, kPN * 128, 1024);
+              const uint32_t a = tmem + kTmemS + pb * kPN + kHK * c;  // (P over the first half of these keys' scores)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)  // 16 keys each
-                umma_pair_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > t.ta + 2 || c > 0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < kHK / 16; ++k)  // 16 keys each
+                mma_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > t.ta + 2 || c > 0 || k > 0) ? 1u : 0u);
             }
-            umma_commit_pair(&bars.v_empty[pb]);
-            umma_commit_pair(&bars.p_empty[pb]);
+            commit(&bars.v_empty[pb]);
+            commit(&bars.p_empty[pb]);
             done_o = T++;
           }
           if (more) {
             issue_s(x++);
-            if (j + 1 == t.tb) umma_commit_pair(&bars.q_empty);   // (every S product of the item)
+            if (j + 1 == t.tb) commit(&bars.q_empty);   // (every S product of the item)
           }
         }
         if (!ok) break;
-        umma_commit_pair(&bars.o_full);
+        commit(&bars.o_full);
         ++it;
       }
       if (!ok) {
@@ -1012,8 +1057,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         // step as below; rows past its last stay what they are, and what comes of them goes nowhere
         if (it > 0) ok = acquire(&bars.q_empty, it - 1);
         if (!ok) break;
-        const int q0 = gw * kRowsV, flat0 = t.i * kRowsI + rank * kPM + q0;
-        const int rows = min(kRowsV, t.nq * p.G - flat0);
+        const int q0 = gw * kRowsQ, flat0 = t.i * kRowsI + rank * kPM + q0;
+        const int rows = min(kRowsQ, t.nq * p.G - flat0);
         const int dt = 4 / p.G, dg = 4 - dt * p.G;     // four rows on
         int tok = (int)((unsigned)(flat0 + g8) / (unsigned)p.G), g = flat0 + g8 - tok * p.G;
         unsigned char* dq = sm + Lay::kOffQ + (q0 + g8) * 128;
@@ -1084,7 +1129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
           const uint32_t d0 = smem_u32(ring + slot * kHalf) + (row0 + g8) * 128;
-          if (!is_v) {
+          if (!PAIR || !is_v) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const int at = __shfl_sync(0xffffffffu, sl[0], 4 * q + g8);
@@ -1115,7 +1160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
         // of a row's later parts take a neighbouring row's (sub_row), so that the eight 16-byte chunks that
         // are stored at a time lie in eight different banks
         auto gather = [&](auto of_v) {
-          constexpr bool k8 = KV == GDA_KV_E4M3, kV = decltype(of_v)::value;
+          constexpr bool k8 = KV == GDA_KV_E4M3, kV = decltype(of_v)::value;   // (kV: half the dimensions of 128 keys)
           constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
           constexpr bool kHalves = k8 && !kV;                      // an e4m3 K row has two places
           constexpr int kPlaceRows = !k8 && kV ? 8 : 4;            // rows from one place to the next
@@ -1127,7 +1172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           const uint32_t pitch = (uint32_t)p.Hkv * (k8 ? kD : kCodeBytes), spitch = (uint32_t)p.Hkv * kScalePair;
           const unsigned char* base = pool + (size_t)t.h * (k8 ? kD : kCodeBytes) + (kV ? rank * (k8 ? 128 : 64) : 0) + part * 16;
           const unsigned char* sbase =
-              k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (kV ? kScaleBytes + rank * 8 : 0) + ((part * 2) & ~3);
+              k8 ? nullptr : p.scales + (size_t)t.h * kScalePair + (is_v ? kScaleBytes : 0) + (kV ? rank * 8 : 0) + ((part * 2) & ~3);
           unsigned char* stage = sm + Lay::kOffStage + (warp - kGatherWarp) * Lay::kStageWarp + lane * 16;
           const int c = k8 ? 2 * part : 4 * part;   // the first of a place's two (4 bits: four) 8-dimension chunks
           constexpr uint32_t kColBlk = kV ? kBlk : kKBlk;
@@ -1220,7 +1265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
           }
           cp_async_wait_all();
         };
-        if (is_v) gather(std::true_type());
+        if (PAIR && is_v) gather(std::integral_constant<bool, PAIR>());
         else gather(std::false_type());
       }
       if (!ok) break;
@@ -1233,22 +1278,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill
   // ---- teardown: every role of both CTAs is done (or gave up and waited for what it started)
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();
+  if (PAIR) cluster_sync_all();
+  else __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    if (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+}  // namespace
+
+template <int KV>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prefill_paged_kernel(const __grid_constant__ PagedParams p) {
+  paged_body<KV, true>(p);
+}
+template <int KV>
+__global__ void __launch_bounds__(kThreads, 1) prefill_paged_few_kernel(const __grid_constant__ PagedParams p) {
+  paged_body<KV, false>(p);
 }
 
 // Joins the parts of the item that the start of share c = blockIdx.x + 1 cuts first:
 //   m = max m_k, w_k = 2^(m_k - m), O = sum w_k O_k / (sum w_k l_k + sink)
-// in the order of the shares.  A thread has eight dimensions of a row, neighbouring threads
-// neighbouring rows (as the parts are laid out); blocks blockIdx.y take 256 such pieces each, as many
-// as the item's rows make.
-constexpr int kJoinThreads = 256, kJoinY = kPagedRows * (kD / 8) / kJoinThreads;
+// A thread has eight dimensions of a row, neighbouring threads neighbouring rows (as the parts are
+// laid out).  Where an item has few rows and many parts, 2, 4 or 8 groups of a block's threads take
+// a run of the parts each, and the first joins the runs.  Each in the order of the shares, and the
+// groups a function of the counts: the same bits every time.  (One token
+// at 8192 positions, whole call: 18.4 us, one group 46.7; at 131072 58 and 89.)
+constexpr int kJoinThreads = 256, kJoinLog = 3, kJoinGroups = 1 << kJoinLog;
+template <bool PAIR>
 __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int kRowsI = Geo<PAIR>::kRows;
   __shared__ int part[kPagedMaxShares + 1];
   __shared__ int count[kJoinThreads / 32];
+  __shared__ float runs[kJoinGroups - 1][11][kJoinThreads / kJoinGroups];   // (fewer groups: fewer runs of more threads)
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   // (all that the cuts table has to say in one trip to memory; places past the last share end the table)
@@ -1261,8 +1324,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   if (c >= used || me.x >= p.B || me.w == 0 || (same(before) && before.w > 0)) return;
   const int q0 = seq.x, flat0 = me.z * kRowsI;
   const int rows = min(kRowsI, seq.y * p.G - flat0);
-  const int x = blockIdx.y * kJoinThreads + tid;
-  if ((int)(blockIdx.y * kJoinThreads) >= rows * (kD / 8)) return;
+  if ((int)(blockIdx.y * (kJoinThreads / kJoinGroups)) >= rows * (kD / 8)) return;
   // the parts: share c - 1's last one, then the first ones of the shares that start in the item; empty
   // shares are left out, the list in order by ballots
   int mine = -1;
@@ -1278,8 +1340,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   if (mine >= 0) part[at + __popc(ball & ((1u << (tid & 31)) - 1u))] = mine;
   if (tid == 0) part[0] = 2 * (c - 1) + 1;
   __syncthreads();
-  const int r = x % rows, c8 = x / rows;
-  if (c8 >= kD / 8) return;
+  // groups: as many as the blocks of a full item have threads for, four parts and more to each
+  int lg = 0;   // log2 of their number
+  while (lg < kJoinLog && (rows << (lg + 1)) <= kRowsI && parts > (4 << lg)) ++lg;
+  const int pieces = kJoinThreads >> lg, group = tid / (kJoinThreads / kJoinGroups) >> (kJoinLog - lg), piece = tid & (pieces - 1);
+  const int x = blockIdx.y * pieces + piece;
+  if ((int)(blockIdx.y * pieces) >= rows * (kD / 8)) return;
+  const bool in = x < rows * (kD / 8);
+  const int c8 = in ? x / rows : 0, r = in ? x - c8 * rows : 0;
   const int tok = (int)((unsigned)(flat0 + r) / (unsigned)p.G), head = me.y * p.G + (flat0 + r - tok * p.G);
   uint4 g = make_uint4(0u, 0u, 0u, 0u);
   if (p.gate)
@@ -1287,20 +1355,45 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   // running max, so that a part's sums and values come in one trip
   float m = -INFINITY, l = 0.0f, e = 0.0f;
   float o[8] = {};
+  auto add = [&](float pm, float pl, float pe, const float* po) {
+    if (pl != 0.0f) {  // (0: no visible key in this part)
+      const float top = fmaxf(m, pm), w = exp2f(pm - top), old = exp2f(m - top);
+      m = top;
+      l = l * old + w * pl;
+      e = e * old + w * pe;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = o[i] * old + w * po[i];
+    }
+  };
+  const int k1 = (group + 1) * parts >> lg;
 #pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
+  for (int k = group * parts >> lg; k < k1; ++k) {
     const float4 s = __ldcg(p.part_ml + (size_t)part[k] * kRowsI + r);
     const float4* src = p.part_o + ((size_t)part[k] * 64 + 2 * c8) * kRowsI + r;
     const float4 u = __ldcg(src), v = __ldcg(src + kRowsI);
-    if (s.y != 0.0f) {  // (0: no visible key in this part)
-      const float top = fmaxf(m, s.x), w = exp2f(s.x - top), old = exp2f(m - top);
-      m = top;
-      l = l * old + w * s.y;
-      e = e * old + w * s.z;
-      o[0] = o[0] * old + w * u.x, o[1] = o[1] * old + w * u.y, o[2] = o[2] * old + w * u.z, o[3] = o[3] * old + w * u.w;
-      o[4] = o[4] * old + w * v.x, o[5] = o[5] * old + w * v.y, o[6] = o[6] * old + w * v.z, o[7] = o[7] * old + w * v.w;
+    const float po[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    add(s.x, s.y, s.z, po);
+  }
+  if (lg > 0) {
+    float* run = &runs[0][0][0] + piece;   // [group - 1][value][piece]
+    if (group > 0) {
+      float* to = run + (group - 1) * 11 * pieces;
+      to[0] = m, to[pieces] = l, to[2 * pieces] = e;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[(3 + i) * pieces] = o[i];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll 1
+    for (int g1 = 0; g1 < (1 << lg) - 1; ++g1) {
+      const float* from = run + g1 * 11 * pieces;
+      float po[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) po[i] = from[(3 + i) * pieces];
+      add(from[0], from[pieces], from[2 * pieces], po);
     }
   }
+  if (!in) return;
   float wo = 1.0f;
   if (p.sinks) join_sink(p, head, m, l, e, wo);
   if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + q0 + tok] = lse_of(m, e);
@@ -1320,24 +1413,44 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
 
 namespace {
 
-template <int KV>
-cudaError_t launch(const PagedParams& p, int grid, cudaStream_t stream) {
+// a programmatic dependent of the kernel before it
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const PagedParams& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<KV>::kBytes;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_paged_kernel<KV>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <bool PAIR>
+cudaError_t launch_all(const PagedParams& p, int kv_dtype, int sms, cudaStream_t stream) {
+  constexpr int kCtas = Geo<PAIR>::kCtas;
+  const int shares = min(sms / kCtas, kPagedMaxShares / kCtas);
+  if (shares < 1) return cudaErrorInvalidDevice;
+  const dim3 grid((unsigned)(shares * kCtas));
+  auto run = [&](auto kv) {
+    constexpr int KV = decltype(kv)::value;
+    return launch(PAIR ? prefill_paged_kernel<KV> : prefill_paged_few_kernel<KV>, grid, kThreads, Layout<KV>::kBytes, stream, p);
+  };
+  const cudaError_t e = kv_dtype == GDA_KV_BF16   ? run(std::integral_constant<int, GDA_KV_BF16>())
+                        : kv_dtype == GDA_KV_E4M3 ? run(std::integral_constant<int, GDA_KV_E4M3>())
+                                                  : run(std::integral_constant<int, GDA_KV_E2M1>());
+  if (e != cudaSuccess || shares < 2) return e;
+  const dim3 join((unsigned)(shares - 1), (unsigned)(Geo<PAIR>::kRows * (kD / 8) / kJoinThreads));
+  return launch(prefill_paged_join_kernel<PAIR>, join, kJoinThreads, 0, stream, p);
 }
 template <int KV>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(prefill_paged_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Layout<KV>::kBytes);
+  const cudaError_t e = cudaFuncSetAttribute(prefill_paged_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Layout<KV>::kBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(prefill_paged_few_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<KV>::kBytes);
 }
 
 }  // namespace
@@ -1359,22 +1472,8 @@ cudaError_t launch_prefill_paged(const PagedParams& params, int kv_dtype, cudaSt
   if (e == cudaSuccess) e = sigmoid_table(&p.table);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int shares = sms / 2 < kPagedMaxShares ? sms / 2 : kPagedMaxShares;
-  if (shares < 1) return cudaErrorInvalidDevice;
-  if (kv_dtype == GDA_KV_BF16) e = launch<GDA_KV_BF16>(p, 2 * shares, stream);
-  else if (kv_dtype == GDA_KV_E4M3) e = launch<GDA_KV_E4M3>(p, 2 * shares, stream);
-  else e = launch<GDA_KV_E2M1>(p, 2 * shares, stream);
-  if (e != cudaSuccess || shares < 2) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(shares - 1), kJoinY);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_paged_join_kernel, p);
+  const bool few = (long long)p.Tq * p.G <= (long long)kFewRows * p.B;
+  return few ? launch_all<false>(p, kv_dtype, sms, stream) : launch_all<true>(p, kv_dtype, sms, stream);
 }
 
 }  // namespace gda

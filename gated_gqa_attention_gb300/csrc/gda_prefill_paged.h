@@ -31,14 +31,14 @@ struct PagedParams {
   const uint16_t* table;       // BF16 sigmoid of every BF16 code
   // workspace: where the shares of the work start, and what shares that cut an item leave of it
   int4* cuts;                  // {number of shares, -, -, -}, each share's start, each one's first sequence {row, tokens, -, -}
-  float4* part_ml;             // [2 kPagedMaxShares][256] {row max (log2), sum, unrounded sum, -}
-  float4* part_o;              // [2 kPagedMaxShares][64][256]: four dimensions of a row
+  float4* part_ml;             // [2 parts of a share][rows] {row max (log2), sum, unrounded sum, -}
+  float4* part_o;              // [2 parts of a share][64][rows]: four dimensions of a row
 };
 
-constexpr int kPagedRows = 256;       // rows of an item: 128 in each CTA of a pair
-constexpr int kPagedMaxShares = 80;   // pairs of CTAs
+constexpr int kPagedMaxShares = 160;  // CTAs, or twice as many as pairs of them
+constexpr int kPagedRows = 128;       // rows of a part: one CTA's (a pair's part takes two)
 // bytes of each part of the workspace
-constexpr size_t kPagedCutBytes = 4096;
+constexpr size_t kPagedCutBytes = 8192;
 constexpr size_t kPagedMlBytes = (size_t)2 * kPagedMaxShares * kPagedRows * 16;
 constexpr size_t kPagedOBytes = (size_t)2 * kPagedMaxShares * 64 * kPagedRows * 16;
 static_assert((2 * kPagedMaxShares + 1) * 16 <= kPagedCutBytes, "cut table");

@@ -364,6 +364,48 @@ def test_every_gate_code(gda):
         assert torch.equal(out.view(torch.int16)[~nan], w.view(torch.int16)[~nan])
 
 
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads", [(16, 2), (24, 1), (12, 4)], ids=str)
+@pytest.mark.parametrize("empty", [0, 80])
+def test_long_and_short_by_either_kernel(gda, kv, heads, empty):
+    """The same sequences, alone and with so many empty ones that the batch goes by a CTA to an item: blocks of 256
+    and of 128 rows, tiles of 128 and of 64 keys, parts joined."""
+    b = Batch([(150, 900), (1, 2300), (40, 40), (9, 3), (17, 4097)] + [(0, 0)] * empty, *heads, kv=kv, sinks=True, seed=31)
+    for window, first in ((0, 0), (100, 70), (64, 0), (1, 1)):
+        o, lse = b.check(gda, window, first)
+        o2, lse2 = b.call(gda, window, first)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("tokens, positions", [(1, 500), (1, 30000), (4, 20000), (9, 5000), (16, 9000), (20, 12000)])
+def test_one_sequence_in_many_parts(gda, kv, tokens, positions):
+    b = Batch([(tokens, positions)], kv=kv, seed=32)
+    o, lse = b.check(gda)
+    o2, lse2 = b.call(gda)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_wait_limit_with_few_rows(gda):
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for kv in KV:
+        b = Batch([(1, 3000), (2, 500), (0, 3), (1, 700)], kv=kv, seed=33)
+        want, _ = b.call(gda, error_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        try:
+            gda.debug_wait_limit(200)           # SM cycles: below the latency of a first load
+            b.call(gda, error_word=err)
+            torch.cuda.synchronize()            # the call returns
+        finally:
+            gda.debug_wait_limit(0)
+        assert int(err.item()) & gda.DEVERR_TIMEOUT
+        err.zero_()
+        got, _ = b.call(gda, error_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and torch.equal(got, want)
+
+
 def test_many_short_sequences(gda):
     import random
     r = random.Random(5)

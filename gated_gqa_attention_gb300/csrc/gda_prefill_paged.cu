@@ -45,10 +45,12 @@
 //   full rows (2048 tokens at 34816, 8 heads a group, BF16): 690 us, 1640 TFLOP/s, tensor pipe 73 %
 //     busy.  A tile's chain is softmax 1.1 us, MMAs 1.05 us and the hops between the two CTAs, with
 //     two tiles under way: 1.33-1.55 us a tile
-//   few rows, BF16 (64 sequences, a window of 1024): 101 us for 540 MB, 5.3 TB/s with both kernels,
-//     of which the first reads 5.6 TB/s.  An item ends with about 6 us that read nothing
-//   few rows, codes (64 sequences of 4 tokens, e4m3): 125 us, 2.3 TB/s: the four widening warps,
-//     1.5-1.7 us a tile (eight of them: no faster; codes widened from registers: 2.7 us a tile)
+//   few rows, BF16 (64 sequences of one token, a window of 4096): 98 us for 540 MB, 5.5 TB/s with
+//     both kernels.  An item ends with 4-6 us that read nothing
+//   few rows, codes (64 sequences of 4 tokens, e4m3): 94 us, 3.0 TB/s, 1.0-1.2 us a tile of 64 keys.
+//     Shared memory: a tile is written twice (codes, FP16) and read twice, and its MMAs read Q's 64 KiB,
+//     2048 clocks in all.  (Without widening 94, without softmax 91, without both and the copies 81.
+//     Four S products under way: 94.  Widened from registers: twice the time)
 //   one short sequence: 12.8 us, of which a share is found and the first rows come in 7-8 us and the
 //     parts are joined in 3-4 us
 // A TMA gather of four rows a time (tile::gather4) brought 3.95 us a 64 KiB tile, 2.5 TB/s in all,
@@ -86,6 +88,7 @@ constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
 // registers of a thread (softmax, planner and issuer, gatherers) share out what the block has at its
 // launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room
 constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
+static_assert(kRegsSoftmax >= 128 && kRegsIssue <= 128 && kRegsGather <= 128, "the softmax warps grow, the others shrink");
 static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + 32 * kGatherers * kRegsGather <= kThreads * 128, "register shares");
 constexpr int kRowsK = 64 / (kGatherers / 2), kRowsQ = kPM / (kGatherers / 2);  // of a tile and of Q per gathering warp
 // arrivals that make a CTA's part of a tile complete: every copying thread's, or one of each widening warp
@@ -1162,6 +1165,9 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
         auto gather = [&](auto of_v) {
           constexpr bool k8 = KV == GDA_KV_E4M3, kV = decltype(of_v)::value;   // (kV: half the dimensions of 128 keys)
           constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
+          // (a tile's steps of e4m3 unrolled: with their counts at run time the warps were bound by instructions,
+          // 64 x 4 tokens 113 us instead of 94; 4 bits, whose steps are longer: unrolled 391 and 90 us, rolled 388 and 88)
+          constexpr int kUnroll = k8 ? kSubs : 1;
           constexpr bool kHalves = k8 && !kV;                      // an e4m3 K row has two places
           constexpr int kPlaceRows = !k8 && kV ? 8 : 4;            // rows from one place to the next
           constexpr int kStepRows = (kHalves ? kU / 2 : kU) * kPlaceRows;
@@ -1179,62 +1185,23 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           unsigned char* dst0 = ring + (row0 + sub_row) * 128 + (c >> 3) * kColBlk;
           const int sw[2] = {((c & 7) ^ (sub_row & 7)) << 4, ((c & 7) ^ ((4 + sub_row) & 7)) << 4};  // of rows 8 n, 8 n + 4
           int sl[kPer];        // the slots of the tile that is being copied, ij
-          int ij = t.ta, isub = 0, islot = 0, wslot = 0;
+          int ij = t.ta, islot = 0, wslot = 0;
           auto next_slots = [&](int* from) {
 #pragma unroll
             for (int x = 0; x < kPer; ++x) sl[x] = slot_of(from[x]);
           };
           next_slots(n0);
-          const int total = (t.tb - t.ta) * kSubs;
-          int sub = 0;
-#pragma unroll 1
-          for (int s = -kStages; s < total; ++s) {
-            if (s >= 0) {
-              if (sub == 0 && use > 0) ok = acquire(&empty[slot], use - 1);
-              if (!ok) break;
-              asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-              unsigned char* dst = dst0 + slot * kHalf + sub * kStepRows * 128;
-              const unsigned char* from = stage + wslot * Lay::kStageBytes;
-              uint4 raw[kU];    // (all of the step's loads first)
-              uint32_t s4[kU];
-#pragma unroll
-              for (int u = 0; u < kU; ++u) {
-                raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
-                if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + Lay::kStageCodes + u * 128);
-              }
-#pragma unroll
-              for (int u = 0; u < kU; ++u) {
-                unsigned char* at = dst + row_of(u) * 128 + (kHalves ? (u & 1) * 2 * kColBlk : 0);
-                const int x7 = sw[(row_of(u) >> 2) & 1];
-                if (k8) {
-                  *reinterpret_cast<uint4*>(at + x7) = e4m3x8_to_f16(raw[u].x, raw[u].y);
-                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e4m3x8_to_f16(raw[u].z, raw[u].w);
-                } else {
-                  const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
-                  const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
-                  *reinterpret_cast<uint4*>(at + x7) = e2m1x8_to_f16(raw[u].x, s_lo);
-                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e2m1x8_to_f16(raw[u].y, s_lo);
-                  *reinterpret_cast<uint4*>(at + (x7 ^ 32)) = e2m1x8_to_f16(raw[u].z, s_hi);
-                  *reinterpret_cast<uint4*>(at + (x7 ^ 48)) = e2m1x8_to_f16(raw[u].w, s_hi);
-                }
-              }
-              wslot = wslot + 1 == kStages ? 0 : wslot + 1;
-              if (++sub == kSubs) {
-                sub = 0;
-                landed(&land[slot]);
-                if (++slot == slots) {
-                  slot = 0;
-                  ++use;
-                }
-              }
-            }
+          const uint32_t stage_to = smem_u32(stage);
+          // step isub of tile ij into the staging ring
+          auto copy = [&](int isub) {
             if (ij < t.tb) {
-              const uint32_t to = smem_u32(stage) + islot * Lay::kStageBytes;
+              const uint32_t to = stage_to + islot * Lay::kStageBytes;
               const int first = isub * kStepRows;   // (a step's rows lie in one of the two registers of slots)
               const int mine = first < 32 ? sl[0] : sl[kPer - 1];
               int at[kU];
 #pragma unroll
-              for (int u = 0; u < kU; ++u) at[u] = __shfl_sync(0xffffffffu, mine, (first + row_of(u) + sub_row) & 31);
+              for (int u = 0; u < kU; ++u)
+                at[u] = kHalves && (u & 1) ? at[u - 1] : __shfl_sync(0xffffffffu, mine, (first + row_of(u) + sub_row) & 31);
 #pragma unroll
               for (int u = 0; u < kU; ++u) {
                 const uint32_t o = (uint32_t)max(at[u], 0);
@@ -1244,8 +1211,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
                                "l"(sbase + (size_t)o * spitch), "r"(at[u] >= 0 ? 4 : 0) : "memory");
               }
               islot = islot + 1 == kStages ? 0 : islot + 1;
-              if (++isub == kSubs) {
-                isub = 0;
+              if (isub == kSubs - 1) {
                 ++ij;
                 next_slots(n1);
 #pragma unroll
@@ -1262,6 +1228,49 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
               }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+          };
+#pragma unroll 1
+          for (int s = 0; s < kStages; ++s) copy(s % kSubs);
+#pragma unroll 1
+          for (int j = t.ta; j < t.tb; ++j) {
+            if (use > 0) ok = acquire(&empty[slot], use - 1);
+            if (!ok) break;
+            unsigned char* dst = dst0 + slot * kHalf;
+#pragma unroll kUnroll
+            for (int sub = 0; sub < kSubs; ++sub) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+              const unsigned char* from = stage + wslot * Lay::kStageBytes;
+              uint4 raw[kU];    // (all of the step's loads first)
+              uint32_t s4[kU];
+#pragma unroll
+              for (int u = 0; u < kU; ++u) {
+                raw[u] = *reinterpret_cast<const uint4*>(from + u * 512);
+                if (!k8) s4[u] = *reinterpret_cast<const uint32_t*>(from - lane * 12 + Lay::kStageCodes + u * 128);
+              }
+#pragma unroll
+              for (int u = 0; u < kU; ++u) {
+                unsigned char* at = dst + (sub * kStepRows + row_of(u)) * 128 + (kHalves ? (u & 1) * 2 * kColBlk : 0);
+                const int x7 = sw[(row_of(u) >> 2) & 1];
+                if (k8) {
+                  *reinterpret_cast<uint4*>(at + x7) = e4m3x8_to_f16(raw[u].x, raw[u].y);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e4m3x8_to_f16(raw[u].z, raw[u].w);
+                } else {
+                  const uint32_t f = e4m3x2_to_f16x2(s4[u] >> (16 * (part & 1)));
+                  const uint32_t s_lo = __byte_perm(f, f, 0x1010), s_hi = __byte_perm(f, f, 0x3232);
+                  *reinterpret_cast<uint4*>(at + x7) = e2m1x8_to_f16(raw[u].x, s_lo);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 16)) = e2m1x8_to_f16(raw[u].y, s_lo);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 32)) = e2m1x8_to_f16(raw[u].z, s_hi);
+                  *reinterpret_cast<uint4*>(at + (x7 ^ 48)) = e2m1x8_to_f16(raw[u].w, s_hi);
+                }
+              }
+              wslot = wslot + 1 == kStages ? 0 : wslot + 1;
+              copy((sub + kStages) % kSubs);
+            }
+            landed(&land[slot]);
+            if (++slot == slots) {
+              slot = 0;
+              ++use;
+            }
           }
           cp_async_wait_all();
         };

@@ -98,15 +98,16 @@ constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per
 
 // What an item costs besides its tiles, in half tiles (about 6 us: its last softmax and PV, the epilogue,
 // the next one's first S).  With 4, 10, 14 and 18: mixed batch of 4-bit rows 488, 395, 402, 410 us; 64
-// sequences of 4 tokens, e4m3, 130, 125, 125, 127; single tokens and prompts within 2 %.
+// sequences of 4 tokens, e4m3, by pairs 130, 125, 125, 127; single tokens and prompts within 2 %.  Lone
+// CTAs' tiles are half as long, their items end sooner: 6, 10, 16: 98, 94, 93 us for those sequences.
 constexpr int kItemCost = 10;
 
 // The batch's kernel: a CTA to an item (128 rows, tiles of 64 keys) where a sequence has no more than
 // kFewRows rows (tokens times G) on average, else a pair (256 rows, 128 keys).  The pair's MMAs take the
 // same time for any number of rows, a lone CTA's are half of a tile's; its items end side by side.
-// 48 sequences at 3000 to 5000 positions, 8 heads a group, lone against pair: single tokens BF16 78 and
-// 83 us, e4m3 86 and 92, 4-bit 79 and 90; 16 tokens 96 and 100, 109 and 116, 101 and 114; 24 tokens
-// (two blocks of 128) 155 and 107, 186 and 122, 174 and 120.  One sequence of one token: within 5 %.
+// 48 sequences at 3000 to 5000 positions, 8 heads a group, lone against pair: single tokens BF16 79 and
+// 84 us, e4m3 70 and 84, 4-bit 68 and 86; 16 tokens 96 and 101, 93 and 109, 92 and 109; 24 tokens (two
+// blocks of 128) 155 and 108, 155 and 113, 156 and 114.  One sequence of one token: 2-5 % slower.
 constexpr int kFewRows = 128;
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB

@@ -48,10 +48,10 @@
 //   few rows, BF16 (64 sequences of one token, a window of 4096): 98 us for 540 MB, 5.5 TB/s with
 //     both kernels.  An item ends with 4-6 us that read nothing
 //   few rows, codes (64 sequences of 4 tokens, e4m3): 94 us, 3.0 TB/s, 1.0-1.2 us a tile of 64 keys.
-//     Shared memory: a tile is written twice (codes, FP16) and read twice, and its MMAs read Q's 64 KiB,
-//     2048 clocks in all.  (Without widening 94, without softmax 91, without both and the copies 81.
-//     Four S products under way: 94.  Widened from registers: twice the time)
-//   one short sequence: 12.8 us, of which a share is found and the first rows come in 7-8 us and the
+//     No unit is near its limit (tensor pipe 32 %, issue slots 31 %): a tile's steps wait for one
+//     another.  Without widening 94, without softmax 91, without both and the copies 81; eight
+//     gathering warps 100, four S products under way 94, widened from registers twice the time
+//   one short sequence: 12.5 us, of which a share is found and the first rows come in 7-8 us and the
 //     parts are joined in 3-4 us
 // A TMA gather of four rows a time (tile::gather4) brought 3.95 us a 64 KiB tile, 2.5 TB/s in all,
 // against 1.36 us of the cp.async here.
@@ -553,7 +553,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint4*>(p.gate) + g_at),
                        "r"(2 * kD) : "memory");
       }
-      // running row max (log2 units), the sum of the probabilities as the MMA multiplies them (the
+      // running row max (log2 units; for FP16 less a constant), the sum of the probabilities as the MMA multiplies them (the
       // weights of a row add up to 1), and their sum before that rounding (for lse)
       float m_run = -INFINITY, l_run = 0.0f, e_run = 0.0f;
       float factor = p.scale_log2;
@@ -602,13 +602,16 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
         if (some) {
           const float mx = fmaxf(hm, xbuf[(sb * 2 + (1 - hc)) * kPM + r]) * factor;
           // lazy max: it moves only by more than 2^8, so probabilities stay below 2^8 (both
-          // halves of a row take the same decisions from the same values)
+          // halves of a row take the same decisions from the same values).  For FP16 it is held
+          // 2^7 lower: their range ends at 2^15 instead, and weights down to 2^-21 of the row's
+          // largest are normal numbers, those below lose bits under 2^-32 of it
+          constexpr float kLift = KV == GDA_KV_BF16 ? 0.0f : 7.0f;
           float alpha = 1.0f;
-          if (mx > m_run + 8.0f) {
-            alpha = (m_run == -INFINITY) ? 0.0f : exp2f(m_run - mx);
+          if (mx > m_run + (8.0f + kLift)) {
+            alpha = (m_run == -INFINITY) ? 0.0f : exp2f(m_run - (mx - kLift));
             l_run *= alpha;
             e_run *= alpha;
-            m_run = mx;
+            m_run = mx - kLift;
           }
           if (j > t.ta && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV of the tile before it is rescaled; this warp rescales its half of O

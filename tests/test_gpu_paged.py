@@ -386,6 +386,35 @@ def test_one_sequence_in_many_parts(gda, kv, tokens, positions):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "fp4"])
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("spike", [0, 59900])
+def test_many_small_weights_beside_a_large_one(gda, kv, tokens, spike):
+    """One key's weight is 1, all others' 2^-24.6 (4 bits hold 1 as 1.03: 2^-25.4): their sum, 2.4e-3 (1.4e-3), is the
+    whole of O.  FP16 probabilities are held 2^7 higher than that, so each is within 2^-11 relative, or 2^-32 of
+    the largest."""
+    b = Batch([(tokens, 60000)], kv=kv, seed=34, kd=1.0, vd=1.0, gate=False)
+    slots = b.k64.shape[0]
+    k, v = torch.zeros(slots, 2, D), torch.ones(slots, 2, D)
+    at = int(b.indices[spike])
+    k[at, :, 0], v[at] = 1.0, 0.0
+    k, v = k.bfloat16(), v.bfloat16()
+    if kv == "e4m3":
+        b.k_pool, b.v_pool = (paged64.quantise8(x, 1.0).cuda().view(torch.float8_e4m3fn) for x in (k, v))
+    else:
+        (ck, sk), (cv, sv) = plain64.quantise(k, 1.0), plain64.quantise(v, 1.0)
+        b.k_pool, b.v_pool = ck.cuda(), cv.cuda()
+        b.kw = dict(kv_scales=torch.stack([sk, sv], 2).contiguous().cuda(), k_descale=1.0, v_descale=1.0)
+        k, v = plain64.values(ck, sk, 1.0), plain64.values(cv, sv, 1.0)
+    b.k64, b.v64 = k.double().cuda(), v.double().cuda()
+    b.q[:] = 0
+    b.q[..., 0] = 273.0
+    o, lse = b.call(gda)
+    want = b.want()
+    tol = plain64.bound_out(want, 2.0 ** -11, 0) + 60000 * 2.0 ** -32
+    assert bool((want.out > 1e-3).all()) and bool(((o.double() - want.out).abs() <= tol).all())
+
+
 def test_wait_limit_with_few_rows(gda):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     for kv in KV:

@@ -107,7 +107,9 @@ constexpr int kItemCost = 10;
 // same time for any number of rows, a lone CTA's are half of a tile's; its items end side by side.
 // 48 sequences at 3000 to 5000 positions, 8 heads a group, lone against pair: single tokens BF16 79 and
 // 84 us, e4m3 70 and 84, 4-bit 68 and 86; 16 tokens 96 and 101, 93 and 109, 92 and 109; 24 tokens (two
-// blocks of 128) 155 and 108, 155 and 113, 156 and 114.  One sequence of one token: 2-5 % slower.
+// blocks of 128) 155 and 108, 155 and 113, 156 and 114.  63 tokens beside a chunk of 512 (71 rows on
+// average), all at 4096: 131 and 139, e4m3 143 and 147; of 1024 (135) 159 and 160, 174 and 168.  One
+// sequence of one token: 2-5 % slower.
 constexpr int kFewRows = 128;
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB

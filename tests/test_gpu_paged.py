@@ -415,6 +415,27 @@ def test_many_small_weights_beside_a_large_one(gda, kv, tokens, spike):
     assert bool((want.out > 1e-3).all()) and bool(((o.double() - want.out).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("heads", [(144, 1), (300, 1), (260, 2)], ids=str)
+@pytest.mark.parametrize("lens", [[(1, 700)], [(3, 200), (1, 129), (0, 4)], [(9, 9), (1, 500)]], ids=str)
+def test_a_token_in_several_blocks(gda, heads, lens):
+    """More query heads to a KV head than a block has rows."""
+    for kv in ("bf16", "e4m3"):
+        Batch(lens, *heads, kv=kv, sinks=True, seed=35).check(gda, 100, 3)
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_strides_of_q_and_gate_apart(gda, kv):
+    b = Batch([(3, 200), (40, 700), (1, 1300)], kv=kv, seed=36)
+    o, lse = b.check(gda)
+    wide = torch.full((44, 16 * D + 8), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :16 * D] = b.gate.reshape(44, 16 * D)
+    b.q, b.gate = b.q.contiguous(), wide[:, :16 * D].unflatten(1, (16, D))
+    o2, lse2 = b.call(gda)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    b.q, b.gate = b.gate, b.q                      # and the other way round
+    b.check(gda)
+
+
 def test_wait_limit_with_few_rows(gda):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     for kv in KV:

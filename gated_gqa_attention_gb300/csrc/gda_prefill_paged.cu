@@ -152,8 +152,8 @@ struct Bars {
   // both CTAs arrive: q_full and k_full (both parts have), pv_full (P written and both parts of V),
   // o_empty (O read).  Commits arrive in both CTAs
   uint64_t q_land, q_full, q_empty;                 // (q_empty: the item's S products have read it)
-  uint64_t k_land[3], k_full[3], k_empty[3], v_land[2], v_empty[2];
-  uint64_t s_full[2], pv_full[2], p_empty[2];       // per S / P buffer
+  uint64_t k_land[3], k_full[3], k_empty[3], v_land[2];
+  uint64_t s_full[2], pv_full[2], p_empty[2];       // per S / P buffer (p_empty: its PV product is complete, V's slot free)
   uint64_t xm[4][2];                                // per row quarter and tile parity: both maxima stored
   uint64_t pr[4];                                   // per row quarter: both halves' epilogues are here
   uint64_t o_full, o_empty, v_free;                 // the item's O complete; read; its staging read
@@ -433,7 +433,6 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars.v_land[x], kLandings<KV>);
-      mbar_init(&bars.v_empty[x], 1);
       mbar_init(&bars.s_full[x], 1);
       mbar_init(&bars.pv_full[x], kCtas * (kSoftmaxWarps + 1));
       mbar_init(&bars.p_empty[x], 1);
@@ -907,7 +906,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
             mma_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
         }
         commit(&bars.s_full[x & 1]);
-        commit(&bars.k_empty[slot]);
+        if (KV == GDA_KV_BF16) commit(&bars.k_empty[slot]);
         done_s = x;
         if (++slot == kKSlots) {
           slot = 0;
@@ -945,7 +944,6 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
               for (int k = 0; k < kHK / 16; ++k)  // 16 keys each
                 mma_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > t.ta + 2 || c > 0 || k > 0) ? 1u : 0u);
             }
-            commit(&bars.v_empty[pb]);
             commit(&bars.p_empty[pb]);
             done_o = T++;
           }
@@ -1014,7 +1012,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
     const int slots = is_v ? 2 : kKSlots;
     unsigned char* ring = sm + (is_v ? Lay::kOffV : Lay::kOffK);
     uint64_t* land = is_v ? bars.v_land : bars.k_land;
-    uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+    uint64_t* empty = is_v ? bars.p_empty : KV == GDA_KV_BF16 ? bars.k_empty : bars.s_full;  // (a ring of two goes by parity, as S does)
     const unsigned char* pool = is_v ? p.v_pool : p.k_pool;
     int it = 0, slot = 0, use = 0;
     bool ok = true;

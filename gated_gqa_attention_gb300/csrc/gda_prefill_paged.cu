@@ -28,7 +28,7 @@
 // Roles of a CTA's 16 warps, tied by mbarriers whose every wait is bounded:
 //   0-7    softmax and epilogue (row quarter warp % 4, keys or dimensions half warp / 4)
 //   8      planner: the share's items, one ahead
-//   9      issuer (in rank 0 alone, one thread): PV of tile T, then S of tile T + 2
+//   9      issuer (in rank 0 alone, one lane of it): PV of tile T, then S of tile T + 2
 //   10, 11 relays: what landed in the CTA -> proxy fence -> rank 0's barriers
 //   12-13  gather K;  14-15 gather Q and V
 // BF16 rows are copied by cp.async whose completion arrives at the ring's barrier; codes are copied
@@ -42,7 +42,7 @@
 // maxima, sums, O and the parts are FP32.
 //
 // What bounds it (GPU time, without the host's):
-//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 690 us, 1640 TFLOP/s, tensor pipe 73 %
+//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 645 us, 1760 TFLOP/s, tensor pipe 75-80 %
 //     busy.  A tile's chain is softmax 1.1 us, MMAs 1.05 us and the hops between the two CTAs, with
 //     two tiles under way: 1.33-1.55 us a tile
 //   few rows, BF16 (64 sequences of one token, a window of 4096): 98 us for 540 MB, 5.5 TB/s with
@@ -86,7 +86,8 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr int kGatherers = 4;       // half of them for K, half for Q and V
 constexpr int kThreads = 32 * (kGatherWarp + kGatherers);
 // registers of a thread (softmax, planner and issuer, gatherers) share out what the block has at its
-// launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room
+// launch, 128 each.  Spills are dear here: shared memory leaves the L1 little room.  (Without shares 48
+// single tokens over 4 bits take 75 us instead of 69, over e4m3 72 instead of 70)
 constexpr int kRegsSoftmax = 168, kRegsIssue = 56, kRegsGather = 120;
 static_assert(kRegsSoftmax >= 128 && kRegsIssue <= 128 && kRegsGather <= 128, "the softmax warps grow, the others shrink");
 static_assert(256 * kRegsSoftmax + 128 * kRegsIssue + 32 * kGatherers * kRegsGather <= kThreads * 128, "register shares");
@@ -349,6 +350,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
 template <int N>
 __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -418,7 +425,8 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
   float* xbuf = reinterpret_cast<float*>(sm + Lay::kOffX);
   float* ebuf = reinterpret_cast<float*>(sm + Lay::kOffE);
   float* qscale = reinterpret_cast<float*>(sm + Lay::kOffScale);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (so the compiler knows it to be the warp's)
   const int rank = PAIR ? (int)cluster_rank() : 0;
   const int share = (int)blockIdx.x / kCtas, shares = (int)gridDim.x / kCtas;
 
@@ -474,7 +482,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
   __syncwarp();
   if (PAIR) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
-  const uint32_t tmem = bars.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   volatile int* abort_flag = &bars.abort;
   auto fail = [&]() {
     if (bars.abort == 0) atomicOr(p.error, kErrTimeout);
@@ -878,11 +886,12 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
         }
       }
       if (!ok && lane == 0) fail();
-    } else if (rank == 0 && lane == 0 && warp == kMmaWarp) {
-      // ---------------- issuer: S(T) = Q K(T)^T into S buffer T % 2, O += P(T) V(T).  A wait in the issuing
-      // thread lets the tensor pipe run empty, so there are few, all before a group of MMAs: PV(T) and
-      // S(T + 2).  One thread's MMAs run in order: S(T + 2) follows PV(T), whose P its scores replace,
-      // without a wait between them
+    } else if (rank == 0 && warp == kMmaWarp) {
+      // ---------------- issuer: S(T) = Q K(T)^T into S buffer T % 2, O += P(T) V(T).  The whole warp goes
+      // through the loop and one lane issues, so that the MMAs' operands are in uniform registers (one lane
+      // alone in this branch: 2048 tokens 675 us instead of 645).  A wait here lets the tensor pipe run
+      // empty, so there are few, all before a group of MMAs: PV(T) and S(T + 2).  One thread's MMAs run in
+      // order: S(T + 2) follows PV(T), whose P its scores replace, without a wait between them
       const uint32_t sQ = smem_u32(sm + Lay::kOffQ), sK = smem_u32(sm + Lay::kOffK), sV = smem_u32(sm + Lay::kOffV);
       constexpr uint32_t idS = idesc_of<KV>(kRowsI, kPN, 0), idO = idesc_of<KV>(kRowsI, kD, 1);
       int it = 0, T = 0, slot = 0, use = 0;
@@ -898,66 +907,77 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
       };
       auto issue_s = [&](int x) {
         const uint32_t kb = sK + slot * kHalf;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {  // 64 head dimensions
-          const uint64_t ad = sdesc_sw128(sQ + c * kBlk, 16, 1024), bd = sdesc_sw128(kb + c * kKBlk, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 16 each (32 bytes; descriptors count 16)
-            mma_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
+          for (int c = 0; c < 4; ++c) {  // 64 head dimensions
+            const uint64_t ad = sdesc_sw128(sQ + c * kBlk, 16, 1024), bd = sdesc_sw128(kb + c * kKBlk, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 each (32 bytes; descriptors count 16)
+              mma_ss(tmem + kTmemS + (x & 1) * kPN, ad + 2 * k, bd + 2 * k, idS, (c > 0 || k > 0) ? 1u : 0u);
+          }
+          commit(&bars.s_full[x & 1]);
+          if (KV == GDA_KV_BF16) commit(&bars.k_empty[slot]);
         }
-        commit(&bars.s_full[x & 1]);
-        if (KV == GDA_KV_BF16) commit(&bars.k_empty[slot]);
+        __syncwarp();
         done_s = x;
         if (++slot == kKSlots) {
           slot = 0;
           ++use;
         }
       };
+      auto wait_all = [&](uint64_t* bar, int parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
       for (int n = 0;; ++n) {
-        Item t;
-        ok = get_item(n, &t);
+        ok = wait_all(&bars.i_full[n & 1], n >> 1);
         if (!ok) break;
-        mbar_arrive(&bars.i_empty[n & 1]);
-        if (t.b < 0) break;
-        if (t.tb == t.ta) continue;
+        const int ib = __shfl_sync(0xffffffffu, bars.item[n & 1].b, 0);
+        const int ta = __shfl_sync(0xffffffffu, bars.item[n & 1].ta, 0), tb = __shfl_sync(0xffffffffu, bars.item[n & 1].tb, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.i_empty[n & 1]);
+        if (ib < 0) break;
+        if (tb == ta) continue;
         // (S product x, two tiles ahead of PV product T)
-        ok = wait(&bars.q_full, it);
+        ok = wait_all(&bars.q_full, it);
         int x = T;
 #pragma unroll 1
-        for (int j = t.ta; j < t.tb + 2 && ok; ++j) {
-          const bool more = j < t.tb;   // S product j of the item, after PV of tile j - 2
-          if (more) ok = wait(&bars.k_full[slot], use);
+        for (int j = ta; j < tb + 2 && ok; ++j) {
+          const bool more = j < tb;   // S product j of the item, after PV of tile j - 2
+          if (more) ok = wait_all(&bars.k_full[slot], use);
           const int pb = T & 1;
-          if (j >= t.ta + 2) {
-            if (ok && j == t.ta + 2 && it > 0) ok = wait(&bars.o_empty, it - 1);  // the epilogues have read the previous O
-            ok = ok && wait(&bars.pv_full[pb], T >> 1);
+          if (j >= ta + 2) {
+            if (ok && j == ta + 2 && it > 0) ok = wait_all(&bars.o_empty, it - 1);  // the epilogues have read the previous O
+            ok = ok && wait_all(&bars.pv_full[pb], T >> 1);
           }
           if (!ok) break;
           tc_fence_after();
-          if (j >= t.ta + 2) {
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {  // a half's keys; V is MN-major (dims contiguous): LBO = stride between a
-              // CTA's 64-dim blocks, SBO = 8 key rows
-              const uint64_t bd = sdesc_sw128(sV + pb * kHalf + c * kHK * 128, kPN * 128, 1024);
-              const uint32_t a = tmem + kTmemS + pb * kPN + kHK * c;  // (P over the first half of these keys' scores)
+          if (j >= ta + 2) {
+            if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < kHK / 16; ++k)  // 16 keys each
-                mma_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > t.ta + 2 || c > 0 || k > 0) ? 1u : 0u);
+              for (int c = 0; c < 2; ++c) {  // a half's keys; V is MN-major (dims contiguous): LBO = stride between a
+                // CTA's 64-dim blocks, SBO = 8 key rows
+                const uint64_t bd = sdesc_sw128(sV + pb * kHalf + c * kHK * 128, kPN * 128, 1024);
+                const uint32_t a = tmem + kTmemS + pb * kPN + kHK * c;  // (P over the first half of these keys' scores)
+#pragma unroll
+                for (int k = 0; k < kHK / 16; ++k)  // 16 keys each
+                  mma_ts(tmem + kTmemO, a + 8 * k, bd + 128 * k, idO, (j > ta + 2 || c > 0 || k > 0) ? 1u : 0u);
+              }
+              commit(&bars.p_empty[pb]);
             }
-            commit(&bars.p_empty[pb]);
+            __syncwarp();
             done_o = T++;
           }
           if (more) {
             issue_s(x++);
-            if (j + 1 == t.tb) commit(&bars.q_empty);   // (every S product of the item)
+            if (j + 1 == tb && elect_one()) commit(&bars.q_empty);   // (every S product of the item)
+            __syncwarp();
           }
         }
         if (!ok) break;
-        commit(&bars.o_full);
+        if (elect_one()) commit(&bars.o_full);
+        __syncwarp();
         ++it;
       }
       if (!ok) {
-        fail();
+        if (lane == 0) fail();
         // the last commits cover every MMA issued before them
         if (done_s >= 0) drain(&bars.s_full[done_s & 1], done_s >> 1);
         if (done_o >= 0) drain(&bars.p_empty[done_o & 1], done_o >> 1);
@@ -1169,9 +1189,10 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
         auto gather = [&](auto of_v) {
           constexpr bool k8 = KV == GDA_KV_E4M3, kV = decltype(of_v)::value;   // (kV: half the dimensions of 128 keys)
           constexpr int kU = kPlaces, kSubs = k8 ? 4 : 2;
-          // (a tile's steps of e4m3 unrolled: with their counts at run time the warps were bound by instructions,
-          // 64 x 4 tokens 113 us instead of 94; 4 bits, whose steps are longer: unrolled 391 and 90 us, rolled 388 and 88)
-          constexpr int kUnroll = k8 ? kSubs : 1;
+          // (a tile's steps unrolled: with their counts at run time the warps were bound by instructions, 64 x 4
+          // tokens e4m3 113 us instead of 94, 48 single tokens over 4 bits 69.8 instead of 67.8.  Pairs over 4 bits,
+          // whose softmax warps have more to do: unrolled 391 us, rolled 388)
+          constexpr int kUnroll = k8 || !PAIR ? kSubs : 1;
           constexpr bool kHalves = k8 && !kV;                      // an e4m3 K row has two places
           constexpr int kPlaceRows = !k8 && kV ? 8 : 4;            // rows from one place to the next
           constexpr int kStepRows = (kHalves ? kU / 2 : kU) * kPlaceRows;

@@ -42,15 +42,16 @@
 // maxima, sums, O and the parts are FP32.
 //
 // What bounds it (GPU time, without the host's):
-//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 645 us, 1760 TFLOP/s, tensor pipe 75-80 %
-//     busy.  A tile's chain is softmax 1.1 us, MMAs 1.05 us and the hops between the two CTAs, with
-//     two tiles under way: 1.33-1.55 us a tile
+//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 645 us, 1760 TFLOP/s, tensor pipe 80 % busy.
+//     1.43 us a tile, 1.31 at the measured rate of library products.  A tile's chain is softmax 1.1 us, its
+//     MMAs and the hops between the two CTAs, with two tiles under way
 //   few rows, BF16 (64 sequences of one token, a window of 4096): 98 us for 540 MB, 5.5 TB/s with
 //     both kernels.  An item ends with 4-6 us that read nothing
-//   few rows, codes (64 sequences of 4 tokens, e4m3): 94 us, 3.0 TB/s, 1.0-1.2 us a tile of 64 keys.
-//     No unit is near its limit (tensor pipe 32 %, issue slots 31 %): a tile's steps wait for one
-//     another.  Without widening 94, without softmax 91, without both and the copies 81; eight
-//     gathering warps 100, four S products under way 94, widened from registers twice the time
+//   few rows, codes (64 sequences of 4 tokens, e4m3): 91 us, 3.1 TB/s, 1.0-1.2 us a tile of 64 keys.
+//     No unit is near its limit (tensor pipe 33 %, issue slots 31 %): a tile's steps wait for one
+//     another.  (Of 94 us before the issuing warp was converged: without widening 94, without softmax
+//     91, without both and the copies 81; eight gathering warps 100.  Four S products under way: 91;
+//     widened from registers: twice the time)
 //   one short sequence: 12.5 us, of which a share is found and the first rows come in 7-8 us and the
 //     parts are joined in 3-4 us
 // A TMA gather of four rows a time (tile::gather4) brought 3.95 us a 64 KiB tile, 2.5 TB/s in all,

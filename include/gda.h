@@ -389,7 +389,7 @@ int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
  *             first keep_first (keep_first without a window has no effect)
  *   error_word  as gda_prefill; gda_prefill_read_error reads the library's
  * A query that sees no key (more tokens than positions) gives out = 0, lse = -inf or its sink.
- * Positions that no query of the 256 rows computed together (the query heads of neighbouring tokens)
+ * Positions that no query of the rows computed together (query heads of neighbouring tokens, up to 256)
  * sees are not read.  Within these a non-finite V row that one query sees may also reach another
  * that does not see it (its probability there is 0, and 0 times it is NaN); other sequences' rows and
  * those behind a sequence's end never do.
@@ -398,7 +398,8 @@ int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
  * the call) must not be shared by calls that may overlap.  The first call on a device and stream
  * capture are as for gda_prefill.  The lengths are read on the device: two kernels, no read back,
  * no plan to keep, and a captured call follows cu_seqlens, kv_indptr and kv_indices as they are at
- * each replay.  Results do not depend on timing: the same call gives the same bits.
+ * each replay.  Results do not depend on timing: the same call gives the same bits (where a
+ * sequence's keys are cut into parts follows from the whole batch, so its last bits may too).
  */
 typedef struct gda_paged_args {
     const gda_bf16* q;

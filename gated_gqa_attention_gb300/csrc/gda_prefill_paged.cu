@@ -614,10 +614,11 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           // lazy max: it moves only by more than 2^8, so probabilities stay below 2^8 (both
           // halves of a row take the same decisions from the same values).  For FP16 it is held
           // 2^7 lower: their range ends at 2^15 instead, and weights down to 2^-21 of the row's
-          // largest are normal numbers, those below lose bits under 2^-32 of it
+          // largest are normal numbers, those below lose bits under 2^-32 of it.  The difference is compared: beyond 2^24
+          // a sum would be rounded, by enough that a probability could reach 2^16, FP16's infinity
           constexpr float kLift = KV == GDA_KV_BF16 ? 0.0f : 7.0f;
           float alpha = 1.0f;
-          if (mx > m_run + (8.0f + kLift)) {
+          if (mx - m_run > 8.0f + kLift) {
             alpha = (m_run == -INFINITY) ? 0.0f : exp2f(m_run - (mx - kLift));
             l_run *= alpha;
             e_run *= alpha;

@@ -1,0 +1,59 @@
+"""Attention over a paged cache at the ends of its arguments' ranges, against float64: scores of many
+millions, queries and descales near the ends of FP32, slots at the end of int32."""
+import math
+
+import pytest
+import torch
+
+import plain64
+from test_gpu_paged import Batch, P_STEP
+
+pytestmark = pytest.mark.gpu
+D = 256
+CODES = ["e4m3", "fp4"]
+LN2 = float(torch.tensor(math.log(2.0)))      # float32(ln 2) log2(e) is 1 in float32: log2 scores are q . k
+
+
+def set_keys(b, lens, digits):
+    """K rows that are 0 but for three dimensions (0, 16, 32), whose values digits(j) gives for position j."""
+    slots = b.k64.shape[0]
+    k = torch.zeros(slots, b.hkv, D, dtype=torch.float64)
+    at = 0
+    for _, L in lens:
+        slot = b.indices[at:at + L].long().cpu()
+        for d, x in zip((0, 16, 32), digits(torch.arange(L))):
+            k[slot, :, d] = x.double()[:, None]
+        at += L
+    b.k64 = k.cuda()
+    if b.kv == "e4m3":
+        b.k_pool = k.float().to(torch.float8_e4m3fn).cuda()
+        assert torch.equal(b.k_pool.double(), b.k64)
+    else:   # each value is its block's scale, times the code of 1
+        codes = torch.zeros(slots, b.hkv, D // 2, dtype=torch.uint8)
+        codes[..., [0, 8, 16]] = 2
+        scales = b.kw["kv_scales"].cpu()
+        scales[:, :, 0] = 0
+        scales[:, :, 0, :3] = k[..., [0, 16, 32]].float().to(torch.float8_e4m3fn).view(torch.uint8)
+        b.k_pool, b.kw["kv_scales"] = codes.cuda(), scales.cuda()
+        assert torch.equal(plain64.values(codes, scales[:, :, 0]), k)
+    b.kw["k_descale"] = 1.0
+
+
+@pytest.mark.parametrize("kv", CODES)
+@pytest.mark.parametrize("log2_base, step", [(24, 8), (25, 8), (26, 8), (27, 16)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("tokens, tile", [(1, 64), (17, 128)], ids=["lone", "pair"])
+def test_large_scores_that_rise_slowly(gda, kv, log2_base, step, sign, tokens, tile):
+    """Log2 scores of +-2^24 to +-2^27 (FP32 holds them 1 to 16 apart) that rise by 8 or 16 from tile to tile.  The
+    scores are exact (sums of three products of powers of two and digits), so the bounds have no term for them."""
+    n = 20 if tokens == 1 else 12
+    lens = [(tokens, tile * n + 5)] * (60 if tokens == 1 else 24)
+    b = Batch(lens, 8, 1, kv=kv, seed=40, gate=False)
+    # (to 16 in 4 bits: 256 + 16 * 15 and more digits than 12 or 20 tiles need)
+    set_keys(b, lens, lambda j: (torch.full_like(j, 256), (j // tile) % 16, (j // tile) // 16))
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0], b.q[..., 16], b.q[..., 32] = sign * 2.0 ** (log2_base - 8), step, 16 * step
+    o, lse = b.call(gda, scale=LN2)
+    a = b.want(scale=LN2)
+    a.sabs = torch.zeros_like(a.sabs)
+    plain64.check(o, lse.t(), a, P_STEP[kv], b.longest)

@@ -1137,8 +1137,10 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
                 o[e] = f16x2_rn(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xFFFF0000u) * up);
               *reinterpret_cast<uint4*>(at + c * kBlk) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (l8 == 0)  // (a factor below FP32's normal range would make a masked score's NaN)
-              qscale[(it & 3) * kPM + q0 + 4 * q + g8] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f);
+            // (a factor of 0 would make a masked score's NaN, an infinite one that of a score of 0)
+            if (l8 == 0)
+              qscale[(it & 3) * kPM + q0 + 4 * q + g8] =
+                  fminf(fmaxf(p.scale_log2 * __uint_as_float((uint32_t)ex << 23), 1.17549435e-38f), 3.40282347e+38f);
           }
         }
         landed(&bars.q_land);

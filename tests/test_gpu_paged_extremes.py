@@ -57,3 +57,13 @@ def test_large_scores_that_rise_slowly(gda, kv, log2_base, step, sign, tokens, t
     a = b.want(scale=LN2)
     a.sabs = torch.zeros_like(a.sabs)
     plain64.check(o, lse.t(), a, P_STEP[kv], b.longest)
+
+
+@pytest.mark.parametrize("kv", CODES)
+def test_scores_of_zero_under_a_factor_past_fp32(gda, kv):
+    """A scale times a query past 2^128: keys of zeros still score 0, and weigh the same."""
+    b = Batch([(3, 500), (1, 2000)], kv=kv, seed=44)
+    b.k_pool = torch.zeros_like(b.k_pool.view(torch.uint8)).view(b.k_pool.dtype)
+    b.k64 = torch.zeros_like(b.k64)
+    b.q = torch.ldexp(b.q.float(), torch.tensor(124, device="cuda")).bfloat16()
+    b.check(gda, scale=1024.0)

@@ -1125,8 +1125,8 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
             top >>= 23;                                             // its exponent
-            // (0 and subnormals, and infinities and NaNs, stay as they are)
-            const int ex = (top == 0u || top == 255u) ? 127 : min(max((int)top, 30), 250);
+            // (subnormal rows as if it were 1; infinities and NaNs stay as they are)
+            const int ex = top == 255u ? 127 : min(max((int)top, 1), 250);
             const float up = __uint_as_float((uint32_t)(254 - ex) << 23);   // 2^(127 - ex)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {

@@ -59,6 +59,26 @@ def test_large_scores_that_rise_slowly(gda, kv, log2_base, step, sign, tokens, t
     plain64.check(o, lse.t(), a, P_STEP[kv], b.longest)
 
 
+@pytest.mark.parametrize("kv, log2_q, log2_scale", [
+    *[("bf16", e, -4 - e) for e in (-60, 60, 100)],
+    *[(kv, e, s) for kv in CODES for e, s in ((60, -64), (100, -104), (124, -125), (-60, 56), (-90, 86), (-110, 106), (-131, 126))]])
+def test_queries_near_the_ends_of_their_range(gda, kv, log2_q, log2_scale):
+    """Query rows near 2^124, and down to subnormal ones, with a scale that brings the scores to ordinary size."""
+    b = Batch([(40, 300), (1, 2000), (3, 3)], kv=kv, seed=42)
+    b.q = torch.ldexp(b.q.float(), torch.tensor(log2_q, device="cuda")).bfloat16()
+    assert bool(b.q.isfinite().all()) and bool((b.q != 0).any())
+    b.check(gda, scale=2.0 ** log2_scale)
+
+
+@pytest.mark.parametrize("kv", CODES)
+def test_rows_of_many_sizes_in_one_call(gda, kv):
+    """Query rows from 2^-100 to 2^100 side by side: the smaller ones' scores are 0, the larger ones' of order 1."""
+    b = Batch([(40, 300)], kv=kv, seed=43)
+    e = torch.randint(-100, 101, (40, 16, 1), generator=torch.Generator().manual_seed(1)).cuda()
+    b.q = torch.ldexp(b.q.float(), e).bfloat16()
+    b.check(gda, scale=2.0 ** -104)
+
+
 @pytest.mark.parametrize("kv", CODES)
 def test_scores_of_zero_under_a_factor_past_fp32(gda, kv):
     """A scale times a query past 2^128: keys of zeros still score 0, and weigh the same."""

@@ -877,7 +877,9 @@ int gda_prefill_paged(const gda_paged_args* a, void* workspace, size_t workspace
   p.window = a->window < a->nnz ? a->window : 0;  // (no sequence is longer than nnz)
   p.keep = a->keep_first;
   p.scale_log2 = (float)factor;
-  p.v_descale = codes ? a->v_descale : 1.0f;
+  int v_exp = 0;
+  p.v_digits = 2.0f * frexpf(codes ? a->v_descale : 1.0f, &v_exp);
+  p.v_power = ldexpf(1.0f, v_exp - 1);
   p.wait_limit = wait_limit();
   char* ws = static_cast<char*>(workspace);
   p.cuts = reinterpret_cast<int4*>(ws);

@@ -752,7 +752,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
       if (p.lse && hc == 0 && r < rows) p.lse[(size_t)head * p.Tq + t.q0 + tok] = lse_of(m, e);
       unsigned char* stage = sm + Lay::kOffV;
       if (tiles) {
-        const float inv = (l == 0.0f) ? 0.0f : wo * p.v_descale / l;
+        const float inv = (l == 0.0f) ? 0.0f : wo * p.v_digits / l;
         // a dead row is 0 also where a value that its block's other rows see was not finite
         const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
         ok = __all_sync(0xffffffffu, wait(&bars.o_full, it));
@@ -772,7 +772,8 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
             uint32_t b4[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float2 v = mul_f32x2(make_float2(o[8 * u + 2 * x], o[8 * u + 2 * x + 1]), make_float2(inv, inv));
+              float2 v = mul_f32x2(make_float2(o[8 * u + 2 * x], o[8 * u + 2 * x + 1]), make_float2(inv, inv));
+              if (KV != GDA_KV_BF16) v = mul_f32x2(v, make_float2(p.v_power, p.v_power));
               b4[x] = bf16x2_rn(v.x, v.y) & keep;
             }
             *reinterpret_cast<uint4*>(dst + 16 * (x7 ^ u)) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
@@ -1435,11 +1436,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_paged_join_kernel(const 
   float wo = 1.0f;
   if (p.sinks) join_sink(p, head, m, l, e, wo);
   if (p.lse && c8 == 0) p.lse[(size_t)head * p.Tq + q0 + tok] = lse_of(m, e);
-  const float inv = (l == 0.0f) ? 0.0f : wo * p.v_descale / l;
+  const float inv = (l == 0.0f) ? 0.0f : wo * p.v_digits / l;
   const uint32_t keep = (l == 0.0f || wo == 0.0f) ? 0u : 0xFFFFFFFFu;
   uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = bf16x2_rn(o[2 * i] * inv, o[2 * i + 1] * inv) & keep;
+  for (int i = 0; i < 4; ++i) b[i] = bf16x2_rn(o[2 * i] * inv * p.v_power, o[2 * i + 1] * inv * p.v_power) & keep;
   if (p.gate) {
     uint32_t sg[4] = {g.x, g.y, g.z, g.w};
     sigmoids<1>(sg, p.table);

@@ -26,7 +26,7 @@ struct PagedParams {
   int B, Tq, nnz, Hq, Hkv, G;
   int window, keep;            // window > 0: the last `window` positions and the first `keep`
   float scale_log2;            // scale * k_descale * log2(e)
-  float v_descale;
+  float v_digits, v_power;     // V's descale: 1 <= v_digits < 2 times a power of two (a sum may be 2^46 times that)
   long long wait_limit;
   const uint16_t* table;       // BF16 sigmoid of every BF16 code
   // workspace: where the shares of the work start, and what shares that cut an item leave of it

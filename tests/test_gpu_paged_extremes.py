@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import paged64
 import plain64
 from test_gpu_paged import Batch, P_STEP
 
@@ -87,3 +88,26 @@ def test_scores_of_zero_under_a_factor_past_fp32(gda, kv):
     b.k64 = torch.zeros_like(b.k64)
     b.q = torch.ldexp(b.q.float(), torch.tensor(124, device="cuda")).bfloat16()
     b.check(gda, scale=1024.0)
+
+
+@pytest.mark.parametrize("kv", CODES)
+@pytest.mark.parametrize("vd", [2.0 ** -133, 1e-37, 3e34])
+@pytest.mark.parametrize("lens", [[(1, 30000)], [(1, 800)] * 300, [(20, 3000)] * 40], ids=["parts", "lone", "pair"])
+def test_v_descales_near_the_ends_of_their_range(gda, kv, vd, lens):
+    """A V descale below the normal numbers, near the smallest of them and far up, with outputs that BF16 holds as normal
+    numbers; the sums that O is divided by are of hundreds of thousands and millions."""
+    b = Batch(lens, 2 if len(lens) > 100 else 8, 1, kv=kv, seed=45, gate=False)
+    b.q = torch.zeros_like(b.q)
+    if kv == "e4m3":
+        codes = 0x78 | (b.v_pool.view(torch.uint8) & 0x06)                # 256 to 448
+        b.v_pool, b.v64 = codes.view(torch.float8_e4m3fn), paged64.values8(codes).cuda()
+    else:
+        b.v_pool = b.v_pool & 0x77
+        b.kw["kv_scales"][:, :, 1] = 0x7E                                  # 448 times 0 to 6
+        b.v64 = plain64.values(b.v_pool, b.kw["kv_scales"][:, :, 1]).cuda()
+    b.kw["v_descale"] = vd = float(torch.tensor(vd))
+    o, lse = b.call(gda)
+    a = b.want()
+    assert bool((a.out * vd > 2.0 ** -125).all()) and bool((a.out * vd < 1e38).all())
+    # the bound's absolute terms are for values of ordinary size: without the descale on both sides
+    plain64.check(o.double() / vd, lse.t(), a, P_STEP[kv], b.longest)

@@ -645,8 +645,9 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           // half of this warp's scores
           const float mneg = (m_run == -INFINITY) ? 0.0f : -m_run;
           // huge scores: the product is rounded first, as in the row max, or its rounding error alone
-          // could be a large exponent
-          const bool huge = __any_sync(0xffffffffu, fabsf(m_run) > 262144.0f && m_run != -INFINITY);
+          // could be a large exponent (a row's own choice: its bits do not depend on its neighbours)
+          const bool is_huge = fabsf(m_run) > 262144.0f && m_run != -INFINITY;
+          const bool huge = __any_sync(0xffffffffu, is_huge);
           float2 l2 = make_float2(0.0f, 0.0f), e2 = l2;
 #pragma unroll 1
           for (int c0 = 0; c0 < kHK; c0 += 16) {
@@ -661,9 +662,10 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
             }
             float f = factor;
             if (huge) {
+              const float before = is_huge ? factor : 1.0f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) s[c] *= factor;
-              f = 1.0f;
+              for (int c = 0; c < 16; ++c) s[c] *= before;
+              if (is_huge) f = 1.0f;
             }
             uint32_t w[8];
 #pragma unroll

@@ -11,6 +11,7 @@ from test_gpu_paged import Batch, P_STEP
 
 pytestmark = pytest.mark.gpu
 D = 256
+KV = ["bf16", "e4m3", "fp4"]
 CODES = ["e4m3", "fp4"]
 LN2 = float(torch.tensor(math.log(2.0)))      # float32(ln 2) log2(e) is 1 in float32: log2 scores are q . k
 
@@ -58,6 +59,23 @@ def test_large_scores_that_rise_slowly(gda, kv, log2_base, step, sign, tokens, t
     a = b.want(scale=LN2)
     a.sabs = torch.zeros_like(a.sabs)
     plain64.check(o, lse.t(), a, P_STEP[kv], b.longest)
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_a_large_row_leaves_its_neighbours_bits(gda, kv):
+    """A row whose scores are of many millions changes no bit of the rows computed beside it."""
+    b = Batch([(16, 900), (1, 400)], kv=kv, seed=41)
+    o, lse = b.call(gda)
+    for row, head in ((0, 0), (5, 11), (15, 7), (16, 3)):
+        q = b.q.clone()
+        b.q = q.clone()
+        b.q[row, head] *= 2.0 ** 30
+        o2, lse2 = b.call(gda)
+        b.q = q
+        rest = torch.ones(17, 16, dtype=torch.bool, device="cuda")
+        rest[row, head] = False
+        assert bool(o2.isfinite().all())
+        assert torch.equal(o[rest], o2[rest]) and torch.equal(lse.t()[rest], lse2.t()[rest])
 
 
 @pytest.mark.parametrize("kv, log2_q, log2_scale", [

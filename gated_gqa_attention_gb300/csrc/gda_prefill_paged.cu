@@ -1065,23 +1065,27 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
       // tiles ahead, looked at when used; kUnseen where no row of the item sees the position
       constexpr int kUnseen = INT_MIN, kPer = kRowsV / 32;
       int n0[kPer], n1[kPer], n2[kPer];
+      auto seen_at = [&](int j, int x, int& pos) -> bool {
+        pos = (j < t.f ? j : j - t.f + t.tl) * kPN + key0 + lane + 32 * x;
+        return (is_v || 32 * x + lane < kRowsK) && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep);
+      };
       auto look_up = [&](int j, int* to) {
-        const int base = (j < t.f ? j : j - t.f + t.tl) * kPN + key0 + lane;
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
-          const int pos = base + 32 * x;
-          const bool own = is_v || 32 * x + lane < kRowsK;
+          int pos;
           to[x] = kUnseen;
-          if (own && j < t.tb && pos < t.hi && (pos >= t.lo || pos < p.keep)) to[x] = __ldg(p.indices + t.kb + pos);
+          if (seen_at(j, x, pos)) to[x] = __ldg(p.indices + t.kb + pos);
         }
       };
       look_up(t.ta, n0);
       look_up(t.ta + 1, n1);
       if (KV != GDA_KV_BF16) look_up(t.ta + 2, n2);
-      // -1: zeros.  A row outside the pools reads as zeros and is reported
-      auto slot_of = [&](int v) -> int {
+      // the slot of tile j's key x, or -1: zeros.  A row outside the pools reads as zeros and is reported (kUnseen may
+      // be what `indices` has for a seen position; to change it there would be to wait for the load)
+      auto slot_of = [&](int v, int j, int x) -> int {
         if (v >= 0 && (long long)v < p.num_slots) return v;
-        if (v != kUnseen) atomicOr(p.error, kErrIndex);
+        int pos;
+        if (v != kUnseen || seen_at(j, x, pos)) atomicOr(p.error, kErrIndex);
         return -1;
       };
       if (is_v && ok) {
@@ -1159,7 +1163,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           look_up(j + 2, n2);
           int sl[kPer];
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n0[x]), n0[x] = n1[x], n1[x] = n2[x];
+          for (int x = 0; x < kPer; ++x) sl[x] = slot_of(n0[x], j, x), n0[x] = n1[x], n1[x] = n2[x];
           if (use > 0) ok = acquire(&empty[slot], use - 1);
           if (!ok) break;
           const uint32_t d0 = smem_u32(ring + slot * kHalf) + (row0 + g8) * 128;
@@ -1220,7 +1224,7 @@ __device__ __forceinline__ void paged_body(const PagedParams& p) {
           int ij = t.ta, islot = 0, wslot = 0;
           auto next_slots = [&](int* from) {
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) sl[x] = slot_of(from[x]);
+            for (int x = 0; x < kPer; ++x) sl[x] = slot_of(from[x], ij, x);
           };
           next_slots(n0);
           const uint32_t stage_to = smem_u32(stage);

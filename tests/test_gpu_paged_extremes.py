@@ -129,3 +129,15 @@ def test_v_descales_near_the_ends_of_their_range(gda, kv, vd, lens):
     assert bool((a.out * vd > 2.0 ** -125).all()) and bool((a.out * vd < 1e38).all())
     # the bound's absolute terms are for values of ordinary size: without the descale on both sides
     plain64.check(o.double() / vd, lse.t(), a, P_STEP[kv], b.longest)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("slot", [-2 ** 31, -2 ** 31 + 1, -2])
+def test_the_lowest_slots_are_reported(gda, kv, slot):
+    b = Batch([(4, 300), (1, 200)], kv=kv, seed=46)
+    b.indices[10] = slot
+    o, lse = b.call(gda)
+    torch.cuda.synchronize()
+    assert gda.prefill_read_error() == gda.DEVERR_INDEX
+    plain64.check(o, lse.t(), b.want(), P_STEP[kv], b.longest)
+    b.check(gda, window=50)                        # no query sees it (asserts that the error word stays 0)

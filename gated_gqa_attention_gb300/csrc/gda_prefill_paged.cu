@@ -22,7 +22,7 @@
 // max, sum, unnormalised O in FP32) in the workspace, at most two, and a second kernel joins them in
 // the order of the shares, so a result does not depend on which ends first.  What an item costs is
 // taken as linear in its number within the sequence, and as constant from the block on whose window
-// is full, so that sums over items have a closed form (linear to the last block, the prompts under a
+// and first tokens are full, so that sums over items have a closed form (linear to the last block, the prompts under a
 // window took 195 us instead of 167).
 //
 // Roles of a CTA's 16 warps, tied by mbarriers whose every wait is bounded:
@@ -206,7 +206,8 @@ __device__ __forceinline__ Range range_of(const PagedParams& p, const Seq& s, in
   return r;
 }
 // Costs of a sequence's blocks, per KV head: linear up to block `knee`, constant from there.  (Tiles
-// grow with the positions up to the last block, or to the first one whose window leaves positions out.)
+// grow with the positions up to the last block, or to the first one where the window and the first
+// tokens are both full: only from there on does a later row see no more than an earlier one.)
 template <bool PAIR>
 struct Costs {
   int mt, knee;            // blocks
@@ -220,8 +221,8 @@ struct Costs {
       first = 2LL * n0 + kItemCost;
       if (mt > 1) {
         knee = mt - 1;
-        if (p.window > 0)  // the block of the token whose position is the window's length
-          knee = (int)min((long long)knee, max(0LL, (long long)p.window - s.L + s.nq) * p.G / Geo<PAIR>::kRows + 1);
+        if (p.window > 0)  // the block of the token whose position is the window's length and p.keep
+          knee = (int)min((long long)knee, max(0LL, (long long)p.window + p.keep - s.L + s.nq) * p.G / Geo<PAIR>::kRows + 1);
         rise = ((2LL * (range_of<PAIR>(p, s, knee).n - n0)) << 16) / knee;
       }
     }

@@ -727,9 +727,10 @@ def prefill_paged(q, gate_t, k_pool, v_pool, cu_seqlens, kv_indptr, kv_indices, 
     kv_scales); a slot outside the pools reads as zeros and sets DEVERR_INDEX in the error word.
     A query sees the positions up to its own; with ``window`` the last ``window`` of them and the
     sequence's first ``keep_first``.  sinks: [Hq] float32 sink logits.  out: [Tq, Hq, D] contiguous
-    (rows of no sequence are left as they are: zeros in an ``out`` allocated here); lse: [Hq, Tq] float32
-    or None; workspace: at least prefill_paged_workspace_bytes(...) bytes (None: allocated here), not
-    shared by calls that may overlap; error_word as in prefill."""
+    (rows of no sequence are left as they are: zeros in an ``out`` allocated here, which is filled first);
+    lse: [Hq, Tq] float32 or None; workspace: at least prefill_paged_workspace_bytes(...) bytes, 42 MB
+    (None: allocated here), not shared by calls that may overlap; error_word as in prefill.
+    A batch of single tokens alone goes faster through ``decode_ex`` where the cache holds codes."""
     torch = _torch()
     sq = _tokens("q", q)
     dev = q.get_device()

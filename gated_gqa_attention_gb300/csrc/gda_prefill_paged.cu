@@ -42,9 +42,10 @@
 // maxima, sums, O and the parts are FP32.
 //
 // What bounds it (GPU time, without the host's):
-//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 645 us, 1760 TFLOP/s, tensor pipe 80 % busy.
-//     1.43 us a tile, 1.31 at the measured rate of library products.  A tile's chain is softmax 1.1 us, its
-//     MMAs and the hops between the two CTAs, with two tiles under way
+//   full rows (2048 tokens at 34816, 8 heads a group, BF16): 640 to 700 us, as the power cap has it, 1620 to
+//     1770 TFLOP/s, tensor pipe 80 % busy.  At best 1.43 us a tile, 1.31 at the measured rate of library
+//     products.  A tile's chain is softmax 1.1 us, its MMAs and the hops between the two CTAs, with two tiles
+//     under way
 //   few rows, BF16 (64 sequences of one token, a window of 4096): 98 us for 540 MB, 5.5 TB/s with
 //     both kernels.  An item ends with 4-6 us that read nothing
 //   few rows, codes (64 sequences of 4 tokens, e4m3): 91 us, 3.1 TB/s, 1.0-1.2 us a tile of 64 keys.
@@ -54,6 +55,10 @@
 //     widened from registers: twice the time)
 //   one short sequence: 12.5 us, of which a share is found and the first rows come in 7-8 us and the
 //     parts are joined in 3-4 us
+//   single tokens over codes: 48 sequences at 3000 to 5000 positions 65 us (e4m3) and 67 us (4-bit) where the
+//     decode kernels take 51 and 38, which have no chain of roles per tile (BF16: 75 and 76)
+//   prompts under a window (two of 4097, window 1024): 163 us.  A pair has 6.8 items with 58 tiles: 84 us of tiles,
+//     8 of start and join, 7 % more on the fullest share than on average, and 9 us for each item's end
 // A TMA gather of four rows a time (tile::gather4) brought 3.95 us a 64 KiB tile, 2.5 TB/s in all,
 // against 1.36 us of the cp.async here.
 #include <limits.h>
@@ -98,8 +103,8 @@ template <int KV>
 constexpr int kLandings = KV == GDA_KV_BF16 ? 16 * kGatherers : kGatherers / 2;
 constexpr int kPlaces = 16 / kGatherers;  // codes: 16-byte pieces of a step per thread
 
-// What an item costs besides its tiles, in half tiles (about 6 us: its last softmax and PV, the epilogue,
-// the next one's first S).  With 4, 10, 14 and 18: mixed batch of 4-bit rows 488, 395, 402, 410 us; 64
+// What an item costs besides its tiles, in half tiles (7 us of a pair's tiles: its last softmax and PV, the
+// epilogue, the next one's first S).  With 4, 10, 14 and 18: mixed batch of 4-bit rows 488, 395, 402, 410 us; 64
 // sequences of 4 tokens, e4m3, by pairs 130, 125, 125, 127; single tokens and prompts within 2 %.  Lone
 // CTAs' tiles are half as long, their items end sooner: 6, 10, 16: 98, 94, 93 us for those sequences.
 constexpr int kItemCost = 10;
@@ -112,6 +117,9 @@ constexpr int kItemCost = 10;
 // blocks of 128) 155 and 108, 155 and 113, 156 and 114.  63 tokens beside a chunk of 512 (71 rows on
 // average), all at 4096: 131 and 139, e4m3 143 and 147; of 1024 (135) 159 and 160, 174 and 168.  One
 // sequence of one token: 2-5 % slower.
+// The rule knows the tensors' sizes alone: empty sequences and rows of no sequence count, and a few long
+// sequences among many short ones go by lone CTAs.  2048 tokens at 18048 beside 300 empty sequences: 495 us
+// instead of 338 (e4m3 576, 376); 2000 at 18000 beside 200 single tokens: 615, by pairs 563 (e4m3 694, 554).
 constexpr int kFewRows = 128;
 
 constexpr uint32_t kBlk = 128 * 128;               // one 64-column block of 128 rows: 16 KiB

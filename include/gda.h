@@ -393,6 +393,10 @@ int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
  * sees are not read.  Within these a non-finite V row that one query sees may also reach another
  * that does not see it (its probability there is 0, and 0 times it is NaN); other sequences' rows and
  * those behind a sequence's end never do.
+ * Held in fewer bits than FP32: the probabilities, rounded to BF16 over a BF16 cache and to FP16 over codes
+ * (the divisor of O sums them as rounded; lse sums them unrounded); over codes q in FP16, each row times a
+ * power of two that brings its largest element to [1, 2) (2^124 and more: to 32 at most), where elements
+ * below 2^-14 lose bits under 2^-24; O and the sigmoid in BF16 as above.  Scores have to stay within FP32's range.
  * scale must be finite and > 0, and scale * k_descale a normal FP32 value (GDA_ERR_ARG).  D = 256.
  * The workspace (gda_prefill_paged_workspace_bytes, 256-byte aligned, contents free before and after
  * the call) must not be shared by calls that may overlap.  The first call on a device and stream
@@ -400,6 +404,11 @@ int gda_prefill_packed(const gda_packed_args* args, gda_stream_t stream);
  * no plan to keep, and a captured call follows cu_seqlens, kv_indptr and kv_indices as they are at
  * each replay.  Results do not depend on timing: the same call gives the same bits (where a
  * sequence's keys are cut into parts follows from the whole batch, so its last bits may too).
+ * Single tokens of a whole batch are gda_decode_ex's: over codes it is 1.3 (e4m3) to 1.8 times (4-bit) as fast, with
+ * one short sequence twice as fast; this call has the window whose first tokens stay visible, and mixed batches.
+ * Which of two kernels runs follows from the sizes alone: the one for few rows where total_q * Hq / Hkv is at most
+ * 128 * B.  Empty sequences and rows of no sequence count, and a captured call keeps its kernel: a long chunk in a
+ * batch padded with many empty sequences takes about 1.5 times as long as by itself, so pad with few.
  */
 typedef struct gda_paged_args {
     const gda_bf16* q;
@@ -424,7 +433,8 @@ typedef struct gda_paged_args {
     uint32_t* error_word;
 } gda_paged_args;
 
-/* Bytes of workspace gda_prefill_paged needs for these sizes (0 for invalid ones). */
+/* Bytes of workspace gda_prefill_paged needs for these sizes (0 for invalid ones): 42 MB for all of them at
+ * present, so a program keeps one and passes it. */
 size_t gda_prefill_paged_workspace_bytes(int64_t total_q, int B, int Hq, int Hkv, int D);
 
 int gda_prefill_paged(const gda_paged_args* args, void* workspace, size_t workspace_bytes, gda_stream_t stream);
